@@ -28,6 +28,7 @@ EXPORTED = (
     "mmq_debug_product_dots", "mmq_debug_refuse_smem", "mmq_debug_set_wait_limit",
     "mmq_debug_small_route", "mmq_debug_expand_tiling", "mmq_gemm_grouped_q6_k", "mmq_debug_small_ksplit",
     "mmq_debug_small_grid",
+    "mmq_kv_block_bytes", "mmq_kv_append", "mmq_kv_read", "mmq_kv_workspace_bytes", "mmq_kv_attend",
 )
 
 
@@ -320,3 +321,17 @@ def mmq_linear(x, wq, fmt: str, N: int, xq=None, out=None, stream=None):
     fn = "mmq_linear_" + fmt
     _check(fn, getattr(_lib, fn)(_ptr(x), M, K, _ptr(wq), N, _ptr(xq), _ptr(out), _stream(stream)))
     return out
+
+
+_KV = ("KVBatch", "KVCache", "Rope", "mmq_kv_append", "mmq_kv_attend", "mmq_kv_block_bytes", "mmq_kv_read",
+       "mmq_kv_workspace_bytes")
+
+
+def __getattr__(name):
+    """The key/value cache's names come with their module (which imports torch) when first used."""
+    if name in _KV:
+        from . import kv
+        for n in _KV:
+            globals()[n] = getattr(kv, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

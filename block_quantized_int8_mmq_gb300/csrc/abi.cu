@@ -28,6 +28,8 @@ int launch_status(const char* fn) {
 }
 
 bool tc_available();
+unsigned kv_cache_take_error();
+unsigned kv_attend_take_error();
 
 DeviceShape device_shape() {
     static std::atomic<int> sms[MAX_DEVICES], smem[MAX_DEVICES], l2[MAX_DEVICES];
@@ -277,6 +279,7 @@ const char* mmq_status_string(int status) {
         case MMQ_ERR_CUDA: return "MMQ_ERR_CUDA";
         case MMQ_ERR_ARG: return "MMQ_ERR_ARG";
         case MMQ_ERR_NOMEM: return "MMQ_ERR_NOMEM";
+        case MMQ_ERR_RANGE: return "MMQ_ERR_RANGE";
         default: return "MMQ_ERR_UNKNOWN";
     }
 }
@@ -496,8 +499,9 @@ int mmq_get_device_error(void* stream) {
         fprintf(stderr, "libmmq: mmq_get_device_error: %s\n", cudaGetErrorString(e));
         return MMQ_ERR_CUDA;
     }
-    const unsigned bits = tc_take_error() | tcx_take_error() | small_take_error();
-    return (bits & ERR_TIMEOUT) ? MMQ_ERR_TIMEOUT : MMQ_OK;
+    const unsigned bits = tc_take_error() | tcx_take_error() | small_take_error() | kv_cache_take_error() |
+                          kv_attend_take_error();
+    return (bits & ERR_TIMEOUT) ? MMQ_ERR_TIMEOUT : (bits & ERR_RANGE) ? MMQ_ERR_RANGE : MMQ_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,263 @@
+"""The 8-bit key/value cache: position rotation, appending, attention and reading back
+(include/mmq.h, "8-bit key/value cache").
+
+    cache = KVCache.empty(pages, heads, dim, page=64)       # records in device memory
+    rope = Rope(cos, sin)                                   # f32 [positions, rotary / 2]
+    batch = KVBatch(starts, lens, table, tokens, max_new)   # which rows belong to which sequence
+    q = mmq_kv_append(cache, batch, k, v, q=q, rope=rope)   # k and v into the cache, q rotated
+    out = mmq_kv_attend(cache, batch, q)                    # [tokens, q heads, dim]
+
+The handles only keep tensors alive and their addresses together; a program makes them once
+(a batch once per set of tensors: its tensors' contents may change between calls) and every
+computation runs in the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import MMQError, _lib, _stream
+
+BLOCK_TOKENS = 32
+F32, BF16, F16 = 0, 1, 2
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("seqs", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("table_pages", ctypes.c_int32)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("rotary", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+def _bind():
+    P, I64, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    _lib.mmq_kv_block_bytes.argtypes = [I64]
+    _lib.mmq_kv_block_bytes.restype = ctypes.c_size_t
+    _lib.mmq_kv_workspace_bytes.argtypes = [I64]
+    _lib.mmq_kv_workspace_bytes.restype = ctypes.c_size_t
+    _lib.mmq_kv_append.argtypes = [P, P, I, P, P, P, I64, P, P, P]
+    _lib.mmq_kv_read.argtypes = [P, P, I, P, P, P]
+    _lib.mmq_kv_attend.argtypes = [P, P, I, P, I64, F, I64, P, P, P, ctypes.c_size_t, P]
+
+
+_bind()
+
+
+def _device_tensor(t, dtype, what):
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{what} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
+    return t
+
+
+def mmq_kv_block_bytes(dim: int) -> int:
+    """Bytes of the record of one block: 32 tokens of one head."""
+    return int(_lib.mmq_kv_block_bytes(int(dim)))
+
+
+def mmq_kv_workspace_bytes(dim: int) -> int:
+    return int(_lib.mmq_kv_workspace_bytes(int(dim)))
+
+
+class KVCache:
+    """data: uint8 [pages, heads, page / 32, 64 * dim + 16] records, contiguous, on the GPU.  What
+    it holds for tokens that were never appended does not matter."""
+
+    def __init__(self, data):
+        _device_tensor(data, torch.uint8, "the cache")
+        if data.dim() != 4 or not data.is_contiguous():
+            raise ValueError("the cache is a contiguous [pages, heads, page / 32, record bytes] tensor")
+        self.data = data
+        self.pages, self.heads, blocks, rec = data.shape
+        self.page, self.dim = blocks * BLOCK_TOKENS, (rec - 16) // 64
+        if mmq_kv_block_bytes(self.dim) != rec:
+            raise ValueError(f"records of {rec} bytes: 64 * dim + 16 with dim 64, 128 or 256 are taken")
+        self.device = data.device
+        self._c = _Cache(data.data_ptr(), self.pages, self.page, self.heads, self.dim)
+        self._p = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, page: int = 64, device="cuda"):
+        rec = mmq_kv_block_bytes(dim)
+        if rec == 0 or page < BLOCK_TOKENS or page % BLOCK_TOKENS:
+            raise ValueError("dim must be 64, 128 or 256 and page a multiple of 32")
+        return cls(torch.empty((pages, heads, page // BLOCK_TOKENS, rec), dtype=torch.uint8, device=device))
+
+
+class KVBatch:
+    """Sequences and their new tokens (see include/mmq.h): int32 CUDA tensors starts [seqs + 1],
+    lens [seqs] (the lengths WITH the new tokens) and table [seqs, pages]; tokens: rows of the
+    packed row arrays; max_new: no sequence has more new tokens."""
+
+    def __init__(self, starts, lens, table, tokens: int, max_new: int):
+        for t, what in ((starts, "starts"), (lens, "lens"), (table, "table")):
+            _device_tensor(t, torch.int32, what)
+        seqs = lens.shape[0]
+        if lens.dim() != 1 or starts.shape != (seqs + 1,) or table.dim() != 2 or table.shape[0] != seqs:
+            raise ValueError("starts is [seqs + 1], lens [seqs] and table [seqs, pages]")
+        if not starts.is_contiguous() or not lens.is_contiguous() or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("starts, lens and the rows of table must be contiguous")
+        self.starts, self.lens, self.table, self.tokens, self.max_new = starts, lens, table, int(tokens), int(max_new)
+        stride = table.stride(0) if seqs > 1 else table.shape[1]
+        self._c = _Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), stride, seqs, self.tokens,
+                         self.max_new, table.shape[1])
+        self._p = ctypes.addressof(self._c)
+
+
+class Rope:
+    """Rotation tables cos, sin: f32 [positions, rotary / 2].  Pairs (i, i + rotary / 2), or
+    (2i, 2i + 1) where interleaved."""
+
+    def __init__(self, cos, sin, interleaved: bool = False):
+        for t in (cos, sin):
+            _device_tensor(t, torch.float32, "a rotation table")
+        if cos.dim() != 2 or cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin are contiguous [positions, rotary / 2] tensors")
+        self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
+        self._c = _Rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
+        self._p = ctypes.addressof(self._c)
+
+
+def _rows(t, cache, batch, dtype, heads, what):
+    """A row array's description; strides as the tensor has them (the C entry checks alignment)."""
+    if t.dim() != 3 or t.shape[0] != batch.tokens or t.shape[2] != cache.dim or (heads and t.shape[1] != heads):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}: [{batch.tokens}, {heads or 'heads'}, {cache.dim}] is wanted")
+    if t.dtype != dtype or t.device != cache.device:
+        raise ValueError(f"{what} is {t.dtype} on {t.device}: {dtype} on {cache.device} is wanted")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{what}: the last axis must be contiguous")
+    return _Rows(t.data_ptr(), ts, hs)
+
+
+def _dtype(t):
+    d = _DTYPES.get(t)
+    if d is None:
+        raise ValueError(f"{t}: float32, bfloat16 and float16 are taken")
+    return d
+
+
+def _run(fn, device, stream, made, *args):
+    """Call fn with the stream as its last argument; `made` (tensors allocated here) stay with a
+    stream other than the one they were allocated on."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        s = _stream(stream)
+        if isinstance(stream, torch.cuda.Stream):
+            for t in made:
+                t.record_stream(stream)
+    st = getattr(_lib, fn)(*args, s)
+    if st != 0:
+        raise MMQError(fn, st)
+
+
+def _out(t, shape, dtype, cache, what):
+    if t.shape != shape or t.dtype != dtype or t.device != cache.device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} {tuple(shape)} tensor on {cache.device}")
+    return t
+
+
+def mmq_kv_append(cache, batch, k, v, q=None, rope=None, q_out=None, stream=None):
+    """Keys and values [tokens, cache.heads, dim] into the cache, rotated by `rope` on the way (the
+    values are not rotated); returns the rotated queries [tokens, q heads, dim] where q is given."""
+    dt = k.dtype
+    d = _dtype(dt)
+    kr = _rows(k, cache, batch, dt, cache.heads, "k")
+    vr = _rows(v, cache, batch, dt, cache.heads, "v")
+    made = []
+    qp = qo = None
+    heads = 0
+    if q is not None:
+        qr = _rows(q, cache, batch, dt, 0, "q")
+        qp, heads = ctypes.addressof(qr), q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=cache.device)
+            made.append(q_out)
+        else:
+            _out(q_out, q.shape, dt, cache, "q_out")
+        qo = q_out.data_ptr()
+    _run("mmq_kv_append", cache.device, stream, made, cache._p, batch._p, d, ctypes.addressof(kr), ctypes.addressof(vr),
+         qp, heads, None if rope is None else rope._p, qo)
+    return q_out if q is not None else None
+
+
+def mmq_kv_read(cache, batch, dtype=torch.float32, k_out=None, v_out=None, stream=None):
+    """The cached keys and values of the batch's tokens, [tokens, cache.heads, dim] of `dtype`."""
+    d = _dtype(dtype)
+    shape = torch.Size((batch.tokens, cache.heads, cache.dim))
+    made = []
+    outs = []
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=cache.device)
+            made.append(t)
+        else:
+            _out(t, shape, dtype, cache, what)
+        outs.append(t)
+    _run("mmq_kv_read", cache.device, stream, made, cache._p, batch._p, d, outs[0].data_ptr(), outs[1].data_ptr())
+    return outs[0], outs[1]
+
+
+_workspaces: dict = {}
+
+
+def _workspace(cache, stream):
+    """The package's own workspace of a stream: calls on one stream run one after another."""
+    s = torch._C._cuda_getCurrentRawStream(cache.device.index) if stream is None else int(_stream(stream).value or 0)
+    key = (cache.device.index, s, cache.dim)
+    ws = _workspaces.get(key)
+    if ws is None:
+        ws = torch.empty(mmq_kv_workspace_bytes(cache.dim), dtype=torch.uint8, device=cache.device)
+        if stream is not None:
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                   else torch.cuda.ExternalStream(s, device=cache.device)):
+                ws[:4096].zero_()
+        else:
+            ws[:4096].zero_()
+        _workspaces[key] = ws
+    return ws
+
+
+def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of the rotated queries [tokens, q heads, dim] over the cache: [tokens, q
+    heads, dim].  scale: 1 / sqrt(dim) by default.  window: how many of the latest tokens a row
+    sees (0: all).  lse: an f32 [tokens, q heads] tensor for the logarithm of the softmax's sum.
+    workspace: a uint8 tensor of mmq_kv_workspace_bytes(dim) bytes, its first 4096 zero, for calls
+    that may overlap others of the same stream (a captured graph replayed elsewhere); by default
+    the package keeps one for each stream."""
+    dt = q.dtype
+    d = _dtype(dt)
+    qr = _rows(q, cache, batch, dt, 0, "q")
+    made = []
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=cache.device)
+        made.append(out)
+    else:
+        _out(out, q.shape, dt, cache, "out")
+    if lse is not None:
+        _out(lse, q.shape[:2], torch.float32, cache, "lse")
+    if workspace is None:
+        workspace = _workspace(cache, stream)
+    elif workspace.dtype != torch.uint8 or workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {cache.device}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.dim)
+    _run("mmq_kv_attend", cache.device, stream, made, cache._p, batch._p, d, ctypes.addressof(qr), q.shape[1], scale,
+         window, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out

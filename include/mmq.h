@@ -95,7 +95,8 @@ typedef enum mmq_status {
     MMQ_ERR_TIMEOUT = -7,     /* a device-side bounded wait ran out (device error word) */
     MMQ_ERR_CUDA = -8,        /* another CUDA runtime error (device query, tensor map) */
     MMQ_ERR_ARG = -9,         /* an argument outside its documented set */
-    MMQ_ERR_NOMEM = -10       /* the scratch allocation of the expanded path failed */
+    MMQ_ERR_NOMEM = -10,      /* the scratch allocation of the expanded path failed */
+    MMQ_ERR_RANGE = -11       /* a value in device memory was outside its range (device error word) */
 } mmq_status;
 
 /* Human-readable name of a status code.  Never NULL; the string is static. */
@@ -411,6 +412,135 @@ int mmq_set_path(int path);
  * (MMQ_PATH_SMALL, MMQ_PATH_TC or MMQ_PATH_EXPAND), or 0 before any. */
 int mmq_last_path(void);
 
+/*
+ * ---------------------------------------------------------------- 8-bit key/value cache
+ *
+ * Between the projections of an attention layer: the position rotation, a paged cache of
+ * keys and values held as 8-bit blocks, and attention over that cache.
+ *
+ * A block is 32 consecutive tokens of one sequence and one key/value head; its record is
+ *   int8 kc[32][dim] @0, int8 vc[32][dim] @32*dim, f32 dk @64*dim, f32 dv @64*dim + 4,
+ *   8 reserved bytes: 64*dim + 16 bytes (mmq_kv_block_bytes), and the key of token i is
+ *   kc[i][:] * dk, its value vc[i][:] * dv.  One contiguous 16-byte-strided record brings a
+ *   block's codes and scales in one copy.
+ * The cache is [pages][heads][page/32] records.  Token p of sequence b lies in page
+ * table[b][p / page], block (p % page) / 32, row p % 32.
+ *
+ * A batch is `seqs` sequences with their new tokens packed one sequence after another:
+ * sequence b has the rows starts[b] .. starts[b+1] - 1 (n_b = starts[b+1] - starts[b], 0
+ * allowed) of every row array, and its length lens[b] COUNTS them, so row starts[b] + t is
+ * token (position) lens[b] - n_b + t.  A row whose position is negative (lens[b] < n_b: an idle
+ * slot of a captured batch) is padding: it is not appended and sees no token.  Rows that no
+ * sequence has (before starts[0], past starts[seqs]) are left alone.
+ *
+ * starts, lens and table are device memory, read when the call runs on its stream, so a
+ * captured call follows their contents.  A value there outside its range (starts
+ * decreasing or past `tokens`; a length below 0 or above table_pages * page; more than
+ * max_new new tokens; a page number outside [0, pages) among those that the length needs;
+ * a position past the rotation tables) is never followed: it sets the device error word
+ * (MMQ_ERR_RANGE), and what the call would have done there is skipped.  Table entries past a
+ * sequence's length are not read.
+ */
+typedef struct mmq_kv_cache {
+    void* data;    /* device, 16-byte aligned, pages*heads*(page/32)*mmq_kv_block_bytes(dim) bytes */
+    int64_t pages; /* >= 1 */
+    int32_t page;  /* tokens per page: a positive multiple of 32 */
+    int32_t heads; /* key/value heads */
+    int32_t dim;   /* values per head: 64, 128 or 256 */
+} mmq_kv_cache;
+
+typedef struct mmq_kv_batch {
+    const int32_t* starts; /* device [seqs + 1] */
+    const int32_t* lens;   /* device [seqs] */
+    const int32_t* table;  /* device [seqs][table_stride], the first table_pages of a row are its pages */
+    int64_t table_stride;
+    int32_t seqs;        /* >= 0 */
+    int32_t tokens;      /* rows of the packed row arrays, >= 0 */
+    int32_t max_new;     /* no sequence has more new tokens */
+    int32_t table_pages; /* pages per sequence, at most */
+} mmq_kv_batch;
+
+/* Element types of the row arrays. */
+enum { MMQ_F32 = 0, MMQ_BF16 = 1, MMQ_F16 = 2 };
+
+/* Rows [tokens][heads][dim] in device memory: the dim values contiguous, strides in elements,
+ * every row 16-byte aligned (the base and both strides), so slices of a joint projection do. */
+typedef struct mmq_kv_rows {
+    const void* data;
+    int64_t token_stride, head_stride;
+} mmq_kv_rows;
+
+/* Rotation tables: f32 [rows][rotary/2], 16-byte aligned.  The first `rotary` values of a head
+ * (a multiple of 8, at most dim) turn in pairs, (i, i + rotary/2) or, interleaved,
+ * (2i, 2i + 1); the others pass. */
+typedef struct mmq_kv_rope {
+    const float *cos, *sin;
+    int64_t rows;
+    int32_t rotary, interleaved;
+} mmq_kv_rope;
+
+/* Bytes of one block's record: 64*dim + 16, or 0 for a dim the cache does not take. */
+size_t mmq_kv_block_bytes(int64_t dim);
+
+/*
+ * Append the batch's new keys and values to the cache, rotating keys (and queries) on the way.
+ *   k, v: rows of `dtype`, cache->heads heads.  q (NULL: none): rows of q_heads heads; q_out:
+ *   their rotated rows, [tokens][q_heads][dim] contiguous, `dtype`, 16-byte aligned.
+ *   rope: NULL leaves keys and queries unrotated.
+ * In f32, each product and sum rounded: y1 = x1*cos - x2*sin, y2 = x2*cos + x1*sin, with the
+ * tables' row of the token's position.  For each record that new tokens fall into, keys and
+ * values alike:
+ *   d' = max(d of the record if it keeps older tokens of the sequence, amax(new) / 127),
+ *   0 if below 2^-100;
+ *   older codes become clamp(rint(c * (d / d')), -127, 127) where d' differs from d;
+ *   new codes clamp(rint(x / d'), -127, 127) (IEEE divisions, ties to even; 0 where d' = 0).
+ * Bit-exact by that definition.  Rows of the record past the sequence's end keep their bytes;
+ * padding rows of q_out are left alone.
+ * A record must belong to one sequence of the batch: pages that sequences share are only read.
+ * Finite inputs are required.  Errors: MMQ_ERR_SHAPE, MMQ_ERR_NULL, MMQ_ERR_ALIGN,
+ * MMQ_ERR_ARG (dtype), MMQ_ERR_LAUNCH.
+ */
+int mmq_kv_append(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtype, const mmq_kv_rows* k,
+                  const mmq_kv_rows* v, const mmq_kv_rows* q, int64_t q_heads, const mmq_kv_rope* rope, void* q_out,
+                  void* stream);
+
+/*
+ * The values that the cache holds for the batch's tokens (the last n_b of each sequence):
+ * code * d in f32, rounded once to `dtype`.  k_out, v_out: [tokens][heads][dim] contiguous,
+ * 16-byte aligned; padding rows are left alone.  Errors as mmq_kv_append.
+ */
+int mmq_kv_read(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtype, void* k_out, void* v_out,
+                void* stream);
+
+/* Bytes of mmq_kv_attend's workspace on the current device (152 SMs if none can be queried),
+ * or 0 for a dim the cache does not take. */
+size_t mmq_kv_workspace_bytes(int64_t dim);
+
+/*
+ * Attention of the batch's query rows over the cache.  Row t of sequence b at position p sees
+ * the tokens j <= p, with window > 0 only the last `window` of them (j > p - window); query
+ * head h reads key/value head h / (q_heads / heads).
+ *   out = sum_j w_j v_j,  w = softmax_j(scale * q . k_j);  lse = ln sum_j exp(scale * q . k_j)
+ * A row that sees no token (a padding row) gets zeros and lse -inf.
+ *   q: rows of `dtype`.  out: [tokens][q_heads][dim] contiguous, `dtype`, 16-byte aligned.
+ *   lse (NULL: not wanted): f32 [tokens][q_heads].  scale: finite, > 0.  window >= 0.
+ *   q_heads: a multiple of cache->heads.
+ *   workspace: at least mmq_kv_workspace_bytes(dim) bytes, 256-byte aligned, its first 4096
+ *   bytes zero before its first use; every call leaves them zero again, so one workspace
+ *   serves any number of calls in stream order, but never two that may overlap in time.
+ * Accuracy: the codes and their scales enter exactly; sums, the softmax's statistics and the
+ * output accumulate in f32.  For bf16 and f16 rows the weights are rounded to f16 before the
+ * second product (2^-11 relative); for f32 rows queries and weights are split into two f16
+ * terms each (2^-22).  The order of summation depends on the shapes and lengths alone, so
+ * repeated calls give the same bits.
+ * Codes and scales of rows past a sequence's length may hold anything.  Errors: MMQ_ERR_SHAPE,
+ * MMQ_ERR_NULL, MMQ_ERR_ALIGN, MMQ_ERR_ARG (dtype, scale, window), MMQ_ERR_SMEM,
+ * MMQ_ERR_LAUNCH.
+ */
+int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtype, const mmq_kv_rows* q,
+                  int64_t q_heads, float scale, int64_t window, void* out, float* lse, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 /* Per-kernel device timing, for tests and benchmarks.  While enabled, every kernel the
  * library launches is bracketed by two CUDA events on its stream.  On a stream being
  * captured into a graph the two records become event-record nodes of the graph (their
@@ -430,8 +560,9 @@ int mmq_profile_enable(int on);
 int mmq_profile_read(mmq_kernel_time* out, int capacity, int reset);
 
 /* Synchronizes `stream`, then reads and clears the device error word of every kernel
- * in the library.  Returns MMQ_OK, MMQ_ERR_TIMEOUT (a bounded wait ran out) or
- * MMQ_ERR_CUDA (the synchronize itself failed). */
+ * in the library.  Returns MMQ_OK, MMQ_ERR_TIMEOUT (a bounded wait ran out),
+ * MMQ_ERR_RANGE (a length, start, page number or position that a key/value cache call read
+ * from device memory was outside its range) or MMQ_ERR_CUDA (the synchronize itself failed). */
 int mmq_get_device_error(void* stream);
 
 #ifdef __cplusplus

@@ -1,0 +1,138 @@
+"""The key/value cache without a GPU: record sizes, the refusals of its C entry points (nothing is
+launched, so any aligned address stands for device memory), and the reference the GPU tests compare
+with, pinned by values worked by hand."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import kv_ref
+
+mmq = pytest.importorskip("block_quantized_int8_mmq_gb300")
+torch = pytest.importorskip("torch")
+from block_quantized_int8_mmq_gb300 import kv  # noqa: E402
+
+SHAPE, NULL, ALIGN, ARG = -1, -3, -4, -9
+A = 1 << 20  # a 16-byte aligned address
+
+
+def call(fn, **change):
+    """One of the entries on well-formed arguments but for `change`."""
+    f = dict(data=A, pages=4, page=64, heads=2, dim=128, starts=A, lens=A, table=A, table_stride=8, seqs=1, tokens=0,
+             max_new=1, table_pages=8, dtype=0, k=A, v=A, q=A, ts=512, hs=128, q_heads=4, cos=A, sin=A, rows=64,
+             rotary=128, q_out=A, out=A, lse=A, ws=A, ws_bytes=1 << 40, scale=0.1, window=0, cache=True, batch=True)
+    f.update(change)
+    L = mmq.lib()
+    c = kv._Cache(f["data"], f["pages"], f["page"], f["heads"], f["dim"])
+    b = kv._Batch(f["starts"], f["lens"], f["table"], f["table_stride"], f["seqs"], f["tokens"], f["max_new"],
+                  f["table_pages"])
+    rows = [kv._Rows(f[n], f["ts"], f["hs"]) for n in "kvq"]
+    rope = kv._Rope(f["cos"], f["sin"], f["rows"], f["rotary"], 0)
+    p = ctypes.addressof
+    head = (p(c) if f["cache"] else None, p(b) if f["batch"] else None, f["dtype"])
+    if fn == "append":
+        return L.mmq_kv_append(*head, p(rows[0]), p(rows[1]), p(rows[2]), f["q_heads"], p(rope), f["q_out"], None)
+    if fn == "read":
+        return L.mmq_kv_read(*head, f["k"], f["v"], None)
+    return L.mmq_kv_attend(*head, p(rows[2]), f["q_heads"], f["scale"], f["window"], f["out"], f["lse"], f["ws"],
+                           f["ws_bytes"], None)
+
+
+def test_sizes():
+    assert [mmq.mmq_kv_block_bytes(d) for d in (64, 128, 256)] == [4112, 8208, 16400]
+    assert mmq.mmq_kv_block_bytes(96) == mmq.mmq_kv_block_bytes(0) == mmq.mmq_kv_block_bytes(-64) == 0
+    assert mmq.mmq_kv_workspace_bytes(128) > 4096 and mmq.mmq_kv_workspace_bytes(100) == 0
+    assert mmq.mmq_status_string(-11) == "MMQ_ERR_RANGE"
+
+
+@pytest.mark.parametrize("fn", ["append", "read", "attend"])
+def test_no_tokens_is_no_work(fn):
+    assert call(fn) == 0
+    assert call(fn, k=None, v=None, q=None, out=None, q_out=None) == 0
+    assert call(fn, tokens=5, seqs=0, starts=None, lens=None, table=None) == 0
+
+
+@pytest.mark.parametrize("fn", ["append", "read", "attend"])
+@pytest.mark.parametrize("change,status", [
+    (dict(cache=False), NULL), (dict(batch=False), NULL), (dict(data=None), NULL), (dict(data=A + 8), ALIGN),
+    (dict(dim=96), SHAPE), (dict(dim=0), SHAPE), (dict(page=48), SHAPE), (dict(page=0), SHAPE), (dict(heads=0), SHAPE),
+    (dict(pages=0), SHAPE), (dict(pages=1 << 31), SHAPE), (dict(seqs=-1), SHAPE), (dict(tokens=-1), SHAPE),
+    (dict(max_new=-1), SHAPE), (dict(table_pages=-1), SHAPE), (dict(table_stride=7), SHAPE),
+    (dict(table_pages=1 << 25, table_stride=1 << 25), SHAPE), (dict(starts=None), NULL), (dict(lens=None), NULL),
+    (dict(table=None), NULL), (dict(lens=A + 2), ALIGN), (dict(dtype=3), ARG), (dict(dtype=-1), ARG)])
+def test_refusals_of_the_cache_and_the_batch(fn, change, status, capfd):
+    assert call(fn, **change) == status
+    assert "mmq_kv_" + fn in capfd.readouterr().err
+
+
+@pytest.mark.parametrize("fn,change,status", [
+    ("append", dict(k=None, tokens=1), NULL), ("append", dict(v=None, tokens=1), NULL),
+    ("append", dict(k=A + 8), ALIGN), ("append", dict(ts=514), ALIGN), ("append", dict(hs=130), ALIGN),
+    ("append", dict(dtype=1, hs=132), ALIGN), ("append", dict(q_heads=3), SHAPE), ("append", dict(q_heads=0), SHAPE),
+    ("append", dict(q_out=None, tokens=1), NULL), ("append", dict(q_out=A + 4), ALIGN),
+    ("append", dict(rotary=132), SHAPE), ("append", dict(rotary=12), SHAPE), ("append", dict(cos=None), NULL),
+    ("append", dict(sin=A + 4), ALIGN), ("read", dict(k=None, tokens=1), NULL), ("read", dict(v=A + 8), ALIGN),
+    ("attend", dict(q=None, tokens=1), NULL), ("attend", dict(out=None, tokens=1), NULL), ("attend", dict(out=A + 8), ALIGN),
+    ("attend", dict(lse=A + 2), ALIGN), ("attend", dict(ws=None), NULL), ("attend", dict(ws=A + 16), ALIGN),
+    ("attend", dict(ws_bytes=4096), SHAPE), ("attend", dict(scale=0.0), ARG), ("attend", dict(scale=-1.0), ARG),
+    ("attend", dict(scale=float("nan")), ARG), ("attend", dict(scale=float("inf")), ARG), ("attend", dict(window=-1), ARG),
+    ("attend", dict(q_heads=3), SHAPE)])
+def test_refusals_of_each_call(fn, change, status, capfd):
+    assert call(fn, **change) == status
+    assert "mmq_kv_" + fn in capfd.readouterr().err
+
+
+def test_handles_refuse_host_tensors():
+    with pytest.raises(ValueError):
+        mmq.KVCache(torch.zeros((1, 1, 1, 8208), dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        mmq.KVBatch(torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
+                    torch.zeros((1, 1), dtype=torch.int32), 0, 0)
+    with pytest.raises(ValueError):
+        mmq.Rope(torch.zeros(4, 4), torch.zeros(4, 4))
+    with pytest.raises(ValueError):
+        mmq.KVCache.empty(1, 1, 96)
+
+
+def test_reference_append_by_hand():
+    """Two tokens into a block that keeps one: 127 * 2 and -254 against an older code 100 at scale 1."""
+    dim = 64
+    data = np.zeros((1, 1, 1, kv_ref.rec_bytes(dim)), np.uint8)
+    kc, vc, d = kv_ref.split(data[0, 0, 0], dim)
+    kc[0, :3] = (100, -127, 1)
+    d[:] = (1.0, 4.0)
+    vc[0, 0] = 5
+    vc[1:] = 77  # rows that are not the sequence's
+    k, v = np.zeros((2, 1, dim), np.float32), np.zeros((2, 1, dim), np.float32)
+    k[0, 0, 0], k[1, 0, 1] = 254.0, -3.0
+    v[1, 0, 2] = 508.0
+    kv_ref.append(data, [0, 2], [3], np.array([[0]]), k, v, dim)
+    assert d.tolist() == [2.0, 4.0]
+    assert kc[0, :3].tolist() == [50, -64, 0]  # 100 / 2, rint(-63.5) to even, rint(0.5) to even
+    assert kc[1, 0] == 127 and kc[2, 1] == -2  # rint(-1.5) to even
+    assert vc[0, 0] == 5 and vc[2, 2] == 127 and (vc[3:] == 77).all()
+
+
+def test_reference_attention_by_hand():
+    """One key twice as likely as the other: out = (2 v0 + v1) / 3, lse = ln 3 with s = (ln 2, 0)."""
+    dim = 64
+    data = np.zeros((1, 1, 1, kv_ref.rec_bytes(dim)), np.uint8)
+    kc, vc, d = kv_ref.split(data[0, 0, 0], dim)
+    kc[0, 0] = 100
+    vc[0, 0], vc[1, 1] = 3, 6
+    d[:] = (0.01, 1.0)
+    q = np.zeros((2, 1, dim))
+    q[:, 0, 0] = np.log(2.0) / (100 * float(np.float32(0.01)))
+    out, lse, _, _ = kv_ref.attend(data, [0, 2], [2], np.array([[0]]), q, dim, 1.0)
+    assert np.allclose(out[1, 0, :2], [2.0, 2.0], atol=1e-12) and np.isclose(lse[1, 0], np.log(3.0))
+    assert np.allclose(out[0, 0, :2], [3.0, 0.0])
+    out, _, _, _ = kv_ref.attend(data, [0, 2], [2], np.array([[0]]), q, dim, 1.0, window=1)
+    assert np.allclose(out[1, 0, :2], [0.0, 6.0])
+
+
+def test_reference_rotation_is_a_rotation():
+    cos, sin = np.float32([[1, 1], [0, 0.6]]), np.float32([[0, 0], [1, 0.8]])
+    x = np.float32([1, 2, 3, 4, 5])
+    assert np.allclose(kv_ref.rotate(x, 1, cos, sin, False), [-3, 2 * 0.6 - 4 * 0.8, 1, 4 * 0.6 + 2 * 0.8, 5])
+    assert np.allclose(kv_ref.rotate(x, 1, cos, sin, True), [-2, 1, 3 * 0.6 - 4 * 0.8, 4 * 0.6 + 3 * 0.8, 5])
+    assert kv_ref.rotate(x, 0, cos, sin, True).tolist() == x.tolist()
