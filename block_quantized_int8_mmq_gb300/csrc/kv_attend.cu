@@ -3,9 +3,14 @@
 // the output, with the running maximum and sum of the softmax in f32.
 #include <math.h>
 
-#include "kv.cuh"
+#include "kv_attend.cuh"
 
 namespace mmq {
+
+int kv_stream_rows(int dim);
+int kv_stream_launch(const kv::Attend& a, int rows, cudaStream_t s);
+unsigned kv_stream_take_error();
+
 namespace {
 
 using namespace kv;
@@ -99,6 +104,10 @@ int attend_t(const Cache& c, const Batch& b, const Rows& q, int q_heads, float s
 
 int kv_attend_launch(const Cache& c, const Batch& b, int dtype, const Rows& q, int q_heads, float scale, int window,
                      void* out, float* lse, void* ws, cudaStream_t s) {
+    const int group = q_heads / c.heads;
+    const Attend a{c, b, q, q_heads, group, dtype, window, scale * 1.44269504088896341f, out, lse,
+                   static_cast<uint8_t*>(ws)};
+    if ((long long)b.max_new * group <= kv_stream_rows(c.dim)) return kv_stream_launch(a, b.max_new * group, s);
     return dtype == MMQ_F32    ? attend_t<float>(c, b, q, q_heads, scale, window, out, lse, s)
            : dtype == MMQ_BF16 ? attend_t<__nv_bfloat16>(c, b, q, q_heads, scale, window, out, lse, s)
                                : attend_t<__half>(c, b, q, q_heads, scale, window, out, lse, s);
@@ -114,7 +123,7 @@ unsigned kv_attend_take_error() {
         const unsigned zero = 0;
         cudaMemcpyToSymbol(g_kv_attend_error, &zero, sizeof(zero));
     }
-    return v;
+    return v | kv_stream_take_error();
 }
 
 }  // namespace mmq

@@ -1,0 +1,100 @@
+// What the two attention kernels over the 8-bit cache share: the arguments, the sharing-out of
+// the work and the joining of partial results.
+//
+// The work is the list of all (sequence, [row tile,] head) units, each a run of key/value
+// tiles, laid end to end: T tiles in all.  Worker w of W takes tiles floor(T w / W) ..
+// floor(T (w + 1) / W) - 1, whatever the lengths are, so every SM streams the same number of
+// tiles and no length has to be known on the host.  A unit that lies in one CTA's range is
+// finished there; one that spans CTAs leaves, per CTA, a partial result (O, m, l) in the
+// workspace (a CTA can have one unit that came in, slot 0, and one that goes out, slot 1), and
+// the last CTA to arrive adds the parts in CTA order: the order of summation depends on the
+// lengths alone.  The arrival counter of a unit is that of the CTA in which it starts (only
+// one unit goes out of a CTA), and the last arriver sets it back to zero.
+//
+// The softmax, in base 2, with the value scale folded into the exponent: for a block with
+// scales dk, dv and a query scaled by a = scale * log2(e) * dk,
+//   t_j = a (q . kc_j) + log2 dv,  P_j = 2^(t_j - m),  O = sum P_j vc_j,  l = sum P_j / dv,
+// out = O / l.  The value codes enter the second product as they are, and 1 / dv is applied
+// once per block and row, not once per weight.  m only has to keep 2^(t - m) inside f16: it is
+// set SHIFT below the running maximum and moved when a t passes m + LIMIT, so the accumulators
+// are rescaled a few times per row, not once per tile; weights below 2^-(25 + SHIFT) of the
+// largest vanish in f16.  A block whose values are all zero (dv = 0) stands in with 2^-60.
+#pragma once
+
+#include <math.h>
+
+#include "kv.cuh"
+
+namespace mmq {
+namespace kv {
+
+constexpr float SHIFT = 7.f, LIMIT = 15.f;  // weights up to 2^15 < 65504
+constexpr float M_NONE = -1e30f;            // m of a row that has seen nothing
+constexpr int WS_COUNTERS = 4096;           // bytes of arrival counters before the partial results
+constexpr int WS_ROWS = 256;                // rows a partial result holds at most
+
+struct Attend {
+    Cache c;
+    Batch bt;
+    Rows q;
+    int q_heads, group, dtype, window;
+    float scale2;  // scale * log2(e)
+    void* out;
+    float* lse;
+    uint8_t* ws;
+};
+
+__device__ __forceinline__ int work_start(long long total, int w, int workers) { return (int)(total * w / workers); }
+// the worker whose range holds tile x
+__device__ __forceinline__ int work_owner(int total, int x, int workers) {
+    return (int)((((long long)x + 1) * workers - 1) / total);
+}
+
+__device__ __forceinline__ float* part_slot(const Attend& a, int cta, int slot) {
+    return reinterpret_cast<float*>(a.ws + WS_COUNTERS) + ((long long)cta * 2 + slot) * WS_ROWS * (a.c.dim + 2);
+}
+
+// first key that row 0 of a sequence (at position first) sees
+__device__ __forceinline__ int first_key(const Attend& a, int first) { return a.window > 0 ? max(0, first - a.window + 1) : 0; }
+
+__device__ __forceinline__ float4 load_row4(const Attend& a, long long row, int h, int d) {
+    const long long at = row * a.q.token_stride + h * a.q.head_stride + d;
+    return a.dtype == MMQ_F32    ? Elem<float>::load4(static_cast<const float*>(a.q.data) + at)
+           : a.dtype == MMQ_BF16 ? Elem<__nv_bfloat16>::load4(static_cast<const __nv_bfloat16*>(a.q.data) + at)
+                                 : Elem<__half>::load4(static_cast<const __half*>(a.q.data) + at);
+}
+__device__ __forceinline__ void store_out4(const Attend& a, long long row, int h, int d, float4 v) {
+    const long long at = (row * a.q_heads + h) * a.c.dim + d;
+    if (a.dtype == MMQ_F32)
+        Elem<float>::store4(static_cast<float*>(a.out) + at, v);
+    else if (a.dtype == MMQ_BF16)
+        Elem<__nv_bfloat16>::store4(static_cast<__nv_bfloat16*>(a.out) + at, v);
+    else
+        Elem<__half>::store4(static_cast<__half*>(a.out) + at, v);
+}
+__device__ __forceinline__ void store_lse(const Attend& a, long long row, int h, float m, float l) {
+    if (a.lse) a.lse[row * a.q_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// log2 of a block's value scale and its reciprocal, as the exponent and the sum take them
+__device__ __forceinline__ void value_scale(float dv, float& lv, float& rv) {
+    const float d = dv >= MIN_SCALE ? dv : 0x1p-60f;
+    lv = __log2f(d);
+    rv = __fdividef(1.f, d);
+}
+
+// Power of two that brings a row's largest magnitude into [1, 2) (exactly): 2^-e, and 2^e
+__device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
+    const int e = max(1, min(253, (int)((__float_as_uint(amax) >> 23) & 255)));  // biased
+    down = __uint_as_float((uint32_t)(254 - e) << 23);
+    up = __uint_as_float((uint32_t)e << 23);
+}
+
+}  // namespace kv
+}  // namespace mmq

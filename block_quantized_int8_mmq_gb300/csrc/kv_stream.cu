@@ -1,0 +1,583 @@
+// Attention of a few query rows per sequence and key/value head (single tokens, drafted tokens)
+// over the 8-bit cache: k_kv_attend_stream.
+//
+// Bound: HBM.  Every record in reach is read once (64 D + 16 bytes per 32 tokens and head) and
+// used for all of the head's query rows, up to 8 NT of them.  A warp is a worker (kv_attend.cuh)
+// with a ring of its own: one bulk copy per record, S records in flight, no barrier but its own;
+// the ring runs on over the ends of heads and sequences, so short sequences stream like long
+// ones.  Codes go from shared memory to f16 MMA operands exactly (|c| <= 127), tokens on the
+// M side of both products:
+//   S^T [32 tokens x 8 queries] = K [tokens x d] Q^T,   O^T [d x 8 queries] += V^T [d x tokens] P^T
+// (m16n8k16).  k is permuted alike in both operands of a product, so every lane reads 16
+// consecutive bytes of a record's row; V^T's token pairs are put side by side by byte permutes
+// and P^T comes from S^T's accumulators by 8x8 transposes within the warp.  The queries stay in
+// registers, scaled per row by a power of two into f16's range: one f16 term for bf16 and f16
+// rows (exact but for bits 2^-25 below the row's largest), two for f32 rows (SPLIT), whose
+// weights are split into two f16 terms as well.
+#include "kv_attend.cuh"
+#include "umma.cuh"
+
+namespace mmq {
+namespace {
+
+using namespace kv;
+
+__device__ unsigned g_kv_stream_error;
+
+template <int D, int NT>
+struct Stream {
+    static constexpr int WARPS = D == 256 ? 4 : 8, THREADS = WARPS * 32;
+    static constexpr int STAGES = D == 64 ? 4 : NT == 2 ? 2 : 3;
+    static constexpr int ROWS = 8 * NT, REC = rec_bytes(D);
+    static constexpr int SLOT = ROWS * (D + 2) * 4;  // O [rows][D], m [rows], l [rows]
+    static constexpr int RING = WARPS * STAGES * REC;
+    static constexpr int SMEM = RING + WARPS * SLOT + WARPS * STAGES * 8;
+    static_assert(SLOT <= STAGES * REC && SLOT % 16 == 0, "the outgoing slot reuses the warp's ring");
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t o;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(v));
+    return o;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) { return Elem<__half>::pack2(a, b); }
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// the two f16 terms of a pair
+__device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_h2(a, b);
+    const float2 f = unpack_h2(hi);
+    lo = pack_h2(a - f.x, b - f.y);
+}
+
+// A sequence as the units see it
+struct Seq {
+    int start, n, len, lo_blk, tiles;  // tiles: records in reach, or 1 for a sequence of padding rows; 0: none
+};
+__device__ __forceinline__ Seq load_seq(const Attend& a, int b) {
+    Seq s;
+    seq_range(a.c, a.bt, b, s.start, s.n, s.len, &g_kv_stream_error);
+    s.lo_blk = s.len > 0 ? first_key(a, s.len - s.n) / BT : 0;
+    s.tiles = s.n == 0 ? 0 : max(1, (s.len + BT - 1) / BT - s.lo_blk);
+    return s;
+}
+// the unit after (b, h): the next head, or the first of the next sequence that has rows
+__device__ __forceinline__ void next_unit(const Attend& a, int& b, int& h, Seq& s) {
+    if (++h < a.c.heads) return;
+    h = 0;
+    do ++b;
+    while (b < a.bt.seqs && (s = load_seq(a, b)).tiles == 0);
+}
+
+// Exclusive scan over the CTA; total: the sum.
+template <int WARPS>
+__device__ __forceinline__ int scan_cta(int v, int& total, int* scratch) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[wid] = x;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        if (i < wid) before += scratch[i];
+        total += scratch[i];
+    }
+    __syncthreads();
+    return before + x - v;
+}
+
+template <int D, int NT, bool SPLIT>
+__global__ void __launch_bounds__(Stream<D, NT>::THREADS, 1)
+k_kv_attend_stream(const Attend a) {
+    using C = Stream<D, NT>;
+    constexpr int KS = D / 16;  // k steps of the first product, row tiles of the second
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_scan[C::WARPS], s_b[C::WARPS], s_off[C::WARPS], s_abort, s_last[2];
+    // the incomplete units of the CTA, two slots per warp in work order
+    __shared__ int s_unit[2 * C::WARPS], s_end[2 * C::WARPS], s_seq[2 * C::WARPS], s_head[2 * C::WARPS];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, tq = lane & 3;
+    uint8_t* ring = smem + wid * C::STAGES * C::REC;
+    const uint32_t bars = ptx::smem_u32(smem + C::RING + C::WARPS * C::SLOT) + wid * C::STAGES * 8;
+    if (lane < C::STAGES) ptx::mbar_init(bars + 8 * lane, 1);
+    ptx::fence_barrier_init();
+    if (tid == 0) s_abort = 0;
+    if (lane < 2) s_unit[2 * wid + lane] = -1;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch_dependents();
+
+    // ---- this warp's range of the work
+    const int seqs = a.bt.seqs;
+    const int v0 = tid < seqs ? load_seq(a, tid).tiles * a.c.heads : 0;
+    int total;
+    const int e0 = scan_cta<C::WARPS>(v0, total, s_scan);
+    const int total0 = total;
+    int T = total;
+    for (int base = C::THREADS; base < seqs; base += C::THREADS) {
+        const int i = base + tid;
+        scan_cta<C::WARPS>(i < seqs ? load_seq(a, i).tiles * a.c.heads : 0, total, s_scan);
+        T += total;
+    }
+    const int W = min((int)gridDim.x * C::WARPS, T), w0 = blockIdx.x * C::WARPS;
+    if (w0 >= W) return;
+    for (int base = 0, carry = 0; base < seqs; base += C::THREADS) {
+        const int i = base + tid;
+        int v = v0, e = e0;
+        total = total0;
+        if (base > 0) {
+            v = i < seqs ? load_seq(a, i).tiles * a.c.heads : 0;
+            e = carry + scan_cta<C::WARPS>(v, total, s_scan);
+        }
+        carry += total;
+        for (int k = 0; k < C::WARPS && w0 + k < W; ++k) {
+            const int x = work_start(T, w0 + k, W);
+            if (x >= e && x < e + v) {
+                s_b[k] = i;
+                s_off[k] = x - e;
+            }
+        }
+    }
+    __syncthreads();
+
+    if (w0 + wid < W) {
+        const int x0 = work_start(T, w0 + wid, W), x1 = work_start(T, w0 + wid + 1, W);
+        int b = s_b[wid];
+        Seq sq = load_seq(a, b);
+        int h = s_off[wid] / sq.tiles, o = s_off[wid] - h * sq.tiles;
+        // the fetching side runs STAGES records ahead
+        int fb = b, fh = h, fo = o, fx = x0, tab0 = 0, tabn = 0, tab = -1;
+        Seq fs = sq;
+        uint32_t live = 0, phase = 0;  // stages that a copy was started into, parities
+        auto fetch = [&](int st) {     // the next record of the range into stage st
+            if (fs.len > 0) {
+                const int blk = fs.lo_blk + fo, pg = blk / a.c.blocks;
+                if (pg < tab0 || pg >= tab0 + tabn) {  // 32 page numbers at a time, one per lane
+                    tab0 = pg;
+                    tabn = min(32, (fs.len + a.c.page - 1) / a.c.page - pg);
+                    tab = lane < tabn ? a.bt.table[(long long)fb * a.bt.table_stride + pg + lane] : -1;
+                }
+                const int id = __shfl_sync(0xffffffffu, tab, pg - tab0);
+                if (id >= 0 && id < a.c.pages) {
+                    if (lane == 0) {
+                        const uint8_t* src =
+                            a.c.data + (((long long)id * a.c.heads + fh) * a.c.blocks + (blk - pg * a.c.blocks)) * C::REC;
+                        ptx::mbar_arrive_expect_tx(bars + 8 * st, C::REC);
+                        ptx::bulk_load(ptx::smem_u32(ring + st * C::REC), src, C::REC, bars + 8 * st);
+                    }
+                    live |= 1u << st;
+                } else if (lane == 0) {
+                    atomicOr(&g_kv_stream_error, ERR_RANGE);
+                }
+            }
+            ++fx;
+            if (++fo == fs.tiles) {
+                const int was = fb;
+                next_unit(a, fb, fh, fs);
+                fo = 0;
+                if (fb != was) tabn = 0;
+            }
+        };
+#pragma unroll 1
+        for (int st = 0; st < C::STAGES && fx < x1; ++st) fetch(st);
+
+        uint32_t qf[SPLIT ? 2 : 1][NT][KS][2];
+        float acc[KS][NT][4], m[NT][2], l[NT][2], fq[NT][2];
+        int hi[NT][2], lo[NT][2], hi_min = 0, lo_max = 0, o_from = 0;
+        bool fresh = true, ok = true;
+        int st = 0;
+#pragma unroll 1
+        for (int x = x0; x < x1; ++x) {
+            if (fresh) {  // a new unit: its queries as B operands, its rows' limits
+                fresh = false;
+                o_from = o;
+                const int rows = sq.n * a.group, first = sq.len - sq.n;
+                hi_min = 0x7fffffff;
+                lo_max = 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int r = 8 * nt + g, t = r / a.group;
+                    float4 v[KS];
+                    float am = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        v[ks] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (r < rows)
+                            v[ks] = load_row4(a, sq.start + t, h * a.group + r - t * a.group,
+                                              64 * (ks >> 2) + 16 * tq + 4 * (ks & 3));
+                        am = fmaxf(am, fmaxf(fmaxf(fabsf(v[ks].x), fabsf(v[ks].y)), fmaxf(fabsf(v[ks].z), fabsf(v[ks].w))));
+                    }
+                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+                    float down, up;
+                    row_scale(am, down, up);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        if (SPLIT) {
+                            split_h2(v[ks].x * down, v[ks].y * down, qf[0][nt][ks][0], qf[SPLIT ? 1 : 0][nt][ks][0]);
+                            split_h2(v[ks].z * down, v[ks].w * down, qf[0][nt][ks][1], qf[SPLIT ? 1 : 0][nt][ks][1]);
+                        } else {
+                            qf[0][nt][ks][0] = pack_h2(v[ks].x * down, v[ks].y * down);
+                            qf[0][nt][ks][1] = pack_h2(v[ks].z * down, v[ks].w * down);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {  // this lane's columns of S^T and O^T: rows 2 tq, 2 tq + 1
+                        fq[nt][c] = __shfl_sync(0xffffffffu, up, 4 * (2 * tq + c)) * a.scale2;
+                        const int rc = 8 * nt + 2 * tq + c, pos = first + rc / a.group;
+                        hi[nt][c] = rc < rows ? pos + 1 : 0x7fffffff;
+                        lo[nt][c] = rc < rows && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                        hi_min = min(hi_min, hi[nt][c]);
+                        lo_max = max(lo_max, lo[nt][c]);
+                        m[nt][c] = M_NONE;
+                        l[nt][c] = 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < KS; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[j][nt][c] = 0.f;
+                }
+#pragma unroll
+                for (int off = 1; off <= 2; off <<= 1) {
+                    hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, off));
+                    lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, off));
+                }
+            }
+
+            if (live >> st & 1) {
+                if (!umma::warp_wait(bars + 8 * st, phase >> st & 1, &s_abort, &g_kv_stream_error)) {
+                    ok = false;
+                    break;
+                }
+                phase ^= 1u << st;
+                live &= ~(1u << st);
+                const uint8_t* rec = ring + st * C::REC;
+                // S^T: token slots g and g + 8 of two 16-token tiles, query columns 2 tq and 2 tq + 1
+                float s[2][NT][4];
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[mt][nt][c] = 0.f;
+#pragma unroll
+                for (int sg = 0; sg < D / 64; ++sg) {
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const uint8_t* p = rec + (16 * mt + g) * D + 64 * sg + 16 * tq;
+                        const uint4 ra = *reinterpret_cast<const uint4*>(p);
+                        const uint4 rb = *reinterpret_cast<const uint4*>(p + 8 * D);
+                        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const uint2 ca = umma::i8x4_to_f16x4(wa[u]), cb = umma::i8x4_to_f16x4(wb[u]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < (SPLIT ? 2 : 1); ++e)
+                                    mma16816(s[mt][nt], ca.x, cb.x, ca.y, cb.y, qf[e][nt][4 * sg + u][0],
+                                             qf[e][nt][4 * sg + u][1]);
+                        }
+                    }
+                }
+                const float2 d = *reinterpret_cast<const float2*>(rec + 2 * BT * D);
+                float lv, rv;
+                value_scale(d.y, lv, rv);
+                const int j0 = (sq.lo_blk + o) * BT;
+                const bool edge = j0 + BT > hi_min || j0 < lo_max;
+                bool over = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float a0 = fq[nt][0] * d.x, a1 = fq[nt][1] * d.x;
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float t = fmaf(s[mt][nt][c], c & 1 ? a1 : a0, lv);
+                            if (edge) {
+                                const int j = j0 + 16 * mt + g + 8 * (c >> 1);
+                                if (j >= hi[nt][c & 1] || j < lo[nt][c & 1]) t = -INFINITY;
+                            }
+                            s[mt][nt][c] = t;
+                            over |= t > m[nt][c & 1] + LIMIT;
+                        }
+                }
+                if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float mx = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+#pragma unroll
+                            for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                            const float mn = fmaxf(m[nt][c], mx - SHIFT), f = exp2_approx(m[nt][c] - mn);
+                            m[nt][c] = mn;
+                            l[nt][c] *= f;
+#pragma unroll
+                            for (int j = 0; j < KS; ++j) {
+                                acc[j][nt][c] *= f;
+                                acc[j][nt][c + 2] *= f;
+                            }
+                        }
+                }
+                uint32_t pf[SPLIT ? 2 : 1][2][NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float p0 = exp2_approx(s[mt][nt][2 * r] - m[nt][0]);
+                            const float p1 = exp2_approx(s[mt][nt][2 * r + 1] - m[nt][1]);
+                            sum0 += p0;
+                            sum1 += p1;
+                            if (SPLIT) {
+                                uint32_t ph, pl;
+                                split_h2(p0, p1, ph, pl);
+                                pf[0][mt][nt][r] = transpose8x8(ph);
+                                pf[SPLIT ? 1 : 0][mt][nt][r] = transpose8x8(pl);
+                            } else {
+                                pf[0][mt][nt][r] = transpose8x8(pack_h2(p0, p1));
+                            }
+                        }
+                    l[nt][0] = fmaf(sum0, rv, l[nt][0]);
+                    l[nt][1] = fmaf(sum1, rv, l[nt][1]);
+                }
+                // O^T: lane (g, tq) takes the value columns 16 g .. 16 g + 15 of each 128 (8 g .. of
+                // 64), of tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 of each 16-token tile; row tile j
+                // holds columns 2j (rows 0..7) and 2j + 1 (rows 8..15) of every lane's run
+                constexpr int RUN = D < 128 ? D / 8 : 16, RUNS = D / (8 * RUN), WORDS = RUN / 4;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int hh = 0; hh < RUNS; ++hh) {
+                        const uint8_t* p = rec + BT * D + (16 * mt + 2 * tq) * D + 128 * hh + RUN * g;
+                        uint32_t wv[4][WORDS];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const uint8_t* pu = p + ((u & 1) + 8 * (u >> 1)) * D;
+                            if (WORDS == 4) {
+                                const uint4 t4 = *reinterpret_cast<const uint4*>(pu);
+                                wv[u][0] = t4.x;
+                                wv[u][1] = t4.y;
+                                wv[u][WORDS == 4 ? 2 : 0] = t4.z;
+                                wv[u][WORDS == 4 ? 3 : 0] = t4.w;
+                            } else {
+                                const uint2 t2 = *reinterpret_cast<const uint2*>(pu);
+                                wv[u][0] = t2.x;
+                                wv[u][1] = t2.y;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < RUN / 2; ++j) {
+                            const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+                            const uint2 c0 = umma::i8x4_to_f16x4(__byte_perm(wv[0][j >> 1], wv[1][j >> 1], sel));
+                            const uint2 c1 = umma::i8x4_to_f16x4(__byte_perm(wv[2][j >> 1], wv[3][j >> 1], sel));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < (SPLIT ? 2 : 1); ++e)
+                                    mma16816(acc[hh * (RUN / 2) + j][nt], c0.x, c0.y, c1.x, c1.y, pf[e][mt][nt][0],
+                                             pf[e][mt][nt][1]);
+                        }
+                    }
+                __syncwarp();  // the stage is read
+            }
+            if (fx < x1) fetch(st);
+            if (++st == C::STAGES) st = 0;
+
+            if (++o == sq.tiles || x + 1 == x1) {  // the unit ends, or the range does
+                const int ustart = x + 1 - o, uend = ustart + sq.tiles, rows = sq.n * a.group;
+                const bool whole = o_from == 0 && o == sq.tiles;
+                // incomplete: the CTA's slot 0 if the unit came in to this warp, else 1 (the range ends:
+                // nothing is in flight into the ring any more)
+                float* slot = reinterpret_cast<float*>(o_from > 0 ? smem + C::RING + wid * C::SLOT : ring);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float sum = l[nt][c];
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                        const int r = 8 * nt + 2 * tq + c;
+                        constexpr int RUN = D < 128 ? D / 8 : 16, RUNS = D / (8 * RUN);
+                        const float inv = whole ? (sum > 0.f ? __frcp_rn(sum) : 0.f) : 1.f;
+                        const int t = r / a.group, hq = h * a.group + r - t * a.group;
+                        if (whole && r >= rows) continue;
+#pragma unroll
+                        for (int hh = 0; hh < RUNS; ++hh)
+#pragma unroll
+                            for (int i = 0; i < RUN / 4; ++i) {
+                                const int j = hh * (RUN / 2) + 2 * i, col = 128 * hh + RUN * g + 4 * i;
+                                const float4 v = make_float4(acc[j][nt][c] * inv, acc[j][nt][c + 2] * inv,
+                                                             acc[j + 1][nt][c] * inv, acc[j + 1][nt][c + 2] * inv);
+                                if (whole)
+                                    store_out4(a, sq.start + t, hq, col, v);
+                                else
+                                    *reinterpret_cast<float4*>(slot + r * D + col) = v;
+                            }
+                        if (g == 0) {
+                            if (whole) {
+                                store_lse(a, sq.start + t, hq, m[nt][c], sum);
+                            } else {
+                                slot[C::ROWS * D + r] = m[nt][c];
+                                slot[C::ROWS * (D + 1) + r] = sum;
+                            }
+                        }
+                    }
+                if (!whole && lane == 0) {
+                    const int i = 2 * wid + (o_from > 0 ? 0 : 1);
+                    s_unit[i] = ustart;
+                    s_end[i] = uend;
+                    s_seq[i] = b;
+                    s_head[i] = h;
+                }
+                if (o == sq.tiles && x + 1 < x1) {
+                    next_unit(a, b, h, sq);
+                    o = 0;
+                    fresh = true;
+                }
+            }
+        }
+        if (!ok)  // given up: let what is in flight land before the shared memory goes
+            for (int i = 0; i < C::STAGES; ++i)
+                if (live >> i & 1) umma::drain_bar(bars + 8 * i, phase >> i & 1, &g_kv_stream_error);
+    }
+    __syncthreads();
+    if (s_abort) return;
+
+    // ---- the CTA's incomplete units: parts of one unit lie in consecutive slots
+    const int cta0 = work_start(T, w0, W), cta1 = work_start(T, min(W, w0 + C::WARPS), W);
+    auto row_factor = [](float mi, float M) { return exp2_approx(mi - M); };
+    for (int i = 0; i < 2 * C::WARPS;) {
+        if (s_unit[i] < 0) {
+            ++i;
+            continue;
+        }
+        const int u = s_unit[i], ue = s_end[i], b = s_seq[i], h = s_head[i];
+        int e = i;
+        for (int k = i + 1; k < 2 * C::WARPS; ++k)
+            if (s_unit[k] == u) e = k;
+        const Seq sq = load_seq(a, b);
+        const int rows = sq.n * a.group;
+        const bool whole = u >= cta0 && ue <= cta1;
+        float* part = part_slot(a, blockIdx.x, u >= cta0 ? 1 : 0);
+        for (int idx = tid; idx < rows * (D / 4); idx += C::THREADS) {
+            const int r = idx / (D / 4), col = 4 * (idx % (D / 4));
+            float M = M_NONE, L = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = i; k <= e; ++k) {
+                if (s_unit[k] != u) continue;
+                const float* sl = reinterpret_cast<const float*>(k & 1 ? smem + (k >> 1) * C::STAGES * C::REC
+                                                                       : smem + C::RING + (k >> 1) * C::SLOT);
+                const float mk = sl[C::ROWS * D + r], mn = fmaxf(M, mk), f = row_factor(M, mn), fk = row_factor(mk, mn);
+                const float4 x = *reinterpret_cast<const float4*>(sl + r * D + col);
+                v = make_float4(v.x * f + x.x * fk, v.y * f + x.y * fk, v.z * f + x.z * fk, v.w * f + x.w * fk);
+                L = L * f + sl[C::ROWS * (D + 1) + r] * fk;
+                M = mn;
+            }
+            if (whole) {
+                const float inv = L > 0.f ? __frcp_rn(L) : 0.f;
+                const int t = r / a.group, hq = h * a.group + r - t * a.group;
+                store_out4(a, sq.start + t, hq, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                if (col == 0) store_lse(a, sq.start + t, hq, M, L);
+            } else {
+                *reinterpret_cast<float4*>(part + r * D + col) = v;
+                if (col == 0) {
+                    part[WS_ROWS * D + r] = M;
+                    part[WS_ROWS * (D + 1) + r] = L;
+                }
+            }
+        }
+        if (!whole) {
+            const int c0 = work_owner(T, u, W) / C::WARPS, c1 = work_owner(T, ue - 1, W) / C::WARPS;
+            unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last[0] = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+            __syncthreads();
+            if (s_last[0]) {
+                __threadfence();
+                for (int idx = tid; idx < rows * (D / 4); idx += C::THREADS) {
+                    const int r = idx / (D / 4), col = 4 * (idx % (D / 4));
+                    float M = M_NONE, L = 0.f;
+                    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part_slot(a, c, c == c0) + WS_ROWS * D + r));
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* ps = part_slot(a, c, c == c0);
+                        const float f = row_factor(__ldcg(ps + WS_ROWS * D + r), M);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(ps + r * D + col));
+                        v = make_float4(v.x + x.x * f, v.y + x.y * f, v.z + x.z * f, v.w + x.w * f);
+                        L += __ldcg(ps + WS_ROWS * (D + 1) + r) * f;
+                    }
+                    const float inv = L > 0.f ? __frcp_rn(L) : 0.f;
+                    const int t = r / a.group, hq = h * a.group + r - t * a.group;
+                    store_out4(a, sq.start + t, hq, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                    if (col == 0) store_lse(a, sq.start + t, hq, M, L);
+                }
+                if (tid == 0) *counter = 0;
+            }
+        }
+        i = e + 1;
+    }
+}
+
+template <int D, int NT, bool SPLIT>
+int launch(const Attend& a, cudaStream_t s) {
+    using C = Stream<D, NT>;
+    static SmemAttr attr;
+    const char* fn = "mmq_kv_attend";
+    const void* func = reinterpret_cast<const void*>(&k_kv_attend_stream<D, NT, SPLIT>);
+    const int st = ensure_smem(func, C::SMEM, attr);
+    if (st != MMQ_OK) {
+        report(fn, st, "the attention stream's shared memory was refused");
+        return st;
+    }
+    // no more warps than records can be in reach
+    const long long most = (long long)a.bt.seqs * a.c.heads * a.bt.table_pages * a.c.blocks;
+    const long long ctas = (most + C::WARPS - 1) / C::WARPS, sms = device_shape().sms;
+    const dim3 grid((unsigned)(ctas < 1 ? 1 : ctas < sms ? ctas : sms));
+    ProfScope ps("k_kv_attend_stream", s);
+    return pdl_status(launch_pdl(&k_kv_attend_stream<D, NT, SPLIT>, grid, dim3(C::THREADS), C::SMEM, s, a), fn);
+}
+
+template <bool SPLIT>
+int launch_rows(const Attend& a, int rows, cudaStream_t s) {
+    if (a.c.dim == 64) return rows <= 8 ? launch<64, 1, SPLIT>(a, s) : launch<64, 2, SPLIT>(a, s);
+    if (a.c.dim == 128) return rows <= 8 ? launch<128, 1, SPLIT>(a, s) : launch<128, 2, SPLIT>(a, s);
+    return launch<256, 1, SPLIT>(a, s);
+}
+
+}  // namespace
+
+// The most query rows of one sequence and head that the stream takes.
+int kv_stream_rows(int dim) { return dim == 256 ? 8 : 16; }
+
+int kv_stream_launch(const Attend& a, int rows, cudaStream_t s) {
+    return a.dtype == MMQ_F32 ? launch_rows<true>(a, rows, s) : launch_rows<false>(a, rows, s);
+}
+
+unsigned kv_stream_take_error() {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_kv_stream_error, sizeof(v)) != cudaSuccess) return 0;
+    if (v) {
+        const unsigned zero = 0;
+        cudaMemcpyToSymbol(g_kv_stream_error, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace mmq

@@ -450,9 +450,10 @@ def test_values_out_of_range_are_not_followed(what, new):
     torch.cuda.synchronize()
     assert mmq.mmq_get_device_error() == MMQ_ERR_RANGE
     assert mmq.mmq_get_device_error() == 0
-    if what in ("page", "length", "negative"):
-        keep = [r for r in range(3 * new) if not new <= r < 2 * new]
-        assert torch.equal(out[keep], good[keep])
+    if what in ("page", "length", "negative"):  # the other sequences' rows are right
+        rest = out.clone()
+        rest[new:2 * new] = good[new:2 * new]
+        compare_attend(c, rest, None, q.cpu(), 1 / 8.0)
     if what in ("length", "negative"):
         assert (out[new:2 * new] == 9.0).all()
     mmq.mmq_kv_append(cache, batch, k, v, q=q, rope=None)
