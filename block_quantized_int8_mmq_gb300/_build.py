@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmmq.so")
 SOURCES = ["abi.cu", "quantize.cu", "gemm_small.cu", "gemm_tc.cu", "gemm_expand.cu", "grouped.cu", "profile.cu",
-           "kv_abi.cu", "kv_cache.cu", "kv_attend.cu", "kv_stream.cu"]
+           "kv_abi.cu", "kv_cache.cu", "kv_stream.cu", "kv_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
                 "-I", os.path.join(ROOT, "include")]

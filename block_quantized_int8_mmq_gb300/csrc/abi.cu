@@ -29,7 +29,8 @@ int launch_status(const char* fn) {
 
 bool tc_available();
 unsigned kv_cache_take_error();
-unsigned kv_attend_take_error();
+unsigned kv_stream_take_error();
+unsigned kv_tile_take_error();
 
 DeviceShape device_shape() {
     static std::atomic<int> sms[MAX_DEVICES], smem[MAX_DEVICES], l2[MAX_DEVICES];
@@ -500,7 +501,7 @@ int mmq_get_device_error(void* stream) {
         return MMQ_ERR_CUDA;
     }
     const unsigned bits = tc_take_error() | tcx_take_error() | small_take_error() | kv_cache_take_error() |
-                          kv_attend_take_error();
+                          kv_stream_take_error() | kv_tile_take_error();
     return (bits & ERR_TIMEOUT) ? MMQ_ERR_TIMEOUT : (bits & ERR_RANGE) ? MMQ_ERR_RANGE : MMQ_OK;
 }
 

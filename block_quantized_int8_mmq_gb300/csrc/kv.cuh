@@ -113,10 +113,6 @@ struct Elem<__half> {
 int kv_append_launch(const kv::Cache& c, const kv::Batch& b, int dtype, const kv::Rows& k, const kv::Rows& v,
                      const kv::Rows& q, int q_heads, const kv::Rope& rope, void* q_out, cudaStream_t s);
 int kv_read_launch(const kv::Cache& c, const kv::Batch& b, int dtype, void* k_out, void* v_out, cudaStream_t s);
-int kv_attend_launch(const kv::Cache& c, const kv::Batch& b, int dtype, const kv::Rows& q, int q_heads, float scale,
-                     int window, void* out, float* lse, void* ws, cudaStream_t s);
-size_t kv_attend_workspace(int dim);
 unsigned kv_cache_take_error();
-unsigned kv_attend_take_error();
 
 }  // namespace mmq

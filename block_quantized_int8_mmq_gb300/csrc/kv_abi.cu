@@ -1,9 +1,9 @@
 // C entry points of the 8-bit key/value cache: argument checks, then the launchers
-// (kv_cache.cu, kv_attend.cu).  The error protocol is that of the whole library: a refused
+// (kv_cache.cu; kv_stream.cu or kv_tile.cu).  The error protocol is that of the whole library: a refused
 // call launches nothing, writes nothing and prints one line.
 #include <math.h>
 
-#include "kv.cuh"
+#include "kv_attend.cuh"
 
 namespace mmq {
 namespace {
@@ -79,7 +79,10 @@ extern "C" {
 
 size_t mmq_kv_block_bytes(int64_t dim) { return dim_ok(dim) ? (size_t)rec_bytes((int)dim) : 0; }
 
-size_t mmq_kv_workspace_bytes(int64_t dim) { return dim_ok(dim) ? kv_attend_workspace((int)dim) : 0; }
+// the arrival counters, then two partial results for every SM
+size_t mmq_kv_workspace_bytes(int64_t dim) {
+    return dim_ok(dim) ? WS_COUNTERS + (size_t)device_shape().sms * 2 * WS_ROWS * (dim + 2) * 4 : 0;
+}
 
 int mmq_kv_append(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtype, const mmq_kv_rows* k,
                   const mmq_kv_rows* v, const mmq_kv_rows* q, int64_t q_heads, const mmq_kv_rope* rope, void* q_out,
@@ -156,8 +159,12 @@ int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtyp
     if (b.seqs == 0 || b.tokens == 0 || b.max_new == 0) return MMQ_OK;
     // a window past every length is none
     const int w = window >= (int64_t)b.table_pages * c.page ? 0 : (int)window;
-    return kv_attend_launch(c, b, dtype, qr, (int)q_heads, scale, w, out, lse, workspace,
-                            static_cast<cudaStream_t>(stream));
+    const int group = (int)(q_heads / c.heads);
+    const Attend a{c, b, qr, (int)q_heads, group, dtype, w, scale * 1.44269504088896341f, out, lse,
+                   static_cast<uint8_t*>(workspace)};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t rows = (int64_t)b.max_new * group;
+    return rows <= kv_stream_rows(c.dim) ? kv_stream_launch(a, (int)rows, s) : kv_tile_launch(a, s);
 }
 
 }  // extern "C"

@@ -96,5 +96,43 @@ __device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
     up = __uint_as_float((uint32_t)e << 23);
 }
 
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) { return Elem<__half>::pack2(a, b); }
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// the two f16 terms of a pair
+__device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_h2(a, b);
+    const float2 f = unpack_h2(hi);
+    lo = pack_h2(a - f.x, b - f.y);
+}
+
+// Exclusive scan over the CTA; total: the sum.
+template <int WARPS>
+__device__ __forceinline__ int scan_cta(int v, int& total, int* scratch) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[wid] = x;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        if (i < wid) before += scratch[i];
+        total += scratch[i];
+    }
+    __syncthreads();
+    return before + x - v;
+}
+
 }  // namespace kv
+// The two kernels: up to kv_stream_rows(dim) query rows per sequence and head (kv_stream.cu), any
+// number (kv_tile.cu).
+int kv_stream_rows(int dim);
+int kv_stream_launch(const kv::Attend& a, int rows, cudaStream_t s);
+int kv_tile_launch(const kv::Attend& a, cudaStream_t s);
+
 }  // namespace mmq

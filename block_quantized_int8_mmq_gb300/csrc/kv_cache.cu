@@ -77,8 +77,8 @@ __device__ __forceinline__ void turn(float4& a, float4& b, const Octet& o, const
         return;
     }
     const long long at = (long long)pos * (r.rotary / 2) + o.pair;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(r.cos + at));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(r.sin + at));
+    const float4 c = *reinterpret_cast<const float4*>(r.cos + at);
+    const float4 s = *reinterpret_cast<const float4*>(r.sin + at);
     if (r.interleaved) {
         turn1(a.x, a.y, c.x, s.x);
         turn1(a.z, a.w, c.y, s.y);

@@ -48,15 +48,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(v));
     return o;
 }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) { return Elem<__half>::pack2(a, b); }
-__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-// the two f16 terms of a pair
-__device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_h2(a, b);
-    const float2 f = unpack_h2(hi);
-    lo = pack_h2(a - f.x, b - f.y);
-}
-
 // A sequence as the units see it
 struct Seq {
     int start, n, len, lo_blk, tiles;  // tiles: records in reach, or 1 for a sequence of padding rows; 0: none
@@ -74,29 +65,6 @@ __device__ __forceinline__ void next_unit(const Attend& a, int& b, int& h, Seq& 
     h = 0;
     do ++b;
     while (b < a.bt.seqs && (s = load_seq(a, b)).tiles == 0);
-}
-
-// Exclusive scan over the CTA; total: the sum.
-template <int WARPS>
-__device__ __forceinline__ int scan_cta(int v, int& total, int* scratch) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) scratch[wid] = x;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-        if (i < wid) before += scratch[i];
-        total += scratch[i];
-    }
-    __syncthreads();
-    return before + x - v;
 }
 
 template <int D, int NT, bool SPLIT>

@@ -1,0 +1,623 @@
+// Attention of many query rows per sequence and key/value head (prompts, chunks of prompts, many
+// drafted tokens) over the 8-bit cache: k_kv_attend_tile.
+//
+// Bound: the tensor cores (4 D operations per row and key). A CTA takes units (kv_attend.cuh) of MT
+// tiles of 128 rows; a row is a (token, query head) pair of one key/value head's group, so that
+// the heads that share keys fill a tile together and a tile of keys and values, once converted,
+// serves MT * 128 rows.  Roles:
+//   converter warps (4)  records from global memory to registers one tile ahead, codes to exact
+//                        f16 in shared memory, in the core-matrix order of tcgen05 (8 x 16
+//                        bytes): keys as the K-major B operand of S = Q K^T, values in the same
+//                        physical order as the MN-major B operand of O += P V (no transpose);
+//   softmax warps (4 per row tile), a thread per row: S from TMEM, the running maximum, P as f16
+//                        back into S's own columns as the A operand of the second product, the
+//                        (rare) rescaling of O in TMEM, and at the end of a unit its output;
+//   one thread of each row tile's first warp issues that tile's MMAs: the two row tiles
+//                        alternate, one's products run while the other's softmax does.
+// S of a tile and its P share columns: the products of one row tile run in issue order, and a
+// row's thread has read its S before it writes its P.  f32 rows (SPLIT): queries and weights as
+// two f16 terms each, twice the products.
+#include "kv_attend.cuh"
+#include "umma.cuh"
+
+namespace mmq {
+namespace {
+
+using namespace kv;
+
+__device__ unsigned g_kv_tile_error;
+
+template <int D, bool SPLIT>
+struct Tile {
+    static constexpr int MT = D == 256 ? 1 : 2;                  // row tiles of a CTA
+    static constexpr int KT = D == 64 ? 128 : D == 128 ? (SPLIT ? 64 : 128) : 64;  // keys per tile
+    static constexpr int ST = D == 256 && SPLIT ? 1 : 2;         // converted tiles in shared memory
+    static constexpr int TERMS = SPLIT ? 2 : 1;
+    static constexpr int SOFT = 4 * MT, CONV = 4, WARPS = SOFT + CONV, THREADS = 32 * WARPS;
+    static constexpr int ROWS = 128 * MT;
+    static constexpr int KV = KT * D * 2, Q = 128 * D * 2;       // bytes of a converted tile, of a row tile's term
+    // the queries last: every operand read stays inside the allocation
+    static constexpr int OFF_V = ST * KV, OFF_Q = 2 * ST * KV, OFF_BAR = OFF_Q + MT * TERMS * Q;
+    static constexpr int NBAR = 4 * ST + 4 * MT;
+    static constexpr int USED = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of TMEM
+    static constexpr int COL_O = MT * KT;                        // TMEM columns: S of each row tile, then O
+    static_assert(MT * (KT + D) <= 512 && SMEM <= 232448 - 1024, "tile sizes");
+    static constexpr int BLK = KT / BT;                          // records per key tile
+};
+
+// A unit: a run of ROWS rows of one sequence and head, and the key tiles that they see.
+struct Unit {
+    int b, u, h;              // sequence, row run, head
+    int start, n, len, rows;  // of the sequence; rows: n * group
+    int lo, hi, kt0, tiles;   // keys that some row sees, first key tile, key tiles (0: no such unit)
+};
+template <int ROWS, int KT>
+__device__ __forceinline__ void unit_span(const Attend& a, Unit& w) {
+    const int r0 = w.u * ROWS;
+    if (r0 >= w.rows) {
+        w.tiles = 0;
+        return;
+    }
+    const int first = w.len - w.n, t0 = r0 / a.group, t1 = min(w.n - 1, (r0 + ROWS - 1) / a.group);
+    w.hi = first + t1 + 1;
+    w.lo = w.hi > 0 ? first_key(a, first + t0) : 0;
+    w.kt0 = w.lo / KT;
+    w.tiles = max(1, (w.hi + KT - 1) / KT - w.kt0);  // a unit of padding rows alone: one tile, all of it masked
+}
+template <int ROWS, int KT>
+__device__ __forceinline__ void unit_load(const Attend& a, Unit& w, int b, int u) {
+    seq_range(a.c, a.bt, b, w.start, w.n, w.len, &g_kv_tile_error);
+    w.rows = w.n * a.group;
+    w.b = b;
+    w.u = u;
+    w.h = 0;
+    unit_span<ROWS, KT>(a, w);
+}
+// units in order: row runs of a sequence, the heads of each
+template <int ROWS, int KT>
+__device__ __forceinline__ void unit_next(const Attend& a, Unit& w) {
+    if (++w.h < a.c.heads) return;
+    w.h = 0;
+    ++w.u;
+    unit_span<ROWS, KT>(a, w);
+    while (w.tiles == 0 && ++w.b < a.bt.seqs) unit_load<ROWS, KT>(a, w, w.b, 0);
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(Tile<D, SPLIT>::THREADS, 1)
+k_kv_attend_tile(const Attend a) {
+    using C = Tile<D, SPLIT>;
+    constexpr int KT = C::KT, ST = C::ST, MT = C::MT, SBO = D * 16;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_scan[C::WARPS], s_pref[C::THREADS + 1], s_at[3], s_last[MT];
+    __shared__ float4 s_sc[4][C::BLK];  // dk, log2 dv, 1 / dv of the blocks of four consecutive tiles
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const uint32_t base = ptx::smem_u32(smem), bars = base + C::OFF_BAR;
+    const uint32_t k_full = bars, k_empty = bars + 8 * ST, v_full = bars + 16 * ST, v_empty = bars + 24 * ST;
+    const uint32_t s_full = bars + 32 * ST, o_full = s_full + 8 * MT, p_ready = o_full + 8 * MT, joined = p_ready + 8 * MT;
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            ptx::mbar_init(k_full + 8 * i, C::CONV);
+            ptx::mbar_init(v_full + 8 * i, C::CONV);
+            ptx::mbar_init(k_empty + 8 * i, MT);
+            ptx::mbar_init(v_empty + 8 * i, MT);
+        }
+        for (int i = 0; i < MT; ++i) {
+            ptx::mbar_init(s_full + 8 * i, 1);
+            ptx::mbar_init(o_full + 8 * i, 1);
+            ptx::mbar_init(p_ready + 8 * i, 4);
+            ptx::mbar_init(joined + 8 * i, 1);
+        }
+        ptx::fence_barrier_init();
+        s_abort = 0;
+    }
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch_dependents();
+
+    // ---- this CTA's range of the work: sequences THREADS at a time, their row runs spread over the threads
+    int T = 0, W = 0, x0 = 0, x1 = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        int carry = 0;
+        for (int b0 = 0; b0 < a.bt.seqs; b0 += C::THREADS) {
+            int runs = 0, total;
+            if (b0 + tid < a.bt.seqs) {
+                int start, n, len;
+                seq_range(a.c, a.bt, b0 + tid, start, n, len, &g_kv_tile_error);
+                runs = (n * a.group + C::ROWS - 1) / C::ROWS;
+            }
+            s_pref[tid] = scan_cta<C::WARPS>(runs, total, s_scan);
+            __syncthreads();
+            for (int i0 = 0; i0 < total; i0 += C::THREADS) {
+                const int i = i0 + tid;
+                Unit w;
+                w.tiles = 0;
+                if (i < total) {
+                    int lo = 0, hi = C::THREADS - 1;  // the last sequence that begins at or before run i
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) / 2;
+                        if (s_pref[mid] <= i)
+                            lo = mid;
+                        else
+                            hi = mid - 1;
+                    }
+                    unit_load<C::ROWS, KT>(a, w, b0 + lo, i - s_pref[lo]);
+                }
+                int sum;
+                const int v = w.tiles * a.c.heads, e = carry + scan_cta<C::WARPS>(v, sum, s_scan);
+                carry += sum;
+                if (pass == 1 && x0 >= e && x0 < e + v) {
+                    s_at[0] = w.b;
+                    s_at[1] = w.u;
+                    s_at[2] = x0 - e;
+                }
+            }
+            __syncthreads();
+        }
+        if (pass == 0) {
+            T = carry;
+            W = min((int)gridDim.x, T);
+            if ((int)blockIdx.x >= W) return;
+            x0 = work_start(T, blockIdx.x, W);
+            x1 = work_start(T, blockIdx.x + 1, W);
+        }
+    }
+    if (wid == 0) {
+        ptx::tmem_alloc(ptx::smem_u32(&s_tmem), 512);
+        ptx::tmem_relinquish();
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* abort = &s_abort;
+    unsigned* err = &g_kv_tile_error;
+
+    Unit w;
+    unit_load<C::ROWS, KT>(a, w, s_at[0], s_at[1]);
+    w.h = s_at[2] / w.tiles;
+    int o = s_at[2] - w.h * w.tiles;
+
+    if (wid >= C::SOFT) {
+        // ------------------------------------------------ converters: warp cw takes tokens KT/4 cw ..
+        constexpr int NL = KT * D / 2048, PER = D / 64;
+        const int cw = wid - C::SOFT, r8 = lane & 7, cq = lane >> 3;
+        const int tok0 = cw * (KT / 4), bi = tok0 / BT, sub = tok0 % BT;
+        // the record of this warp's tokens in the walk's tile: its page number (-1: none to load),
+        // fetched a tile before the codes
+        auto page_of = [&](const Unit& q, int ot, int& in) -> int {
+            const int blk = (q.kt0 + ot) * C::BLK + bi;
+            if (blk * BT >= q.hi || blk * BT + BT <= q.lo) return -1;
+            const int pg = blk / a.c.blocks;
+            in = blk - pg * a.c.blocks;
+            return a.bt.table[(long long)q.b * a.bt.table_stride + pg];
+        };
+        auto rec_of = [&](int id, int in, int h) -> const uint8_t* {
+            if (id < 0 || id >= a.c.pages) return nullptr;
+            return a.c.data + (((long long)id * a.c.heads + h) * a.c.blocks + in) * rec_bytes(D);
+        };
+        const int off = (sub + r8) * D + 16 * cq;
+        auto load = [&](uint4 (&buf)[NL], const uint8_t* p) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                buf[i] = p ? *reinterpret_cast<const uint4*>(p + off + 8 * (i / PER) * D + 64 * (i % PER))
+                           : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto store = [&](const uint4 (&buf)[NL], uint8_t* dst) {
+            uint8_t* d0 = dst + (tok0 >> 3) * SBO + 2 * cq * 128 + r8 * 16;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                uint8_t* p = d0 + (i / PER) * SBO + 8 * (i % PER) * 128;
+                const uint2 c0 = umma::i8x4_to_f16x4(buf[i].x), c1 = umma::i8x4_to_f16x4(buf[i].y);
+                const uint2 c2 = umma::i8x4_to_f16x4(buf[i].z), c3 = umma::i8x4_to_f16x4(buf[i].w);
+                *reinterpret_cast<uint4*>(p) = make_uint4(c0.x, c0.y, c1.x, c1.y);
+                *reinterpret_cast<uint4*>(p + 128) = make_uint4(c2.x, c2.y, c3.x, c3.y);
+            }
+        };
+        uint4 kb[NL], vb[NL];
+        float2 sc = make_float2(0.f, 0.f);
+        int in = 0, id = page_of(w, o, in);
+        if (id < -1 || id >= a.c.pages) atomicOr(err, ERR_RANGE);
+        const uint8_t* rec = rec_of(id, in, w.h);
+        load(kb, rec);
+        load(vb, rec ? rec + BT * D : nullptr);
+        if (rec) sc = *reinterpret_cast<const float2*>(rec + 2 * BT * D);
+        bool some = rec != nullptr;
+        for (int x = x0, n = 0; x < x1; ++x, ++n) {
+            const int st = n % ST;
+            // the next tile's place
+            if (++o == w.tiles) {
+                unit_next<C::ROWS, KT>(a, w);
+                o = 0;
+            }
+            const bool more = x + 1 < x1;
+            if (more) id = page_of(w, o, in);
+            const uint32_t par = ((n / ST) & 1) ^ 1;
+            if (!umma::warp_wait(k_empty + 8 * st, par, abort, err)) break;
+            store(kb, smem + st * C::KV);
+            if (lane == 0 && sub == 0) {
+                float lv = -INFINITY, rv = 0.f;
+                if (some) value_scale(sc.y, lv, rv);
+                s_sc[n & 3][bi] = make_float4(some ? sc.x : 0.f, lv, rv, 0.f);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(k_full + 8 * st);
+            rec = nullptr;
+            if (more) {
+                if (id != -1 && (id < 0 || id >= a.c.pages)) atomicOr(err, ERR_RANGE);
+                rec = rec_of(id, in, w.h);
+                load(kb, rec);
+                if (rec) sc = *reinterpret_cast<const float2*>(rec + 2 * BT * D);
+                some = rec != nullptr;
+            }
+            if (!umma::warp_wait(v_empty + 8 * st, par, abort, err)) break;
+            store(vb, smem + C::OFF_V + st * C::KV);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(v_full + 8 * st);
+            if (more) load(vb, rec ? rec + BT * D : nullptr);
+        }
+    } else {
+        // ------------------------------------------------ softmax: thread = row, and the MMA issue
+        const int gt = wid >> 2, row = tid & 127;  // row tile, row in it
+        const bool leader = (wid & 3) == 0 && lane == 0;
+        const uint32_t lane_off = (uint32_t)((wid & 3) * 32) << 16;
+        const uint32_t t_s = tmem + gt * KT, t_o = tmem + C::COL_O + gt * D;
+        const uint32_t sf = s_full + 8 * gt, of = o_full + 8 * gt, pr = p_ready + 8 * gt, jn = joined + 8 * gt;
+        const uint32_t q_addr = base + C::OFF_Q + gt * C::TERMS * C::Q;
+        uint8_t* q_smem = smem + C::OFF_Q + gt * C::TERMS * C::Q;
+        constexpr uint32_t idesc_s = umma::make_idesc(128, KT), idesc_o = umma::make_idesc(128, D) | (1u << 16);
+        uint32_t n_pr = 0, n_sf = 0, n_of = 0, n_jn = 0;  // phases
+        auto issue_s = [&](int st) {  // S = Q K^T
+            const uint64_t bd = umma::sdesc(base + st * C::KV, SBO);
+#pragma unroll
+            for (int e = 0; e < C::TERMS; ++e) {
+                const uint64_t ad = umma::sdesc(q_addr + e * C::Q, SBO);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    ptx::umma_f16(t_s, ad + 16 * ks, bd + 16 * ks, idesc_s, e + ks > 0);
+            }
+            ptx::umma_commit(k_empty + 8 * st);
+            ptx::umma_commit(sf);
+        };
+        // values: 8-column groups 128 B apart (stride offset), 8-token groups SBO apart (leading offset)
+        auto issue_o = [&](int st, bool first) {
+            const uint32_t va = base + C::OFF_V + st * C::KV;
+            const uint64_t bd = (uint64_t)((va & 0x3FFFFu) >> 4) | ((uint64_t)(SBO >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
+                                (1ull << 46);
+#pragma unroll
+            for (int ks = 0; ks < KT / 16; ++ks)
+#pragma unroll
+                for (int e = 0; e < C::TERMS; ++e)
+                    ptx::umma_f16_ts(t_o, t_s + 32 * (ks >> 1) + 16 * e + 8 * (ks & 1), bd + (uint64_t)(2 * SBO >> 4) * ks, idesc_o,
+                                     !(first && ks + e == 0));
+            ptx::umma_commit(v_empty + 8 * st);
+        };
+        auto signal = [&](uint32_t bar) {  // this warp's part is in place
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar);
+        };
+        bool ok = true;
+        for (int x = x0, n = 0; x < x1 && ok;) {
+            const int o0 = o, tiles = min(w.tiles - o, x1 - x);  // this unit's tiles here
+            const int rloc = gt * 128 + row, r = w.u * C::ROWS + rloc;
+            if (w.u * C::ROWS + gt * 128 >= w.rows) {
+                // no rows in this row tile: only pass the converted tiles on
+                if (leader)
+                    for (int i = 0; i < tiles && ok; ++i) {
+                        const int st = (n + i) % ST, par = ((n + i) / ST) & 1;
+                        ok = umma::wait_bar(k_full + 8 * st, par, abort, err);
+                        if (ok) ptx::mbar_arrive(k_empty + 8 * st);
+                        ok = ok && umma::wait_bar(v_full + 8 * st, par, abort, err);
+                        if (ok) ptx::mbar_arrive(v_empty + 8 * st);
+                    }
+                ok = __all_sync(0xffffffffu, ok);
+            } else {
+                const bool real = r < w.rows;
+                const int t = r / a.group, hq = w.h * a.group + r - t * a.group, pos = w.len - w.n + t;
+                // the row's queries, scaled into f16's range, in core-matrix order
+                float up = 1.f;
+                {
+                    float am = 0.f, down = 1.f;
+                    if (real) {
+#pragma unroll 8
+                        for (int d = 0; d < D; d += 4) {
+                            const float4 v = load_row4(a, w.start + t, hq, d);
+                            am = fmaxf(am, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                        }
+                        row_scale(am, down, up);
+                    }
+                    uint8_t* dst = q_smem + (row >> 3) * SBO + (row & 7) * 16;
+#pragma unroll 4
+                    for (int d = 0; d < D; d += 8) {
+                        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+                        if (real) {
+                            u = load_row4(a, w.start + t, hq, d);
+                            v = load_row4(a, w.start + t, hq, d + 4);
+                        }
+                        uint4 hi4, lo4;
+                        split_h2(u.x * down, u.y * down, hi4.x, lo4.x);
+                        split_h2(u.z * down, u.w * down, hi4.y, lo4.y);
+                        split_h2(v.x * down, v.y * down, hi4.z, lo4.z);
+                        split_h2(v.z * down, v.w * down, hi4.w, lo4.w);
+                        *reinterpret_cast<uint4*>(dst + d * 16) = hi4;
+                        if (SPLIT) *reinterpret_cast<uint4*>(dst + C::Q + d * 16) = lo4;
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                const float fq = up * a.scale2;
+                const int hi = real ? pos + 1 : 0x7fffffff, lo = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                const int hi_min = __reduce_min_sync(0xffffffffu, hi), lo_max = __reduce_max_sync(0xffffffffu, lo);
+                signal(pr);
+                if (leader) {
+                    ok = umma::wait_bar(pr, n_pr & 1, abort, err) &&
+                         umma::wait_bar(k_full + 8 * (n % ST), (n / ST) & 1, abort, err);
+                    if (ok) {
+                        ptx::tc_fence_after();
+                        issue_s(n % ST);
+                    }
+                }
+                ++n_pr;
+                float m = M_NONE, l = 0.f;
+                for (int i = 0; i < tiles; ++i) {
+                    const int nn = n + i, j0 = (w.kt0 + o0 + i) * KT;
+                    if (!umma::warp_wait(sf, n_sf++ & 1, abort, err)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const float4* scv = s_sc[nn & 3];
+                    const bool edge = j0 + KT > hi_min || j0 < lo_max;
+                    float tm = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < C::BLK; ++c) {
+                        uint32_t sr[32];
+                        ptx::tmem_ld32(t_s + lane_off + 32 * c, sr);
+                        const float4 s4 = scv[c];
+                        const float af = fq * s4.x;
+                        ptx::tmem_ld_wait(sr);
+                        if (!edge) {
+                            float mx = __uint_as_float(sr[0]);
+#pragma unroll
+                            for (int k = 1; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(sr[k]));
+                            tm = fmaxf(tm, fmaf(mx, af, s4.y));
+                        } else {
+                            const int jc = j0 + 32 * c;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (jc + k >= lo && jc + k < hi) tm = fmaxf(tm, fmaf(__uint_as_float(sr[k]), af, s4.y));
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, tm > m + LIMIT)) {
+                        const float mn = fmaxf(m, tm - SHIFT), f = exp2_approx(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (i > 0) {  // the products so far are done: S came after them
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t ov[32];
+                                ptx::tmem_ld32(t_o + lane_off + 32 * c, ov);
+                                ptx::tmem_ld_wait(ov);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+                                ptx::tmem_st32(t_o + lane_off + 32 * c, ov);
+                            }
+                        }
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < C::BLK; ++c) {
+                        uint32_t sr[32];
+                        ptx::tmem_ld32(t_s + lane_off + 32 * c, sr);
+                        const float4 s4 = scv[c];
+                        const float af = fq * s4.x, bf = s4.y - m;
+                        ptx::tmem_ld_wait(sr);
+                        if (edge) {
+                            const int jc = j0 + 32 * c;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float tk = fmaf(__uint_as_float(sr[k]), af, bf);
+                                sr[k] = __float_as_uint(jc + k >= lo && jc + k < hi ? exp2_approx(tk) : 0.f);
+                            }
+                        } else {
+                            const unsigned long long a2 = ptx::f2_bits(af, af), b2 = ptx::f2_bits(bf, bf);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const unsigned long long t2 =
+                                    ptx::fma_f32x2(ptx::f2_bits(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), a2, b2);
+                                sr[k] = __float_as_uint(exp2_approx(__uint_as_float((uint32_t)t2)));
+                                sr[k + 1] = __float_as_uint(exp2_approx(__uint_as_float((uint32_t)(t2 >> 32))));
+                            }
+                        }
+                        unsigned long long sum2 = 0ull, sum3 = 0ull;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            sum2 = ptx::add_f32x2(sum2, ptx::f2_bits(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])));
+                            sum3 = ptx::add_f32x2(sum3, ptx::f2_bits(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])));
+                        }
+                        sum2 = ptx::add_f32x2(sum2, sum3);
+                        l = fmaf(__uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32)), s4.z, l);
+                        if (SPLIT) {
+                            uint32_t pw[32];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                split_h2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]), pw[k], pw[16 + k]);
+                            ptx::tmem_st32(t_s + lane_off + 32 * c, pw);
+                        } else {
+                            uint32_t pw[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                pw[k] = pack_h2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
+                            ptx::tmem_st16(t_s + lane_off + 32 * c, pw);
+                        }
+                    }
+                    ptx::tmem_st_wait();
+                    signal(pr);
+                    if (leader) {
+                        const int st = nn % ST, par = (nn / ST) & 1, s2 = (nn + 1) % ST, par2 = ((nn + 1) / ST) & 1;
+                        ok = umma::wait_bar(pr, n_pr & 1, abort, err) && umma::wait_bar(v_full + 8 * st, par, abort, err);
+                        if (ok) {
+                            ptx::tc_fence_after();
+                            issue_o(st, i == 0);
+                            if (i + 1 == tiles) {
+                                ptx::umma_commit(of);
+                            } else {
+                                ok = umma::wait_bar(k_full + 8 * s2, par2, abort, err);
+                                if (ok) issue_s(s2);
+                            }
+                        }
+                    }
+                    ++n_pr;
+                }
+                ok = __all_sync(0xffffffffu, ok) && umma::warp_wait(of, n_of++ & 1, abort, err);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                // ---- the unit's output, or this CTA's part of it
+                const int ustart = x - o0, uend = ustart + w.tiles;
+                const bool whole = o0 == 0 && tiles == w.tiles;
+                // a part's layout: [D / 4][128 rows] float4, then m, l of the rows
+                auto part = [&](int cta, int slot) {
+                    return part_slot(a, cta, slot) + gt * 128 * (D + 2);
+                };
+                float* mine = part(blockIdx.x, o0 == 0 ? 1 : 0);
+                const float inv = whole ? (l > 0.f ? __frcp_rn(l) : 0.f) : 1.f;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t ov[32];
+                    ptx::tmem_ld32(t_o + lane_off + 32 * c, ov);
+                    ptx::tmem_ld_wait(ov);
+                    if (real) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 v = make_float4(__uint_as_float(ov[k]) * inv, __uint_as_float(ov[k + 1]) * inv,
+                                                         __uint_as_float(ov[k + 2]) * inv, __uint_as_float(ov[k + 3]) * inv);
+                            if (whole)
+                                store_out4(a, w.start + t, hq, 32 * c + k, v);
+                            else
+                                *reinterpret_cast<float4*>(mine + ((8 * c + k / 4) * 128 + row) * 4) = v;
+                        }
+                    }
+                }
+                ptx::tc_fence_before();
+                if (whole) {
+                    if (real) store_lse(a, w.start + t, hq, m, l);
+                } else {
+                    if (real) {
+                        mine[128 * D + row] = m;
+                        mine[128 * (D + 1) + row] = l;
+                    }
+                    const int c0 = work_owner(T, ustart, W), c1 = work_owner(T, uend - 1, W);
+                    __threadfence();
+                    signal(pr);
+                    if (leader) {
+                        ok = umma::wait_bar(pr, n_pr & 1, abort, err);
+                        unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0 * 2 + gt;
+                        s_last[gt] = 0;
+                        if (ok && atomicAdd(counter, 1u) == (unsigned)(c1 - c0)) {
+                            *counter = 0;
+                            s_last[gt] = 1;
+                        }
+                        __threadfence();
+                        ptx::mbar_arrive(jn);
+                    }
+                    ++n_pr;
+                    ok = __all_sync(0xffffffffu, ok) && umma::warp_wait(jn, n_jn++ & 1, abort, err);
+                    if (!ok) break;
+                    if (s_last[gt]) {
+                        __threadfence();
+                        if (real) {
+                            float M = M_NONE, L = 0.f;
+#pragma unroll 4
+                            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c, c == c0) + 128 * D + row));
+#pragma unroll 4
+                            for (int c = c0; c <= c1; ++c) {
+                                const float* p = part(c, c == c0);
+                                L += __ldcg(p + 128 * (D + 1) + row) * exp2_approx(__ldcg(p + 128 * D + row) - M);
+                            }
+                            const float invl = L > 0.f ? __frcp_rn(L) : 0.f;
+#pragma unroll 1
+                            for (int k = 0; k < D / 4; k += 4) {
+                                float4 v[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                                for (int c = c0; c <= c1; ++c) {
+                                    const float* p = part(c, c == c0);
+                                    const float f = exp2_approx(__ldcg(p + 128 * D + row) - M);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p) + (k + e) * 128 + row);
+                                        v[e] = make_float4(v[e].x + y.x * f, v[e].y + y.y * f, v[e].z + y.z * f,
+                                                           v[e].w + y.w * f);
+                                    }
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    store_out4(a, w.start + t, hq, 4 * (k + e),
+                                               make_float4(v[e].x * invl, v[e].y * invl, v[e].z * invl, v[e].w * invl));
+                            }
+                            store_lse(a, w.start + t, hq, M, L);
+                        }
+                    }
+                }
+            }
+            x += tiles;
+            n += tiles;
+            o = 0;
+            if (x < x1) unit_next<C::ROWS, KT>(a, w);
+        }
+        // given up: the products in flight end before TMEM and the shared memory go
+        if (leader && *abort) {
+            ptx::umma_commit(jn);
+            umma::drain_bar(jn, n_jn & 1, err);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (wid == 0) ptx::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool SPLIT>
+int launch(const Attend& a, cudaStream_t s) {
+    using C = Tile<D, SPLIT>;
+    static SmemAttr attr;
+    const char* fn = "mmq_kv_attend";
+    const long long runs = (long long)a.bt.tokens * a.group / C::ROWS + a.bt.seqs;
+    const long long tiles = runs * a.c.heads * ((long long)a.bt.table_pages * a.c.page / C::KT + 1);
+    if (tiles > 0x7fffffff || (long long)a.bt.max_new * a.group > 0x7fffffff - C::ROWS) {
+        report(fn, MMQ_ERR_SHAPE, "too many row and key tiles (rows / 128 * heads * keys / 64 above 2^31)");
+        return MMQ_ERR_SHAPE;
+    }
+    const int st = ensure_smem(reinterpret_cast<const void*>(&k_kv_attend_tile<D, SPLIT>), C::SMEM, attr);
+    if (st != MMQ_OK) {
+        report(fn, st, "the attention tiles' shared memory was refused");
+        return st;
+    }
+    const long long sms = device_shape().sms;
+    ProfScope ps("k_kv_attend_tile", s);
+    return pdl_status(launch_pdl(&k_kv_attend_tile<D, SPLIT>, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(C::THREADS),
+                                 C::SMEM, s, a),
+                      fn);
+}
+
+}  // namespace
+
+int kv_tile_launch(const Attend& a, cudaStream_t s) {
+    const bool split = a.dtype == MMQ_F32;
+    if (a.c.dim == 64) return split ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    if (a.c.dim == 128) return split ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    return split ? launch<256, true>(a, s) : launch<256, false>(a, s);
+}
+
+unsigned kv_tile_take_error() {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_kv_tile_error, sizeof(v)) != cudaSuccess) return 0;
+    if (v) {
+        const unsigned zero = 0;
+        cudaMemcpyToSymbol(g_kv_tile_error, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace mmq
