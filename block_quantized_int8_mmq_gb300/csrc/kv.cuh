@@ -79,7 +79,9 @@ struct Elem<float> {
 template <>
 struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        return widen(*reinterpret_cast<const uint2*>(p));
+    }
+    static __device__ __forceinline__ float4 widen(uint2 u) {
         return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                            __uint_as_float(u.y & 0xffff0000u));
     }
@@ -93,8 +95,8 @@ struct Elem<__nv_bfloat16> {
 };
 template <>
 struct Elem<__half> {
-    static __device__ __forceinline__ float4 load4(const __half* p) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
+    static __device__ __forceinline__ float4 load4(const __half* p) { return widen(*reinterpret_cast<const uint2*>(p)); }
+    static __device__ __forceinline__ float4 widen(uint2 u) {
         const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
         const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
         return make_float4(a.x, a.y, b.x, b.y);

@@ -72,6 +72,21 @@ __device__ __forceinline__ void store_out4(const Attend& a, long long row, int h
     else
         Elem<__half>::store4(static_cast<__half*>(a.out) + at, v);
 }
+__device__ __forceinline__ void store_out8(const Attend& a, long long row, int h, int d, float4 u, float4 v) {
+    const long long at = (row * a.q_heads + h) * a.c.dim + d;
+    if (a.dtype == MMQ_F32) {
+        Elem<float>::store4(static_cast<float*>(a.out) + at, u);
+        Elem<float>::store4(static_cast<float*>(a.out) + at + 4, v);
+    } else if (a.dtype == MMQ_BF16) {
+        using E = Elem<__nv_bfloat16>;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) =
+            make_uint4(E::pack2(u.x, u.y), E::pack2(u.z, u.w), E::pack2(v.x, v.y), E::pack2(v.z, v.w));
+    } else {
+        using E = Elem<__half>;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) =
+            make_uint4(E::pack2(u.x, u.y), E::pack2(u.z, u.w), E::pack2(v.x, v.y), E::pack2(v.z, v.w));
+    }
+}
 __device__ __forceinline__ void store_lse(const Attend& a, long long row, int h, float m, float l) {
     if (a.lse) a.lse[row * a.q_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -89,11 +104,12 @@ __device__ __forceinline__ void value_scale(float dv, float& lv, float& rv) {
     rv = __fdividef(1.f, d);
 }
 
-// Power of two that brings a row's largest magnitude into [1, 2) (exactly): 2^-e, and 2^e
+// Powers of two: `down` brings a row's largest magnitude into [2^8, 2^9) (exactly; f16 then keeps
+// what lies down to 2^-33 below it), `up` takes it back.
 __device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
-    const int e = max(1, min(253, (int)((__float_as_uint(amax) >> 23) & 255)));  // biased
-    down = __uint_as_float((uint32_t)(254 - e) << 23);
-    up = __uint_as_float((uint32_t)e << 23);
+    const int e = max(9, min(253, (int)((__float_as_uint(amax) >> 23) & 255)));  // biased
+    down = __uint_as_float((uint32_t)(262 - e) << 23);
+    up = __uint_as_float((uint32_t)(e - 8) << 23);
 }
 
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) { return Elem<__half>::pack2(a, b); }

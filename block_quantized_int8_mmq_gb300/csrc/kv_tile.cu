@@ -29,21 +29,31 @@ __device__ unsigned g_kv_tile_error;
 
 template <int D, bool SPLIT>
 struct Tile {
-    static constexpr int MT = D == 256 ? 1 : 2;                  // row tiles of a CTA
-    static constexpr int KT = D == 64 ? 128 : D == 128 ? (SPLIT ? 64 : 128) : 64;  // keys per tile
-    static constexpr int ST = D == 256 && SPLIT ? 1 : 2;         // converted tiles in shared memory
+    // D = 256: the two groups of softmax warps share one tile of rows and take half of the value
+    // columns each (S is formed twice; a group's TMEM and registers are those of D = 128)
+    static constexpr bool HALF = D == 256;
+    static constexpr int OD = HALF ? D / 2 : D;                  // value columns of a group
+    static constexpr int KT = !SPLIT ? (HALF ? 64 : 128) : (HALF ? 32 : 64);  // keys per tile
+    static constexpr int ST = 2;                                 // converted tiles in shared memory
     static constexpr int TERMS = SPLIT ? 2 : 1;
-    static constexpr int SOFT = 4 * MT, CONV = 4, WARPS = SOFT + CONV, THREADS = 32 * WARPS;
-    static constexpr int ROWS = 128 * MT;
+    static constexpr int SOFT = 8, CONV = 4, WARPS = SOFT + CONV, THREADS = 32 * WARPS;
+    static constexpr int ROWS = HALF ? 128 : 256;
     static constexpr int KV = KT * D * 2, Q = 128 * D * 2;       // bytes of a converted tile, of a row tile's term
     // the queries last: every operand read stays inside the allocation
-    static constexpr int OFF_V = ST * KV, OFF_Q = 2 * ST * KV, OFF_BAR = OFF_Q + MT * TERMS * Q;
-    static constexpr int NBAR = 4 * ST + 4 * MT;
+    static constexpr int OFF_V = ST * KV, OFF_Q = 2 * ST * KV, OFF_BAR = OFF_Q + (HALF ? 1 : 2) * TERMS * Q;
+    static constexpr int NBAR = 4 * ST + 2 * 5 + 2;
     static constexpr int USED = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of TMEM
-    static constexpr int COL_O = MT * KT;                        // TMEM columns: S of each row tile, then O
-    static_assert(MT * (KT + D) <= 512 && SMEM <= 232448 - 1024, "tile sizes");
+    static constexpr int COL_O = 2 * KT;                         // TMEM columns: S of each group, then O
     static constexpr int BLK = KT / BT;                          // records per key tile
+    // SPLIT: O leaves TMEM for f32 registers every 256 keys: the tensor core's accumulation rounds
+    // towards zero, and its error grows with the number of products added (f32 rows of 1500 tokens:
+    // 2.3e-6 off in all without it)
+    static constexpr int FLUSH = 256 / KT;
+    // registers: the softmax warps' and the converters' shares of the launch's 384 x 168
+    static constexpr int R_SOFT = SPLIT ? 216 : 200, R_CONV = SPLIT ? 72 : 104;
+    static_assert(2 * (KT + OD) <= 512 && SMEM <= 232448 - 1024, "tile sizes");
+    static_assert(256 * R_SOFT + 128 * R_CONV <= 384 * 168, "register shares");
 };
 
 // A unit: a run of ROWS rows of one sequence and head, and the key tiles that they see.
@@ -84,31 +94,59 @@ __device__ __forceinline__ void unit_next(const Attend& a, Unit& w) {
     while (w.tiles == 0 && ++w.b < a.bt.seqs) unit_load<ROWS, KT>(a, w, w.b, 0);
 }
 
+// What a unit costs beside its key tiles (queries in, output out), in key tiles: a unit takes
+// OVERHEAD + tiles places in the list of work, and the first OVERHEAD of them hold nothing.
+constexpr int OVERHEAD = 3;
+
+// The next run of key tiles [t0, t1) of this CTA's places x .. x1 - 1; pos: place in unit w.
+template <int ROWS, int KT>
+__device__ __forceinline__ bool next_piece(const Attend& a, Unit& w, int& pos, int& x, int x1, int& t0, int& t1) {
+    while (x < x1) {
+        if (pos == w.tiles + OVERHEAD) {
+            unit_next<ROWS, KT>(a, w);
+            pos = 0;
+        }
+        const int span = min(w.tiles + OVERHEAD - pos, x1 - x);
+        t0 = max(0, pos - OVERHEAD);
+        t1 = max(0, pos + span - OVERHEAD);
+        pos += span;
+        x += span;
+        if (t1 > t0) return true;
+    }
+    return false;
+}
+
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(Tile<D, SPLIT>::THREADS, 1)
 k_kv_attend_tile(const Attend a) {
     using C = Tile<D, SPLIT>;
-    constexpr int KT = C::KT, ST = C::ST, MT = C::MT, SBO = D * 16;
+    constexpr int KT = C::KT, ST = C::ST, OD = C::OD, SBO = D * 16;
+    constexpr bool HALF = C::HALF;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_scan[C::WARPS], s_pref[C::THREADS + 1], s_at[3], s_last[MT];
+    __shared__ int s_abort, s_scan[C::WARPS], s_pref[C::THREADS + 1], s_at[3], s_last[2];
     __shared__ float4 s_sc[4][C::BLK];  // dk, log2 dv, 1 / dv of the blocks of four consecutive tiles
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const uint32_t base = ptx::smem_u32(smem), bars = base + C::OFF_BAR;
     const uint32_t k_full = bars, k_empty = bars + 8 * ST, v_full = bars + 16 * ST, v_empty = bars + 24 * ST;
-    const uint32_t s_full = bars + 32 * ST, o_full = s_full + 8 * MT, p_ready = o_full + 8 * MT, joined = p_ready + 8 * MT;
+    const uint32_t s_full = bars + 32 * ST, o_full = s_full + 16, p_ready = o_full + 16, joined = p_ready + 16;
+    const uint32_t turn = joined + 16;  // the groups issue their products in turn
+    const uint32_t q_ready = turn + 16, q_free = q_ready + 8;  // HALF: of the queries that both groups use
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             ptx::mbar_init(k_full + 8 * i, C::CONV);
             ptx::mbar_init(v_full + 8 * i, C::CONV);
-            ptx::mbar_init(k_empty + 8 * i, MT);
-            ptx::mbar_init(v_empty + 8 * i, MT);
+            ptx::mbar_init(k_empty + 8 * i, 2);
+            ptx::mbar_init(v_empty + 8 * i, 2);
         }
-        for (int i = 0; i < MT; ++i) {
+        ptx::mbar_init(q_ready, C::SOFT);
+        ptx::mbar_init(q_free, C::SOFT);
+        for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(s_full + 8 * i, 1);
             ptx::mbar_init(o_full + 8 * i, 1);
             ptx::mbar_init(p_ready + 8 * i, 4);
             ptx::mbar_init(joined + 8 * i, 1);
+            ptx::mbar_init(turn + 8 * i, 1);
         }
         ptx::fence_barrier_init();
         s_abort = 0;
@@ -118,7 +156,8 @@ k_kv_attend_tile(const Attend a) {
 
     // ---- this CTA's range of the work: sequences THREADS at a time, their row runs spread over the threads
     int T = 0, W = 0, x0 = 0, x1 = 0;
-    for (int pass = 0; pass < 2; ++pass) {
+    bool located = false;
+    for (int pass = 0; pass < 2 && !located; ++pass) {
         int carry = 0;
         for (int b0 = 0; b0 < a.bt.seqs; b0 += C::THREADS) {
             int runs = 0, total;
@@ -131,8 +170,8 @@ k_kv_attend_tile(const Attend a) {
             __syncthreads();
             for (int i0 = 0; i0 < total; i0 += C::THREADS) {
                 const int i = i0 + tid;
-                Unit w;
-                w.tiles = 0;
+                Unit q;
+                q.tiles = 0;
                 if (i < total) {
                     int lo = 0, hi = C::THREADS - 1;  // the last sequence that begins at or before run i
                     while (lo < hi) {
@@ -142,14 +181,21 @@ k_kv_attend_tile(const Attend a) {
                         else
                             hi = mid - 1;
                     }
-                    unit_load<C::ROWS, KT>(a, w, b0 + lo, i - s_pref[lo]);
+                    unit_load<C::ROWS, KT>(a, q, b0 + lo, i - s_pref[lo]);
                 }
                 int sum;
-                const int v = w.tiles * a.c.heads, e = carry + scan_cta<C::WARPS>(v, sum, s_scan);
+                const int v = q.tiles ? (q.tiles + OVERHEAD) * a.c.heads : 0;
+                const int e = carry + scan_cta<C::WARPS>(v, sum, s_scan);
                 carry += sum;
-                if (pass == 1 && x0 >= e && x0 < e + v) {
-                    s_at[0] = w.b;
-                    s_at[1] = w.u;
+                if (pass == 0 && a.bt.seqs <= C::THREADS && total <= C::THREADS) {  // that was all of it
+                    located = true;
+                    T = carry;
+                    W = min((int)gridDim.x, T);
+                    x0 = work_start(T, min((int)blockIdx.x, W), W);
+                }
+                if ((pass == 1 || located) && x0 >= e && x0 < e + v) {
+                    s_at[0] = q.b;
+                    s_at[1] = q.u;
                     s_at[2] = x0 - e;
                 }
             }
@@ -175,11 +221,12 @@ k_kv_attend_tile(const Attend a) {
 
     Unit w;
     unit_load<C::ROWS, KT>(a, w, s_at[0], s_at[1]);
-    w.h = s_at[2] / w.tiles;
-    int o = s_at[2] - w.h * w.tiles;
+    w.h = s_at[2] / (w.tiles + OVERHEAD);
+    int place = s_at[2] - w.h * (w.tiles + OVERHEAD), x = x0, o0 = 0, o1 = 0;  // place in the unit, key tiles of the piece
 
     if (wid >= C::SOFT) {
         // ------------------------------------------------ converters: warp cw takes tokens KT/4 cw ..
+        ptx::regs_dec<C::R_CONV>();
         constexpr int NL = KT * D / 2048, PER = D / 64;
         const int cw = wid - C::SOFT, r8 = lane & 7, cq = lane >> 3;
         const int tok0 = cw * (KT / 4), bi = tok0 / BT, sub = tok0 % BT;
@@ -216,21 +263,21 @@ k_kv_attend_tile(const Attend a) {
         };
         uint4 kb[NL], vb[NL];
         float2 sc = make_float2(0.f, 0.f);
-        int in = 0, id = page_of(w, o, in);
+        bool more = next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1);
+        int o = o0, in = 0, id = more ? page_of(w, o, in) : -1;
         if (id < -1 || id >= a.c.pages) atomicOr(err, ERR_RANGE);
         const uint8_t* rec = rec_of(id, in, w.h);
         load(kb, rec);
         load(vb, rec ? rec + BT * D : nullptr);
         if (rec) sc = *reinterpret_cast<const float2*>(rec + 2 * BT * D);
         bool some = rec != nullptr;
-        for (int x = x0, n = 0; x < x1; ++x, ++n) {
+        for (int n = 0; more; ++n) {
             const int st = n % ST;
             // the next tile's place
-            if (++o == w.tiles) {
-                unit_next<C::ROWS, KT>(a, w);
-                o = 0;
+            if (++o == o1) {
+                more = next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1);
+                o = o0;
             }
-            const bool more = x + 1 < x1;
             if (more) id = page_of(w, o, in);
             const uint32_t par = ((n / ST) & 1) ^ 1;
             if (!umma::warp_wait(k_empty + 8 * st, par, abort, err)) break;
@@ -260,30 +307,32 @@ k_kv_attend_tile(const Attend a) {
         }
     } else {
         // ------------------------------------------------ softmax: thread = row, and the MMA issue
-        const int gt = wid >> 2, row = tid & 127;  // row tile, row in it
+        ptx::regs_inc<C::R_SOFT>();
+        const int gt = wid >> 2, row = tid & 127, wrow = (wid & 3) * 32;  // group, row of its tile, the warp's first
+        const int tile0 = HALF ? 0 : gt * 128, col0 = HALF ? gt * OD : 0;  // first row of the unit, first value column
         const bool leader = (wid & 3) == 0 && lane == 0;
-        const uint32_t lane_off = (uint32_t)((wid & 3) * 32) << 16;
-        const uint32_t t_s = tmem + gt * KT, t_o = tmem + C::COL_O + gt * D;
+        const uint32_t lane_off = (uint32_t)wrow << 16;
+        const uint32_t t_s = tmem + gt * KT, t_o = tmem + C::COL_O + gt * OD;
         const uint32_t sf = s_full + 8 * gt, of = o_full + 8 * gt, pr = p_ready + 8 * gt, jn = joined + 8 * gt;
-        const uint32_t q_addr = base + C::OFF_Q + gt * C::TERMS * C::Q;
-        uint8_t* q_smem = smem + C::OFF_Q + gt * C::TERMS * C::Q;
-        constexpr uint32_t idesc_s = umma::make_idesc(128, KT), idesc_o = umma::make_idesc(128, D) | (1u << 16);
-        uint32_t n_pr = 0, n_sf = 0, n_of = 0, n_jn = 0;  // phases
-        auto issue_s = [&](int st) {  // S = Q K^T
+        const uint32_t q_addr = base + C::OFF_Q + (HALF ? 0 : gt * C::TERMS * C::Q);
+        uint8_t* q_smem = smem + C::OFF_Q + (HALF ? 0 : gt * C::TERMS * C::Q);
+        constexpr uint32_t idesc_s = umma::make_idesc(128, KT), idesc_o = umma::make_idesc(128, OD) | (1u << 16);
+        uint32_t n_pr = 0, n_sf = 0, n_of = 0, n_jn = 0, n_unit = 0;  // phases
+        auto issue_s = [&](int st) {  // S = Q K^T, the small terms first
             const uint64_t bd = umma::sdesc(base + st * C::KV, SBO);
 #pragma unroll
-            for (int e = 0; e < C::TERMS; ++e) {
+            for (int e = C::TERMS - 1; e >= 0; --e) {
                 const uint64_t ad = umma::sdesc(q_addr + e * C::Q, SBO);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    ptx::umma_f16(t_s, ad + 16 * ks, bd + 16 * ks, idesc_s, e + ks > 0);
+                    ptx::umma_f16(t_s, ad + 16 * ks, bd + 16 * ks, idesc_s, e < C::TERMS - 1 || ks > 0);
             }
             ptx::umma_commit(k_empty + 8 * st);
             ptx::umma_commit(sf);
         };
         // values: 8-column groups 128 B apart (stride offset), 8-token groups SBO apart (leading offset)
         auto issue_o = [&](int st, bool first) {
-            const uint32_t va = base + C::OFF_V + st * C::KV;
+            const uint32_t va = base + C::OFF_V + st * C::KV + col0 * 16;
             const uint64_t bd = (uint64_t)((va & 0x3FFFFu) >> 4) | ((uint64_t)(SBO >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
                                 (1ull << 46);
 #pragma unroll
@@ -294,73 +343,129 @@ k_kv_attend_tile(const Attend a) {
                                      !(first && ks + e == 0));
             ptx::umma_commit(v_empty + 8 * st);
         };
+        // The groups alternate batch by batch (O += P V, then the next S): batches that ran side by
+        // side would end together, and then both groups' softmaxes would run side by side too.
+        uint32_t n_turn = gt == 0 ? 1 : 0;
+        auto take_turn = [&]() { return umma::wait_bar(turn + 8 * gt, n_turn++ & 1, abort, err); };
+        auto pass_turn = [&]() { ptx::mbar_arrive(turn + 8 * (1 - gt)); };
         auto signal = [&](uint32_t bar) {  // this warp's part is in place
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar);
         };
         bool ok = true;
-        for (int x = x0, n = 0; x < x1 && ok;) {
-            const int o0 = o, tiles = min(w.tiles - o, x1 - x);  // this unit's tiles here
-            const int rloc = gt * 128 + row, r = w.u * C::ROWS + rloc;
-            if (w.u * C::ROWS + gt * 128 >= w.rows) {
+        for (int n = 0; ok && next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1);) {
+            const int tiles = o1 - o0;  // this unit's tiles here
+            const int row0 = w.u * C::ROWS + tile0, r = row0 + row;
+            if (row0 >= w.rows) {
                 // no rows in this row tile: only pass the converted tiles on
                 if (leader)
-                    for (int i = 0; i < tiles && ok; ++i) {
-                        const int st = (n + i) % ST, par = ((n + i) / ST) & 1;
-                        ok = umma::wait_bar(k_full + 8 * st, par, abort, err);
-                        if (ok) ptx::mbar_arrive(k_empty + 8 * st);
-                        ok = ok && umma::wait_bar(v_full + 8 * st, par, abort, err);
-                        if (ok) ptx::mbar_arrive(v_empty + 8 * st);
+                    for (int i = 0; i <= tiles && ok; ++i) {
+                        if (i > 0) {
+                            ok = umma::wait_bar(v_full + 8 * ((n + i - 1) % ST), ((n + i - 1) / ST) & 1, abort, err);
+                            if (ok) ptx::mbar_arrive(v_empty + 8 * ((n + i - 1) % ST));
+                        }
+                        if (i < tiles && ok) {
+                            ok = umma::wait_bar(k_full + 8 * ((n + i) % ST), ((n + i) / ST) & 1, abort, err);
+                            if (ok) ptx::mbar_arrive(k_empty + 8 * ((n + i) % ST));
+                        }
+                        ok = ok && take_turn();
+                        if (ok) pass_turn();
                     }
                 ok = __all_sync(0xffffffffu, ok);
             } else {
                 const bool real = r < w.rows;
                 const int t = r / a.group, hq = w.h * a.group + r - t * a.group, pos = w.len - w.n + t;
-                // the row's queries, scaled into f16's range, in core-matrix order
+                // the warp's rows of queries, scaled into f16's range, in core-matrix order: eight rows at
+                // a time, lane (row % 8, 16-byte chunk % 4); HALF: each group writes half of the columns
+                if (HALF && n_unit > 0 && !umma::warp_wait(q_free, (n_unit - 1) & 1, abort, err)) {
+                    ok = false;
+                    break;
+                }
                 float up = 1.f;
-                {
-                    float am = 0.f, down = 1.f;
-                    if (real) {
-#pragma unroll 8
-                        for (int d = 0; d < D; d += 4) {
-                            const float4 v = load_row4(a, w.start + t, hq, d);
+                constexpr int NC = D / 32, GB = (SPLIT ? 2 : 4) / (HALF ? 2 : 1);  // chunks a lane, row groups in flight
+#pragma unroll 1
+                for (int g0 = 0; g0 < 4; g0 += GB) {
+                    uint4 raw[GB][NC][SPLIT ? 2 : 1];
+#pragma unroll
+                    for (int gi = 0; gi < GB; ++gi) {
+                        const int rr = row0 + wrow + 8 * (g0 + gi) + (lane & 7), tt = rr / a.group;
+                        const long long at = (long long)(w.start + tt) * a.q.token_stride +
+                                             (long long)(w.h * a.group + rr - tt * a.group) * a.q.head_stride + 8 * (lane >> 3);
+                        const uint8_t* src = static_cast<const uint8_t*>(a.q.data) + at * (SPLIT ? 4 : 2);
+#pragma unroll
+                        for (int i = 0; i < NC; ++i)
+#pragma unroll
+                            for (int e = 0; e < (SPLIT ? 2 : 1); ++e)
+                                raw[gi][i][e] = rr < w.rows ? *reinterpret_cast<const uint4*>(src + i * (SPLIT ? 128 : 64) + 16 * e)
+                                                            : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int gi = 0; gi < GB; ++gi) {
+                        const int rl = wrow + 8 * (g0 + gi) + (lane & 7);
+                        auto eight = [&](int i, float4& u, float4& v) {
+                            const uint4 p = raw[gi][i][0], q = raw[gi][i][SPLIT ? 1 : 0];
+                            if (SPLIT) {
+                                u = make_float4(__uint_as_float(p.x), __uint_as_float(p.y), __uint_as_float(p.z), __uint_as_float(p.w));
+                                v = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
+                            } else if (a.dtype == MMQ_BF16) {
+                                u = Elem<__nv_bfloat16>::widen(make_uint2(p.x, p.y));
+                                v = Elem<__nv_bfloat16>::widen(make_uint2(p.z, p.w));
+                            } else {
+                                u = Elem<__half>::widen(make_uint2(p.x, p.y));
+                                v = Elem<__half>::widen(make_uint2(p.z, p.w));
+                            }
+                        };
+                        float am = 0.f;
+#pragma unroll
+                        for (int i = 0; i < NC; ++i) {
+                            float4 u, v;
+                            eight(i, u, v);
+                            am = fmaxf(am, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))));
                             am = fmaxf(am, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
                         }
-                        row_scale(am, down, up);
-                    }
-                    uint8_t* dst = q_smem + (row >> 3) * SBO + (row & 7) * 16;
-#pragma unroll 4
-                    for (int d = 0; d < D; d += 8) {
-                        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-                        if (real) {
-                            u = load_row4(a, w.start + t, hq, d);
-                            v = load_row4(a, w.start + t, hq, d + 4);
+                        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 8));
+                        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
+                        float down, upr;
+                        row_scale(am, down, upr);
+                        if (lane >> 3 == g0 + gi) up = upr;
+                        uint8_t* dst = q_smem + (rl >> 3) * SBO + (lane >> 3) * 128 + (rl & 7) * 16;
+#pragma unroll
+                        for (int i = 0; i < NC; ++i) {
+                            if (HALF && (i >= NC / 2) != (gt == 1)) continue;
+                            float4 u, v;
+                            eight(i, u, v);
+                            uint4 hi4, lo4;
+                            split_h2(u.x * down, u.y * down, hi4.x, lo4.x);
+                            split_h2(u.z * down, u.w * down, hi4.y, lo4.y);
+                            split_h2(v.x * down, v.y * down, hi4.z, lo4.z);
+                            split_h2(v.z * down, v.w * down, hi4.w, lo4.w);
+                            *reinterpret_cast<uint4*>(dst + 512 * i) = hi4;
+                            if (SPLIT) *reinterpret_cast<uint4*>(dst + C::Q + 512 * i) = lo4;
                         }
-                        uint4 hi4, lo4;
-                        split_h2(u.x * down, u.y * down, hi4.x, lo4.x);
-                        split_h2(u.z * down, u.w * down, hi4.y, lo4.y);
-                        split_h2(v.x * down, v.y * down, hi4.z, lo4.z);
-                        split_h2(v.z * down, v.w * down, hi4.w, lo4.w);
-                        *reinterpret_cast<uint4*>(dst + d * 16) = hi4;
-                        if (SPLIT) *reinterpret_cast<uint4*>(dst + C::Q + d * 16) = lo4;
                     }
-                    ptx::fence_proxy_async_smem();
                 }
+                ptx::fence_proxy_async_smem();
                 const float fq = up * a.scale2;
                 const int hi = real ? pos + 1 : 0x7fffffff, lo = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
                 const int hi_min = __reduce_min_sync(0xffffffffu, hi), lo_max = __reduce_max_sync(0xffffffffu, lo);
-                signal(pr);
+                signal(HALF ? q_ready : pr);
                 if (leader) {
-                    ok = umma::wait_bar(pr, n_pr & 1, abort, err) &&
-                         umma::wait_bar(k_full + 8 * (n % ST), (n / ST) & 1, abort, err);
+                    ok = umma::wait_bar(HALF ? q_ready : pr, HALF ? n_unit & 1 : n_pr & 1, abort, err) &&
+                         umma::wait_bar(k_full + 8 * (n % ST), (n / ST) & 1, abort, err) && take_turn();
                     if (ok) {
                         ptx::tc_fence_after();
                         issue_s(n % ST);
+                        pass_turn();
                     }
                 }
-                ++n_pr;
+                if (!HALF) ++n_pr;
+                ++n_unit;
                 float m = M_NONE, l = 0.f;
+                unsigned long long om[SPLIT ? OD / 2 : 1];  // SPLIT: O so far, pairs of columns
+#pragma unroll
+                for (int k = 0; k < (SPLIT ? OD / 2 : 1); ++k) om[k] = 0ull;
+#pragma unroll 1
                 for (int i = 0; i < tiles; ++i) {
                     const int nn = n + i, j0 = (w.kt0 + o0 + i) * KT;
                     if (!umma::warp_wait(sf, n_sf++ & 1, abort, err)) {
@@ -368,104 +473,135 @@ k_kv_attend_tile(const Attend a) {
                         break;
                     }
                     ptx::tc_fence_after();
+                    if (HALF && i + 1 == tiles) signal(q_free);
+                    uint32_t sr[C::BLK][32];
+#pragma unroll
+                    for (int c = 0; c < C::BLK; ++c) ptx::tmem_ld32(t_s + lane_off + 32 * c, sr[c]);
                     const float4* scv = s_sc[nn & 3];
                     const bool edge = j0 + KT > hi_min || j0 < lo_max;
-                    float tm = -INFINITY;
-#pragma unroll 1
+                    float af[C::BLK], lv[C::BLK], rv[C::BLK];
+#pragma unroll
                     for (int c = 0; c < C::BLK; ++c) {
-                        uint32_t sr[32];
-                        ptx::tmem_ld32(t_s + lane_off + 32 * c, sr);
                         const float4 s4 = scv[c];
-                        const float af = fq * s4.x;
-                        ptx::tmem_ld_wait(sr);
-                        if (!edge) {
-                            float mx = __uint_as_float(sr[0]);
+                        af[c] = fq * s4.x;
+                        lv[c] = s4.y;
+                        rv[c] = s4.z;
+                    }
+                    float tm = -INFINITY;
 #pragma unroll
-                            for (int k = 1; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(sr[k]));
-                            tm = fmaxf(tm, fmaf(mx, af, s4.y));
-                        } else {
-                            const int jc = j0 + 32 * c;
+                    for (int c = 0; c < C::BLK; ++c) ptx::tmem_ld_wait(sr[c]);
+                    if (!edge) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (jc + k >= lo && jc + k < hi) tm = fmaxf(tm, fmaf(__uint_as_float(sr[k]), af, s4.y));
+                        for (int c = 0; c < C::BLK; ++c) {
+                            float mx = __uint_as_float(sr[c][0]), my = __uint_as_float(sr[c][1]);
+#pragma unroll
+                            for (int k = 2; k < 32; k += 4) {
+                                mx = fmaxf(fmaxf(mx, __uint_as_float(sr[c][k])), __uint_as_float(sr[c][k + 1]));
+                                if (k + 3 < 32)
+                                    my = fmaxf(fmaxf(my, __uint_as_float(sr[c][k + 2])), __uint_as_float(sr[c][k + 3]));
+                            }
+                            tm = fmaxf(tm, fmaf(fmaxf(mx, my), af[c], lv[c]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C::BLK; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int j = j0 + 32 * c + k;
+                                const float tk = j >= lo && j < hi ? fmaf(__uint_as_float(sr[c][k]), af[c], lv[c]) : -INFINITY;
+                                tm = fmaxf(tm, tk);
+                                sr[c][k] = __float_as_uint(tk);
+                            }
+                    }
+                    // the products so far are done: S came after them
+                    const bool flush = SPLIT && i > 0 && i % C::FLUSH == 0;
+                    if (SPLIT && flush) {
+#pragma unroll
+                        for (int c = 0; c < OD / 16; ++c) {
+                            uint32_t ov[16];
+                            ptx::tmem_ld16(t_o + lane_off + 16 * c, ov);
+                            ptx::tmem_ld_wait(ov);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                om[SPLIT ? 8 * c + k : 0] = ptx::add_f32x2(
+                                    om[SPLIT ? 8 * c + k : 0], ptx::f2_bits(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1])));
                         }
                     }
                     if (__any_sync(0xffffffffu, tm > m + LIMIT)) {
                         const float mn = fmaxf(m, tm - SHIFT), f = exp2_approx(m - mn);
                         m = mn;
                         l *= f;
-                        if (i > 0) {  // the products so far are done: S came after them
+                        if (SPLIT) {
+                            const unsigned long long f2 = ptx::f2_bits(f, f);
+#pragma unroll
+                            for (int k = 0; k < (SPLIT ? OD / 2 : 1); ++k) om[k] = ptx::mul_f32x2(om[k], f2);
+                        }
+                        if (i > 0 && !flush) {
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t ov[32];
-                                ptx::tmem_ld32(t_o + lane_off + 32 * c, ov);
+                            for (int c = 0; c < OD / 16; ++c) {
+                                uint32_t ov[16];
+                                ptx::tmem_ld16(t_o + lane_off + 16 * c, ov);
                                 ptx::tmem_ld_wait(ov);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-                                ptx::tmem_st32(t_o + lane_off + 32 * c, ov);
+                                for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+                                ptx::tmem_st16(t_o + lane_off + 16 * c, ov);
                             }
                         }
                     }
-#pragma unroll 1
-                    for (int c = 0; c < C::BLK; ++c) {
-                        uint32_t sr[32];
-                        ptx::tmem_ld32(t_s + lane_off + 32 * c, sr);
-                        const float4 s4 = scv[c];
-                        const float af = fq * s4.x, bf = s4.y - m;
-                        ptx::tmem_ld_wait(sr);
-                        if (edge) {
-                            const int jc = j0 + 32 * c;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const float tk = fmaf(__uint_as_float(sr[k]), af, bf);
-                                sr[k] = __float_as_uint(jc + k >= lo && jc + k < hi ? exp2_approx(tk) : 0.f);
-                            }
+                    for (int c = 0; c < C::BLK; ++c) {
+                        if (edge) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                sr[c][k] = __float_as_uint(exp2_approx(__uint_as_float(sr[c][k]) - m));
                         } else {
-                            const unsigned long long a2 = ptx::f2_bits(af, af), b2 = ptx::f2_bits(bf, bf);
+                            const float bf = lv[c] - m;
+                            const unsigned long long a2 = ptx::f2_bits(af[c], af[c]), b2 = ptx::f2_bits(bf, bf);
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
-                                const unsigned long long t2 =
-                                    ptx::fma_f32x2(ptx::f2_bits(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), a2, b2);
-                                sr[k] = __float_as_uint(exp2_approx(__uint_as_float((uint32_t)t2)));
-                                sr[k + 1] = __float_as_uint(exp2_approx(__uint_as_float((uint32_t)(t2 >> 32))));
+                                const unsigned long long t2 = ptx::fma_f32x2(
+                                    ptx::f2_bits(__uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1])), a2, b2);
+                                sr[c][k] = __float_as_uint(exp2_approx(__uint_as_float((uint32_t)t2)));
+                                sr[c][k + 1] = __float_as_uint(exp2_approx(__uint_as_float((uint32_t)(t2 >> 32))));
                             }
                         }
                         unsigned long long sum2 = 0ull, sum3 = 0ull;
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
-                            sum2 = ptx::add_f32x2(sum2, ptx::f2_bits(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])));
-                            sum3 = ptx::add_f32x2(sum3, ptx::f2_bits(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])));
+                            sum2 = ptx::add_f32x2(sum2, ptx::f2_bits(__uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1])));
+                            sum3 = ptx::add_f32x2(sum3,
+                                                  ptx::f2_bits(__uint_as_float(sr[c][k + 2]), __uint_as_float(sr[c][k + 3])));
                         }
                         sum2 = ptx::add_f32x2(sum2, sum3);
-                        l = fmaf(__uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32)), s4.z, l);
+                        l = fmaf(__uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32)), rv[c], l);
+                        uint32_t pw[16];
                         if (SPLIT) {
-                            uint32_t pw[32];
+                            uint32_t pl[16];
 #pragma unroll
                             for (int k = 0; k < 16; ++k)
-                                split_h2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]), pw[k], pw[16 + k]);
-                            ptx::tmem_st32(t_s + lane_off + 32 * c, pw);
+                                split_h2(__uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1]), pw[k], pl[k]);
+                            ptx::tmem_st16(t_s + lane_off + 32 * c + 16, pl);
                         } else {
-                            uint32_t pw[16];
 #pragma unroll
                             for (int k = 0; k < 16; ++k)
-                                pw[k] = pack_h2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
-                            ptx::tmem_st16(t_s + lane_off + 32 * c, pw);
+                                pw[k] = pack_h2(__uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1]));
                         }
+                        ptx::tmem_st16(t_s + lane_off + 32 * c, pw);
                     }
                     ptx::tmem_st_wait();
                     signal(pr);
                     if (leader) {
                         const int st = nn % ST, par = (nn / ST) & 1, s2 = (nn + 1) % ST, par2 = ((nn + 1) / ST) & 1;
-                        ok = umma::wait_bar(pr, n_pr & 1, abort, err) && umma::wait_bar(v_full + 8 * st, par, abort, err);
+                        ok = umma::wait_bar(pr, n_pr & 1, abort, err) && umma::wait_bar(v_full + 8 * st, par, abort, err) &&
+                             (i + 1 == tiles || umma::wait_bar(k_full + 8 * s2, par2, abort, err)) && take_turn();
                         if (ok) {
                             ptx::tc_fence_after();
-                            issue_o(st, i == 0);
-                            if (i + 1 == tiles) {
+                            issue_o(st, i == 0 || flush);
+                            if (i + 1 == tiles)
                                 ptx::umma_commit(of);
-                            } else {
-                                ok = umma::wait_bar(k_full + 8 * s2, par2, abort, err);
-                                if (ok) issue_s(s2);
-                            }
+                            else
+                                issue_s(s2);
+                            pass_turn();
                         }
                     }
                     ++n_pr;
@@ -474,40 +610,46 @@ k_kv_attend_tile(const Attend a) {
                 if (!ok) break;
                 ptx::tc_fence_after();
                 // ---- the unit's output, or this CTA's part of it
-                const int ustart = x - o0, uend = ustart + w.tiles;
+                const int ufirst = x - place + OVERHEAD;  // place of the unit's first key tile
                 const bool whole = o0 == 0 && tiles == w.tiles;
-                // a part's layout: [D / 4][128 rows] float4, then m, l of the rows
-                auto part = [&](int cta, int slot) {
-                    return part_slot(a, cta, slot) + gt * 128 * (D + 2);
-                };
+                // a part's layout: [OD / 4][128 rows] float4, then m, l of the rows
+                auto part = [&](int cta, int slot) { return part_slot(a, cta, slot) + gt * 128 * (OD + 2); };
                 float* mine = part(blockIdx.x, o0 == 0 ? 1 : 0);
                 const float inv = whole ? (l > 0.f ? __frcp_rn(l) : 0.f) : 1.f;
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t ov[32];
-                    ptx::tmem_ld32(t_o + lane_off + 32 * c, ov);
+#pragma unroll
+                for (int c = 0; c < OD / 16; ++c) {
+                    uint32_t ov[16];
+                    ptx::tmem_ld16(t_o + lane_off + 16 * c, ov);
                     ptx::tmem_ld_wait(ov);
                     if (real) {
+                        float f[16];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 v = make_float4(__uint_as_float(ov[k]) * inv, __uint_as_float(ov[k + 1]) * inv,
-                                                         __uint_as_float(ov[k + 2]) * inv, __uint_as_float(ov[k + 3]) * inv);
-                            if (whole)
-                                store_out4(a, w.start + t, hq, 32 * c + k, v);
-                            else
-                                *reinterpret_cast<float4*>(mine + ((8 * c + k / 4) * 128 + row) * 4) = v;
+                        for (int k = 0; k < 16; ++k) {
+                            const unsigned long long o2 = om[SPLIT ? 8 * c + k / 2 : 0];
+                            f[k] = (__uint_as_float(ov[k]) + (SPLIT ? __uint_as_float((uint32_t)(k & 1 ? o2 >> 32 : o2)) : 0.f)) * inv;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; k += 8) {
+                            const float4 f0 = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                            const float4 f1 = make_float4(f[k + 4], f[k + 5], f[k + 6], f[k + 7]);
+                            if (whole) {
+                                store_out8(a, w.start + t, hq, col0 + 16 * c + k, f0, f1);
+                            } else {
+                                *reinterpret_cast<float4*>(mine + ((4 * c + k / 4) * 128 + row) * 4) = f0;
+                                *reinterpret_cast<float4*>(mine + ((4 * c + k / 4 + 1) * 128 + row) * 4) = f1;
+                            }
                         }
                     }
                 }
                 ptx::tc_fence_before();
                 if (whole) {
-                    if (real) store_lse(a, w.start + t, hq, m, l);
+                    if (real && col0 == 0) store_lse(a, w.start + t, hq, m, l);
                 } else {
                     if (real) {
-                        mine[128 * D + row] = m;
-                        mine[128 * (D + 1) + row] = l;
+                        mine[128 * OD + row] = m;
+                        mine[128 * (OD + 1) + row] = l;
                     }
-                    const int c0 = work_owner(T, ustart, W), c1 = work_owner(T, uend - 1, W);
+                    const int c0 = work_owner(T, ufirst, W), c1 = work_owner(T, ufirst + w.tiles - 1, W);
                     __threadfence();
                     signal(pr);
                     if (leader) {
@@ -529,43 +671,45 @@ k_kv_attend_tile(const Attend a) {
                         if (real) {
                             float M = M_NONE, L = 0.f;
 #pragma unroll 4
-                            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c, c == c0) + 128 * D + row));
-#pragma unroll 4
                             for (int c = c0; c <= c1; ++c) {
                                 const float* p = part(c, c == c0);
-                                L += __ldcg(p + 128 * (D + 1) + row) * exp2_approx(__ldcg(p + 128 * D + row) - M);
+                                const float mc = __ldcg(p + 128 * OD + row), lc = __ldcg(p + 128 * (OD + 1) + row);
+                                const float mn = fmaxf(M, mc);
+                                L = L * exp2_approx(M - mn) + lc * exp2_approx(mc - mn);
+                                M = mn;
                             }
                             const float invl = L > 0.f ? __frcp_rn(L) : 0.f;
 #pragma unroll 1
-                            for (int k = 0; k < D / 4; k += 4) {
-                                float4 v[4];
+                            for (int k = 0; k < OD / 4; k += 16) {
+                                float4 v[16];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+                                for (int e = 0; e < 16; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
                                 for (int c = c0; c <= c1; ++c) {
                                     const float* p = part(c, c == c0);
-                                    const float f = exp2_approx(__ldcg(p + 128 * D + row) - M);
+                                    float4 y[16];
+                                    const float f = exp2_approx(__ldcg(p + 128 * OD + row) - M);
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p) + (k + e) * 128 + row);
-                                        v[e] = make_float4(v[e].x + y.x * f, v[e].y + y.y * f, v[e].z + y.z * f,
-                                                           v[e].w + y.w * f);
-                                    }
+                                    for (int e = 0; e < 16; ++e)
+                                        y[e] = __ldcg(reinterpret_cast<const float4*>(p) + (k + e) * 128 + row);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        v[e] = make_float4(v[e].x + y[e].x * f, v[e].y + y[e].y * f, v[e].z + y[e].z * f,
+                                                           v[e].w + y[e].w * f);
                                 }
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    store_out4(a, w.start + t, hq, 4 * (k + e),
-                                               make_float4(v[e].x * invl, v[e].y * invl, v[e].z * invl, v[e].w * invl));
+                                for (int e = 0; e < 16; e += 2)
+                                    store_out8(a, w.start + t, hq, col0 + 4 * (k + e),
+                                               make_float4(v[e].x * invl, v[e].y * invl, v[e].z * invl, v[e].w * invl),
+                                               make_float4(v[e + 1].x * invl, v[e + 1].y * invl, v[e + 1].z * invl,
+                                                           v[e + 1].w * invl));
                             }
-                            store_lse(a, w.start + t, hq, M, L);
+                            if (col0 == 0) store_lse(a, w.start + t, hq, M, L);
                         }
                     }
                 }
             }
-            x += tiles;
             n += tiles;
-            o = 0;
-            if (x < x1) unit_next<C::ROWS, KT>(a, w);
         }
         // given up: the products in flight end before TMEM and the shared memory go
         if (leader && *abort) {
@@ -584,7 +728,7 @@ int launch(const Attend& a, cudaStream_t s) {
     static SmemAttr attr;
     const char* fn = "mmq_kv_attend";
     const long long runs = (long long)a.bt.tokens * a.group / C::ROWS + a.bt.seqs;
-    const long long tiles = runs * a.c.heads * ((long long)a.bt.table_pages * a.c.page / C::KT + 1);
+    const long long tiles = runs * a.c.heads * ((long long)a.bt.table_pages * a.c.page / C::KT + 1 + OVERHEAD);
     if (tiles > 0x7fffffff || (long long)a.bt.max_new * a.group > 0x7fffffff - C::ROWS) {
         report(fn, MMQ_ERR_SHAPE, "too many row and key tiles (rows / 128 * heads * keys / 64 above 2^31)");
         return MMQ_ERR_SHAPE;
