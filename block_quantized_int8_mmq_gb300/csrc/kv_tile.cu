@@ -126,7 +126,7 @@ k_kv_attend_tile(const Attend a) {
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_scan[C::WARPS], s_pref[C::THREADS + 1], s_at[3], s_last[2];
     __shared__ float4 s_sc[4][C::BLK];  // dk, log2 dv, 1 / dv of the blocks of four consecutive tiles
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
     const uint32_t base = ptx::smem_u32(smem), bars = base + C::OFF_BAR;
     const uint32_t k_full = bars, k_empty = bars + 8 * ST, v_full = bars + 16 * ST, v_empty = bars + 24 * ST;
     const uint32_t s_full = bars + 32 * ST, o_full = s_full + 16, p_ready = o_full + 16, joined = p_ready + 16;
@@ -215,7 +215,7 @@ k_kv_attend_tile(const Attend a) {
     }
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     volatile int* abort = &s_abort;
     unsigned* err = &g_kv_tile_error;
 
@@ -310,7 +310,7 @@ k_kv_attend_tile(const Attend a) {
         ptx::regs_inc<C::R_SOFT>();
         const int gt = wid >> 2, row = tid & 127, wrow = (wid & 3) * 32;  // group, row of its tile, the warp's first
         const int tile0 = HALF ? 0 : gt * 128, col0 = HALF ? gt * OD : 0;  // first row of the unit, first value column
-        const bool leader = (wid & 3) == 0 && lane == 0;
+        const bool lead = (wid & 3) == 0;  // the warp that issues the group's products
         const uint32_t lane_off = (uint32_t)wrow << 16;
         const uint32_t t_s = tmem + gt * KT, t_o = tmem + C::COL_O + gt * OD;
         const uint32_t sf = s_full + 8 * gt, of = o_full + 8 * gt, pr = p_ready + 8 * gt, jn = joined + 8 * gt;
@@ -318,7 +318,9 @@ k_kv_attend_tile(const Attend a) {
         uint8_t* q_smem = smem + C::OFF_Q + (HALF ? 0 : gt * C::TERMS * C::Q);
         constexpr uint32_t idesc_s = umma::make_idesc(128, KT), idesc_o = umma::make_idesc(128, OD) | (1u << 16);
         uint32_t n_pr = 0, n_sf = 0, n_of = 0, n_jn = 0, n_unit = 0;  // phases
-        auto issue_s = [&](int st) {  // S = Q K^T, the small terms first
+        auto issue_s = [&](int stage) {  // S = Q K^T, the small terms first
+            const int st = __shfl_sync(0xffffffffu, stage, 0);
+            if (!ptx::elect_one()) return;
             const uint64_t bd = umma::sdesc(base + st * C::KV, SBO);
 #pragma unroll
             for (int e = C::TERMS - 1; e >= 0; --e) {
@@ -331,7 +333,9 @@ k_kv_attend_tile(const Attend a) {
             ptx::umma_commit(sf);
         };
         // values: 8-column groups 128 B apart (stride offset), 8-token groups SBO apart (leading offset)
-        auto issue_o = [&](int st, bool first) {
+        auto issue_o = [&](int stage, bool fresh, bool last) {
+            const int st = __shfl_sync(0xffffffffu, stage, 0), first = __shfl_sync(0xffffffffu, (int)fresh, 0);
+            if (!ptx::elect_one()) return;
             const uint32_t va = base + C::OFF_V + st * C::KV + col0 * 16;
             const uint64_t bd = (uint64_t)((va & 0x3FFFFu) >> 4) | ((uint64_t)(SBO >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
                                 (1ull << 46);
@@ -342,12 +346,16 @@ k_kv_attend_tile(const Attend a) {
                     ptx::umma_f16_ts(t_o, t_s + 32 * (ks >> 1) + 16 * e + 8 * (ks & 1), bd + (uint64_t)(2 * SBO >> 4) * ks, idesc_o,
                                      !(first && ks + e == 0));
             ptx::umma_commit(v_empty + 8 * st);
+            if (last) ptx::umma_commit(of);
         };
         // The groups alternate batch by batch (O += P V, then the next S): batches that ran side by
         // side would end together, and then both groups' softmaxes would run side by side too.
         uint32_t n_turn = gt == 0 ? 1 : 0;
-        auto take_turn = [&]() { return umma::wait_bar(turn + 8 * gt, n_turn++ & 1, abort, err); };
-        auto pass_turn = [&]() { ptx::mbar_arrive(turn + 8 * (1 - gt)); };
+        auto take_turn = [&]() { return umma::warp_wait(turn + 8 * gt, n_turn++ & 1, abort, err); };
+        auto pass_turn = [&]() {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(turn + 8 * (1 - gt));
+        };
         auto signal = [&](uint32_t bar) {  // this warp's part is in place
             ptx::tc_fence_before();
             __syncwarp();
@@ -359,20 +367,19 @@ k_kv_attend_tile(const Attend a) {
             const int row0 = w.u * C::ROWS + tile0, r = row0 + row;
             if (row0 >= w.rows) {
                 // no rows in this row tile: only pass the converted tiles on
-                if (leader)
+                if (lead)
                     for (int i = 0; i <= tiles && ok; ++i) {
                         if (i > 0) {
-                            ok = umma::wait_bar(v_full + 8 * ((n + i - 1) % ST), ((n + i - 1) / ST) & 1, abort, err);
-                            if (ok) ptx::mbar_arrive(v_empty + 8 * ((n + i - 1) % ST));
+                            ok = umma::warp_wait(v_full + 8 * ((n + i - 1) % ST), ((n + i - 1) / ST) & 1, abort, err);
+                            if (ok && lane == 0) ptx::mbar_arrive(v_empty + 8 * ((n + i - 1) % ST));
                         }
                         if (i < tiles && ok) {
-                            ok = umma::wait_bar(k_full + 8 * ((n + i) % ST), ((n + i) / ST) & 1, abort, err);
-                            if (ok) ptx::mbar_arrive(k_empty + 8 * ((n + i) % ST));
+                            ok = umma::warp_wait(k_full + 8 * ((n + i) % ST), ((n + i) / ST) & 1, abort, err);
+                            if (ok && lane == 0) ptx::mbar_arrive(k_empty + 8 * ((n + i) % ST));
                         }
                         ok = ok && take_turn();
                         if (ok) pass_turn();
                     }
-                ok = __all_sync(0xffffffffu, ok);
             } else {
                 const bool real = r < w.rows;
                 const int t = r / a.group, hq = w.h * a.group + r - t * a.group, pos = w.len - w.n + t;
@@ -450,9 +457,9 @@ k_kv_attend_tile(const Attend a) {
                 const int hi = real ? pos + 1 : 0x7fffffff, lo = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
                 const int hi_min = __reduce_min_sync(0xffffffffu, hi), lo_max = __reduce_max_sync(0xffffffffu, lo);
                 signal(HALF ? q_ready : pr);
-                if (leader) {
-                    ok = umma::wait_bar(HALF ? q_ready : pr, HALF ? n_unit & 1 : n_pr & 1, abort, err) &&
-                         umma::wait_bar(k_full + 8 * (n % ST), (n / ST) & 1, abort, err) && take_turn();
+                if (lead) {
+                    ok = umma::warp_wait(HALF ? q_ready : pr, HALF ? n_unit & 1 : n_pr & 1, abort, err) &&
+                         umma::warp_wait(k_full + 8 * (n % ST), (n / ST) & 1, abort, err) && take_turn();
                     if (ok) {
                         ptx::tc_fence_after();
                         issue_s(n % ST);
@@ -590,23 +597,20 @@ k_kv_attend_tile(const Attend a) {
                     }
                     ptx::tmem_st_wait();
                     signal(pr);
-                    if (leader) {
+                    if (lead) {
                         const int st = nn % ST, par = (nn / ST) & 1, s2 = (nn + 1) % ST, par2 = ((nn + 1) / ST) & 1;
-                        ok = umma::wait_bar(pr, n_pr & 1, abort, err) && umma::wait_bar(v_full + 8 * st, par, abort, err) &&
-                             (i + 1 == tiles || umma::wait_bar(k_full + 8 * s2, par2, abort, err)) && take_turn();
+                        ok = umma::warp_wait(pr, n_pr & 1, abort, err) && umma::warp_wait(v_full + 8 * st, par, abort, err) &&
+                             (i + 1 == tiles || umma::warp_wait(k_full + 8 * s2, par2, abort, err)) && take_turn();
                         if (ok) {
                             ptx::tc_fence_after();
-                            issue_o(st, i == 0 || flush);
-                            if (i + 1 == tiles)
-                                ptx::umma_commit(of);
-                            else
-                                issue_s(s2);
+                            issue_o(st, i == 0 || flush, i + 1 == tiles);
+                            if (i + 1 < tiles) issue_s(s2);
                             pass_turn();
                         }
                     }
                     ++n_pr;
                 }
-                ok = __all_sync(0xffffffffu, ok) && umma::warp_wait(of, n_of++ & 1, abort, err);
+                ok = ok && umma::warp_wait(of, n_of++ & 1, abort, err);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 // ---- the unit's output, or this CTA's part of it
@@ -652,19 +656,21 @@ k_kv_attend_tile(const Attend a) {
                     const int c0 = work_owner(T, ufirst, W), c1 = work_owner(T, ufirst + w.tiles - 1, W);
                     __threadfence();
                     signal(pr);
-                    if (leader) {
-                        ok = umma::wait_bar(pr, n_pr & 1, abort, err);
-                        unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0 * 2 + gt;
-                        s_last[gt] = 0;
-                        if (ok && atomicAdd(counter, 1u) == (unsigned)(c1 - c0)) {
-                            *counter = 0;
-                            s_last[gt] = 1;
+                    if (lead) {
+                        ok = umma::warp_wait(pr, n_pr & 1, abort, err);
+                        if (lane == 0) {
+                            unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0 * 2 + gt;
+                            s_last[gt] = 0;
+                            if (ok && atomicAdd(counter, 1u) == (unsigned)(c1 - c0)) {
+                                *counter = 0;
+                                s_last[gt] = 1;
+                            }
+                            __threadfence();
+                            ptx::mbar_arrive(jn);
                         }
-                        __threadfence();
-                        ptx::mbar_arrive(jn);
                     }
                     ++n_pr;
-                    ok = __all_sync(0xffffffffu, ok) && umma::warp_wait(jn, n_jn++ & 1, abort, err);
+                    ok = ok && umma::warp_wait(jn, n_jn++ & 1, abort, err);
                     if (!ok) break;
                     if (s_last[gt]) {
                         __threadfence();
@@ -712,7 +718,7 @@ k_kv_attend_tile(const Attend a) {
             n += tiles;
         }
         // given up: the products in flight end before TMEM and the shared memory go
-        if (leader && *abort) {
+        if (lead && *abort && ptx::elect_one()) {
             ptx::umma_commit(jn);
             umma::drain_bar(jn, n_jn & 1, err);
         }

@@ -103,6 +103,16 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ------------------------------------------------------------------ one thread of a warp
+// True in one lane, always the same, of a converged warp.  Single-thread instructions whose operands
+// are warp-uniform issue from uniform registers inside such a branch; behind a lane comparison every
+// operand is moved there one instruction at a time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(on));
+    return on != 0;
+}
+
 // ------------------------------------------------------------------ registers
 // Per-warpgroup register reallocation (all four warps of a warpgroup execute the same
 // one).  An increase waits until the CTA's pool (threads x registers at launch) has the
