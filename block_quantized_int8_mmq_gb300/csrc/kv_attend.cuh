@@ -57,12 +57,6 @@ __device__ __forceinline__ float* part_slot(const Attend& a, int cta, int slot) 
 // first key that row 0 of a sequence (at position first) sees
 __device__ __forceinline__ int first_key(const Attend& a, int first) { return a.window > 0 ? max(0, first - a.window + 1) : 0; }
 
-__device__ __forceinline__ float4 load_row4(const Attend& a, long long row, int h, int d) {
-    const long long at = row * a.q.token_stride + h * a.q.head_stride + d;
-    return a.dtype == MMQ_F32    ? Elem<float>::load4(static_cast<const float*>(a.q.data) + at)
-           : a.dtype == MMQ_BF16 ? Elem<__nv_bfloat16>::load4(static_cast<const __nv_bfloat16*>(a.q.data) + at)
-                                 : Elem<__half>::load4(static_cast<const __half*>(a.q.data) + at);
-}
 __device__ __forceinline__ void store_out4(const Attend& a, long long row, int h, int d, float4 v) {
     const long long at = (row * a.q_heads + h) * a.c.dim + d;
     if (a.dtype == MMQ_F32)
@@ -111,6 +105,22 @@ __device__ __forceinline__ void row_scale(float amax, float& down, float& up) {
     down = __uint_as_float((uint32_t)(262 - e) << 23);
     up = __uint_as_float((uint32_t)(e - 8) << 23);
 }
+
+// Parts of one row's result as they are added up.
+struct Joined {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = M_NONE, l = 0.f;
+    __device__ __forceinline__ void add(float4 x, float mx, float lx) {
+        const float mn = fmaxf(m, mx), f = exp2_approx(m - mn), g = exp2_approx(mx - mn);
+        o = make_float4(o.x * f + x.x * g, o.y * f + x.y * g, o.z * f + x.z * g, o.w * f + x.w * g);
+        l = l * f + lx * g;
+        m = mn;
+    }
+    __device__ __forceinline__ float4 out() const {
+        const float inv = l > 0.f ? __frcp_rn(l) : 0.f;
+        return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
+};
 
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) { return Elem<__half>::pack2(a, b); }
 __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }

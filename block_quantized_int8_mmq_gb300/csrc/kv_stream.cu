@@ -26,19 +26,18 @@ __device__ unsigned g_kv_stream_error;
 
 template <int D, int NT>
 struct Stream {
-    static constexpr int WARPS = D == 256 ? 4 : 8, THREADS = WARPS * 32;
-    static constexpr int STAGES = D == 64 ? 4 : NT == 2 ? 2 : 3;
+    // as many warps as shared memory holds rings of two records for (dim 64: four), and registers
+    // for two tiles of rows: a block is a chain of dependent steps, and only other warps fill its gaps
+    static constexpr int WARPS = D == 256 ? 6 : NT == 2 ? 8 : 12, THREADS = WARPS * 32;
+    static constexpr int STAGES = D == 64 ? 4 : D == 128 && NT == 2 ? 3 : 2;
     static constexpr int ROWS = 8 * NT, REC = rec_bytes(D);
-    static constexpr int SLOT = ROWS * (D + 2) * 4;  // O [rows][D], m [rows], l [rows]
-    static constexpr int RING = WARPS * STAGES * REC;
-    static constexpr int SMEM = RING + WARPS * SLOT + WARPS * STAGES * 8;
-    static_assert(SLOT <= STAGES * REC && SLOT % 16 == 0, "the outgoing slot reuses the warp's ring");
+    static constexpr int RING = WARPS * STAGES * REC, SMEM = RING + WARPS * STAGES * 8;
+    static_assert(ROWS * (D + 2) * 4 <= STAGES * REC && ROWS * D + WARPS * ROWS * (D + 2) <= WS_ROWS * D, "room for a warp's partial results");
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -48,6 +47,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(v));
     return o;
 }
+// Where a warp keeps an incomplete unit's result, O [ROWS][D], m [ROWS], l [ROWS]: at the beginning of its
+// ring, or (ring: nullptr) in a place of its own in the CTA's first slot of the workspace, behind the
+// rows that the CTA's own partial result takes there.
+template <int D, int ROWS>
+struct KeptAt {
+    static __device__ __forceinline__ float* at(uint8_t* ring, const Attend& a, int warp) {
+        return ring ? reinterpret_cast<float*>(ring) : part_slot(a, blockIdx.x, 0) + ROWS * D + warp * ROWS * (D + 2);
+    }
+};
+
 // A sequence as the units see it
 struct Seq {
     int start, n, len, lo_blk, tiles;  // tiles: records in reach, or 1 for a sequence of padding rows; 0: none
@@ -71,14 +80,20 @@ template <int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(Stream<D, NT>::THREADS, 1)
 k_kv_attend_stream(const Attend a) {
     using C = Stream<D, NT>;
+    using Kept = KeptAt<D, C::ROWS>;
     constexpr int KS = D / 16;  // k steps of the first product, row tiles of the second
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_scan[C::WARPS], s_b[C::WARPS], s_off[C::WARPS], s_abort, s_last[2];
-    // the incomplete units of the CTA, two slots per warp in work order
-    __shared__ int s_unit[2 * C::WARPS], s_end[2 * C::WARPS], s_seq[2 * C::WARPS], s_head[2 * C::WARPS];
+    __shared__ int s_scan[C::WARPS], s_b[C::WARPS], s_off[C::WARPS], s_x[C::WARPS + 1], s_abort;
+    __shared__ int s_out[2], s_first[2], s_final[2];  // the unit that came in, the one that goes out: slot, its CTAs
+    // the incomplete units of the CTA in work order, two slots per warp (the second: its range's end)
+    __shared__ int s_unit[2 * C::WARPS], s_end[2 * C::WARPS], s_head[2 * C::WARPS];
+    __shared__ Seq s_sq[2 * C::WARPS];
+    // its parts in work order, and where in them and in the slots each unit begins
+    __shared__ const float* s_part[2 * C::WARPS];
+    __shared__ int s_runs, s_run[2 * C::WARPS + 1], s_slot[2 * C::WARPS];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, tq = lane & 3;
     uint8_t* ring = smem + wid * C::STAGES * C::REC;
-    const uint32_t bars = ptx::smem_u32(smem + C::RING + C::WARPS * C::SLOT) + wid * C::STAGES * 8;
+    const uint32_t bars = ptx::smem_u32(smem + C::RING) + wid * C::STAGES * 8;
     if (lane < C::STAGES) ptx::mbar_init(bars + 8 * lane, 1);
     ptx::fence_barrier_init();
     if (tid == 0) s_abort = 0;
@@ -100,6 +115,8 @@ k_kv_attend_stream(const Attend a) {
     }
     const int W = min((int)gridDim.x * C::WARPS, T), w0 = blockIdx.x * C::WARPS;
     if (w0 >= W) return;
+    if (tid <= C::WARPS) s_x[tid] = work_start(T, min(w0 + tid, W), W);  // the warps' ranges
+    __syncthreads();
     for (int base = 0, carry = 0; base < seqs; base += C::THREADS) {
         const int i = base + tid;
         int v = v0, e = e0;
@@ -110,7 +127,7 @@ k_kv_attend_stream(const Attend a) {
         }
         carry += total;
         for (int k = 0; k < C::WARPS && w0 + k < W; ++k) {
-            const int x = work_start(T, w0 + k, W);
+            const int x = s_x[k];
             if (x >= e && x < e + v) {
                 s_b[k] = i;
                 s_off[k] = x - e;
@@ -120,7 +137,7 @@ k_kv_attend_stream(const Attend a) {
     __syncthreads();
 
     if (w0 + wid < W) {
-        const int x0 = work_start(T, w0 + wid, W), x1 = work_start(T, w0 + wid + 1, W);
+        const int x0 = s_x[wid], x1 = s_x[wid + 1];
         int b = s_b[wid];
         Seq sq = load_seq(a, b);
         int h = s_off[wid] / sq.tiles, o = s_off[wid] - h * sq.tiles;
@@ -176,14 +193,27 @@ k_kv_attend_stream(const Attend a) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int r = 8 * nt + g, t = r / a.group;
+                    // 16 consecutive values of each 64: one run of loads, whatever the type
+                    uint4 raw[D / 64][SPLIT ? 4 : 2];
+                    const uint8_t* src = static_cast<const uint8_t*>(a.q.data) +
+                                         ((sq.start + t) * a.q.token_stride + (h * a.group + r - t * a.group) * a.q.head_stride +
+                                          16 * tq) * (SPLIT ? 4 : 2);
+#pragma unroll
+                    for (int sg = 0; sg < D / 64; ++sg)
+#pragma unroll
+                        for (int e = 0; e < (SPLIT ? 4 : 2); ++e)
+                            raw[sg][e] = r < rows ? *reinterpret_cast<const uint4*>(src + sg * (SPLIT ? 256 : 128) + 16 * e)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
                     float4 v[KS];
                     float am = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
-                        v[ks] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (r < rows)
-                            v[ks] = load_row4(a, sq.start + t, h * a.group + r - t * a.group,
-                                              64 * (ks >> 2) + 16 * tq + 4 * (ks & 3));
+                        const uint4 p = raw[ks >> 2][SPLIT ? ks & 3 : (ks & 3) >> 1];
+                        const uint2 w = ks & 1 ? make_uint2(p.z, p.w) : make_uint2(p.x, p.y);
+                        v[ks] = SPLIT ? make_float4(__uint_as_float(p.x), __uint_as_float(p.y), __uint_as_float(p.z),
+                                                    __uint_as_float(p.w))
+                                : a.dtype == MMQ_BF16 ? Elem<__nv_bfloat16>::widen(w)
+                                                      : Elem<__half>::widen(w);
                         am = fmaxf(am, fmaxf(fmaxf(fabsf(v[ks].x), fabsf(v[ks].y)), fmaxf(fabsf(v[ks].z), fabsf(v[ks].w))));
                     }
                     am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
@@ -369,9 +399,9 @@ k_kv_attend_stream(const Attend a) {
             if (++o == sq.tiles || x + 1 == x1) {  // the unit ends, or the range does
                 const int ustart = x + 1 - o, uend = ustart + sq.tiles, rows = sq.n * a.group;
                 const bool whole = o_from == 0 && o == sq.tiles;
-                // incomplete: the CTA's slot 0 if the unit came in to this warp, else 1 (the range ends:
-                // nothing is in flight into the ring any more)
-                float* slot = reinterpret_cast<float*>(o_from > 0 ? smem + C::RING + wid * C::SLOT : ring);
+                // incomplete: kept in the ring if the range ends (nothing is in flight any more), else, a
+                // unit that came in and ends here, in the warp's rows of the workspace
+                float* kept = Kept::at(x + 1 == x1 ? ring : nullptr, a, wid);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -394,22 +424,22 @@ k_kv_attend_stream(const Attend a) {
                                 if (whole)
                                     store_out4(a, sq.start + t, hq, col, v);
                                 else
-                                    *reinterpret_cast<float4*>(slot + r * D + col) = v;
+                                    *reinterpret_cast<float4*>(kept + r * D + col) = v;
                             }
                         if (g == 0) {
                             if (whole) {
                                 store_lse(a, sq.start + t, hq, m[nt][c], sum);
                             } else {
-                                slot[C::ROWS * D + r] = m[nt][c];
-                                slot[C::ROWS * (D + 1) + r] = sum;
+                                kept[C::ROWS * D + r] = m[nt][c];
+                                kept[C::ROWS * (D + 1) + r] = sum;
                             }
                         }
                     }
                 if (!whole && lane == 0) {
-                    const int i = 2 * wid + (o_from > 0 ? 0 : 1);
+                    const int i = 2 * wid + (x + 1 == x1 ? 1 : 0);
                     s_unit[i] = ustart;
                     s_end[i] = uend;
-                    s_seq[i] = b;
+                    s_sq[i] = sq;
                     s_head[i] = h;
                 }
                 if (o == sq.tiles && x + 1 < x1) {
@@ -426,80 +456,107 @@ k_kv_attend_stream(const Attend a) {
     __syncthreads();
     if (s_abort) return;
 
-    // ---- the CTA's incomplete units: parts of one unit lie in consecutive slots
-    const int cta0 = work_start(T, w0, W), cta1 = work_start(T, min(W, w0 + C::WARPS), W);
-    auto row_factor = [](float mi, float M) { return exp2_approx(mi - M); };
-    for (int i = 0; i < 2 * C::WARPS;) {
-        if (s_unit[i] < 0) {
-            ++i;
-            continue;
+    // ---- the CTA's incomplete units: the slots in use are the parts, those of one unit in a row
+    if (wid == 0) {
+        const int u = lane < 2 * C::WARPS ? s_unit[lane] : -1;
+        const unsigned used = __ballot_sync(0xffffffffu, u >= 0), before = used & ((1u << lane) - 1);
+        const int prev = __shfl_sync(0xffffffffu, u, before ? 31 - __clz(before) : 0);
+        const bool first = u >= 0 && (before == 0 || prev != u);
+        const unsigned starts = __ballot_sync(0xffffffffu, first);
+        const int j = __popc(before);
+        if (u >= 0) s_part[j] = Kept::at(lane & 1 ? smem + (lane >> 1) * C::STAGES * C::REC : nullptr, a, lane >> 1);
+        if (first) {
+            const int run = __popc(starts & ((1u << lane) - 1));
+            s_slot[run] = lane;
+            s_run[run] = j;
         }
-        const int u = s_unit[i], ue = s_end[i], b = s_seq[i], h = s_head[i];
-        int e = i;
-        for (int k = i + 1; k < 2 * C::WARPS; ++k)
-            if (s_unit[k] == u) e = k;
-        const Seq sq = load_seq(a, b);
-        const int rows = sq.n * a.group;
-        const bool whole = u >= cta0 && ue <= cta1;
-        float* part = part_slot(a, blockIdx.x, u >= cta0 ? 1 : 0);
-        for (int idx = tid; idx < rows * (D / 4); idx += C::THREADS) {
-            const int r = idx / (D / 4), col = 4 * (idx % (D / 4));
+        if (lane == 0) {
+            s_runs = __popc(starts);
+            s_run[__popc(starts)] = __popc(used);
+            s_out[0] = s_out[1] = -1;
+        }
+    }
+    __syncthreads();
+    const int cta0 = s_x[0], cta1 = s_x[min(W - w0, C::WARPS)];
+    const int runs = s_runs, each = a.bt.max_new * a.group * (D / 4), side_by_side = max(1, C::THREADS / each);
+    for (int run = tid / each; run < runs; run += side_by_side)
+        for (int x = tid - tid / each * each; x < each; x += C::THREADS) {
+            if (tid >= side_by_side * each && each < C::THREADS) break;
+            const int r = x / (D / 4), col = 4 * (x % (D / 4)), i = s_slot[run], u = s_unit[i], p0 = s_run[run], p1 = s_run[run + 1];
+            const Seq& sq = s_sq[i];
+            if (r >= sq.n * a.group) continue;
             float M = M_NONE, L = 0.f;
+#pragma unroll 4
+            for (int p = p0; p < p1; ++p) M = fmaxf(M, s_part[p][C::ROWS * D + r]);
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i; k <= e; ++k) {
-                if (s_unit[k] != u) continue;
-                const float* sl = reinterpret_cast<const float*>(k & 1 ? smem + (k >> 1) * C::STAGES * C::REC
-                                                                       : smem + C::RING + (k >> 1) * C::SLOT);
-                const float mk = sl[C::ROWS * D + r], mn = fmaxf(M, mk), f = row_factor(M, mn), fk = row_factor(mk, mn);
-                const float4 x = *reinterpret_cast<const float4*>(sl + r * D + col);
-                v = make_float4(v.x * f + x.x * fk, v.y * f + x.y * fk, v.z * f + x.z * fk, v.w * f + x.w * fk);
-                L = L * f + sl[C::ROWS * (D + 1) + r] * fk;
-                M = mn;
+#pragma unroll 4
+            for (int p = p0; p < p1; ++p) {
+                const float* k = s_part[p];
+                const float f = exp2_approx(k[C::ROWS * D + r] - M);
+                const float4 y = *reinterpret_cast<const float4*>(k + r * D + col);
+                L += f * k[C::ROWS * (D + 1) + r];
+                v = make_float4(v.x + y.x * f, v.y + y.y * f, v.z + y.z * f, v.w + y.w * f);
             }
-            if (whole) {
+            if (u >= cta0 && s_end[i] <= cta1) {
                 const float inv = L > 0.f ? __frcp_rn(L) : 0.f;
-                const int t = r / a.group, hq = h * a.group + r - t * a.group;
+                const int t = r / a.group, hq = s_head[i] * a.group + r - t * a.group;
                 store_out4(a, sq.start + t, hq, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 if (col == 0) store_lse(a, sq.start + t, hq, M, L);
             } else {
+                const int side = u >= cta0 ? 1 : 0;
+                float* part = part_slot(a, blockIdx.x, side);
                 *reinterpret_cast<float4*>(part + r * D + col) = v;
                 if (col == 0) {
                     part[WS_ROWS * D + r] = M;
                     part[WS_ROWS * (D + 1) + r] = L;
+                    s_out[side] = i;
                 }
             }
         }
-        if (!whole) {
-            const int c0 = work_owner(T, u, W) / C::WARPS, c1 = work_owner(T, ue - 1, W) / C::WARPS;
-            unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last[0] = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
-            __syncthreads();
-            if (s_last[0]) {
-                __threadfence();
-                for (int idx = tid; idx < rows * (D / 4); idx += C::THREADS) {
-                    const int r = idx / (D / 4), col = 4 * (idx % (D / 4));
-                    float M = M_NONE, L = 0.f;
-                    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part_slot(a, c, c == c0) + WS_ROWS * D + r));
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* ps = part_slot(a, c, c == c0);
-                        const float f = row_factor(__ldcg(ps + WS_ROWS * D + r), M);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(ps + r * D + col));
-                        v = make_float4(v.x + x.x * f, v.y + x.y * f, v.z + x.z * f, v.w + x.w * f);
-                        L += __ldcg(ps + WS_ROWS * (D + 1) + r) * f;
-                    }
-                    const float inv = L > 0.f ? __frcp_rn(L) : 0.f;
-                    const int t = r / a.group, hq = h * a.group + r - t * a.group;
-                    store_out4(a, sq.start + t, hq, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                    if (col == 0) store_lse(a, sq.start + t, hq, M, L);
-                }
-                if (tid == 0) *counter = 0;
-            }
+    __threadfence();
+    __syncthreads();
+    // ---- the units that other CTAs have parts of: the last to arrive joins them, in CTA order
+    if (tid < 2 && s_out[tid] >= 0) {
+        const int u = s_unit[s_out[tid]], c0 = work_owner(T, u, W) / C::WARPS,
+                  c1 = work_owner(T, s_end[s_out[tid]] - 1, W) / C::WARPS;
+        unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0;
+        __threadfence();
+        if (atomicAdd(counter, 1u) == (unsigned)(c1 - c0)) {
+            *counter = 0;
+            s_first[tid] = c0;
+            s_final[tid] = c1;
+        } else {
+            s_out[tid] = -1;
         }
-        i = e + 1;
+        __threadfence();
+    }
+    __syncthreads();
+    for (int side = 0; side < 2; ++side) {
+        if (s_out[side] < 0) continue;
+        const Seq& sq = s_sq[s_out[side]];
+        const int rows = sq.n * a.group, c0 = s_first[side], c1 = s_final[side];
+        for (int idx = tid; idx < rows * (D / 4); idx += C::THREADS) {
+            const int r = idx / (D / 4), col = 4 * (idx % (D / 4));
+            Joined j;
+            constexpr int B = 8;  // parts in flight
+            for (int c = c0; c <= c1; c += B) {
+                float4 x[B];
+                float m[B], l[B];
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                    const float* ps = part_slot(a, min(c + k, c1), min(c + k, c1) == c0);
+                    x[k] = __ldcg(reinterpret_cast<const float4*>(ps + r * D + col));
+                    m[k] = __ldcg(ps + WS_ROWS * D + r);
+                    l[k] = __ldcg(ps + WS_ROWS * (D + 1) + r);
+                }
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                    if (c + k <= c1) j.add(x[k], m[k], l[k]);
+            }
+            const int t = r / a.group, hq = s_head[s_out[side]] * a.group + r - t * a.group;
+            store_out4(a, sq.start + t, hq, col, j.out());
+            if (col == 0) store_lse(a, sq.start + t, hq, j.m, j.l);
+        }
     }
 }
 

@@ -39,9 +39,10 @@ struct Tile {
     static constexpr int SOFT = 8, CONV = 4, WARPS = SOFT + CONV, THREADS = 32 * WARPS;
     static constexpr int ROWS = HALF ? 128 : 256;
     static constexpr int KV = KT * D * 2, Q = 128 * D * 2;       // bytes of a converted tile, of a row tile's term
-    // the queries last: every operand read stays inside the allocation
-    static constexpr int OFF_V = ST * KV, OFF_Q = 2 * ST * KV, OFF_BAR = OFF_Q + (HALF ? 1 : 2) * TERMS * Q;
-    static constexpr int NBAR = 4 * ST + 2 * 5 + 2;
+    static constexpr int RAW_HALF = KT / 4 * D, RAW = 2 * RAW_HALF + 16;  // a converter warp's codes of a tile, their scales
+    static constexpr int OFF_V = ST * KV, OFF_Q = 2 * ST * KV, OFF_RAW = OFF_Q + (HALF ? 1 : 2) * TERMS * Q;
+    static constexpr int OFF_BAR = OFF_RAW + CONV * RAW;
+    static constexpr int NBAR = 4 * ST + 2 * 5 + 2 + 2 * CONV;
     static constexpr int USED = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of TMEM
     static constexpr int COL_O = 2 * KT;                         // TMEM columns: S of each group, then O
@@ -51,8 +52,8 @@ struct Tile {
     // 2.3e-6 off in all without it)
     static constexpr int FLUSH = 256 / KT;
     // registers: the softmax warps' and the converters' shares of the launch's 384 x 168
-    static constexpr int R_SOFT = SPLIT ? 216 : 200, R_CONV = SPLIT ? 72 : 104;
-    static_assert(2 * (KT + OD) <= 512 && SMEM <= 232448 - 1024, "tile sizes");
+    static constexpr int R_SOFT = 216, R_CONV = 72;
+    static_assert(2 * (KT + OD) <= 512 && SMEM <= 232448 - 2176, "tile sizes");
     static_assert(256 * R_SOFT + 128 * R_CONV <= 384 * 168, "register shares");
 };
 
@@ -132,6 +133,7 @@ k_kv_attend_tile(const Attend a) {
     const uint32_t s_full = bars + 32 * ST, o_full = s_full + 16, p_ready = o_full + 16, joined = p_ready + 16;
     const uint32_t turn = joined + 16;  // the groups issue their products in turn
     const uint32_t q_ready = turn + 16, q_free = q_ready + 8;  // HALF: of the queries that both groups use
+    const uint32_t raw_full = q_free + 8;                      // a converter warp's keys, values
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             ptx::mbar_init(k_full + 8 * i, C::CONV);
@@ -139,6 +141,7 @@ k_kv_attend_tile(const Attend a) {
             ptx::mbar_init(k_empty + 8 * i, 2);
             ptx::mbar_init(v_empty + 8 * i, 2);
         }
+        for (int i = 0; i < 2 * C::CONV; ++i) ptx::mbar_init(raw_full + 8 * i, 1);
         ptx::mbar_init(q_ready, C::SOFT);
         ptx::mbar_init(q_free, C::SOFT);
         for (int i = 0; i < 2; ++i) {
@@ -226,84 +229,123 @@ k_kv_attend_tile(const Attend a) {
 
     if (wid >= C::SOFT) {
         // ------------------------------------------------ converters: warp cw takes tokens KT/4 cw ..
+        // Its codes come by bulk copies into its own staging, keys and values by turns, each requested
+        // as soon as the tile before has been read. Lanes read and write diagonally (row l, chunk
+        // l + s): eight lanes then touch eight bank groups of the codes' rows and of the core matrices.
         ptx::regs_dec<C::R_CONV>();
-        constexpr int NL = KT * D / 2048, PER = D / 64;
-        const int cw = wid - C::SOFT, r8 = lane & 7, cq = lane >> 3;
+        constexpr int GROUPS = KT / 32, PER = D / 64;  // groups of eight rows, 16-byte chunks a lane and group
+        const int cw = wid - C::SOFT, l8 = lane & 7, cq = lane >> 3;
         const int tok0 = cw * (KT / 4), bi = tok0 / BT, sub = tok0 % BT;
-        // the record of this warp's tokens in the walk's tile: its page number (-1: none to load),
-        // fetched a tile before the codes
-        auto page_of = [&](const Unit& q, int ot, int& in) -> int {
-            const int blk = (q.kt0 + ot) * C::BLK + bi;
-            if (blk * BT >= q.hi || blk * BT + BT <= q.lo) return -1;
-            const int pg = blk / a.c.blocks;
-            in = blk - pg * a.c.blocks;
-            return a.bt.table[(long long)q.b * a.bt.table_stride + pg];
-        };
-        auto rec_of = [&](int id, int in, int h) -> const uint8_t* {
-            if (id < 0 || id >= a.c.pages) return nullptr;
-            return a.c.data + (((long long)id * a.c.heads + h) * a.c.blocks + in) * rec_bytes(D);
-        };
-        const int off = (sub + r8) * D + 16 * cq;
-        auto load = [&](uint4 (&buf)[NL], const uint8_t* p) {
-#pragma unroll
-            for (int i = 0; i < NL; ++i)
-                buf[i] = p ? *reinterpret_cast<const uint4*>(p + off + 8 * (i / PER) * D + 64 * (i % PER))
-                           : make_uint4(0u, 0u, 0u, 0u);
-        };
-        auto store = [&](const uint4 (&buf)[NL], uint8_t* dst) {
-            uint8_t* d0 = dst + (tok0 >> 3) * SBO + 2 * cq * 128 + r8 * 16;
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                uint8_t* p = d0 + (i / PER) * SBO + 8 * (i % PER) * 128;
-                const uint2 c0 = umma::i8x4_to_f16x4(buf[i].x), c1 = umma::i8x4_to_f16x4(buf[i].y);
-                const uint2 c2 = umma::i8x4_to_f16x4(buf[i].z), c3 = umma::i8x4_to_f16x4(buf[i].w);
-                *reinterpret_cast<uint4*>(p) = make_uint4(c0.x, c0.y, c1.x, c1.y);
-                *reinterpret_cast<uint4*>(p + 128) = make_uint4(c2.x, c2.y, c3.x, c3.y);
-            }
-        };
-        uint4 kb[NL], vb[NL];
-        float2 sc = make_float2(0.f, 0.f);
-        bool more = next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1);
-        int o = o0, in = 0, id = more ? page_of(w, o, in) : -1;
-        if (id < -1 || id >= a.c.pages) atomicOr(err, ERR_RANGE);
-        const uint8_t* rec = rec_of(id, in, w.h);
-        load(kb, rec);
-        load(vb, rec ? rec + BT * D : nullptr);
-        if (rec) sc = *reinterpret_cast<const float2*>(rec + 2 * BT * D);
-        bool some = rec != nullptr;
-        for (int n = 0; more; ++n) {
-            const int st = n % ST;
-            // the next tile's place
-            if (++o == o1) {
-                more = next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1);
+        uint8_t* raw = smem + C::OFF_RAW + cw * C::RAW;
+        const uint32_t raw_k = raw_full + 16 * cw, raw_v = raw_k + 8;
+        bool more[3];           // whether tiles n, n + 1, n + 2 of this CTA exist
+        const uint8_t* rec[2];  // this warp's record in tiles n, n + 1 (nullptr: nothing in reach there)
+        int o = 0, in = 0, id = -1;  // of tile n + 2: its place in its record's page, its page number (on its way)
+        bool begun = false;
+        auto advance = [&]() -> bool {  // the cursor to the next tile
+            if (!begun || ++o == o1) {
+                begun = true;
+                if (!next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1)) return false;
                 o = o0;
             }
-            if (more) id = page_of(w, o, in);
+            const int blk = (w.kt0 + o) * C::BLK + bi;
+            id = -1;
+            if (blk * BT < w.hi && blk * BT + BT > w.lo) {
+                const int pg = blk / a.c.blocks;
+                in = blk - pg * a.c.blocks;
+                id = a.bt.table[(long long)w.b * a.bt.table_stride + pg];
+                if (id < 0) id = -2;
+            }
+            return true;
+        };
+        auto resolve = [&]() -> const uint8_t* {
+            if (id == -1) return nullptr;
+            if (id < 0 || id >= a.c.pages) {
+                if (lane == 0) atomicOr(err, ERR_RANGE);
+                return nullptr;
+            }
+            return a.c.data + (((long long)id * a.c.heads + w.h) * a.c.blocks + in) * rec_bytes(D);
+        };
+        uint32_t k_asked = 0, k_had = 0, v_asked = 0, v_had = 0;  // copies requested and waited for
+        auto fetch_k = [&](const uint8_t* p) {
+            __syncwarp();
+            if (!p) return;
+            ++k_asked;
+            if (ptx::elect_one()) {
+                ptx::mbar_arrive_expect_tx(raw_k, C::RAW_HALF + 16);
+                ptx::bulk_load(ptx::smem_u32(raw), p + sub * D, C::RAW_HALF, raw_k);
+                ptx::bulk_load(ptx::smem_u32(raw) + 2 * C::RAW_HALF, p + 2 * BT * D, 16, raw_k);
+            }
+        };
+        auto fetch_v = [&](const uint8_t* p) {
+            __syncwarp();
+            if (!p) return;
+            ++v_asked;
+            if (ptx::elect_one()) {
+                ptx::mbar_arrive_expect_tx(raw_v, C::RAW_HALF);
+                ptx::bulk_load(ptx::smem_u32(raw) + C::RAW_HALF, p + (BT + sub) * D, C::RAW_HALF, raw_v);
+            }
+        };
+        auto convert = [&](const uint8_t* src, uint8_t* dst, bool some) {
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int ch = D == 64 ? ((l8 >> 1) + cq) & 3 : (l8 + cq + 4 * i) & (D / 16 - 1);
+                    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                    if (some) q = *reinterpret_cast<const uint4*>(src + (8 * gr + l8) * D + 16 * ch);
+                    uint8_t* p = dst + ((tok0 >> 3) + gr) * SBO + 256 * ch + 16 * l8;
+                    const uint2 c0 = umma::i8x4_to_f16x4(q.x), c1 = umma::i8x4_to_f16x4(q.y);
+                    const uint2 c2 = umma::i8x4_to_f16x4(q.z), c3 = umma::i8x4_to_f16x4(q.w);
+                    *reinterpret_cast<uint4*>(p) = make_uint4(c0.x, c0.y, c1.x, c1.y);
+                    *reinterpret_cast<uint4*>(p + 128) = make_uint4(c2.x, c2.y, c3.x, c3.y);
+                }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+        };
+        more[0] = advance();
+        rec[0] = more[0] ? resolve() : nullptr;
+        fetch_k(rec[0]);
+        fetch_v(rec[0]);
+        more[1] = more[0] && advance();
+        rec[1] = more[1] ? resolve() : nullptr;
+        more[2] = more[1] && advance();
+        for (int n = 0; more[0]; ++n) {
+            const int st = n % ST;
             const uint32_t par = ((n / ST) & 1) ^ 1;
+            const bool some = rec[0] != nullptr;
             if (!umma::warp_wait(k_empty + 8 * st, par, abort, err)) break;
-            store(kb, smem + st * C::KV);
+            if (some && !umma::warp_wait(raw_k, k_had & 1, abort, err)) break;
+            if (some) ++k_had;
             if (lane == 0 && sub == 0) {
-                float lv = -INFINITY, rv = 0.f;
-                if (some) value_scale(sc.y, lv, rv);
-                s_sc[n & 3][bi] = make_float4(some ? sc.x : 0.f, lv, rv, 0.f);
+                float dk = 0.f, lv = -INFINITY, rv = 0.f;
+                if (some) {
+                    const float2 sc = *reinterpret_cast<const float2*>(raw + 2 * C::RAW_HALF);
+                    dk = sc.x;
+                    value_scale(sc.y, lv, rv);
+                }
+                s_sc[n & 3][bi] = make_float4(dk, lv, rv, 0.f);
             }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
+            convert(raw, smem + st * C::KV, some);
             if (lane == 0) ptx::mbar_arrive(k_full + 8 * st);
-            rec = nullptr;
-            if (more) {
-                if (id != -1 && (id < 0 || id >= a.c.pages)) atomicOr(err, ERR_RANGE);
-                rec = rec_of(id, in, w.h);
-                load(kb, rec);
-                if (rec) sc = *reinterpret_cast<const float2*>(rec + 2 * BT * D);
-                some = rec != nullptr;
-            }
+            fetch_k(rec[1]);
             if (!umma::warp_wait(v_empty + 8 * st, par, abort, err)) break;
-            store(vb, smem + C::OFF_V + st * C::KV);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
+            if (some && !umma::warp_wait(raw_v, v_had & 1, abort, err)) break;
+            if (some) ++v_had;
+            convert(raw + C::RAW_HALF, smem + C::OFF_V + st * C::KV, some);
             if (lane == 0) ptx::mbar_arrive(v_full + 8 * st);
-            if (more) load(vb, rec ? rec + BT * D : nullptr);
+            fetch_v(rec[1]);
+            more[0] = more[1];
+            rec[0] = rec[1];
+            more[1] = more[2];
+            rec[1] = more[1] ? resolve() : nullptr;
+            more[2] = more[1] && advance();
+        }
+        // given up: let the copies in flight land before the shared memory goes
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while ((k_had != k_asked || v_had != v_asked) && ptx::globaltimer_ns() - t0 < umma::WAIT_LIMIT_NS) {
+            if (k_had != k_asked && ptx::mbar_test_wait(raw_k, k_had & 1)) ++k_had;
+            if (v_had != v_asked && ptx::mbar_test_wait(raw_v, v_had & 1)) ++v_had;
         }
     } else {
         // ------------------------------------------------ softmax: thread = row, and the MMA issue
