@@ -141,42 +141,48 @@ k_kv_attend_stream(const Attend a) {
         int b = s_b[wid];
         Seq sq = load_seq(a, b);
         int h = s_off[wid] / sq.tiles, o = s_off[wid] - h * sq.tiles;
-        // the fetching side runs STAGES records ahead
-        int fb = b, fh = h, fo = o, fx = x0, tab0 = 0, tabn = 0, tab = -1;
+        // the fetching side runs STAGES records ahead; within a page it only steps to the next record
+        int fb = b, fh = h, fo = o, fx = x0, left = 0, pg = 0, tab0 = 0, tabn = 0, tab = -1;
         Seq fs = sq;
-        uint32_t live = 0, phase = 0;  // stages that a copy was started into, parities
-        auto fetch = [&](int st) {     // the next record of the range into stage st
+        const uint8_t* src = nullptr;   // the next record (nullptr: on no page)
+        uint32_t live = 0, phase = 0;   // stages that a copy was started into, parities
+        auto fetch = [&](int st) {      // the next record of the range into stage st
             if (fs.len > 0) {
-                const int blk = fs.lo_blk + fo, pg = blk / a.c.blocks;
-                if (pg < tab0 || pg >= tab0 + tabn) {  // 32 page numbers at a time, one per lane
-                    tab0 = pg;
-                    tabn = min(32, (fs.len + a.c.page - 1) / a.c.page - pg);
-                    tab = lane < tabn ? a.bt.table[(long long)fb * a.bt.table_stride + pg + lane] : -1;
+                if (left == 0) {  // a new unit or page
+                    const int blk = fs.lo_blk + fo;
+                    pg = blk / a.c.blocks;
+                    const int in = blk - pg * a.c.blocks;
+                    left = a.c.blocks - in;
+                    if (pg < tab0 || pg >= tab0 + tabn) {  // 32 page numbers at a time, one per lane
+                        tab0 = pg;
+                        tabn = min(32, (fs.len + a.c.page - 1) / a.c.page - pg);
+                        tab = lane < tabn ? a.bt.table[(long long)fb * a.bt.table_stride + pg + lane] : -1;
+                    }
+                    const int id = __shfl_sync(0xffffffffu, tab, pg - tab0);
+                    src = nullptr;
+                    if (id >= 0 && id < a.c.pages)
+                        src = a.c.data + (((long long)id * a.c.heads + fh) * a.c.blocks + in) * C::REC;
+                    else if (lane == 0)
+                        atomicOr(&g_kv_stream_error, ERR_RANGE);
                 }
-                const int id = __shfl_sync(0xffffffffu, tab, pg - tab0);
-                if (id >= 0 && id < a.c.pages) {
+                if (src) {
                     if (lane == 0) {
-                        const uint8_t* src =
-                            a.c.data + (((long long)id * a.c.heads + fh) * a.c.blocks + (blk - pg * a.c.blocks)) * C::REC;
                         ptx::mbar_arrive_expect_tx(bars + 8 * st, C::REC);
                         ptx::bulk_load(ptx::smem_u32(ring + st * C::REC), src, C::REC, bars + 8 * st);
                     }
                     live |= 1u << st;
-                } else if (lane == 0) {
-                    atomicOr(&g_kv_stream_error, ERR_RANGE);
+                    src += C::REC;
                 }
+                --left;
             }
             ++fx;
             if (++fo == fs.tiles) {
                 const int was = fb;
                 next_unit(a, fb, fh, fs);
-                fo = 0;
+                fo = left = 0;
                 if (fb != was) tabn = 0;
             }
         };
-#pragma unroll 1
-        for (int st = 0; st < C::STAGES && fx < x1; ++st) fetch(st);
-
         uint32_t qf[SPLIT ? 2 : 1][NT][KS][2];
         float acc[KS][NT][4], m[NT][2], l[NT][2], fq[NT][2];
         int hi[NT][2], lo[NT][2], hi_min = 0, lo_max = 0, o_from = 0;
@@ -190,11 +196,12 @@ k_kv_attend_stream(const Attend a) {
                 const int rows = sq.n * a.group, first = sq.len - sq.n;
                 hi_min = 0x7fffffff;
                 lo_max = 0;
+                // 16 consecutive values of each 64 per lane: one run of loads, whatever the type; the first
+                // unit's go out before the first records, or they would queue behind them
+                uint4 raw[NT][D / 64][SPLIT ? 4 : 2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int r = 8 * nt + g, t = r / a.group;
-                    // 16 consecutive values of each 64: one run of loads, whatever the type
-                    uint4 raw[D / 64][SPLIT ? 4 : 2];
                     const uint8_t* src = static_cast<const uint8_t*>(a.q.data) +
                                          ((sq.start + t) * a.q.token_stride + (h * a.group + r - t * a.group) * a.q.head_stride +
                                           16 * tq) * (SPLIT ? 4 : 2);
@@ -202,13 +209,20 @@ k_kv_attend_stream(const Attend a) {
                     for (int sg = 0; sg < D / 64; ++sg)
 #pragma unroll
                         for (int e = 0; e < (SPLIT ? 4 : 2); ++e)
-                            raw[sg][e] = r < rows ? *reinterpret_cast<const uint4*>(src + sg * (SPLIT ? 256 : 128) + 16 * e)
-                                                  : make_uint4(0u, 0u, 0u, 0u);
+                            raw[nt][sg][e] = r < rows ? *reinterpret_cast<const uint4*>(src + sg * (SPLIT ? 256 : 128) + 16 * e)
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (x == x0) {
+#pragma unroll 1
+                    for (int i = 0; i < C::STAGES && fx < x1; ++i) fetch(i);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
                     float4 v[KS];
                     float am = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
-                        const uint4 p = raw[ks >> 2][SPLIT ? ks & 3 : (ks & 3) >> 1];
+                        const uint4 p = raw[nt][ks >> 2][SPLIT ? ks & 3 : (ks & 3) >> 1];
                         const uint2 w = ks & 1 ? make_uint2(p.z, p.w) : make_uint2(p.x, p.y);
                         v[ks] = SPLIT ? make_float4(__uint_as_float(p.x), __uint_as_float(p.y), __uint_as_float(p.z),
                                                     __uint_as_float(p.w))

@@ -241,7 +241,7 @@ k_kv_attend_tile(const Attend a) {
         bool more[3];           // whether tiles n, n + 1, n + 2 of this CTA exist
         const uint8_t* rec[2];  // this warp's record in tiles n, n + 1 (nullptr: nothing in reach there)
         int o = 0, in = 0, id = -1;  // of tile n + 2: its place in its record's page, its page number (on its way)
-        bool begun = false;
+        bool begun = false, reach = false;  // reach: some row of the tile sees keys of this warp's
         auto advance = [&]() -> bool {  // the cursor to the next tile
             if (!begun || ++o == o1) {
                 begun = true;
@@ -249,17 +249,17 @@ k_kv_attend_tile(const Attend a) {
                 o = o0;
             }
             const int blk = (w.kt0 + o) * C::BLK + bi;
-            id = -1;
+            reach = false;
             if (blk * BT < w.hi && blk * BT + BT > w.lo) {
                 const int pg = blk / a.c.blocks;
                 in = blk - pg * a.c.blocks;
                 id = a.bt.table[(long long)w.b * a.bt.table_stride + pg];
-                if (id < 0) id = -2;
+                reach = true;
             }
             return true;
         };
         auto resolve = [&]() -> const uint8_t* {
-            if (id == -1) return nullptr;
+            if (!reach) return nullptr;
             if (id < 0 || id >= a.c.pages) {
                 if (lane == 0) atomicOr(err, ERR_RANGE);
                 return nullptr;
