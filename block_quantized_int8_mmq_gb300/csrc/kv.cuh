@@ -75,6 +75,8 @@ template <>
 struct Elem<float> {
     static __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
     static __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+    static __device__ __forceinline__ float4 widen(uint2) { return make_float4(0.f, 0.f, 0.f, 0.f); }  // 16-bit types only
+    static __device__ __forceinline__ uint32_t pack2(float, float) { return 0u; }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -109,6 +111,28 @@ struct Elem<__half> {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
     }
 };
+
+// V consecutive elements of a row (V = 4, or 8 of a 16-bit type: one 16-byte load) as f32.
+template <typename T, int V>
+__device__ __forceinline__ void load_run(const T* p, float (&x)[V]) {
+    if (V == 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const float4 a = Elem<T>::widen(make_uint2(u.x, u.y)), b = Elem<T>::widen(make_uint2(u.z, u.w));
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[V - 4] = b.x, x[V - 3] = b.y, x[V - 2] = b.z, x[V - 1] = b.w;
+    } else {
+        const float4 a = Elem<T>::load4(p);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_run(T* p, const float (&x)[V]) {
+    if (V == 8)
+        *reinterpret_cast<uint4*>(p) = make_uint4(Elem<T>::pack2(x[0], x[1]), Elem<T>::pack2(x[2], x[3]),
+                                                  Elem<T>::pack2(x[V - 4], x[V - 3]), Elem<T>::pack2(x[V - 2], x[V - 1]));
+    else
+        Elem<T>::store4(p, make_float4(x[0], x[1], x[2], x[3]));
+}
 
 }  // namespace kv
 

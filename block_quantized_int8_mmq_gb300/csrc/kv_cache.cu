@@ -6,8 +6,8 @@
 // order.  The grid is laid out without knowing the lengths: the blocks that sequence b's new
 // tokens touch are numbered from starts[b] / 32 + 2b (at most n / 32 + 2 blocks, so the ranges
 // of consecutive sequences never overlap), or from b where every sequence has at most one new
-// token; a CTA finds its sequence by counting the sequences whose range begins at or before
-// its own number, and leaves when its block does not exist.
+// token; a CTA looks for the sequence whose range holds its own number, and leaves when there is
+// none or its block does not exist.
 #include "kv.cuh"
 
 namespace mmq {
@@ -26,27 +26,29 @@ struct Where {
 };
 __device__ __forceinline__ bool find_block(const Cache& c, const Batch& bt, Where& w) {
     const int x = blockIdx.x;
+    int start = 0, n = 0, len = 0, nth = 0;
     if (bt.max_new <= 1) {
         w.b = x;
+        if (!seq_range(c, bt, x, start, n, len, &g_kv_cache_error)) return false;
     } else {
-        int cnt = 0;
-        for (int i0 = 0; i0 < bt.seqs; i0 += THREADS) {
-            const int i = i0 + threadIdx.x;
-            cnt += __syncthreads_count(i < bt.seqs && bt.starts[min(i, bt.seqs - 1)] / BT + 2 * i <= x);
+        // one round of loads: a thread whose sequence's range holds x says so (in a disordered list more
+        // than one may, and any of them is as good: what it names is read again, from the L1)
+        __shared__ int found;
+        if (threadIdx.x == 0) found = -1;
+        __syncthreads();
+        for (int i = threadIdx.x; i < bt.seqs; i += THREADS) {
+            int si, ni, li;
+            if (seq_range(c, bt, i, si, ni, li, &g_kv_cache_error) && x >= si / BT + 2 * i && x < (si + ni) / BT + 2 * (i + 1))
+                found = i;
         }
-        w.b = cnt - 1;
-        // every sequence is checked once, also those that no CTA finds in a disordered list
-        if (x == 0 && blockIdx.y == 0)
-            for (int i = threadIdx.x; i < bt.seqs; i += THREADS) {
-                int s, n, l;
-                seq_range(c, bt, i, s, n, l, &g_kv_cache_error);
-            }
-        if (w.b < 0) return false;
+        __syncthreads();
+        w.b = found;
+        if (w.b < 0 || !seq_range(c, bt, w.b, start, n, len, &g_kv_cache_error)) return false;
+        nth = x - (start / BT + 2 * w.b);
     }
-    int start, n, len;
-    if (!seq_range(c, bt, w.b, start, n, len, &g_kv_cache_error) || n == 0) return false;
+    if (n == 0) return false;
     const int first = len - n;  // negative: the first rows are padding
-    w.blk = max(first, 0) / BT + (bt.max_new <= 1 ? 0 : x - (start / BT + 2 * w.b));
+    w.blk = max(first, 0) / BT + nth;
     w.pos0 = w.blk * BT;
     if (w.pos0 >= len) return false;
     w.i0 = max(0, first - w.pos0);
@@ -55,113 +57,150 @@ __device__ __forceinline__ bool find_block(const Cache& c, const Batch& bt, Wher
     return true;
 }
 
-// One octet of a row: eight values as two groups of four, `a` and `b` elements into the row,
-// that turn together (halves: a pair's members lie in different groups; interleaved: side by
-// side).  Each product and sum rounded on its own.
-struct Octet {
+// One unit of a row: 2V values as two runs of V, `a` and `b` elements into the row, that turn
+// together (halves: a pair's members lie in different runs; interleaved: side by side).  V is what
+// one 16-byte load brings, or 4 of a 16-bit type where the rotation ends inside a run of 8.
+struct Unit {
     int a, b, pair;  // pair: first column of the tables, or -1
 };
-__device__ __forceinline__ Octet octet(int o, const Rope& r) {
-    if (8 * o < r.rotary) return r.interleaved ? Octet{8 * o, 8 * o + 4, 4 * o} : Octet{4 * o, 4 * o + r.rotary / 2, 4 * o};
-    return Octet{8 * o, 8 * o + 4, -1};
+template <int V>
+__device__ __forceinline__ Unit unit(int o, const Rope& r) {
+    if (2 * V * o < r.rotary)
+        return r.interleaved ? Unit{2 * V * o, 2 * V * o + V, V * o} : Unit{V * o, V * o + r.rotary / 2, V * o};
+    return Unit{2 * V * o, 2 * V * o + V, -1};
 }
+// each product and sum rounded on its own
 __device__ __forceinline__ void turn1(float& x, float& y, float c, float s) {
     const float a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
     y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
     x = a;
 }
-__device__ __forceinline__ void turn(float4& a, float4& b, const Octet& o, const Rope& r, int pos) {
+template <int V>
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Unit& o, const Rope& r, int pos) {
     if (o.pair < 0) return;
     if (pos >= r.rows) {
         atomicOr(&g_kv_cache_error, ERR_RANGE);
         return;
     }
     const long long at = (long long)pos * (r.rotary / 2) + o.pair;
-    const float4 c = *reinterpret_cast<const float4*>(r.cos + at);
-    const float4 s = *reinterpret_cast<const float4*>(r.sin + at);
-    if (r.interleaved) {
-        turn1(a.x, a.y, c.x, s.x);
-        turn1(a.z, a.w, c.y, s.y);
-        turn1(b.x, b.y, c.z, s.z);
-        turn1(b.z, b.w, c.w, s.w);
-    } else {
-        turn1(a.x, b.x, c.x, s.x);
-        turn1(a.y, b.y, c.y, s.y);
-        turn1(a.z, b.z, c.z, s.z);
-        turn1(a.w, b.w, c.w, s.w);
+    float c[V], s[V];
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 c4 = *reinterpret_cast<const float4*>(r.cos + at + i);
+        const float4 s4 = *reinterpret_cast<const float4*>(r.sin + at + i);
+        c[i] = c4.x, c[i + 1] = c4.y, c[i + 2] = c4.z, c[i + 3] = c4.w;
+        s[i] = s4.x, s[i + 1] = s4.y, s[i + 2] = s4.z, s[i + 3] = s4.w;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (r.interleaved) {
+            if (i & 1) continue;
+            turn1(a[i], a[i + 1], c[i / 2], s[i / 2]);
+            turn1(b[i], b[i + 1], c[V / 2 + i / 2], s[V / 2 + i / 2]);
+        } else {
+            turn1(a[i], b[i], c[i], s[i]);
+        }
     }
 }
-__device__ __forceinline__ float amax4(float4 v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); }
+template <int V>
+__device__ __forceinline__ float amax(const float (&x)[V]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(x[i]));
+    return m;
+}
 
 __device__ __forceinline__ uint32_t code(float q) { return (uint32_t)(max(-127, min(127, __float2int_rn(q))) & 0xff); }
-__device__ __forceinline__ uint32_t codes4(float4 v, float d) {
-    if (d == 0.f) return 0u;
-    return code(__fdiv_rn(v.x, d)) | code(__fdiv_rn(v.y, d)) << 8 | code(__fdiv_rn(v.z, d)) << 16 |
-           code(__fdiv_rn(v.w, d)) << 24;
+template <int V>
+__device__ __forceinline__ void put_codes(uint8_t* p, const float (&x)[V], float d) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        uint32_t w = 0u;
+        if (d != 0.f)
+            w = code(__fdiv_rn(x[i], d)) | code(__fdiv_rn(x[i + 1], d)) << 8 | code(__fdiv_rn(x[i + 2], d)) << 16 |
+                code(__fdiv_rn(x[i + 3], d)) << 24;
+        *reinterpret_cast<uint32_t*>(p + i) = w;
+    }
 }
 // older codes under the new scale: rint(c * r), r = d / d'
-__device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
-    uint32_t o = 0;
+template <int V>
+__device__ __forceinline__ void rescale_codes(uint8_t* p, float r) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o |= code(__fmul_rn((float)(int8_t)(w >> (8 * i)), r)) << (8 * i);
-    return o;
+    for (int i = 0; i < V; i += 4) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p + i);
+        uint32_t o = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o |= code(__fmul_rn((float)(int8_t)(w >> (8 * k)), r)) << (8 * k);
+        *reinterpret_cast<uint32_t*>(p + i) = o;
+    }
 }
 
 // grid (blocks, kv heads [+ kv heads for the queries' rotation]).  A CTA of the first kind
 // holds its block's keys and values in registers (D / 4 values a thread), so the rows are read
-// once; the second kind turns the block's rows of one group of query heads.
-template <typename T, int D>
-__global__ void __launch_bounds__(THREADS)
+// once; the second kind turns the block's rows of one group of query heads, a few rows' loads in
+// flight at a time.
+template <typename T, int D, int V>
+__global__ void __launch_bounds__(THREADS, D == 256 ? 2 : 4)
 k_kv_append(Cache c, Batch bt, Rows kr, Rows vr, Rows qr, int group, Rope rope, T* __restrict__ q_out) {
-    constexpr int O = D / 8, RP = THREADS / O, PASSES = BT / RP;  // octets a row, rows a pass
+    constexpr int O = D / (2 * V), RP = THREADS / O, PASSES = BT > RP ? BT / RP : 1;  // units a row, rows a pass
     __shared__ float part[2][THREADS / 32];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch_dependents();
     Where w;
     if (!find_block(c, bt, w)) return;
     const int tid = threadIdx.x;
-    const Octet o = octet(tid % O, rope);
+    const Unit o = unit<V>(tid % O, rope);
     if (blockIdx.y >= c.heads) {
+        constexpr int B = 16 / V;
         const int h0 = (blockIdx.y - c.heads) * group, q_heads = c.heads * group;
         const int rows = (w.i1 - w.i0) * group;
-        for (int r = tid / O; r < rows; r += RP) {
-            const int i = w.i0 + r / group, h = h0 + r % group;
-            const T* src = static_cast<const T*>(qr.data) + (long long)(w.row + i) * qr.token_stride + h * qr.head_stride;
-            float4 a = Elem<T>::load4(src + o.a), b = Elem<T>::load4(src + o.b);
-            turn(a, b, o, rope, w.pos0 + i);
-            T* dst = q_out + ((long long)(w.row + i) * q_heads + h) * D;
-            Elem<T>::store4(dst + o.a, a);
-            Elem<T>::store4(dst + o.b, b);
+        for (int r0 = tid / O; r0 < rows; r0 += B * RP) {
+            float a[B][V], b[B][V];
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                const int r = min(r0 + u * RP, rows - 1), i = w.i0 + r / group, h = h0 + r % group;
+                const T* src = static_cast<const T*>(qr.data) + (long long)(w.row + i) * qr.token_stride + h * qr.head_stride;
+                load_run<T, V>(src + o.a, a[u]);
+                load_run<T, V>(src + o.b, b[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                const int r = r0 + u * RP, i = w.i0 + r / group, h = h0 + r % group;
+                if (r >= rows) break;
+                turn<V>(a[u], b[u], o, rope, w.pos0 + i);
+                T* dst = q_out + ((long long)(w.row + i) * q_heads + h) * D;
+                store_run<T, V>(dst + o.a, a[u]);
+                store_run<T, V>(dst + o.b, b[u]);
+            }
         }
         return;
     }
     const int h = blockIdx.y;
-    uint8_t* rec = record(c, bt, w.b, w.blk, h, &g_kv_cache_error);
-    if (!rec) return;
-    const float dk_old = *reinterpret_cast<const float*>(rec + 2 * BT * D);
-    const float dv_old = *reinterpret_cast<const float*>(rec + 2 * BT * D + 4);
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 ka[PASSES], kb[PASSES], va[PASSES], vb[PASSES];
+    float ka[PASSES][V], kb[PASSES][V], va[PASSES][V], vb[PASSES][V];
 #pragma unroll
     for (int u = 0; u < PASSES; ++u) {
         const int i = u * RP + tid / O;
-        ka[u] = kb[u] = va[u] = vb[u] = zero;
+#pragma unroll
+        for (int e = 0; e < V; ++e) ka[u][e] = kb[u][e] = va[u][e] = vb[u][e] = 0.f;
         if (i >= w.i0 && i < w.i1) {
             const T* ks = static_cast<const T*>(kr.data) + (long long)(w.row + i) * kr.token_stride + h * kr.head_stride;
             const T* vs = static_cast<const T*>(vr.data) + (long long)(w.row + i) * vr.token_stride + h * vr.head_stride;
-            ka[u] = Elem<T>::load4(ks + o.a);
-            kb[u] = Elem<T>::load4(ks + o.b);
-            va[u] = Elem<T>::load4(vs + o.a);
-            vb[u] = Elem<T>::load4(vs + o.b);
+            load_run<T, V>(ks + o.a, ka[u]);
+            load_run<T, V>(ks + o.b, kb[u]);
+            load_run<T, V>(vs + o.a, va[u]);
+            load_run<T, V>(vs + o.b, vb[u]);
         }
     }
+    uint8_t* rec = record(c, bt, w.b, w.blk, h, &g_kv_cache_error);  // while the rows are on their way
+    if (!rec) return;
+    const float2 d_old = *reinterpret_cast<const float2*>(rec + 2 * BT * D);
     float mk = 0.f, mv = 0.f;
 #pragma unroll
     for (int u = 0; u < PASSES; ++u) {
         const int i = u * RP + tid / O;
-        if (i >= w.i0 && i < w.i1) turn(ka[u], kb[u], o, rope, w.pos0 + i);
-        mk = fmaxf(mk, fmaxf(amax4(ka[u]), amax4(kb[u])));
-        mv = fmaxf(mv, fmaxf(amax4(va[u]), amax4(vb[u])));
+        if (i >= w.i0 && i < w.i1) turn<V>(ka[u], kb[u], o, rope, w.pos0 + i);
+        mk = fmaxf(mk, fmaxf(amax<V>(ka[u]), amax<V>(kb[u])));
+        mv = fmaxf(mv, fmaxf(amax<V>(va[u]), amax<V>(vb[u])));
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
@@ -182,35 +221,33 @@ k_kv_append(Cache c, Batch bt, Rows kr, Rows vr, Rows qr, int group, Rope rope, 
     const bool kept = w.i0 > 0;
     float dk = __fdiv_rn(mk, 127.0f), dv = __fdiv_rn(mv, 127.0f);
     if (kept) {
-        dk = fmaxf(dk, dk_old);
-        dv = fmaxf(dv, dv_old);
+        dk = fmaxf(dk, d_old.x);
+        dv = fmaxf(dv, d_old.y);
     }
     if (dk < MIN_SCALE) dk = 0.f;
     if (dv < MIN_SCALE) dv = 0.f;
-    const bool grew_k = kept && dk != dk_old, grew_v = kept && dv != dv_old;
-    const float rk = grew_k && dk != 0.f ? __fdiv_rn(dk_old, dk) : 0.f;
-    const float rv = grew_v && dv != 0.f ? __fdiv_rn(dv_old, dv) : 0.f;
+    const bool grew_k = kept && dk != d_old.x, grew_v = kept && dv != d_old.y;
+    const float rk = grew_k && dk != 0.f ? __fdiv_rn(d_old.x, dk) : 0.f;
+    const float rv = grew_v && dv != 0.f ? __fdiv_rn(d_old.y, dv) : 0.f;
 #pragma unroll
     for (int u = 0; u < PASSES; ++u) {
         const int i = u * RP + tid / O;
         uint8_t* kc = rec + i * D;
         uint8_t* vc = kc + BT * D;
-        uint32_t *k0 = reinterpret_cast<uint32_t*>(kc + o.a), *k1 = reinterpret_cast<uint32_t*>(kc + o.b);
-        uint32_t *v0 = reinterpret_cast<uint32_t*>(vc + o.a), *v1 = reinterpret_cast<uint32_t*>(vc + o.b);
         if (i < w.i0) {
             if (grew_k) {
-                *k0 = rescale4(*k0, rk);
-                *k1 = rescale4(*k1, rk);
+                rescale_codes<V>(kc + o.a, rk);
+                rescale_codes<V>(kc + o.b, rk);
             }
             if (grew_v) {
-                *v0 = rescale4(*v0, rv);
-                *v1 = rescale4(*v1, rv);
+                rescale_codes<V>(vc + o.a, rv);
+                rescale_codes<V>(vc + o.b, rv);
             }
         } else if (i < w.i1) {
-            *k0 = codes4(ka[u], dk);
-            *k1 = codes4(kb[u], dk);
-            *v0 = codes4(va[u], dv);
-            *v1 = codes4(vb[u], dv);
+            put_codes<V>(kc + o.a, ka[u], dk);
+            put_codes<V>(kc + o.b, kb[u], dk);
+            put_codes<V>(vc + o.a, va[u], dv);
+            put_codes<V>(vc + o.b, vb[u], dv);
         }
     }
     if (tid == 0) *reinterpret_cast<float2*>(rec + 2 * BT * D) = make_float2(dk, dv);
@@ -260,7 +297,14 @@ int append_t(const Cache& c, const Batch& b, const Rows& k, const Rows& v, const
         return pdl_status(launch_pdl(kernel, grid, dim3(THREADS), 0, s, c, b, k, v, q, group, rope, static_cast<T*>(q_out)),
                           "mmq_kv_append");
     };
-    return c.dim == 64 ? go(k_kv_append<T, 64>) : c.dim == 128 ? go(k_kv_append<T, 128>) : go(k_kv_append<T, 256>);
+    constexpr int W = sizeof(T) == 2 ? 8 : 4;
+    if (rope.rotary % (2 * W) == 0)
+        return c.dim == 64    ? go(k_kv_append<T, 64, W>)
+               : c.dim == 128 ? go(k_kv_append<T, 128, W>)
+                              : go(k_kv_append<T, 256, W>);
+    return c.dim == 64    ? go(k_kv_append<T, 64, 4>)
+           : c.dim == 128 ? go(k_kv_append<T, 128, 4>)
+                          : go(k_kv_append<T, 256, 4>);
 }
 
 template <typename T>

@@ -112,6 +112,9 @@ class KVBatch:
             raise ValueError("starts is [seqs + 1], lens [seqs] and table [seqs, pages]")
         if not starts.is_contiguous() or not lens.is_contiguous() or (table.shape[1] > 1 and table.stride(1) != 1):
             raise ValueError("starts, lens and the rows of table must be contiguous")
+        if lens.device != starts.device or table.device != starts.device:
+            raise ValueError("starts, lens and table must be on one device")
+        self.device = starts.device
         self.starts, self.lens, self.table, self.tokens, self.max_new = starts, lens, table, int(tokens), int(max_new)
         stride = table.stride(0) if seqs > 1 else table.shape[1]
         self._c = _Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), stride, seqs, self.tokens,
@@ -128,43 +131,39 @@ class Rope:
             _device_tensor(t, torch.float32, "a rotation table")
         if cos.dim() != 2 or cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
             raise ValueError("cos and sin are contiguous [positions, rotary / 2] tensors")
+        if cos.device != sin.device:
+            raise ValueError("cos and sin must be on one device")
+        self.device = cos.device
         self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
         self._c = _Rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
         self._p = ctypes.addressof(self._c)
 
 
-def _rows(t, cache, batch, dtype, heads, what):
-    """A row array's description; strides as the tensor has them (the C entry checks alignment)."""
-    if t.dim() != 3 or t.shape[0] != batch.tokens or t.shape[2] != cache.dim or (heads and t.shape[1] != heads):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}: [{batch.tokens}, {heads or 'heads'}, {cache.dim}] is wanted")
-    if t.dtype != dtype or t.device != cache.device:
-        raise ValueError(f"{what} is {t.dtype} on {t.device}: {dtype} on {cache.device} is wanted")
-    ts, hs, es = t.stride()
-    if es != 1:
-        raise ValueError(f"{what}: the last axis must be contiguous")
-    return _Rows(t.data_ptr(), ts, hs)
+def _refuse(t, what, shape, dtype, device):
+    """Why a row array is refused (the calls' own checks are one comparison each)."""
+    if t.dim() != 3 or t.shape[0] != shape[0] or t.shape[2] != shape[2] or (shape[1] and t.shape[1] != shape[1]):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}: [{shape[0]}, {shape[1] or 'heads'}, {shape[2]}] is wanted")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{what} is {t.dtype}: float32, bfloat16 and float16 are taken")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what} is {t.dtype} on {t.device}: {dtype} on {device} is wanted")
+    raise ValueError(f"{what}: the last axis must be contiguous")
 
 
-def _dtype(t):
-    d = _DTYPES.get(t)
-    if d is None:
-        raise ValueError(f"{t}: float32, bfloat16 and float16 are taken")
-    return d
+def _elsewhere(what, t, device):
+    raise ValueError(f"{what} is on {t.device}, the cache on {device}")
 
 
-def _run(fn, device, stream, made, *args):
-    """Call fn with the stream as its last argument; `made` (tensors allocated here) stay with a
-    stream other than the one they were allocated on."""
+def _stream_of(device, stream, made):
+    """The raw stream of a call; `made` (tensors allocated here) stay with a stream other than the
+    one they were allocated on."""
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        s = _stream(stream)
-        if isinstance(stream, torch.cuda.Stream):
-            for t in made:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if isinstance(stream, torch.cuda.Stream):
+        for t in made:
+            if t is not None:
                 t.record_stream(stream)
-    st = getattr(_lib, fn)(*args, s)
-    if st != 0:
-        raise MMQError(fn, st)
+    return _stream(stream)
 
 
 def _out(t, shape, dtype, cache, what):
@@ -173,45 +172,74 @@ def _out(t, shape, dtype, cache, what):
     return t
 
 
+_ROW_BYTES = ctypes.sizeof(_Rows)
+
+
+class _Rows3(ctypes.Structure):
+    _fields_ = [(f"{n}{i}", t) for i in range(3) for n, t in _Rows._fields_]
+
+
 def mmq_kv_append(cache, batch, k, v, q=None, rope=None, q_out=None, stream=None):
     """Keys and values [tokens, cache.heads, dim] into the cache, rotated by `rope` on the way (the
     values are not rotated); returns the rotated queries [tokens, q heads, dim] where q is given."""
-    dt = k.dtype
-    d = _dtype(dt)
-    kr = _rows(k, cache, batch, dt, cache.heads, "k")
-    vr = _rows(v, cache, batch, dt, cache.heads, "v")
-    made = []
-    qp = qo = None
-    heads = 0
-    if q is not None:
-        qr = _rows(q, cache, batch, dt, 0, "q")
-        qp, heads = ctypes.addressof(qr), q.shape[1]
+    dt, dev, shape = k.dtype, cache.device, (batch.tokens, cache.heads, cache.dim)
+    d = _DTYPES.get(dt)
+    ks, vs = k.stride(), v.stride()
+    if d is None or k.shape != shape or k.device != dev or ks[-1] != 1:
+        _refuse(k, "k", shape, dt, dev)
+    if v.dtype != dt or v.shape != shape or v.device != dev or vs[-1] != 1:
+        _refuse(v, "v", shape, dt, dev)
+    if batch.device != dev:
+        _elsewhere("the batch", batch, dev)
+    turn = None
+    if rope is not None:
+        if rope.device != dev:
+            _elsewhere("the rotation tables", rope, dev)
+        turn = rope._p
+    if q is None:
+        rows = _Rows3(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
+        p = ctypes.addressof(rows)
+        st = _lib.mmq_kv_append(cache._p, batch._p, d, p, p + _ROW_BYTES, None, 0, turn, None, _stream_of(dev, stream, ()))
+    else:
+        qs, qshape = q.stride(), q.shape
+        if q.dtype != dt or len(qshape) != 3 or qshape[0] != shape[0] or qshape[2] != shape[2] or q.device != dev or qs[-1] != 1:
+            _refuse(q, "q", (shape[0], 0, shape[2]), dt, dev)
+        made = None
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=cache.device)
-            made.append(q_out)
+            q_out = made = torch.empty(qshape, dtype=dt, device=dev)
         else:
-            _out(q_out, q.shape, dt, cache, "q_out")
-        qo = q_out.data_ptr()
-    _run("mmq_kv_append", cache.device, stream, made, cache._p, batch._p, d, ctypes.addressof(kr), ctypes.addressof(vr),
-         qp, heads, None if rope is None else rope._p, qo)
+            _out(q_out, qshape, dt, cache, "q_out")
+        rows = _Rows3(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], q.data_ptr(), qs[0], qs[1])
+        p = ctypes.addressof(rows)
+        st = _lib.mmq_kv_append(cache._p, batch._p, d, p, p + _ROW_BYTES, p + 2 * _ROW_BYTES, qshape[1], turn,
+                                q_out.data_ptr(), _stream_of(dev, stream, (made,)))
+    if st != 0:
+        raise MMQError("mmq_kv_append", st)
     return q_out if q is not None else None
 
 
 def mmq_kv_read(cache, batch, dtype=torch.float32, k_out=None, v_out=None, stream=None):
     """The cached keys and values of the batch's tokens, [tokens, cache.heads, dim] of `dtype`."""
-    d = _dtype(dtype)
-    shape = torch.Size((batch.tokens, cache.heads, cache.dim))
+    d, dev, shape = _DTYPES.get(dtype), cache.device, (batch.tokens, cache.heads, cache.dim)
+    if d is None:
+        raise ValueError(f"{dtype}: float32, bfloat16 and float16 are taken")
+    if batch.device != dev:
+        _elsewhere("the batch", batch, dev)
     made = []
-    outs = []
-    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=cache.device)
-            made.append(t)
-        else:
-            _out(t, shape, dtype, cache, what)
-        outs.append(t)
-    _run("mmq_kv_read", cache.device, stream, made, cache._p, batch._p, d, outs[0].data_ptr(), outs[1].data_ptr())
-    return outs[0], outs[1]
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        made.append(k_out)
+    else:
+        _out(k_out, shape, dtype, cache, "k_out")
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        made.append(v_out)
+    else:
+        _out(v_out, shape, dtype, cache, "v_out")
+    st = _lib.mmq_kv_read(cache._p, batch._p, d, k_out.data_ptr(), v_out.data_ptr(), _stream_of(dev, stream, made))
+    if st != 0:
+        raise MMQError("mmq_kv_read", st)
+    return k_out, v_out
 
 
 _workspaces: dict = {}
@@ -241,23 +269,29 @@ def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=No
     workspace: a uint8 tensor of mmq_kv_workspace_bytes(dim) bytes, its first 4096 zero, for calls
     that may overlap others of the same stream (a captured graph replayed elsewhere); by default
     the package keeps one for each stream."""
-    dt = q.dtype
-    d = _dtype(dt)
-    qr = _rows(q, cache, batch, dt, 0, "q")
-    made = []
+    dt, dev, qs, qshape = q.dtype, cache.device, q.stride(), q.shape
+    d = _DTYPES.get(dt)
+    if d is None or len(qshape) != 3 or qshape[0] != batch.tokens or qshape[2] != cache.dim or q.device != dev or qs[-1] != 1:
+        _refuse(q, "q", (batch.tokens, 0, cache.dim), dt, dev)
+    if batch.device != dev:
+        _elsewhere("the batch", batch, dev)
+    made = None
     if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=cache.device)
-        made.append(out)
+        out = made = torch.empty(qshape, dtype=dt, device=dev)
     else:
-        _out(out, q.shape, dt, cache, "out")
+        _out(out, qshape, dt, cache, "out")
     if lse is not None:
-        _out(lse, q.shape[:2], torch.float32, cache, "lse")
+        _out(lse, qshape[:2], torch.float32, cache, "lse")
     if workspace is None:
         workspace = _workspace(cache, stream)
     elif workspace.dtype != torch.uint8 or workspace.device != cache.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {cache.device}")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.dim)
-    _run("mmq_kv_attend", cache.device, stream, made, cache._p, batch._p, d, ctypes.addressof(qr), q.shape[1], scale,
-         window, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    rows = _Rows(q.data_ptr(), qs[0], qs[1])
+    st = _lib.mmq_kv_attend(cache._p, batch._p, d, ctypes.addressof(rows), qshape[1], scale, window, out.data_ptr(),
+                            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                            _stream_of(dev, stream, (made,)))
+    if st != 0:
+        raise MMQError("mmq_kv_attend", st)
     return out
