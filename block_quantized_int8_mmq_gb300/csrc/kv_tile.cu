@@ -95,9 +95,11 @@ __device__ __forceinline__ void unit_next(const Attend& a, Unit& w) {
     while (w.tiles == 0 && ++w.b < a.bt.seqs) unit_load<ROWS, KT>(a, w, w.b, 0);
 }
 
-// What a unit costs beside its key tiles (queries in, output out), in key tiles: a unit takes
-// OVERHEAD + tiles places in the list of work, and the first OVERHEAD of them hold nothing.
-constexpr int OVERHEAD = 3;
+// What a unit costs beside its key tiles (queries in, output out, joining), in key tiles: a unit
+// takes OVERHEAD + tiles places in the list of work, and the first OVERHEAD of them hold nothing.
+// Measured at 3 / 6: a 2048-token bf16 prompt 72.9 / 70.9 us, four prompts of 100..300 tokens on
+// 200..600 40.6 / 32.6 us, drafted tokens 31.0 / 30.6 us.
+constexpr int OVERHEAD = 6;
 
 // The next run of key tiles [t0, t1) of this CTA's places x .. x1 - 1; pos: place in unit w.
 template <int ROWS, int KT>
@@ -457,31 +459,39 @@ k_kv_attend_tile(const Attend a) {
                             if (SPLIT) {
                                 u = make_float4(__uint_as_float(p.x), __uint_as_float(p.y), __uint_as_float(p.z), __uint_as_float(p.w));
                                 v = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
-                            } else if (a.dtype == MMQ_BF16) {
+                            } else {
                                 u = Elem<__nv_bfloat16>::widen(make_uint2(p.x, p.y));
                                 v = Elem<__nv_bfloat16>::widen(make_uint2(p.z, p.w));
-                            } else {
-                                u = Elem<__half>::widen(make_uint2(p.x, p.y));
-                                v = Elem<__half>::widen(make_uint2(p.z, p.w));
                             }
                         };
-                        float am = 0.f;
+                        float down = 1.f, upr = 1.f;
+                        if (SPLIT || a.dtype == MMQ_BF16) {  // f16 rows are operands as they are
+                            // magnitudes order as their bits do; bf16 pairs as two 16-bit numbers
+                            uint32_t am = 0u;
 #pragma unroll
-                        for (int i = 0; i < NC; ++i) {
-                            float4 u, v;
-                            eight(i, u, v);
-                            am = fmaxf(am, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))));
-                            am = fmaxf(am, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                                for (int e = 0; e < (SPLIT ? 2 : 1); ++e) {
+                                    const uint4 p = raw[gi][i][e];
+                                    const uint32_t mask = SPLIT ? 0x7fffffffu : 0x7fff7fffu;
+                                    const uint32_t p0 = p.x & mask, p1 = p.y & mask, p2 = p.z & mask, p3 = p.w & mask;
+                                    am = SPLIT ? max(max(am, max(p0, p1)), max(p2, p3))
+                                               : __vmaxu2(__vmaxu2(am, __vmaxu2(p0, p1)), __vmaxu2(p2, p3));
+                                }
+                            if (!SPLIT) am = max(am & 0xffffu, am >> 16) << 16;
+                            am = max(am, __shfl_xor_sync(0xffffffffu, am, 8));
+                            am = max(am, __shfl_xor_sync(0xffffffffu, am, 16));
+                            row_scale(__uint_as_float(am), down, upr);
                         }
-                        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 8));
-                        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
-                        float down, upr;
-                        row_scale(am, down, upr);
                         if (lane >> 3 == g0 + gi) up = upr;
                         uint8_t* dst = q_smem + (rl >> 3) * SBO + (lane >> 3) * 128 + (rl & 7) * 16;
 #pragma unroll
                         for (int i = 0; i < NC; ++i) {
                             if (HALF && (i >= NC / 2) != (gt == 1)) continue;
+                            if (!SPLIT && a.dtype == MMQ_F16) {
+                                *reinterpret_cast<uint4*>(dst + 512 * i) = raw[gi][i][0];
+                                continue;
+                            }
                             float4 u, v;
                             eight(i, u, v);
                             uint4 hi4, lo4;
@@ -715,7 +725,6 @@ k_kv_attend_tile(const Attend a) {
                     ok = ok && umma::warp_wait(jn, n_jn++ & 1, abort, err);
                     if (!ok) break;
                     if (s_last[gt]) {
-                        __threadfence();
                         if (real) {
                             float M = M_NONE, L = 0.f;
 #pragma unroll 4
@@ -733,17 +742,21 @@ k_kv_attend_tile(const Attend a) {
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-                                for (int c = c0; c <= c1; ++c) {
-                                    const float* p = part(c, c == c0);
-                                    float4 y[16];
-                                    const float f = exp2_approx(__ldcg(p + 128 * OD + row) - M);
+                                for (int c = c0; c <= c1; c += 2) {  // two parts' loads in flight
+                                    const int d = min(c + 1, c1);
+                                    const float *p = part(c, c == c0), *q = part(d, d == c0);
+                                    float4 y[16], z[16];
+                                    const float mp = __ldcg(p + 128 * OD + row), mq = __ldcg(q + 128 * OD + row);
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e)
+                                    for (int e = 0; e < 16; ++e) {
                                         y[e] = __ldcg(reinterpret_cast<const float4*>(p) + (k + e) * 128 + row);
+                                        z[e] = __ldcg(reinterpret_cast<const float4*>(q) + (k + e) * 128 + row);
+                                    }
+                                    const float f = exp2_approx(mp - M), g = d > c ? exp2_approx(mq - M) : 0.f;
 #pragma unroll
                                     for (int e = 0; e < 16; ++e)
-                                        v[e] = make_float4(v[e].x + y[e].x * f, v[e].y + y[e].y * f, v[e].z + y[e].z * f,
-                                                           v[e].w + y[e].w * f);
+                                        v[e] = make_float4(v[e].x + y[e].x * f + z[e].x * g, v[e].y + y[e].y * f + z[e].y * g,
+                                                           v[e].z + y[e].z * f + z[e].z * g, v[e].w + y[e].w * f + z[e].w * g);
                                 }
 #pragma unroll
                                 for (int e = 0; e < 16; e += 2)
