@@ -81,7 +81,7 @@ size_t mmq_kv_block_bytes(int64_t dim) { return dim_ok(dim) ? (size_t)rec_bytes(
 
 // the arrival counters, then two partial results for every SM
 size_t mmq_kv_workspace_bytes(int64_t dim) {
-    return dim_ok(dim) ? WS_COUNTERS + (size_t)device_shape().sms * 2 * WS_ROWS * (dim + 2) * 4 : 0;
+    return dim_ok(dim) ? WS_COUNTERS + (size_t)device_shape().sms * 2 * WS_ROWS * (dim + WS_ROW_STATS) * 4 : 0;
 }
 
 int mmq_kv_append(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtype, const mmq_kv_rows* k,

@@ -8,8 +8,10 @@
 // finished there; one that spans CTAs leaves, per CTA, a partial result (O, m, l) in the
 // workspace (a CTA can have one unit that came in, slot 0, and one that goes out, slot 1), and
 // the last CTA to arrive adds the parts in CTA order: the order of summation depends on the
-// lengths alone.  The arrival counter of a unit is that of the CTA in which it starts (only
-// one unit goes out of a CTA), and the last arriver sets it back to zero.
+// lengths alone.  The stream's parts, a few rows each, are added in one go; the tiles', up to 64 KB a
+// row tile, eight at a time: the last arriver of eight neighbours puts their sum in the first
+// one's place and arrives for them one level up.  An arrival counter belongs to the CTA, and to
+// the slot, where the parts that it counts begin, and the last arriver sets it back to zero.
 //
 // The softmax, in base 2, with the value scale folded into the exponent: for a block with
 // scales dk, dv and a query scaled by a = scale * log2(e) * dk,
@@ -30,8 +32,9 @@ namespace kv {
 
 constexpr float SHIFT = 7.f, LIMIT = 15.f;  // weights up to 2^15 < 65504
 constexpr float M_NONE = -1e30f;            // m of a row that has seen nothing
-constexpr int WS_COUNTERS = 4096;           // bytes of arrival counters before the partial results
-constexpr int WS_ROWS = 256;                // rows a partial result holds at most
+constexpr int WS_COUNTERS = 16384;          // bytes of arrival counters before the partial results
+constexpr int WS_ROWS = 256;                // rows a partial result holds at most,
+constexpr int WS_ROW_STATS = 6;             // values beside O: m and l, for each level of joining
 
 struct Attend {
     Cache c;
@@ -51,7 +54,7 @@ __device__ __forceinline__ int work_owner(int total, int x, int workers) {
 }
 
 __device__ __forceinline__ float* part_slot(const Attend& a, int cta, int slot) {
-    return reinterpret_cast<float*>(a.ws + WS_COUNTERS) + ((long long)cta * 2 + slot) * WS_ROWS * (a.c.dim + 2);
+    return reinterpret_cast<float*>(a.ws + WS_COUNTERS) + ((long long)cta * 2 + slot) * WS_ROWS * (a.c.dim + WS_ROW_STATS);
 }
 
 // first key that row 0 of a sequence (at position first) sees

@@ -587,7 +587,7 @@ int launch(const Attend& a, cudaStream_t s) {
     }
     // no more warps than records can be in reach
     const long long most = (long long)a.bt.seqs * a.c.heads * a.bt.table_pages * a.c.blocks;
-    const long long ctas = (most + C::WARPS - 1) / C::WARPS, sms = device_shape().sms;
+    const long long ctas = (most + C::WARPS - 1) / C::WARPS, sms = device_shape().sms < 341 ? device_shape().sms : 341;
     const dim3 grid((unsigned)(ctas < 1 ? 1 : ctas < sms ? ctas : sms));
     ProfScope ps("k_kv_attend_stream", s);
     return pdl_status(launch_pdl(&k_kv_attend_stream<D, NT, SPLIT>, grid, dim3(C::THREADS), C::SMEM, s, a), fn);

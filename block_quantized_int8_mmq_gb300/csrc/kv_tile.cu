@@ -100,6 +100,7 @@ __device__ __forceinline__ void unit_next(const Attend& a, Unit& w) {
 // Measured at 3 / 6: a 2048-token bf16 prompt 72.9 / 70.9 us, four prompts of 100..300 tokens on
 // 200..600 40.6 / 32.6 us, drafted tokens 31.0 / 30.6 us.
 constexpr int OVERHEAD = 6;
+constexpr int JOIN = 8;  // parts joined at a time (three levels: up to 512 CTAs)
 
 // The next run of key tiles [t0, t1) of this CTA's places x .. x1 - 1; pos: place in unit w.
 template <int ROWS, int KT>
@@ -117,6 +118,13 @@ __device__ __forceinline__ bool next_piece(const Attend& a, Unit& w, int& pos, i
         if (t1 > t0) return true;
     }
     return false;
+}
+
+// How many CTAs share T places in U units: all, but for few units no more than 2 sqrt(T / U) a unit, where
+// fewer tiles a CTA and more parts to join balance. Measured at 1.4, 2 and without the limit: 26 tokens x 8
+// heads of 256 on 3838 tokens (two units) 49.8 / 47.5 / 63.6 us, 8 tokens on 65536 (four units) 69 / 65 / 65.
+__device__ __forceinline__ int workers(int T, int U) {
+    return min(min((int)gridDim.x, T), max(U, (int)(2.f * sqrtf((float)T * (float)U))));
 }
 
 template <int D, bool SPLIT>
@@ -160,11 +168,11 @@ k_kv_attend_tile(const Attend a) {
     ptx::grid_dep_launch_dependents();
 
     // ---- this CTA's range of the work: sequences THREADS at a time, their row runs spread over the threads
-    int T = 0, W = 0, x0 = 0, x1 = 0;
+    int T = 0, U = 0, W = 0, x0 = 0, x1 = 0;
     bool located = false;
     for (int pass = 0; pass < 2 && !located; ++pass) {
         int carry = 0;
-        for (int b0 = 0; b0 < a.bt.seqs; b0 += C::THREADS) {
+        for (int b0 = 0, units = 0; b0 < a.bt.seqs; b0 += C::THREADS) {
             int runs = 0, total;
             if (b0 + tid < a.bt.seqs) {
                 int start, n, len;
@@ -173,6 +181,7 @@ k_kv_attend_tile(const Attend a) {
             }
             s_pref[tid] = scan_cta<C::WARPS>(runs, total, s_scan);
             __syncthreads();
+            U = (units += total) * a.c.heads;
             for (int i0 = 0; i0 < total; i0 += C::THREADS) {
                 const int i = i0 + tid;
                 Unit q;
@@ -195,7 +204,7 @@ k_kv_attend_tile(const Attend a) {
                 if (pass == 0 && a.bt.seqs <= C::THREADS && total <= C::THREADS) {  // that was all of it
                     located = true;
                     T = carry;
-                    W = min((int)gridDim.x, T);
+                    W = workers(T, total * a.c.heads);
                     x0 = work_start(T, min((int)blockIdx.x, W), W);
                 }
                 if ((pass == 1 || located) && x0 >= e && x0 < e + v) {
@@ -208,7 +217,7 @@ k_kv_attend_tile(const Attend a) {
         }
         if (pass == 0) {
             T = carry;
-            W = min((int)gridDim.x, T);
+            W = workers(T, U);
             if ((int)blockIdx.x >= W) return;
             x0 = work_start(T, blockIdx.x, W);
             x1 = work_start(T, blockIdx.x + 1, W);
@@ -668,8 +677,8 @@ k_kv_attend_tile(const Attend a) {
                 // ---- the unit's output, or this CTA's part of it
                 const int ufirst = x - place + OVERHEAD;  // place of the unit's first key tile
                 const bool whole = o0 == 0 && tiles == w.tiles;
-                // a part's layout: [OD / 4][128 rows] float4, then m, l of the rows
-                auto part = [&](int cta, int slot) { return part_slot(a, cta, slot) + gt * 128 * (OD + 2); };
+                // a part's layout: [OD / 4][128 rows] float4, then m, l of the rows, for each level of joining
+                auto part = [&](int cta, int slot) { return part_slot(a, cta, slot) + gt * 128 * (OD + WS_ROW_STATS); };
                 float* mine = part(blockIdx.x, o0 == 0 ? 1 : 0);
                 const float inv = whole ? (l > 0.f ? __frcp_rn(l) : 0.f) : 1.f;
 #pragma unroll
@@ -706,68 +715,121 @@ k_kv_attend_tile(const Attend a) {
                         mine[128 * (OD + 1) + row] = l;
                     }
                     const int c0 = work_owner(T, ufirst, W), c1 = work_owner(T, ufirst + w.tiles - 1, W);
-                    __threadfence();
-                    signal(pr);
-                    if (lead) {
-                        ok = umma::warp_wait(pr, n_pr & 1, abort, err);
-                        if (lane == 0) {
-                            unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0 * 2 + gt;
-                            s_last[gt] = 0;
-                            if (ok && atomicAdd(counter, 1u) == (unsigned)(c1 - c0)) {
-                                *counter = 0;
-                                s_last[gt] = 1;
+                    // few rows: several threads a row, a share of the columns each
+                    const int nr = min(128, w.rows - row0), lg = nr > 64 ? 7 : nr > 32 ? 6 : 5;
+                    const int jr = row & ((1 << lg) - 1), seg = row >> lg, span = (OD / 4) >> (7 - lg);
+                    int at = blockIdx.x - c0, step = 1;  // this part among the level's, their distance in CTAs
+                    for (int level = 0;; ++level) {
+                        const int all = (c1 - c0 + step) / step, begin = at / JOIN * JOIN, count = min(JOIN, all - begin);
+                        const int first = c0 + begin * step;
+                        __threadfence();
+                        signal(pr);
+                        if (lead) {
+                            ok = umma::warp_wait(pr, n_pr & 1, abort, err);
+                            if (lane == 0) {
+                                unsigned* counter = reinterpret_cast<unsigned*>(a.ws) +
+                                                    ((level * (int)gridDim.x + first) * 2 + (first == c0)) * 2 + gt;
+                                s_last[gt] = 0;
+                                if (ok && atomicAdd(counter, 1u) == (unsigned)(count - 1)) {
+                                    *counter = 0;
+                                    s_last[gt] = 1;
+                                }
+                                __threadfence();
+                                ptx::mbar_arrive(jn);
                             }
-                            __threadfence();
-                            ptx::mbar_arrive(jn);
                         }
-                    }
-                    ++n_pr;
-                    ok = ok && umma::warp_wait(jn, n_jn++ & 1, abort, err);
-                    if (!ok) break;
-                    if (s_last[gt]) {
-                        if (real) {
-                            float M = M_NONE, L = 0.f;
-#pragma unroll 4
-                            for (int c = c0; c <= c1; ++c) {
-                                const float* p = part(c, c == c0);
-                                const float mc = __ldcg(p + 128 * OD + row), lc = __ldcg(p + 128 * (OD + 1) + row);
-                                const float mn = fmaxf(M, mc);
-                                L = L * exp2_approx(M - mn) + lc * exp2_approx(mc - mn);
-                                M = mn;
-                            }
-                            const float invl = L > 0.f ? __frcp_rn(L) : 0.f;
-#pragma unroll 1
-                            for (int k = 0; k < OD / 4; k += 16) {
-                                float4 v[16];
+                        ++n_pr;
+                        ok = ok && umma::warp_wait(jn, n_jn++ & 1, abort, err);
+                        if (!ok || !s_last[gt]) break;
+                        const bool final = count == all;
+                        if (jr < nr) {
+                            const int rj = row0 + jr, tj = rj / a.group, hj = w.h * a.group + rj - tj * a.group;
+                            float M = M_NONE, L = 0.f, f[JOIN], lp[JOIN];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int i = 0; i < JOIN; ++i) {
+                                f[i] = M_NONE;
+                                lp[i] = 0.f;
+                                if (i < count) {
+                                    const int c = first + i * step;
+                                    const float* p = part(c, c == c0) + 128 * OD + level * 256 + jr;
+                                    f[i] = __ldcg(p);
+                                    lp[i] = __ldcg(p + 128);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < JOIN; ++i) M = fmaxf(M, f[i]);
+#pragma unroll
+                            for (int i = 0; i < JOIN; ++i) {
+                                f[i] = exp2_approx(f[i] - M);
+                                L += lp[i] * f[i];
+                            }
+                            const float sc = final ? (L > 0.f ? __frcp_rn(L) : 0.f) : 1.f;
+                            float* to = part(first, first == c0);
+                            auto put = [&](int k, float4 x, float4 y) {  // float4 k and k + 1 of the row
+                                x = make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
+                                y = make_float4(y.x * sc, y.y * sc, y.z * sc, y.w * sc);
+                                if (final) {
+                                    store_out8(a, w.start + tj, hj, col0 + 4 * k, x, y);
+                                } else {
+                                    *reinterpret_cast<float4*>(to + (k * 128 + jr) * 4) = x;
+                                    *reinterpret_cast<float4*>(to + ((k + 1) * 128 + jr) * 4) = y;
+                                }
+                            };
+                            if (count == 2 && lg == 7) {  // the usual end: a long run of both parts' columns in flight
+                                const float4* p = reinterpret_cast<const float4*>(to) + jr;
+                                const float4* q = reinterpret_cast<const float4*>(part(first + step, 0)) + jr;
+                                const float fp = f[0], fq2 = f[1];
 #pragma unroll 1
-                                for (int c = c0; c <= c1; c += 2) {  // two parts' loads in flight
-                                    const int d = min(c + 1, c1);
-                                    const float *p = part(c, c == c0), *q = part(d, d == c0);
+                                for (int k = 0; k < OD / 4; k += 16) {
                                     float4 y[16], z[16];
-                                    const float mp = __ldcg(p + 128 * OD + row), mq = __ldcg(q + 128 * OD + row);
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) {
-                                        y[e] = __ldcg(reinterpret_cast<const float4*>(p) + (k + e) * 128 + row);
-                                        z[e] = __ldcg(reinterpret_cast<const float4*>(q) + (k + e) * 128 + row);
+                                        y[e] = __ldcg(p + (k + e) * 128);
+                                        z[e] = __ldcg(q + (k + e) * 128);
                                     }
-                                    const float f = exp2_approx(mp - M), g = d > c ? exp2_approx(mq - M) : 0.f;
 #pragma unroll
                                     for (int e = 0; e < 16; ++e)
-                                        v[e] = make_float4(v[e].x + y[e].x * f + z[e].x * g, v[e].y + y[e].y * f + z[e].y * g,
-                                                           v[e].z + y[e].z * f + z[e].z * g, v[e].w + y[e].w * f + z[e].w * g);
-                                }
+                                        y[e] = make_float4(y[e].x * fp + z[e].x * fq2, y[e].y * fp + z[e].y * fq2,
+                                                           y[e].z * fp + z[e].z * fq2, y[e].w * fp + z[e].w * fq2);
 #pragma unroll
-                                for (int e = 0; e < 16; e += 2)
-                                    store_out8(a, w.start + t, hq, col0 + 4 * (k + e),
-                                               make_float4(v[e].x * invl, v[e].y * invl, v[e].z * invl, v[e].w * invl),
-                                               make_float4(v[e + 1].x * invl, v[e + 1].y * invl, v[e + 1].z * invl,
-                                                           v[e + 1].w * invl));
+                                    for (int e = 0; e < 16; e += 2) put(k + e, y[e], y[e + 1]);
+                                }
+                            } else {
+#pragma unroll 1
+                                for (int k = seg * span; k < (seg + 1) * span; k += 4) {
+                                    float4 v[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                    for (int i = 0; i < JOIN; ++i) {
+                                        if (i >= count) break;
+                                        const int c = first + i * step;
+                                        const float4* p = reinterpret_cast<const float4*>(part(c, c == c0)) + k * 128 + jr;
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) {
+                                            const float4 y = __ldcg(p + e * 128);
+                                            v[e] = make_float4(v[e].x + y.x * f[i], v[e].y + y.y * f[i], v[e].z + y.z * f[i],
+                                                               v[e].w + y.w * f[i]);
+                                        }
+                                    }
+                                    put(k, v[0], v[1]);
+                                    put(k + 2, v[2], v[3]);
+                                }
                             }
-                            if (col0 == 0) store_lse(a, w.start + t, hq, M, L);
+                            if (seg == 0) {
+                                if (!final) {
+                                    to[128 * OD + (level + 1) * 256 + jr] = M;
+                                    to[128 * OD + (level + 1) * 256 + 128 + jr] = L;
+                                } else if (col0 == 0) {
+                                    store_lse(a, w.start + tj, hj, M, L);
+                                }
+                            }
                         }
+                        if (final) break;
+                        at /= JOIN;
+                        step *= JOIN;
                     }
+                    if (!ok) break;
                 }
             }
             n += tiles;
@@ -799,7 +861,7 @@ int launch(const Attend& a, cudaStream_t s) {
         report(fn, st, "the attention tiles' shared memory was refused");
         return st;
     }
-    const long long sms = device_shape().sms;
+    const long long sms = device_shape().sms < 341 ? device_shape().sms : 341;  // the counters' room
     ProfScope ps("k_kv_attend_tile", s);
     return pdl_status(launch_pdl(&k_kv_attend_tile<D, SPLIT>, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(C::THREADS),
                                  C::SMEM, s, a),

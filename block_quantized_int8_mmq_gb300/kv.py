@@ -242,6 +242,7 @@ def mmq_kv_read(cache, batch, dtype=torch.float32, k_out=None, v_out=None, strea
     return k_out, v_out
 
 
+_WS_ZERO = 16384  # bytes at a workspace's beginning that start at zero
 _workspaces: dict = {}
 
 
@@ -255,9 +256,9 @@ def _workspace(cache, stream):
         if stream is not None:
             with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                                    else torch.cuda.ExternalStream(s, device=cache.device)):
-                ws[:4096].zero_()
+                ws[:_WS_ZERO].zero_()
         else:
-            ws[:4096].zero_()
+            ws[:_WS_ZERO].zero_()
         _workspaces[key] = ws
     return ws
 
@@ -266,7 +267,7 @@ def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=No
     """Causal attention of the rotated queries [tokens, q heads, dim] over the cache: [tokens, q
     heads, dim].  scale: 1 / sqrt(dim) by default.  window: how many of the latest tokens a row
     sees (0: all).  lse: an f32 [tokens, q heads] tensor for the logarithm of the softmax's sum.
-    workspace: a uint8 tensor of mmq_kv_workspace_bytes(dim) bytes, its first 4096 zero, for calls
+    workspace: a uint8 tensor of mmq_kv_workspace_bytes(dim) bytes, its first 16384 zero, for calls
     that may overlap others of the same stream (a captured graph replayed elsewhere); by default
     the package keeps one for each stream."""
     dt, dev, qs, qshape = q.dtype, cache.device, q.stride(), q.shape

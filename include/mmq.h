@@ -525,7 +525,7 @@ size_t mmq_kv_workspace_bytes(int64_t dim);
  *   q: rows of `dtype`.  out: [tokens][q_heads][dim] contiguous, `dtype`, 16-byte aligned.
  *   lse (NULL: not wanted): f32 [tokens][q_heads].  scale: finite, > 0.  window >= 0.
  *   q_heads: a multiple of cache->heads.
- *   workspace: at least mmq_kv_workspace_bytes(dim) bytes, 256-byte aligned, its first 4096
+ *   workspace: at least mmq_kv_workspace_bytes(dim) bytes, 256-byte aligned, its first 16384
  *   bytes zero before its first use; every call leaves them zero again, so one workspace
  *   serves any number of calls in stream order, but never two that may overlap in time.
  * Accuracy: the codes and their scales enter exactly; sums, the softmax's statistics and the

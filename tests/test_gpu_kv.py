@@ -404,7 +404,7 @@ def test_other_stream_and_graph(new):
         kv_ref.append(ref, c.starts, lens, c.table, k.cpu().numpy(), v.cpu().numpy(), 64, rope)
         assert np.array_equal(cache.data.cpu().numpy(), ref)
         compare_attend(c, got, None, turned.cpu(), 0.2, data=ref)
-    assert (ws[:4096] == 0).all()
+    assert (ws[:16384] == 0).all()
 
 
 def test_workspace_is_left_clean_and_shared():
@@ -418,7 +418,7 @@ def test_workspace_is_left_clean_and_shared():
         out = mmq.mmq_kv_attend(cache, batch, q.cuda(), scale=0.1, workspace=ws)
         clean()
         compare_attend(c, out, None, q, 0.1)
-        assert (ws[:4096] == 0).all()
+        assert (ws[:16384] == 0).all()
 
 
 @pytest.mark.parametrize("new", [1, 40])
