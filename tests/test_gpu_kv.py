@@ -316,6 +316,28 @@ def test_attend_many_sequences(new):
     check_attend(Case(29, lens, [new] * 600, 2, 1, 64, 32, "bf16"))
 
 
+@pytest.mark.parametrize("dtype,length,dim", [("bf16", 20000, 64), ("f32", 20000, 128), ("f16", 9000, 256),
+                                              ("bf16", 140000, 64)])
+@pytest.mark.parametrize("new", [1, 3])
+def test_attend_many_parts(dtype, length, dim, new):
+    """One long sequence of one key/value head: its parts are joined in one, two and three steps."""
+    c = Case(length, [length], [new], 8, 1, dim, 256, dtype)
+    check_attend(c)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attend_drawn(seed):
+    """Shapes, types, windows and lengths drawn with a fixed seed."""
+    r = np.random.default_rng(1000 + seed)
+    kh, group = [(1, 7), (2, 4), (4, 1), (1, 8), (3, 2), (1, 16)][r.integers(6)]
+    dim, page = int(r.choice([64, 128, 256])), int(r.choice([32, 64, 96, 256]))
+    seqs = int(r.integers(1, 7))
+    news = np.exp(r.uniform(0, np.log(150), seqs)).astype(int) if seed % 2 else r.integers(1, 5, seqs)
+    lens = news + (np.exp(r.uniform(0, np.log(700), seqs)).astype(int) - 1) * (r.random(seqs) < 0.8)
+    c = Case(seed, lens.tolist(), news.tolist(), kh * group, kh, dim, page, ["f32", "bf16", "f16"][seed % 3])
+    check_attend(c, window=int(r.choice([0, 0, 50, 200])), qscale=float(r.choice([0.3, 1.0, 3.0])))
+
+
 def test_attend_query_range():
     """Rows of very different sizes, a row of zeros, elements far below their row's largest."""
     for dtype in ("f32", "bf16", "f16"):
@@ -526,3 +548,16 @@ def test_profiler_names():
     finally:
         mmq.mmq_profile_enable(prev)
     assert {"k_kv_append", "k_kv_read"} <= set(names) and any(n.startswith("k_kv_attend") for n in names)
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_k"])
+def test_attention_layer_example(fmt):
+    """Projections, append and attention together: prompts, then captured single-token steps. The
+    bound is the f32 one of the tests above for scores up to S = 60 or so: 2^-19 (4 + S) < 1.3e-4."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.run(fmt, prompts=(90, 33, 5), steps=5, page=32, quiet=True, hidden=512, heads=8, kv_heads=2, dim=64) < 1.3e-4
