@@ -75,15 +75,15 @@ __device__ __forceinline__ void turn1(float& x, float& y, float c, float s) {
     y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
     x = a;
 }
+// a unit's columns of the tables at a position; false: not rotated, or past the tables
 template <int V>
-__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Unit& o, const Rope& r, int pos) {
-    if (o.pair < 0) return;
+__device__ __forceinline__ bool table(const Unit& o, const Rope& r, int pos, float (&c)[V], float (&s)[V]) {
+    if (o.pair < 0) return false;
     if (pos >= r.rows) {
         atomicOr(&g_kv_cache_error, ERR_RANGE);
-        return;
+        return false;
     }
     const long long at = (long long)pos * (r.rotary / 2) + o.pair;
-    float c[V], s[V];
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
         const float4 c4 = *reinterpret_cast<const float4*>(r.cos + at + i);
@@ -91,6 +91,10 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Unit& o
         c[i] = c4.x, c[i + 1] = c4.y, c[i + 2] = c4.z, c[i + 3] = c4.w;
         s[i] = s4.x, s[i + 1] = s4.y, s[i + 2] = s4.z, s[i + 3] = s4.w;
     }
+    return true;
+}
+template <int V>
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Rope& r, const float (&c)[V], const float (&s)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (r.interleaved) {
@@ -135,13 +139,15 @@ __device__ __forceinline__ void rescale_codes(uint8_t* p, float r) {
     }
 }
 
-// grid (blocks, kv heads [+ kv heads for the queries' rotation]).  A CTA of the first kind
-// holds its block's keys and values in registers (D / 4 values a thread), so the rows are read
-// once; the second kind turns the block's rows of one group of query heads, a few rows' loads in
-// flight at a time.
+constexpr int QH = 8;  // query heads of a CTA that rotates queries
+
+// grid (blocks, kv heads [+ eighths of the query heads]).  A CTA of the first kind holds its
+// block's keys and values in registers (D / 4 values a thread), so the rows are read once; the
+// second kind turns the block's rows of up to eight query heads, a few rows' loads in flight at a
+// time.
 template <typename T, int D, int V>
 __global__ void __launch_bounds__(THREADS, D == 256 ? 2 : 4)
-k_kv_append(Cache c, Batch bt, Rows kr, Rows vr, Rows qr, int group, Rope rope, T* __restrict__ q_out) {
+k_kv_append(Cache c, Batch bt, Rows kr, Rows vr, Rows qr, int q_heads, Rope rope, T* __restrict__ q_out) {
     constexpr int O = D / (2 * V), RP = THREADS / O, PASSES = BT > RP ? BT / RP : 1;  // units a row, rows a pass
     __shared__ float part[2][THREADS / 32];
     ptx::grid_dep_wait();
@@ -152,25 +158,48 @@ k_kv_append(Cache c, Batch bt, Rows kr, Rows vr, Rows qr, int group, Rope rope, 
     const Unit o = unit<V>(tid % O, rope);
     if (blockIdx.y >= c.heads) {
         constexpr int B = 16 / V;
-        const int h0 = (blockIdx.y - c.heads) * group, q_heads = c.heads * group;
-        const int rows = (w.i1 - w.i0) * group;
-        for (int r0 = tid / O; r0 < rows; r0 += B * RP) {
-            float a[B][V], b[B][V];
+        const int h0 = (blockIdx.y - c.heads) * QH, group = min(QH, q_heads - h0), tokens = w.i1 - w.i0;
+        const T* q = static_cast<const T*>(qr.data) + (long long)w.row * qr.token_stride + h0 * qr.head_stride;
+        T* to = q_out + ((long long)w.row * q_heads + h0) * D;
+        float ct[V], st[V], a[B][V], b[B][V];
+        if (2 * tokens > RP) {  // a token per thread: its columns of the tables serve all heads
+            for (int i = w.i0 + tid / O; i < w.i1; i += RP) {
+                const bool on = table<V>(o, rope, w.pos0 + i, ct, st);
+                for (int h = 0; h < group; h += B) {
 #pragma unroll
-            for (int u = 0; u < B; ++u) {
-                const int r = min(r0 + u * RP, rows - 1), i = w.i0 + r / group, h = h0 + r % group;
-                const T* src = static_cast<const T*>(qr.data) + (long long)(w.row + i) * qr.token_stride + h * qr.head_stride;
-                load_run<T, V>(src + o.a, a[u]);
-                load_run<T, V>(src + o.b, b[u]);
+                    for (int u = 0; u < B; ++u) {
+                        const T* src = q + i * qr.token_stride + min(h + u, group - 1) * qr.head_stride;
+                        load_run<T, V>(src + o.a, a[u]);
+                        load_run<T, V>(src + o.b, b[u]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < B; ++u) {
+                        if (h + u >= group) break;
+                        if (on) turn<V>(a[u], b[u], rope, ct, st);
+                        T* dst = to + ((long long)i * q_heads + h + u) * D;
+                        store_run<T, V>(dst + o.a, a[u]);
+                        store_run<T, V>(dst + o.b, b[u]);
+                    }
+                }
             }
+        } else {  // few tokens: a row per thread
+            for (int r0 = tid / O; r0 < tokens * group; r0 += B * RP) {
 #pragma unroll
-            for (int u = 0; u < B; ++u) {
-                const int r = r0 + u * RP, i = w.i0 + r / group, h = h0 + r % group;
-                if (r >= rows) break;
-                turn<V>(a[u], b[u], o, rope, w.pos0 + i);
-                T* dst = q_out + ((long long)(w.row + i) * q_heads + h) * D;
-                store_run<T, V>(dst + o.a, a[u]);
-                store_run<T, V>(dst + o.b, b[u]);
+                for (int u = 0; u < B; ++u) {
+                    const int r = min(r0 + u * RP, tokens * group - 1), i = w.i0 + r / group;
+                    const T* src = q + i * qr.token_stride + (r % group) * qr.head_stride;
+                    load_run<T, V>(src + o.a, a[u]);
+                    load_run<T, V>(src + o.b, b[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < B; ++u) {
+                    const int r = r0 + u * RP, i = w.i0 + r / group;
+                    if (r >= tokens * group) break;
+                    if (table<V>(o, rope, w.pos0 + i, ct, st)) turn<V>(a[u], b[u], rope, ct, st);
+                    T* dst = to + ((long long)i * q_heads + r % group) * D;
+                    store_run<T, V>(dst + o.a, a[u]);
+                    store_run<T, V>(dst + o.b, b[u]);
+                }
             }
         }
         return;
@@ -198,7 +227,8 @@ k_kv_append(Cache c, Batch bt, Rows kr, Rows vr, Rows qr, int group, Rope rope, 
 #pragma unroll
     for (int u = 0; u < PASSES; ++u) {
         const int i = u * RP + tid / O;
-        if (i >= w.i0 && i < w.i1) turn<V>(ka[u], kb[u], o, rope, w.pos0 + i);
+        float ct[V], st[V];
+        if (i >= w.i0 && i < w.i1 && table<V>(o, rope, w.pos0 + i, ct, st)) turn<V>(ka[u], kb[u], rope, ct, st);
         mk = fmaxf(mk, fmaxf(amax<V>(ka[u]), amax<V>(kb[u])));
         mv = fmaxf(mv, fmaxf(amax<V>(va[u]), amax<V>(vb[u])));
     }
@@ -289,12 +319,12 @@ unsigned block_grid(const Batch& b) {
 }
 
 template <typename T>
-int append_t(const Cache& c, const Batch& b, const Rows& k, const Rows& v, const Rows& q, int group, const Rope& rope,
+int append_t(const Cache& c, const Batch& b, const Rows& k, const Rows& v, const Rows& q, int q_heads, const Rope& rope,
              void* q_out, cudaStream_t s) {
-    const dim3 grid(block_grid(b), q.data ? 2 * c.heads : c.heads);
+    const dim3 grid(block_grid(b), c.heads + (q.data ? (q_heads + QH - 1) / QH : 0));
     ProfScope ps("k_kv_append", s);
     auto go = [&](auto kernel) {
-        return pdl_status(launch_pdl(kernel, grid, dim3(THREADS), 0, s, c, b, k, v, q, group, rope, static_cast<T*>(q_out)),
+        return pdl_status(launch_pdl(kernel, grid, dim3(THREADS), 0, s, c, b, k, v, q, q_heads, rope, static_cast<T*>(q_out)),
                           "mmq_kv_append");
     };
     constexpr int W = sizeof(T) == 2 ? 8 : 4;
@@ -322,10 +352,9 @@ int read_t(const Cache& c, const Batch& b, void* k_out, void* v_out, cudaStream_
 
 int kv_append_launch(const Cache& c, const Batch& b, int dtype, const Rows& k, const Rows& v, const Rows& q, int q_heads,
                      const Rope& rope, void* q_out, cudaStream_t s) {
-    const int group = q.data ? q_heads / c.heads : 0;
-    return dtype == MMQ_F32    ? append_t<float>(c, b, k, v, q, group, rope, q_out, s)
-           : dtype == MMQ_BF16 ? append_t<__nv_bfloat16>(c, b, k, v, q, group, rope, q_out, s)
-                               : append_t<__half>(c, b, k, v, q, group, rope, q_out, s);
+    return dtype == MMQ_F32    ? append_t<float>(c, b, k, v, q, q_heads, rope, q_out, s)
+           : dtype == MMQ_BF16 ? append_t<__nv_bfloat16>(c, b, k, v, q, q_heads, rope, q_out, s)
+                               : append_t<__half>(c, b, k, v, q, q_heads, rope, q_out, s);
 }
 
 int kv_read_launch(const Cache& c, const Batch& b, int dtype, void* k_out, void* v_out, cudaStream_t s) {
