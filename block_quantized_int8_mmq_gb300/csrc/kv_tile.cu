@@ -659,9 +659,12 @@ k_kv_attend_tile(const Attend a) {
                     ptx::tmem_st_wait();
                     signal(pr);
                     if (lead) {
+                        // the next tile's keys are converted after this one's values: one wait for both
                         const int st = nn % ST, par = (nn / ST) & 1, s2 = (nn + 1) % ST, par2 = ((nn + 1) / ST) & 1;
-                        ok = umma::warp_wait(pr, n_pr & 1, abort, err) && umma::warp_wait(v_full + 8 * st, par, abort, err) &&
-                             (i + 1 == tiles || umma::warp_wait(k_full + 8 * s2, par2, abort, err)) && take_turn();
+                        ok = umma::warp_wait(pr, n_pr & 1, abort, err) &&
+                             (i + 1 == tiles ? umma::warp_wait(v_full + 8 * st, par, abort, err)
+                                             : umma::warp_wait(k_full + 8 * s2, par2, abort, err)) &&
+                             take_turn();
                         if (ok) {
                             ptx::tc_fence_after();
                             issue_o(st, i == 0 || flush, i + 1 == tiles);
