@@ -164,7 +164,7 @@ int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtyp
                    static_cast<uint8_t*>(workspace)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t rows = (int64_t)b.max_new * group;
-    return rows <= kv_stream_rows(c.dim) ? kv_stream_launch(a, (int)rows, s) : kv_tile_launch(a, s);
+    return rows <= kv_stream_rows(c.dim, dtype) ? kv_stream_launch(a, (int)rows, s) : kv_tile_launch(a, s);
 }
 
 }  // extern "C"

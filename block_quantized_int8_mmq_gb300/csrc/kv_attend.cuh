@@ -158,9 +158,9 @@ __device__ __forceinline__ int scan_cta(int v, int& total, int* scratch) {
 }
 
 }  // namespace kv
-// The two kernels: up to kv_stream_rows(dim) query rows per sequence and head (kv_stream.cu), any
+// The two kernels: up to kv_stream_rows(dim, dtype) query rows per sequence and head (kv_stream.cu), any
 // number (kv_tile.cu).
-int kv_stream_rows(int dim);
+int kv_stream_rows(int dim, int dtype);
 int kv_stream_launch(const kv::Attend& a, int rows, cudaStream_t s);
 int kv_tile_launch(const kv::Attend& a, cudaStream_t s);
 

@@ -2,7 +2,8 @@
 // over the 8-bit cache: k_kv_attend_stream.
 //
 // Bound: HBM.  Every record in reach is read once (64 D + 16 bytes per 32 tokens and head) and
-// used for all of the head's query rows, up to 8 NT of them.  A warp is a worker (kv_attend.cuh)
+// used for 8 NT of the head's query rows; more rows are units of their own, next to each other in the
+// list of work, so that they read the records from the L2.  A warp is a worker (kv_attend.cuh)
 // with a ring of its own: one bulk copy per record, S records in flight, no barrier but its own;
 // the ring runs on over the ends of heads and sequences, so short sequences stream like long
 // ones.  Codes go from shared memory to f16 MMA operands exactly (|c| <= 127), tokens on the
@@ -28,11 +29,16 @@ template <int D, int NT>
 struct Stream {
     // as many warps as shared memory holds rings of two records for (dim 64: four), and registers
     // for two tiles of rows: a block is a chain of dependent steps, and only other warps fill its gaps
-    static constexpr int WARPS = D == 256 ? 6 : NT == 2 ? 8 : 12, THREADS = WARPS * 32;
-    static constexpr int STAGES = D == 64 ? 4 : D == 128 && NT == 2 ? 3 : 2;
+    static constexpr int WARPS = D == 256 ? 6 : NT > 1 ? 8 : 12, THREADS = WARPS * 32;
+    static constexpr int STAGES = D == 64 ? 4 : D == 128 && NT > 1 ? 3 : 2;
     static constexpr int ROWS = 8 * NT, REC = rec_bytes(D);
     static constexpr int RING = WARPS * STAGES * REC, SMEM = RING + WARPS * STAGES * 8;
-    static_assert(ROWS * (D + 2) * 4 <= STAGES * REC && ROWS * D + WARPS * ROWS * (D + 2) <= WS_ROWS * D, "room for a warp's partial results");
+    // a kept result: rows of O, then m and l.  16-byte piece i of the values that lane group g holds of a row
+    // is at 8 i + g, and two rows are 8 floats past a multiple of 32 apart: stores and loads without conflicts
+    static constexpr int KD = D + 4, KEPT = ROWS * (KD + 2);
+    static constexpr int RUN = D < 128 ? D / 8 : 16;  // consecutive values of O that a lane group holds
+    static __device__ __forceinline__ int column(int piece) { return 128 * (piece / 32) + RUN * (piece % 8) + piece % 32 / 8 * 4; }
+    static_assert(KEPT * 4 <= STAGES * REC && ROWS * D + WARPS * KEPT <= WS_ROWS * D, "room for a warp's partial results");
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -47,46 +53,64 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(v));
     return o;
 }
-// Where a warp keeps an incomplete unit's result, O [ROWS][D], m [ROWS], l [ROWS]: at the beginning of its
+// Where a warp keeps an incomplete unit's result: at the beginning of its
 // ring, or (ring: nullptr) in a place of its own in the CTA's first slot of the workspace, behind the
 // rows that the CTA's own partial result takes there.
-template <int D, int ROWS>
-struct KeptAt {
-    static __device__ __forceinline__ float* at(uint8_t* ring, const Attend& a, int warp) {
-        return ring ? reinterpret_cast<float*>(ring) : part_slot(a, blockIdx.x, 0) + ROWS * D + warp * ROWS * (D + 2);
-    }
-};
+template <class C, int D>
+__device__ __forceinline__ float* kept_at(uint8_t* ring, const Attend& a, int warp) {
+    return ring ? reinterpret_cast<float*>(ring) : part_slot(a, blockIdx.x, 0) + C::ROWS * D + warp * C::KEPT;
+}
 
-// A sequence as the units see it
+// Adds parts c .. c + B - 1, c1 at most, of the unit whose first part is CTA c0's, all of them in flight.
+template <int B, int D>
+__device__ __forceinline__ void add_parts(const Attend& a, Joined& j, int r, int piece, int c, int c0, int c1) {
+    float4 x[B];
+    float m[B], l[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+        const float* ps = part_slot(a, min(c + k, c1), min(c + k, c1) == c0);
+        x[k] = __ldcg(reinterpret_cast<const float4*>(ps + r * D + 4 * piece));
+        m[k] = __ldcg(ps + WS_ROWS * D + r);
+        l[k] = __ldcg(ps + WS_ROWS * (D + 1) + r);
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+        if (c + k <= c1) j.add(x[k], m[k], l[k]);
+}
+
+// A sequence as the units see it: heads * groups units, unit h of head h / groups and rows
+// (h % groups) * ROWS ..
 struct Seq {
-    int start, n, len, lo_blk, tiles;  // tiles: records in reach, or 1 for a sequence of padding rows; 0: none
+    int start, n, len, lo_blk, groups, tiles;  // tiles: records in reach, or 1 for a sequence of padding rows; 0: none
 };
+template <int ROWS>
 __device__ __forceinline__ Seq load_seq(const Attend& a, int b) {
     Seq s;
     seq_range(a.c, a.bt, b, s.start, s.n, s.len, &g_kv_stream_error);
     s.lo_blk = s.len > 0 ? first_key(a, s.len - s.n) / BT : 0;
     s.tiles = s.n == 0 ? 0 : max(1, (s.len + BT - 1) / BT - s.lo_blk);
+    s.groups = a.bt.max_new * a.group <= ROWS ? 1 : max(1, (s.n * a.group + ROWS - 1) / ROWS);
     return s;
 }
-// the unit after (b, h): the next head, or the first of the next sequence that has rows
+// the unit after (b, h): the sequence's next, or the first of the next sequence that has rows
+template <int ROWS>
 __device__ __forceinline__ void next_unit(const Attend& a, int& b, int& h, Seq& s) {
-    if (++h < a.c.heads) return;
+    if (++h < a.c.heads * s.groups) return;
     h = 0;
     do ++b;
-    while (b < a.bt.seqs && (s = load_seq(a, b)).tiles == 0);
+    while (b < a.bt.seqs && (s = load_seq<ROWS>(a, b)).tiles == 0);
 }
 
 template <int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(Stream<D, NT>::THREADS, 1)
 k_kv_attend_stream(const Attend a) {
     using C = Stream<D, NT>;
-    using Kept = KeptAt<D, C::ROWS>;
     constexpr int KS = D / 16;  // k steps of the first product, row tiles of the second
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_scan[C::WARPS], s_b[C::WARPS], s_off[C::WARPS], s_x[C::WARPS + 1], s_abort;
     __shared__ int s_out[2], s_first[2], s_final[2];  // the unit that came in, the one that goes out: slot, its CTAs
     // the incomplete units of the CTA in work order, two slots per warp (the second: its range's end)
-    __shared__ int s_unit[2 * C::WARPS], s_end[2 * C::WARPS], s_head[2 * C::WARPS];
+    __shared__ int s_unit[2 * C::WARPS], s_end[2 * C::WARPS], s_head[2 * C::WARPS], s_row[2 * C::WARPS];
     __shared__ Seq s_sq[2 * C::WARPS];
     // its parts in work order, and where in them and in the slots each unit begins
     __shared__ const float* s_part[2 * C::WARPS];
@@ -103,14 +127,18 @@ k_kv_attend_stream(const Attend a) {
 
     // ---- this warp's range of the work
     const int seqs = a.bt.seqs;
-    const int v0 = tid < seqs ? load_seq(a, tid).tiles * a.c.heads : 0;
+    auto places = [&](int i) {
+        const Seq s = load_seq<C::ROWS>(a, i);
+        return s.tiles * s.groups * a.c.heads;
+    };
+    const int v0 = tid < seqs ? places(tid) : 0;
     int total;
     const int e0 = scan_cta<C::WARPS>(v0, total, s_scan);
     const int total0 = total;
     int T = total;
     for (int base = C::THREADS; base < seqs; base += C::THREADS) {
         const int i = base + tid;
-        scan_cta<C::WARPS>(i < seqs ? load_seq(a, i).tiles * a.c.heads : 0, total, s_scan);
+        scan_cta<C::WARPS>(i < seqs ? places(i) : 0, total, s_scan);
         T += total;
     }
     const int W = min((int)gridDim.x * C::WARPS, T), w0 = blockIdx.x * C::WARPS;
@@ -122,7 +150,7 @@ k_kv_attend_stream(const Attend a) {
         int v = v0, e = e0;
         total = total0;
         if (base > 0) {
-            v = i < seqs ? load_seq(a, i).tiles * a.c.heads : 0;
+            v = i < seqs ? places(i) : 0;
             e = carry + scan_cta<C::WARPS>(v, total, s_scan);
         }
         carry += total;
@@ -139,7 +167,7 @@ k_kv_attend_stream(const Attend a) {
     if (w0 + wid < W) {
         const int x0 = s_x[wid], x1 = s_x[wid + 1];
         int b = s_b[wid];
-        Seq sq = load_seq(a, b);
+        Seq sq = load_seq<C::ROWS>(a, b);
         int h = s_off[wid] / sq.tiles, o = s_off[wid] - h * sq.tiles;
         // the fetching side runs STAGES records ahead; within a page it only steps to the next record
         int fb = b, fh = h, fo = o, fx = x0, left = 0, pg = 0, tab0 = 0, tabn = 0, tab = -1;
@@ -161,7 +189,7 @@ k_kv_attend_stream(const Attend a) {
                     const int id = __shfl_sync(0xffffffffu, tab, pg - tab0);
                     src = nullptr;
                     if (id >= 0 && id < a.c.pages)
-                        src = a.c.data + (((long long)id * a.c.heads + fh) * a.c.blocks + in) * C::REC;
+                        src = a.c.data + (((long long)id * a.c.heads + fh / fs.groups) * a.c.blocks + in) * C::REC;
                     else if (lane == 0)
                         atomicOr(&g_kv_stream_error, ERR_RANGE);
                 }
@@ -178,7 +206,7 @@ k_kv_attend_stream(const Attend a) {
             ++fx;
             if (++fo == fs.tiles) {
                 const int was = fb;
-                next_unit(a, fb, fh, fs);
+                next_unit<C::ROWS>(a, fb, fh, fs);
                 fo = left = 0;
                 if (fb != was) tabn = 0;
             }
@@ -186,6 +214,7 @@ k_kv_attend_stream(const Attend a) {
         uint32_t qf[SPLIT ? 2 : 1][NT][KS][2];
         float acc[KS][NT][4], m[NT][2], l[NT][2], fq[NT][2];
         int hi[NT][2], lo[NT][2], hi_min = 0, lo_max = 0, o_from = 0;
+        int head = 0, row0 = 0;  // of the unit
         bool fresh = true, ok = true;
         int st = 0;
 #pragma unroll 1
@@ -193,6 +222,8 @@ k_kv_attend_stream(const Attend a) {
             if (fresh) {  // a new unit: its queries as B operands, its rows' limits
                 fresh = false;
                 o_from = o;
+                head = h / sq.groups;
+                row0 = (h - head * sq.groups) * C::ROWS;
                 const int rows = sq.n * a.group, first = sq.len - sq.n;
                 hi_min = 0x7fffffff;
                 lo_max = 0;
@@ -201,9 +232,9 @@ k_kv_attend_stream(const Attend a) {
                 uint4 raw[NT][D / 64][SPLIT ? 4 : 2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int r = 8 * nt + g, t = r / a.group;
+                    const int r = row0 + 8 * nt + g, t = r / a.group;
                     const uint8_t* src = static_cast<const uint8_t*>(a.q.data) +
-                                         ((sq.start + t) * a.q.token_stride + (h * a.group + r - t * a.group) * a.q.head_stride +
+                                         ((sq.start + t) * a.q.token_stride + (head * a.group + r - t * a.group) * a.q.head_stride +
                                           16 * tq) * (SPLIT ? 4 : 2);
 #pragma unroll
                     for (int sg = 0; sg < D / 64; ++sg)
@@ -247,7 +278,7 @@ k_kv_attend_stream(const Attend a) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {  // this lane's columns of S^T and O^T: rows 2 tq, 2 tq + 1
                         fq[nt][c] = __shfl_sync(0xffffffffu, up, 4 * (2 * tq + c)) * a.scale2;
-                        const int rc = 8 * nt + 2 * tq + c, pos = first + rc / a.group;
+                        const int rc = row0 + 8 * nt + 2 * tq + c, pos = first + rc / a.group;
                         hi[nt][c] = rc < rows ? pos + 1 : 0x7fffffff;
                         lo[nt][c] = rc < rows && a.window > 0 ? max(0, pos - a.window + 1) : 0;
                         hi_min = min(hi_min, hi[nt][c]);
@@ -415,7 +446,7 @@ k_kv_attend_stream(const Attend a) {
                 const bool whole = o_from == 0 && o == sq.tiles;
                 // incomplete: kept in the ring if the range ends (nothing is in flight any more), else, a
                 // unit that came in and ends here, in the warp's rows of the workspace
-                float* kept = Kept::at(x + 1 == x1 ? ring : nullptr, a, wid);
+                float* kept = kept_at<C, D>(x + 1 == x1 ? ring : nullptr, a, wid);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -423,11 +454,11 @@ k_kv_attend_stream(const Attend a) {
                         float sum = l[nt][c];
 #pragma unroll
                         for (int off = 4; off <= 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                        const int r = 8 * nt + 2 * tq + c;
-                        constexpr int RUN = D < 128 ? D / 8 : 16, RUNS = D / (8 * RUN);
+                        const int r = 8 * nt + 2 * tq + c, rs = row0 + r;  // in the unit, in the sequence
+                        constexpr int RUN = C::RUN, RUNS = D / (8 * RUN);
                         const float inv = whole ? (sum > 0.f ? __frcp_rn(sum) : 0.f) : 1.f;
-                        const int t = r / a.group, hq = h * a.group + r - t * a.group;
-                        if (whole && r >= rows) continue;
+                        const int t = rs / a.group, hq = head * a.group + rs - t * a.group;
+                        if (rs >= rows) continue;
 #pragma unroll
                         for (int hh = 0; hh < RUNS; ++hh)
 #pragma unroll
@@ -438,14 +469,14 @@ k_kv_attend_stream(const Attend a) {
                                 if (whole)
                                     store_out4(a, sq.start + t, hq, col, v);
                                 else
-                                    *reinterpret_cast<float4*>(kept + r * D + col) = v;
+                                    *reinterpret_cast<float4*>(kept + r * C::KD + 128 * hh + 32 * i + 4 * g) = v;
                             }
                         if (g == 0) {
                             if (whole) {
                                 store_lse(a, sq.start + t, hq, m[nt][c], sum);
                             } else {
-                                kept[C::ROWS * D + r] = m[nt][c];
-                                kept[C::ROWS * (D + 1) + r] = sum;
+                                kept[C::ROWS * C::KD + r] = m[nt][c];
+                                kept[C::ROWS * (C::KD + 1) + r] = sum;
                             }
                         }
                     }
@@ -454,10 +485,11 @@ k_kv_attend_stream(const Attend a) {
                     s_unit[i] = ustart;
                     s_end[i] = uend;
                     s_sq[i] = sq;
-                    s_head[i] = h;
+                    s_head[i] = head;
+                    s_row[i] = row0;
                 }
                 if (o == sq.tiles && x + 1 < x1) {
-                    next_unit(a, b, h, sq);
+                    next_unit<C::ROWS>(a, b, h, sq);
                     o = 0;
                     fresh = true;
                 }
@@ -478,7 +510,7 @@ k_kv_attend_stream(const Attend a) {
         const bool first = u >= 0 && (before == 0 || prev != u);
         const unsigned starts = __ballot_sync(0xffffffffu, first);
         const int j = __popc(before);
-        if (u >= 0) s_part[j] = Kept::at(lane & 1 ? smem + (lane >> 1) * C::STAGES * C::REC : nullptr, a, lane >> 1);
+        if (u >= 0) s_part[j] = kept_at<C, D>(lane & 1 ? smem + (lane >> 1) * C::STAGES * C::REC : nullptr, a, lane >> 1);
         if (first) {
             const int run = __popc(starts & ((1u << lane) - 1));
             s_slot[run] = lane;
@@ -492,43 +524,52 @@ k_kv_attend_stream(const Attend a) {
     }
     __syncthreads();
     const int cta0 = s_x[0], cta1 = s_x[min(W - w0, C::WARPS)];
-    const int runs = s_runs, each = a.bt.max_new * a.group * (D / 4), side_by_side = max(1, C::THREADS / each);
-    for (int run = tid / each; run < runs; run += side_by_side)
-        for (int x = tid - tid / each * each; x < each; x += C::THREADS) {
-            if (tid >= side_by_side * each && each < C::THREADS) break;
-            const int r = x / (D / 4), col = 4 * (x % (D / 4)), i = s_slot[run], u = s_unit[i], p0 = s_run[run], p1 = s_run[run + 1];
-            const Seq& sq = s_sq[i];
-            if (r >= sq.n * a.group) continue;
-            float M = M_NONE, L = 0.f;
-#pragma unroll 4
-            for (int p = p0; p < p1; ++p) M = fmaxf(M, s_part[p][C::ROWS * D + r]);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int p = p0; p < p1; ++p) {
-                const float* k = s_part[p];
-                const float f = exp2_approx(k[C::ROWS * D + r] - M);
-                const float4 y = *reinterpret_cast<const float4*>(k + r * D + col);
-                L += f * k[C::ROWS * (D + 1) + r];
-                v = make_float4(v.x + y.x * f, v.y + y.y * f, v.z + y.z * f, v.w + y.w * f);
+    const int each = min(C::ROWS, a.bt.max_new * a.group) * (D / 4), items = s_runs * each;
+    // a unit's last part may be the one in the workspace: three of them at a time are on their way
+    constexpr int U = 3;
+    for (int base = tid; base < items; base += U * C::THREADS) {
+        float4 y[U];
+        float my[U], ly[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int idx = base + k * C::THREADS, run = idx / each, x = idx - run * each, r = x / (D / 4);
+            if (idx >= items) break;
+            const float* part = s_part[s_run[run + 1] - 1];
+            y[k] = *reinterpret_cast<const float4*>(part + r * C::KD + 4 * (x % (D / 4)));
+            my[k] = part[C::ROWS * C::KD + r];
+            ly[k] = part[C::ROWS * (C::KD + 1) + r];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int idx = base + k * C::THREADS, run = idx / each, x = idx - run * each, r = x / (D / 4), piece = x % (D / 4);
+            if (idx >= items) break;
+            const int i = s_slot[run], u = s_unit[i], rs = s_row[i] + r;
+            if (rs >= s_sq[i].n * a.group) continue;
+            Joined j;
+            j.add(y[k], my[k], ly[k]);
+#pragma unroll 1
+            for (int p = s_run[run]; p < s_run[run + 1] - 1; ++p) {
+                const float* part = s_part[p];
+                j.add(*reinterpret_cast<const float4*>(part + r * C::KD + 4 * piece), part[C::ROWS * C::KD + r],
+                      part[C::ROWS * (C::KD + 1) + r]);
             }
             if (u >= cta0 && s_end[i] <= cta1) {
-                const float inv = L > 0.f ? __frcp_rn(L) : 0.f;
-                const int t = r / a.group, hq = s_head[i] * a.group + r - t * a.group;
-                store_out4(a, sq.start + t, hq, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                if (col == 0) store_lse(a, sq.start + t, hq, M, L);
+                const int t = rs / a.group, hq = s_head[i] * a.group + rs - t * a.group;
+                store_out4(a, s_sq[i].start + t, hq, C::column(piece), j.out());
+                if (piece == 0) store_lse(a, s_sq[i].start + t, hq, j.m, j.l);
             } else {
                 const int side = u >= cta0 ? 1 : 0;
                 float* part = part_slot(a, blockIdx.x, side);
-                *reinterpret_cast<float4*>(part + r * D + col) = v;
-                if (col == 0) {
-                    part[WS_ROWS * D + r] = M;
-                    part[WS_ROWS * (D + 1) + r] = L;
+                *reinterpret_cast<float4*>(part + r * D + 4 * piece) = j.o;
+                if (piece == 0) {
+                    part[WS_ROWS * D + r] = j.m;
+                    part[WS_ROWS * (D + 1) + r] = j.l;
                     s_out[side] = i;
                 }
             }
         }
-    __threadfence();
-    __syncthreads();
+    }
+    __syncthreads();  // with the fence of the thread that counts below, the CTA's parts are there first
     // ---- the units that other CTAs have parts of: the last to arrive joins them, in CTA order
     if (tid < 2 && s_out[tid] >= 0) {
         const int u = s_unit[s_out[tid]], c0 = work_owner(T, u, W) / C::WARPS,
@@ -548,26 +589,17 @@ k_kv_attend_stream(const Attend a) {
     for (int side = 0; side < 2; ++side) {
         if (s_out[side] < 0) continue;
         const Seq& sq = s_sq[s_out[side]];
-        const int rows = sq.n * a.group, c0 = s_first[side], c1 = s_final[side];
+        const int row0 = s_row[s_out[side]], rows = min(C::ROWS, sq.n * a.group - row0), c0 = s_first[side], c1 = s_final[side];
         for (int idx = tid; idx < rows * (D / 4); idx += C::THREADS) {
-            const int r = idx / (D / 4), col = 4 * (idx % (D / 4));
+            const int r = idx / (D / 4), piece = idx % (D / 4), col = C::column(piece);
             Joined j;
-            constexpr int B = 8;  // parts in flight
-            for (int c = c0; c <= c1; c += B) {
-                float4 x[B];
-                float m[B], l[B];
-#pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    const float* ps = part_slot(a, min(c + k, c1), min(c + k, c1) == c0);
-                    x[k] = __ldcg(reinterpret_cast<const float4*>(ps + r * D + col));
-                    m[k] = __ldcg(ps + WS_ROWS * D + r);
-                    l[k] = __ldcg(ps + WS_ROWS * (D + 1) + r);
-                }
-#pragma unroll
-                for (int k = 0; k < B; ++k)
-                    if (c + k <= c1) j.add(x[k], m[k], l[k]);
-            }
-            const int t = r / a.group, hq = s_head[s_out[side]] * a.group + r - t * a.group;
+            // (code that runs once costs its own fetching: two parts are not worth the steps of eight)
+            for (int c = c0; c <= c1; c += 8)
+                if (c1 - c < 4)
+                    add_parts<4, D>(a, j, r, piece, c, c0, c1);
+                else
+                    add_parts<8, D>(a, j, r, piece, c, c0, c1);
+            const int rs = row0 + r, t = rs / a.group, hq = s_head[s_out[side]] * a.group + rs - t * a.group;
             store_out4(a, sq.start + t, hq, col, j.out());
             if (col == 0) store_lse(a, sq.start + t, hq, j.m, j.l);
         }
@@ -586,24 +618,51 @@ int launch(const Attend& a, cudaStream_t s) {
         return st;
     }
     // no more warps than records can be in reach
-    const long long most = (long long)a.bt.seqs * a.c.heads * a.bt.table_pages * a.c.blocks;
+    const long long groups = ((long long)a.bt.max_new * a.group + C::ROWS - 1) / C::ROWS;
+    const long long most = (long long)a.bt.seqs * a.c.heads * a.bt.table_pages * a.c.blocks * groups;
+    if (most > 0x7fffffff) {
+        report(fn, MMQ_ERR_SHAPE, "seqs * heads * table_pages * page / 32 * rows / 8 must be below 2^31");
+        return MMQ_ERR_SHAPE;
+    }
     const long long ctas = (most + C::WARPS - 1) / C::WARPS, sms = device_shape().sms < 341 ? device_shape().sms : 341;
     const dim3 grid((unsigned)(ctas < 1 ? 1 : ctas < sms ? ctas : sms));
     ProfScope ps("k_kv_attend_stream", s);
     return pdl_status(launch_pdl(&k_kv_attend_stream<D, NT, SPLIT>, grid, dim3(C::THREADS), C::SMEM, s, a), fn);
 }
 
+// Rows a unit holds: as many as its warps' registers do.
 template <bool SPLIT>
 int launch_rows(const Attend& a, int rows, cudaStream_t s) {
-    if (a.c.dim == 64) return rows <= 8 ? launch<64, 1, SPLIT>(a, s) : launch<64, 2, SPLIT>(a, s);
-    if (a.c.dim == 128) return rows <= 8 ? launch<128, 1, SPLIT>(a, s) : launch<128, 2, SPLIT>(a, s);
-    return launch<256, 1, SPLIT>(a, s);
+    if (a.c.dim == 256) return launch<256, 1, SPLIT>(a, s);
+    if (a.c.dim == 64)
+        return rows <= 8 ? launch<64, 1, SPLIT>(a, s) : rows <= 16 ? launch<64, 2, SPLIT>(a, s) : launch<64, 3, SPLIT>(a, s);
+    if (rows <= 8) return launch<128, 1, SPLIT>(a, s);
+    return SPLIT || rows <= 16 ? launch<128, 2, SPLIT>(a, s) : launch<128, SPLIT ? 2 : 3, SPLIT>(a, s);
 }
 
 }  // namespace
 
-// The most query rows of one sequence and head that the stream takes.
-int kv_stream_rows(int dim) { return dim == 256 ? 8 : 16; }
+// The most query rows of one sequence and head, by the longest sequence, that go to the stream: past it the
+// tiles' time, which hardly changes from 8 to 128 rows, is shorter.  Measured, stream / tiles in us, 8 heads,
+// as sequences x tokens, all sequences with the same rows:
+//                      50 x 150      8 x 2000     200 x 200     1 x 65536    50 x 12000
+//   128, 16-bit, 24   31.7 / 40.9   28.3 / 40.3   84.5 / 144   56.3 / 88      322 / 612
+//                48   48.1 / 42.4   42.1 / 41.5    123 / 145   86.7 / 94      618 / 614
+//                64   50.0 / 42.5   49.0 / 41.4                 120 / 93      912 / 614
+//   128, f32,    48   40.8 / 54.1   41.9 / 55.0    113 / 252    110 / 153     842 / 1112
+//                64   49.1 / 55.3   49.0 / 55.3                 137 / 152    1112 / 1114
+//    64, 16-bit, 48   31.1 / 34.6   30.1 / 33.1   74.2 / 108   59.4 / 70      428 / 481
+//                64   33.2 / 34.5   35.1 / 33.1                81.2 / 69      633 / 481
+//   256, 16-bit, 16   39.0 / 44.0   37.9 / 43.6   99.7 / 184   94.0 / 121     754 / 906
+//                24   46.5 / 45.1   47.1 / 43.9    131 / 191    131 / 122    1111 / 909
+//   256, f32,    32   57.7 / 67.3   67.6 / 79.0    188 / 299    204 / 245    1720 / 2010
+//                48   72.1 / 72.2   92.9 / 82.6    271 / 320    297 / 254    2536 / 2015
+// Where most sequences have fewer rows than the longest one the stream gains, the tiles do not: 8 sequences
+// of 517 to 3001 tokens with 14 to 35 rows of 128 take 30.1 us there, 32.2 in the tiles.
+int kv_stream_rows(int dim, int dtype) {
+    if (dim == 256) return dtype == MMQ_F32 ? 32 : 16;
+    return 48;
+}
 
 int kv_stream_launch(const Attend& a, int rows, cudaStream_t s) {
     return a.dtype == MMQ_F32 ? launch_rows<true>(a, rows, s) : launch_rows<false>(a, rows, s);

@@ -265,6 +265,17 @@ def test_attend_few_rows(dtype, news, window):
     check_attend(Case(13, [90, 300, 77, 129], news, 8, 2, 128, 64, dtype), window=window)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news,group", [([4, 0, 1, 3], 4), ([3, 3, 2, 1], 7), ([6, 1, 5, 0], 4), ([12, 0, 7, 9], 4),
+                                        ([48, 17, 1, 25], 1), ([2, 1, 2, 2], 24)])
+@pytest.mark.parametrize("window", [0, 45])
+def test_attend_row_groups(dtype, dim, news, group, window):
+    """Sequences whose 9 to 48 rows are several units of the same records, beside some with one."""
+    c = Case(dim + group, [90, 700, 77, 129], news, 2 * group, 2, dim, 64, dtype, pad_rows=1)
+    check_attend(c, window=window)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 1 << 30, 1 << 40])
 def test_attend_window(dtype, window):
