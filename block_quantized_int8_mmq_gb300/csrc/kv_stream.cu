@@ -569,21 +569,20 @@ k_kv_attend_stream(const Attend a) {
             }
         }
     }
-    __syncthreads();  // with the fence of the thread that counts below, the CTA's parts are there first
+    __syncthreads();  // with the release of the thread that counts below, the CTA's parts are there first
     // ---- the units that other CTAs have parts of: the last to arrive joins them, in CTA order
     if (tid < 2 && s_out[tid] >= 0) {
         const int u = s_unit[s_out[tid]], c0 = work_owner(T, u, W) / C::WARPS,
                   c1 = work_owner(T, s_end[s_out[tid]] - 1, W) / C::WARPS;
         unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0;
-        __threadfence();
-        if (atomicAdd(counter, 1u) == (unsigned)(c1 - c0)) {
+        // one step for the parts of this CTA before and those of the others behind it
+        if (ptx::atom_inc_acq_rel(counter) == (unsigned)(c1 - c0)) {
             *counter = 0;
             s_first[tid] = c0;
             s_final[tid] = c1;
         } else {
             s_out[tid] = -1;
         }
-        __threadfence();
     }
     __syncthreads();
     for (int side = 0; side < 2; ++side) {

@@ -725,19 +725,17 @@ k_kv_attend_tile(const Attend a) {
                     for (int level = 0;; ++level) {
                         const int all = (c1 - c0 + step) / step, begin = at / JOIN * JOIN, count = min(JOIN, all - begin);
                         const int first = c0 + begin * step;
-                        __threadfence();
-                        signal(pr);
+                        signal(pr);  // with the counter's release and acquire: the rows' parts are there first
                         if (lead) {
                             ok = umma::warp_wait(pr, n_pr & 1, abort, err);
                             if (lane == 0) {
                                 unsigned* counter = reinterpret_cast<unsigned*>(a.ws) +
                                                     ((level * (int)gridDim.x + first) * 2 + (first == c0)) * 2 + gt;
                                 s_last[gt] = 0;
-                                if (ok && atomicAdd(counter, 1u) == (unsigned)(count - 1)) {
+                                if (ok && ptx::atom_inc_acq_rel(counter) == (unsigned)(count - 1)) {
                                     *counter = 0;
                                     s_last[gt] = 1;
                                 }
-                                __threadfence();
                                 ptx::mbar_arrive(jn);
                             }
                         }

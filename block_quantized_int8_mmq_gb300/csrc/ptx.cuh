@@ -103,6 +103,15 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ------------------------------------------------------------------ counters
+// Adds one and returns what was there; releases what this thread has seen (the CTA's writes, after a barrier) and
+// acquires what the threads that counted before have released.
+__device__ __forceinline__ uint32_t atom_inc_acq_rel(unsigned* p) {
+    uint32_t v;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // ------------------------------------------------------------------ one thread of a warp
 // True in one lane, always the same, of a converged warp.  Single-thread instructions whose operands
 // are warp-uniform issue from uniform registers inside such a branch; behind a lane comparison every
