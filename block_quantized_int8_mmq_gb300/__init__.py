@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmmq.so")
@@ -265,7 +266,11 @@ def mmq_last_path() -> int:
 
 
 def mmq_get_device_error(stream=None) -> int:
-    return int(_lib.mmq_get_device_error(_stream(stream)))
+    st = int(_lib.mmq_get_device_error(_stream(stream)))
+    kv = sys.modules.get(__name__ + ".kv")
+    if st == -7 and kv is not None:  # MMQ_ERR_TIMEOUT
+        kv._clean_workspaces()
+    return st
 
 
 def mmq_gemm_q5_k(xq, wq, M, N, K, out=None, stream=None):

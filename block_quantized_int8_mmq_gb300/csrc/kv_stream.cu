@@ -15,6 +15,13 @@
 // registers, scaled per row by a power of two into f16's range: one f16 term for bf16 and f16
 // rows (exact but for bits 2^-25 below the row's largest), two for f32 rows (SPLIT), whose
 // weights are split into two f16 terms as well.
+//
+// Measured (GB300): 64 sequences of 1000 to 8191 tokens, 4 rows a head, 614 MB of records: 108 us,
+// 5.7 TB/s, 0.84 of the copy rate, with an issue slot used in 0.45 of the cycles and the tensor pipe in
+// 0.14.  One sequence of 131069 tokens, 135 MB: 36 us; a CTA's prologue (lengths, first table entries,
+// first records: three dependent trips to memory), its parts' join and the CTAs' are about 15 us of any
+// call, and one of 777 tokens takes 12.2 us.  Past 8 rows the warps' instructions bound it: a record
+// takes a warp 2.6 us at 24 rows of 128 where eight share an SM.
 #include "kv_attend.cuh"
 #include "umma.cuh"
 

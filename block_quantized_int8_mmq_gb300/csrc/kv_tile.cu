@@ -5,18 +5,26 @@
 // tiles of 128 rows; a row is a (token, query head) pair of one key/value head's group, so that
 // the heads that share keys fill a tile together and a tile of keys and values, once converted,
 // serves MT * 128 rows.  Roles:
-//   converter warps (4)  records from global memory to registers one tile ahead, codes to exact
-//                        f16 in shared memory, in the core-matrix order of tcgen05 (8 x 16
+//   converter warps (4)  records by bulk copies into a staging of their own, one tile ahead; codes to
+//                        exact f16 in shared memory, in the core-matrix order of tcgen05 (8 x 16
 //                        bytes): keys as the K-major B operand of S = Q K^T, values in the same
 //                        physical order as the MN-major B operand of O += P V (no transpose);
 //   softmax warps (4 per row tile), a thread per row: S from TMEM, the running maximum, P as f16
 //                        back into S's own columns as the A operand of the second product, the
 //                        (rare) rescaling of O in TMEM, and at the end of a unit its output;
-//   one thread of each row tile's first warp issues that tile's MMAs: the two row tiles
+//   one elected thread of each row tile's first warp issues that tile's MMAs: the two row tiles
 //                        alternate, one's products run while the other's softmax does.
 // S of a tile and its P share columns: the products of one row tile run in issue order, and a
 // row's thread has read its S before it writes its P.  f32 rows (SPLIT): queries and weights as
 // two f16 terms each, twice the products.
+//
+// Measured (GB300): 1024 new of 32768 tokens, 32 heads of 128 over 8: 472 us, 1.15 PFLOP/s, 0.60 of
+// the library's rate for a plain product; tensor pipe 0.47 of the cycles, issue slots 0.45.  Two row tiles of
+// 128 x 128 keys take 4000 to 4300 cycles, 1024 of them the products' own at the tensor rate: the
+// products' operands, the staged codes and the converted tiles move 320 KB through shared memory (2560
+// cycles), and S, maximum, weights and P are a chain that the other tile's products cover in part.  Short
+// prompts pay a unit's ends (queries to f16 tiles, an empty pipeline, its output) and the join of the
+// parts: 2048 tokens, 28 heads over 4, 70 us where the same work inside a long one would be 26.
 #include "kv_attend.cuh"
 #include "umma.cuh"
 

@@ -247,20 +247,27 @@ _workspaces: dict = {}
 
 
 def _workspace(cache, stream):
-    """The package's own workspace of a stream: calls on one stream run one after another."""
+    """The package's own workspace of a stream: calls on one stream run one after another.  A capture
+    on a stream that has none yet gets one of the graph's memory, zeroed in the graph."""
     s = torch._C._cuda_getCurrentRawStream(cache.device.index) if stream is None else int(_stream(stream).value or 0)
     key = (cache.device.index, s, cache.dim)
     ws = _workspaces.get(key)
     if ws is None:
-        ws = torch.empty(mmq_kv_workspace_bytes(cache.dim), dtype=torch.uint8, device=cache.device)
-        if stream is not None:
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                   else torch.cuda.ExternalStream(s, device=cache.device)):
-                ws[:_WS_ZERO].zero_()
-        else:
+        with torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream)
+                               else torch.cuda.ExternalStream(s, device=cache.device)):
+            ws = torch.empty(mmq_kv_workspace_bytes(cache.dim), dtype=torch.uint8, device=cache.device)
             ws[:_WS_ZERO].zero_()
-        _workspaces[key] = ws
+            if not torch.cuda.is_current_stream_capturing():
+                _workspaces[key] = ws
     return ws
+
+
+def _clean_workspaces():
+    """A call that gave up may have left counts in its workspace."""
+    torch.cuda.synchronize()
+    for ws in _workspaces.values():
+        ws[:_WS_ZERO].zero_()
+    torch.cuda.synchronize()
 
 
 def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=None, workspace=None, stream=None):

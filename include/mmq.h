@@ -497,8 +497,9 @@ size_t mmq_kv_block_bytes(int64_t dim);
  * Bit-exact by that definition.  Rows of the record past the sequence's end keep their bytes;
  * padding rows of q_out are left alone.
  * A record must belong to one sequence of the batch: pages that sequences share are only read.
- * Finite inputs are required.  Errors: MMQ_ERR_SHAPE, MMQ_ERR_NULL, MMQ_ERR_ALIGN,
- * MMQ_ERR_ARG (dtype), MMQ_ERR_LAUNCH.
+ * Finite inputs are required: a NaN or an infinity leaves the codes and the scale of its own
+ * record (keys or values) unspecified, and a rotated query row its own values.  Errors:
+ * MMQ_ERR_SHAPE, MMQ_ERR_NULL, MMQ_ERR_ALIGN, MMQ_ERR_ARG (dtype), MMQ_ERR_LAUNCH.
  */
 int mmq_kv_append(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtype, const mmq_kv_rows* k,
                   const mmq_kv_rows* v, const mmq_kv_rows* q, int64_t q_heads, const mmq_kv_rope* rope, void* q_out,
@@ -528,6 +529,7 @@ size_t mmq_kv_workspace_bytes(int64_t dim);
  *   workspace: at least mmq_kv_workspace_bytes(dim) bytes, 256-byte aligned, its first 16384
  *   bytes zero before its first use; every call leaves them zero again, so one workspace
  *   serves any number of calls in stream order, but never two that may overlap in time.
+ *   (After MMQ_ERR_TIMEOUT from mmq_get_device_error they have to be zeroed once more.)
  * Accuracy: the codes and their scales enter exactly; sums, the softmax's statistics and the
  * output accumulate in f32.  For bf16 and f16 rows the weights are rounded to f16 before the
  * second product (2^-11 relative); for f32 rows queries and weights are split into two f16

@@ -440,6 +440,56 @@ def test_other_stream_and_graph(new):
     assert (ws[:16384] == 0).all()
 
 
+def test_graphs_without_a_workspace():
+    """Two captures on a stream that no call has run on, replayed in the other order, then a call on it."""
+    c = Case(53, [900, 2100], [1, 2], 8, 2, 128, 64, "bf16")
+    cache, batch = c.upload()
+    q = c.rows(8)
+    qd, side, graphs, outs = q.cuda(), torch.cuda.Stream(), [], []
+    for _ in range(2):
+        out = torch.zeros_like(qd)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            for _ in range(2):  # two calls of one graph
+                mmq.mmq_kv_attend(cache, batch, qd, scale=0.1, out=out)
+        graphs.append(graph)
+        outs.append(out)
+    for i in (1, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        clean()
+        compare_attend(c, outs[i], None, q, 0.1)
+    with torch.cuda.stream(side):
+        out = mmq.mmq_kv_attend(cache, batch, qd, scale=0.1)
+    clean()
+    compare_attend(c, out, None, q, 0.1)
+
+
+def test_package_workspaces_are_zeroed_after_a_timeout(monkeypatch):
+    """The error word's status is a stand-in: no wait runs out."""
+    from block_quantized_int8_mmq_gb300 import kv
+    c = Case(59, [900], [1], 8, 2, 128, 64, "bf16")
+    cache, batch = c.upload()
+    q = c.rows(8)
+    mmq.mmq_kv_attend(cache, batch, q.cuda(), scale=0.1)
+    clean()
+    for ws in kv._workspaces.values():
+        ws[:16384] = 1
+
+    class Lib:
+        def mmq_get_device_error(self, stream):
+            return -7
+
+    monkeypatch.setattr(mmq, "_lib", Lib())
+    assert mmq.mmq_get_device_error() == -7
+    monkeypatch.undo()
+    assert all((ws[:16384] == 0).all() for ws in kv._workspaces.values())
+    out = mmq.mmq_kv_attend(cache, batch, q.cuda(), scale=0.1)
+    clean()
+    compare_attend(c, out, None, q, 0.1)
+
+
 def test_workspace_is_left_clean_and_shared():
     """Calls of other shapes follow one another on one workspace."""
     ws = torch.zeros(mmq.mmq_kv_workspace_bytes(128), dtype=torch.uint8, device="cuda")
