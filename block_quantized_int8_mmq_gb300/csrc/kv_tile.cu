@@ -18,13 +18,13 @@
 // row's thread has read its S before it writes its P.  f32 rows (SPLIT): queries and weights as
 // two f16 terms each, twice the products.
 //
-// Measured (GB300): 1024 new of 32768 tokens, 32 heads of 128 over 8: 472 us, 1.15 PFLOP/s, 0.60 of
+// Measured (GB300): 1024 new of 32768 tokens, 32 heads of 128 over 8: 467 us, 1.16 PFLOP/s, 0.61 of
 // the library's rate for a plain product; tensor pipe 0.47 of the cycles, issue slots 0.45.  Two row tiles of
 // 128 x 128 keys take 4000 to 4300 cycles, 1024 of them the products' own at the tensor rate: the
 // products' operands, the staged codes and the converted tiles move 320 KB through shared memory (2560
 // cycles), and S, maximum, weights and P are a chain that the other tile's products cover in part.  Short
 // prompts pay a unit's ends (queries to f16 tiles, an empty pipeline, its output) and the join of the
-// parts: 2048 tokens, 28 heads over 4, 70 us where the same work inside a long one would be 26.
+// parts: 2048 tokens, 28 heads over 4, 68.7 us where the same work inside a long one would be 26.
 #include "kv_attend.cuh"
 #include "umma.cuh"
 
@@ -103,14 +103,17 @@ __device__ __forceinline__ void unit_next(const Attend& a, Unit& w) {
     while (w.tiles == 0 && ++w.b < a.bt.seqs) unit_load<ROWS, KT>(a, w, w.b, 0);
 }
 
-// What a unit costs beside its key tiles (queries in, output out, joining), in key tiles: a unit
+// What a unit costs beside its key tiles (queries in, output out, an empty pipeline), in key tiles: a unit
 // takes OVERHEAD + tiles places in the list of work, and the first OVERHEAD of them hold nothing.
-// Measured at 3 / 6: a 2048-token bf16 prompt 72.9 / 70.9 us, four prompts of 100..300 tokens on
-// 200..600 40.6 / 32.6 us, drafted tokens 31.0 / 30.6 us.
+// Fitted to the CTAs' clocks: a tile 4050 cycles, a piece of a unit 20000 beside its tiles, a join 8000.
+// Measured at 4 / 5 / 6: a 2048-token bf16 prompt 68.5 / 68.4 / 68.7 us, 8192 tokens 551 / 524 / 509, 1024
+// tokens 43.0 / 36.5 / 37.4.
 constexpr int OVERHEAD = 6;
 constexpr int JOIN = 8;  // parts joined at a time (three levels: up to 512 CTAs)
 
-// The next run of key tiles [t0, t1) of this CTA's places x .. x1 - 1; pos: place in unit w.
+// The next run of key tiles [t0, t1) of this CTA's places x .. x1 - 1; pos: place in unit w.  A unit's last tile
+// is not parted from the one before: the range that ends there takes it, the next one begins behind it
+// (with / without: 1024 tokens 37.4 / 41.4 us, 2048 68.7 / 70.0, 700 of 3000 with heads of 64 36.9 / 35.3).
 template <int ROWS, int KT>
 __device__ __forceinline__ bool next_piece(const Attend& a, Unit& w, int& pos, int& x, int x1, int& t0, int& t1) {
     while (x < x1) {
@@ -118,7 +121,8 @@ __device__ __forceinline__ bool next_piece(const Attend& a, Unit& w, int& pos, i
             unit_next<ROWS, KT>(a, w);
             pos = 0;
         }
-        const int span = min(w.tiles + OVERHEAD - pos, x1 - x);
+        int span = min(w.tiles + OVERHEAD - pos, x1 - x);
+        if (w.tiles + OVERHEAD - pos - span == 1) ++span;
         t0 = max(0, pos - OVERHEAD);
         t1 = max(0, pos + span - OVERHEAD);
         pos += span;
@@ -245,6 +249,7 @@ k_kv_attend_tile(const Attend a) {
     unit_load<C::ROWS, KT>(a, w, s_at[0], s_at[1]);
     w.h = s_at[2] / (w.tiles + OVERHEAD);
     int place = s_at[2] - w.h * (w.tiles + OVERHEAD), x = x0, o0 = 0, o1 = 0;  // place in the unit, key tiles of the piece
+    if (place == w.tiles + OVERHEAD - 1) ++place, ++x;  // the CTA before has taken it
 
     if (wid >= C::SOFT) {
         // ------------------------------------------------ converters: warp cw takes tokens KT/4 cw ..
@@ -725,7 +730,7 @@ k_kv_attend_tile(const Attend a) {
                         mine[128 * OD + row] = m;
                         mine[128 * (OD + 1) + row] = l;
                     }
-                    const int c0 = work_owner(T, ufirst, W), c1 = work_owner(T, ufirst + w.tiles - 1, W);
+                    const int c0 = work_owner(T, ufirst, W), c1 = work_owner(T, ufirst + w.tiles - 2, W);
                     // few rows: several threads a row, a share of the columns each
                     const int nr = min(128, w.rows - row0), lg = nr > 64 ? 7 : nr > 32 ? 6 : 5;
                     const int jr = row & ((1 << lg) - 1), seg = row >> lg, span = (OD / 4) >> (7 - lg);
