@@ -18,13 +18,13 @@
 // row's thread has read its S before it writes its P.  f32 rows (SPLIT): queries and weights as
 // two f16 terms each, twice the products.
 //
-// Measured (GB300): 1024 new of 32768 tokens, 32 heads of 128 over 8: 467 us, 1.16 PFLOP/s, 0.61 of
+// Measured (GB300): 1024 new of 32768 tokens, 32 heads of 128 over 8: 464 us, 1.17 PFLOP/s, 0.61 of
 // the library's rate for a plain product; tensor pipe 0.47 of the cycles, issue slots 0.45.  Two row tiles of
 // 128 x 128 keys take 4000 to 4300 cycles, 1024 of them the products' own at the tensor rate: the
 // products' operands, the staged codes and the converted tiles move 320 KB through shared memory (2560
 // cycles), and S, maximum, weights and P are a chain that the other tile's products cover in part.  Short
 // prompts pay a unit's ends (queries to f16 tiles, an empty pipeline, its output) and the join of the
-// parts: 2048 tokens, 28 heads over 4, 68.7 us where the same work inside a long one would be 26.
+// parts: 2048 tokens, 28 heads over 4, 54.4 us where the same work inside a long one would be 26.
 #include "kv_attend.cuh"
 #include "umma.cuh"
 
@@ -93,16 +93,6 @@ __device__ __forceinline__ void unit_load(const Attend& a, Unit& w, int b, int u
     w.h = 0;
     unit_span<ROWS, KT>(a, w);
 }
-// units in order: row runs of a sequence, the heads of each
-template <int ROWS, int KT>
-__device__ __forceinline__ void unit_next(const Attend& a, Unit& w) {
-    if (++w.h < a.c.heads) return;
-    w.h = 0;
-    ++w.u;
-    unit_span<ROWS, KT>(a, w);
-    while (w.tiles == 0 && ++w.b < a.bt.seqs) unit_load<ROWS, KT>(a, w, w.b, 0);
-}
-
 // What a unit costs beside its key tiles (queries in, output out, an empty pipeline), in key tiles: a unit
 // takes OVERHEAD + tiles places in the list of work, and the first OVERHEAD of them hold nothing.
 // Fitted to the CTAs' clocks: a tile 4050 cycles, a piece of a unit 20000 beside its tiles, a join 8000.
@@ -111,26 +101,14 @@ __device__ __forceinline__ void unit_next(const Attend& a, Unit& w) {
 constexpr int OVERHEAD = 6;
 constexpr int JOIN = 8;  // parts joined at a time (three levels: up to 512 CTAs)
 
-// The next run of key tiles [t0, t1) of this CTA's places x .. x1 - 1; pos: place in unit w.  A unit's last tile
-// is not parted from the one before: the range that ends there takes it, the next one begins behind it
-// (with / without: 1024 tokens 37.4 / 41.4 us, 2048 68.7 / 70.0, 700 of 3000 with heads of 64 36.9 / 35.3).
-template <int ROWS, int KT>
-__device__ __forceinline__ bool next_piece(const Attend& a, Unit& w, int& pos, int& x, int x1, int& t0, int& t1) {
-    while (x < x1) {
-        if (pos == w.tiles + OVERHEAD) {
-            unit_next<ROWS, KT>(a, w);
-            pos = 0;
-        }
-        int span = min(w.tiles + OVERHEAD - pos, x1 - x);
-        if (w.tiles + OVERHEAD - pos - span == 1) ++span;
-        t0 = max(0, pos - OVERHEAD);
-        t1 = max(0, pos + span - OVERHEAD);
-        pos += span;
-        x += span;
-        if (t1 > t0) return true;
-    }
-    return false;
-}
+// Units that are short beside a CTA's share are dealt whole instead: the longest first, round after round in
+// turning order (0 .. W - 1, W - 1 .. 0, ..), where the longest of the shares that come of it is at most
+// CUT key tiles above the even share: what cutting costs (a second piece of a unit, a join).
+// Measured dealt / cut, us: one prompt of 1024 tokens 33.0 / 39.3, 2048 54.4 / 70.9, 4096 157 / 189, 8192 465 / 507; sixteen
+// of 100 to 900 on 900 to 1200 196 / 236; f32 79.4 / 87.7; where it would leave SMs idle (700 of 3000 with 16 heads of
+// 64: 48 units) 55.8 / 38.7.  The ranking itself is up to 4 us of those that are cut all the same.
+constexpr int CUT = 9;
+__device__ __forceinline__ int dealt_unit(int round, int cta, int W) { return round * W + (round & 1 ? W - 1 - cta : cta); }
 
 // How many CTAs share T places in U units: all, but for few units no more than 2 sqrt(T / U) a unit, where
 // fewer tiles a CTA and more parts to join balance. Measured at 1.4, 2 and without the limit: 26 tokens x 8
@@ -147,7 +125,9 @@ k_kv_attend_tile(const Attend a) {
     constexpr bool HALF = C::HALF;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_scan[C::WARPS], s_pref[C::THREADS + 1], s_at[3], s_last[2];
+    __shared__ int s_abort, s_scan[C::WARPS], s_at[3], s_last[2];
+    __shared__ __align__(16) int s_pref[C::THREADS];
+    __shared__ int s_work[3];  // T, W, U (below): not in registers throughout
     __shared__ float4 s_sc[4][C::BLK];  // dk, log2 dv, 1 / dv of the blocks of four consecutive tiles
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
     const uint32_t base = ptx::smem_u32(smem), bars = base + C::OFF_BAR;
@@ -181,7 +161,8 @@ k_kv_attend_tile(const Attend a) {
 
     // ---- this CTA's range of the work: sequences THREADS at a time, their row runs spread over the threads
     int T = 0, U = 0, W = 0, x0 = 0, x1 = 0;
-    bool located = false;
+    int my_tiles = 0, my_run = 0;  // the thread's row run, where every run has a thread
+    bool located = false, dealt = false;
     for (int pass = 0; pass < 2 && !located; ++pass) {
         int carry = 0;
         for (int b0 = 0, units = 0; b0 < a.bt.seqs; b0 += C::THREADS) {
@@ -218,6 +199,8 @@ k_kv_attend_tile(const Attend a) {
                     T = carry;
                     W = workers(T, total * a.c.heads);
                     x0 = work_start(T, min((int)blockIdx.x, W), W);
+                    my_tiles = q.tiles;
+                    my_run = q.b << 16 | q.u;
                 }
                 if ((pass == 1 || located) && x0 >= e && x0 < e + v) {
                     s_at[0] = q.b;
@@ -230,9 +213,40 @@ k_kv_attend_tile(const Attend a) {
         if (pass == 0) {
             T = carry;
             W = workers(T, U);
+            if (located) {  // the runs by falling tiles, and the longest share when they are dealt
+                s_pref[tid] = my_tiles;
+                __syncthreads();
+                int rank = 0, share = 0;
+                for (int i = 0; i < U / a.c.heads; i += 4) {
+                    const int4 v = *reinterpret_cast<const int4*>(s_pref + i);
+                    rank += (v.x > my_tiles || (v.x == my_tiles && i < tid)) + (v.y > my_tiles || (v.y == my_tiles && i + 1 < tid)) +
+                            (v.z > my_tiles || (v.z == my_tiles && i + 2 < tid)) + (v.w > my_tiles || (v.w == my_tiles && i + 3 < tid));
+                }
+                __syncthreads();
+                if (my_tiles > 0) s_pref[rank] = my_tiles;
+                __syncthreads();
+                const int all = min((int)gridDim.x, U);
+                if (tid < all)
+                    for (int r, k = 0; (r = dealt_unit(k, tid, all)) < U; ++k) share += s_pref[r / a.c.heads] + OVERHEAD;
+                share = __reduce_max_sync(0xffffffffu, share);
+                if (lane == 0) s_scan[wid] = share;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < C::WARPS; ++i) share = max(share, s_scan[i]);
+                dealt = (long long)(share - CUT) * W <= T;
+                if (dealt) {
+                    W = all;
+                    if (my_tiles > 0) s_pref[rank] = my_run;
+                }
+            }
             if ((int)blockIdx.x >= W) return;
             x0 = work_start(T, blockIdx.x, W);
-            x1 = work_start(T, blockIdx.x + 1, W);
+            x1 = dealt ? -1 : work_start(T, blockIdx.x + 1, W);
+            if (tid == 0) {
+                s_work[0] = T;
+                s_work[1] = W;
+                s_work[2] = U;
+            }
         }
     }
     if (wid == 0) {
@@ -250,6 +264,51 @@ k_kv_attend_tile(const Attend a) {
     w.h = s_at[2] / (w.tiles + OVERHEAD);
     int place = s_at[2] - w.h * (w.tiles + OVERHEAD), x = x0, o0 = 0, o1 = 0;  // place in the unit, key tiles of the piece
     if (place == w.tiles + OVERHEAD - 1) ++place, ++x;  // the CTA before has taken it
+    if (x1 < 0) x = 0;  // dealt: its round
+    // The next run of key tiles [o0, o1) of this CTA: a dealt unit, or what its places x .. x1 - 1 hold of the next
+    // one in order (row runs of a sequence, the heads of each).  A unit's last tile is not parted from the one
+    // before: the range that ends there takes it, the next one begins behind it (with / without: 1024 tokens
+    // 37.4 / 41.4 us, 2048 68.7 / 70.0, 700 of 3000 with heads of 64 36.9 / 35.3).
+    auto next = [&]() -> bool {
+        for (;;) {
+            int b = w.b, u = w.u, h = w.h;
+            bool other = x1 < 0;
+            if (x1 < 0) {
+                const int r = dealt_unit(x, blockIdx.x, s_work[1]);
+                if (r >= s_work[2]) return false;
+                const int run = r / a.c.heads, at = s_pref[run];
+                b = at >> 16;
+                u = at & 0xffff;
+                h = r - run * a.c.heads;
+            } else {
+                if (x >= x1) return false;
+                if (place == w.tiles + OVERHEAD) {
+                    place = 0;
+                    if (++h == a.c.heads) {
+                        h = 0;
+                        ++u;
+                        other = true;
+                    }
+                }
+            }
+            if (other)
+                for (; unit_load<C::ROWS, KT>(a, w, b, u), w.tiles == 0 && ++b < a.bt.seqs;) u = 0;
+            w.h = h;
+            if (x1 < 0) {
+                o0 = 0;
+                o1 = w.tiles;
+                ++x;
+                return true;
+            }
+            int span = min(w.tiles + OVERHEAD - place, x1 - x);
+            if (w.tiles + OVERHEAD - place - span == 1) ++span;
+            o0 = max(0, place - OVERHEAD);
+            o1 = max(0, place + span - OVERHEAD);
+            place += span;
+            x += span;
+            if (o1 > o0) return true;
+        }
+    };
 
     if (wid >= C::SOFT) {
         // ------------------------------------------------ converters: warp cw takes tokens KT/4 cw ..
@@ -269,7 +328,7 @@ k_kv_attend_tile(const Attend a) {
         auto advance = [&]() -> bool {  // the cursor to the next tile
             if (!begun || ++o == o1) {
                 begun = true;
-                if (!next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1)) return false;
+                if (!next()) return false;
                 o = o0;
             }
             const int blk = (w.kt0 + o) * C::BLK + bi;
@@ -428,7 +487,7 @@ k_kv_attend_tile(const Attend a) {
             if (lane == 0) ptx::mbar_arrive(bar);
         };
         bool ok = true;
-        for (int n = 0; ok && next_piece<C::ROWS, KT>(a, w, place, x, x1, o0, o1);) {
+        for (int n = 0; ok && next();) {
             const int tiles = o1 - o0;  // this unit's tiles here
             const int row0 = w.u * C::ROWS + tile0, r = row0 + row;
             if (row0 >= w.rows) {
@@ -730,7 +789,7 @@ k_kv_attend_tile(const Attend a) {
                         mine[128 * OD + row] = m;
                         mine[128 * (OD + 1) + row] = l;
                     }
-                    const int c0 = work_owner(T, ufirst, W), c1 = work_owner(T, ufirst + w.tiles - 2, W);
+                    const int c0 = work_owner(s_work[0], ufirst, s_work[1]), c1 = work_owner(s_work[0], ufirst + w.tiles - 2, s_work[1]);
                     // few rows: several threads a row, a share of the columns each
                     const int nr = min(128, w.rows - row0), lg = nr > 64 ? 7 : nr > 32 ? 6 : 5;
                     const int jr = row & ((1 << lg) - 1), seg = row >> lg, span = (OD / 4) >> (7 - lg);
