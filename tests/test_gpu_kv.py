@@ -327,6 +327,18 @@ def test_attend_many_sequences(new):
     check_attend(Case(29, lens, [new] * 600, 2, 1, 64, 32, "bf16"))
 
 
+@pytest.mark.parametrize("dtype,window", [("bf16", 0), ("f16", 300), ("f32", 0)])
+@pytest.mark.parametrize("lens,news", [([1400], [1400]), ([1100, 640, 33, 900, 257], [800, 640, 33, 400, 256])])
+def test_attend_more_units_than_sms(dtype, window, lens, news):
+    """Units of many lengths, several a CTA, whole or cut."""
+    check_attend(Case(sum(lens), lens, news, 32, 8, 64, 64, dtype), window=window)
+
+
+def test_attend_more_sequences_than_threads():
+    lens = [30 + 7 * i % 50 for i in range(400)]
+    check_attend(Case(61, lens, [30] * 400, 4, 2, 64, 32, "bf16"))
+
+
 @pytest.mark.parametrize("dtype,length,dim", [("bf16", 20000, 64), ("f32", 20000, 128), ("f16", 9000, 256),
                                               ("bf16", 140000, 64)])
 @pytest.mark.parametrize("new", [1, 3])
