@@ -1,10 +1,10 @@
 // Attention of many query rows per sequence and key/value head (prompts, chunks of prompts, many
 // drafted tokens) over the 8-bit cache: k_kv_attend_tile.
 //
-// Bound: the tensor cores (4 D operations per row and key). A CTA takes units (kv_attend.cuh) of MT
-// tiles of 128 rows; a row is a (token, query head) pair of one key/value head's group, so that
+// Bound: the tensor cores (4 D operations per row and key). A CTA takes units (kv_attend.cuh) of two
+// tiles of 128 rows (heads of 256: one); a row is a (token, query head) pair of one key/value head's group, so that
 // the heads that share keys fill a tile together and a tile of keys and values, once converted,
-// serves MT * 128 rows.  Roles:
+// serves all of them.  Roles:
 //   converter warps (4)  records by bulk copies into a staging of their own, one tile ahead; codes to
 //                        exact f16 in shared memory, in the core-matrix order of tcgen05 (8 x 16
 //                        bytes): keys as the K-major B operand of S = Q K^T, values in the same
@@ -18,13 +18,13 @@
 // row's thread has read its S before it writes its P.  f32 rows (SPLIT): queries and weights as
 // two f16 terms each, twice the products.
 //
-// Measured (GB300): 1024 new of 32768 tokens, 32 heads of 128 over 8: 464 us, 1.17 PFLOP/s, 0.61 of
+// Measured (GB300): 1024 new of 32768 tokens, 32 heads of 128 over 8: 463 us, 1.17 PFLOP/s, 0.61 of
 // the library's rate for a plain product; tensor pipe 0.47 of the cycles, issue slots 0.45.  Two row tiles of
-// 128 x 128 keys take 4000 to 4300 cycles, 1024 of them the products' own at the tensor rate: the
+// 128 x 128 keys take about 4050 cycles, 1024 of them the products' own at the tensor rate: the
 // products' operands, the staged codes and the converted tiles move 320 KB through shared memory (2560
 // cycles), and S, maximum, weights and P are a chain that the other tile's products cover in part.  Short
-// prompts pay a unit's ends (queries to f16 tiles, an empty pipeline, its output) and the join of the
-// parts: 2048 tokens, 28 heads over 4, 54.4 us where the same work inside a long one would be 26.
+// prompts pay their units' ends (queries to f16 tiles, an empty pipeline, the output), five tiles' time
+// each: 2048 tokens, 28 heads over 4, 53.4 us where the same work inside a long one would be 26.
 #include "kv_attend.cuh"
 #include "umma.cuh"
 
@@ -93,11 +93,12 @@ __device__ __forceinline__ void unit_load(const Attend& a, Unit& w, int b, int u
     w.h = 0;
     unit_span<ROWS, KT>(a, w);
 }
+
 // What a unit costs beside its key tiles (queries in, output out, an empty pipeline), in key tiles: a unit
 // takes OVERHEAD + tiles places in the list of work, and the first OVERHEAD of them hold nothing.
 // Fitted to the CTAs' clocks: a tile 4050 cycles, a piece of a unit 20000 beside its tiles, a join 8000.
-// Measured at 4 / 5 / 6: a 2048-token bf16 prompt 68.5 / 68.4 / 68.7 us, 8192 tokens 551 / 524 / 509, 1024
-// tokens 43.0 / 36.5 / 37.4.
+// Measured at 4 / 5 / 6, all units cut: a 2048-token bf16 prompt 68.5 / 68.4 / 68.7 us, 8192 tokens 551 / 524 /
+// 509, 1024 tokens 43.0 / 36.5 / 37.4.
 constexpr int OVERHEAD = 6;
 constexpr int JOIN = 8;  // parts joined at a time (three levels: up to 512 CTAs)
 
@@ -267,8 +268,8 @@ k_kv_attend_tile(const Attend a) {
     if (x1 < 0) x = 0;  // dealt: its round
     // The next run of key tiles [o0, o1) of this CTA: a dealt unit, or what its places x .. x1 - 1 hold of the next
     // one in order (row runs of a sequence, the heads of each).  A unit's last tile is not parted from the one
-    // before: the range that ends there takes it, the next one begins behind it (with / without: 1024 tokens
-    // 37.4 / 41.4 us, 2048 68.7 / 70.0, 700 of 3000 with heads of 64 36.9 / 35.3).
+    // before: the range that ends there takes it, the next one begins behind it (with / without, all units cut:
+    // 1024 tokens 37.4 / 41.4 us, 2048 68.7 / 70.0, 700 of 3000 with heads of 64 36.9 / 35.3).
     auto next = [&]() -> bool {
         for (;;) {
             int b = w.b, u = w.u, h = w.h;
