@@ -652,17 +652,17 @@ int launch_rows(const Attend& a, int rows, cudaStream_t s) {
 // tiles' time, which hardly changes from 8 to 128 rows, is shorter.  Measured, stream / tiles in us, 8 heads,
 // as sequences x tokens, all sequences with the same rows:
 //                      50 x 150      8 x 2000     200 x 200     1 x 65536    50 x 12000
-//   128, 16-bit, 24   31.7 / 40.9   28.3 / 40.3   84.5 / 144   56.3 / 88      322 / 612
-//                48   48.1 / 42.4   42.1 / 41.5    123 / 145   86.7 / 94      618 / 614
-//                64   50.0 / 42.5   49.0 / 41.4                 120 / 93      912 / 614
-//   128, f32,    48   40.8 / 54.1   41.9 / 55.0    113 / 252    110 / 153     842 / 1112
-//                64   49.1 / 55.3   49.0 / 55.3                 137 / 152    1112 / 1114
-//    64, 16-bit, 48   31.1 / 34.6   30.1 / 33.1   74.2 / 108   59.4 / 70      428 / 481
-//                64   33.2 / 34.5   35.1 / 33.1                81.2 / 69      633 / 481
-//   256, 16-bit, 16   39.0 / 44.0   37.9 / 43.6   99.7 / 184   94.0 / 121     754 / 906
-//                24   46.5 / 45.1   47.1 / 43.9    131 / 191    131 / 122    1111 / 909
-//   256, f32,    32   57.7 / 67.3   67.6 / 79.0    188 / 299    204 / 245    1720 / 2010
-//                48   72.1 / 72.2   92.9 / 82.6    271 / 320    297 / 254    2536 / 2015
+//   128, 16-bit, 24   31.7 / 41.9   28.3 / 42.2   84.5 / 138   56.3 / 87      322 / 584
+//                48   48.1 / 42.2   42.1 / 43.8    123 / 140   86.7 / 94      618 / 584
+//                64   50.0 / 42.4   49.0 / 43.6    149 / 142    120 / 93      912 / 584
+//   128, f32,    48   40.8 / 52.6   41.9 / 60.4    113 / 249    110 / 164     842 / 1199
+//                64   49.1 / 53.7   49.0 / 60.7    143 / 248    137 / 164    1112 / 1201
+//    64, 16-bit, 48   31.1 / 35.4   30.1 / 35.1   74.2 / 107   59.4 / 74      428 / 508
+//                64   33.2 / 35.4   35.1 / 34.9   91.7 / 108   81.2 / 74      633 / 508
+//   256, 16-bit, 16   39.0 / 42.5   37.9 / 46.5   99.7 / 166   94.0 / 130     754 / 962
+//                24   46.5 / 43.8   47.1 / 47.0    131 / 174    131 / 131    1111 / 965
+//   256, f32,    32   57.7 / 64.2   67.6 / 79.9    188 / 284    204 / 245    1720 / 2026
+//                48   72.1 / 68.5   92.9 / 84.3    271 / 300    297 / 253    2536 / 2031
 // Where most sequences have fewer rows than the longest one the stream gains, the tiles do not: 8 sequences
 // of 517 to 3001 tokens with 14 to 35 rows of 128 take 30.1 us there, 32.2 in the tiles.
 int kv_stream_rows(int dim, int dtype) {

@@ -107,7 +107,9 @@ constexpr int JOIN = 8;  // parts joined at a time (three levels: up to 512 CTAs
 // CUT key tiles above the even share: what cutting costs (a second piece of a unit, a join).
 // Measured dealt / cut, us: one prompt of 1024 tokens 33.0 / 39.3, 2048 54.4 / 70.9, 4096 157 / 189, 8192 465 / 507; sixteen
 // of 100 to 900 on 900 to 1200 196 / 236; f32 79.4 / 87.7; where it would leave SMs idle (700 of 3000 with 16 heads of
-// 64: 48 units) 55.8 / 38.7.  The ranking itself is up to 4 us of those that are cut all the same.
+// 64: 48 units) 55.8 / 38.7.  Its price where units are cut all the same, with / without the code for it: 1 to 4 us of
+// ranking, and long chunks of f32 and of heads of 256, whose registers it takes: 1024 of 32768, 16 heads, f32 561 / 540,
+// 256 829 / 778, 128 in 16 bits 247 / 247; dealt prompts of 2048 with heads of 256 78 / 92, six of 600 72 / 86, f32 60 / 70.
 constexpr int CUT = 9;
 __device__ __forceinline__ int dealt_unit(int round, int cta, int W) { return round * W + (round & 1 ? W - 1 - cta : cta); }
 
