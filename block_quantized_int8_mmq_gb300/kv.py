@@ -9,7 +9,7 @@
 
 The handles only keep tensors alive and their addresses together; a program makes them once
 (a batch once per set of tensors: its tensors' contents may change between calls) and every
-computation runs in the library's kernels.
+computation runs in the library's kernels.  The cache's device has to be the current one.
 """
 from __future__ import annotations
 
@@ -154,6 +154,14 @@ def _elsewhere(what, t, device):
     raise ValueError(f"{what} is on {t.device}, the cache on {device}")
 
 
+def _here(device):
+    """The library launches on the current device, whatever stream and addresses it gets."""
+    current = torch.cuda.current_device()
+    if current != device.index:
+        raise ValueError(f"the cache is on {device}, the current device is cuda:{current}: call it under "
+                         f"torch.cuda.device({device.index})")
+
+
 def _stream_of(device, stream, made):
     """The raw stream of a call; `made` (tensors allocated here) stay with a stream other than the
     one they were allocated on."""
@@ -183,6 +191,7 @@ def mmq_kv_append(cache, batch, k, v, q=None, rope=None, q_out=None, stream=None
     """Keys and values [tokens, cache.heads, dim] into the cache, rotated by `rope` on the way (the
     values are not rotated); returns the rotated queries [tokens, q heads, dim] where q is given."""
     dt, dev, shape = k.dtype, cache.device, (batch.tokens, cache.heads, cache.dim)
+    _here(dev)
     d = _DTYPES.get(dt)
     ks, vs = k.stride(), v.stride()
     if d is None or k.shape != shape or k.device != dev or ks[-1] != 1:
@@ -221,6 +230,7 @@ def mmq_kv_append(cache, batch, k, v, q=None, rope=None, q_out=None, stream=None
 def mmq_kv_read(cache, batch, dtype=torch.float32, k_out=None, v_out=None, stream=None):
     """The cached keys and values of the batch's tokens, [tokens, cache.heads, dim] of `dtype`."""
     d, dev, shape = _DTYPES.get(dtype), cache.device, (batch.tokens, cache.heads, cache.dim)
+    _here(dev)
     if d is None:
         raise ValueError(f"{dtype}: float32, bfloat16 and float16 are taken")
     if batch.device != dev:
@@ -278,6 +288,7 @@ def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=No
     that may overlap others of the same stream (a captured graph replayed elsewhere); by default
     the package keeps one for each stream."""
     dt, dev, qs, qshape = q.dtype, cache.device, q.stride(), q.shape
+    _here(dev)
     d = _DTYPES.get(dt)
     if d is None or len(qshape) != 3 or qshape[0] != batch.tokens or qshape[2] != cache.dim or q.device != dev or qs[-1] != 1:
         _refuse(q, "q", (batch.tokens, 0, cache.dim), dt, dev)

@@ -136,3 +136,57 @@ def test_reference_rotation_is_a_rotation():
     assert np.allclose(kv_ref.rotate(x, 1, cos, sin, False), [-3, 2 * 0.6 - 4 * 0.8, 1, 4 * 0.6 + 2 * 0.8, 5])
     assert np.allclose(kv_ref.rotate(x, 1, cos, sin, True), [-2, 1, 3 * 0.6 - 4 * 0.8, 4 * 0.6 + 3 * 0.8, 5])
     assert kv_ref.rotate(x, 0, cos, sin, True).tolist() == x.tolist()
+
+
+class OnDevice:
+    """A tensor's outside on GPU 1: what a call looks at before it launches."""
+    device, is_cuda = torch.device("cuda", 1), True
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def stride(self):
+        return tuple(int(np.prod(self.shape[i + 1:])) for i in range(len(self.shape)))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+    def numel(self):
+        return 1 << 40
+
+
+class Launches:
+    """The library with its launching entries replaced by a note of the call."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return getattr(mmq.lib(), name)
+        return lambda *a: self.calls.append(name) or 0
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_a_cache_of_another_device_is_refused(current, monkeypatch):
+    """The library launches on the current device, whatever stream and addresses it gets."""
+    from types import SimpleNamespace as S
+    cache, batch = S(device=OnDevice.device, heads=2, dim=64, _p=0), S(device=OnDevice.device, tokens=3, _p=0)
+    k, q, ws = OnDevice(3, 2, 64), OnDevice(3, 4, 64), OnDevice(1 << 20, dtype=torch.uint8)
+    fake = Launches()
+    monkeypatch.setattr(kv, "_lib", fake)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    calls = [lambda: kv.mmq_kv_append(cache, batch, k, k, q=q, q_out=q, stream=0),
+             lambda: kv.mmq_kv_append(cache, batch, k, k, stream=0),
+             lambda: kv.mmq_kv_read(cache, batch, k_out=k, v_out=k, stream=0),
+             lambda: kv.mmq_kv_attend(cache, batch, q, out=q, workspace=ws, stream=0)]
+    for call in calls:
+        if current == 1:
+            call()
+        else:
+            with pytest.raises(ValueError, match="current device"):
+                call()
+    assert len(fake.calls) == (4 if current == 1 else 0)
