@@ -256,18 +256,33 @@ _WS_ZERO = 16384  # bytes at a workspace's beginning that start at zero
 _workspaces: dict = {}
 
 
+_is_capturing = None
+
+
+def _captured(raw):
+    """Whether a raw stream is being captured (torch asks this of the current stream only, and making
+    another one current for the question takes ten times as long)."""
+    global _is_capturing
+    if _is_capturing is None:
+        _is_capturing = ctypes.CDLL("libcuda.so.1").cuStreamIsCapturing
+        _is_capturing.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    status = ctypes.c_int(0)
+    return _is_capturing(raw, ctypes.addressof(status)) == 0 and status.value != 0
+
+
 def _workspace(cache, stream):
-    """The package's own workspace of a stream: calls on one stream run one after another.  A capture
-    on a stream that has none yet gets one of the graph's memory, zeroed in the graph."""
+    """The package's own workspace of a stream: calls on one stream run one after another.  A captured call
+    gets one of the graph's memory, zeroed in the graph: its replays may run beside anything."""
     s = torch._C._cuda_getCurrentRawStream(cache.device.index) if stream is None else int(_stream(stream).value or 0)
+    captured = _captured(s)
     key = (cache.device.index, s, cache.dim)
-    ws = _workspaces.get(key)
+    ws = None if captured else _workspaces.get(key)
     if ws is None:
         with torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream)
                                else torch.cuda.ExternalStream(s, device=cache.device)):
             ws = torch.empty(mmq_kv_workspace_bytes(cache.dim), dtype=torch.uint8, device=cache.device)
             ws[:_WS_ZERO].zero_()
-            if not torch.cuda.is_current_stream_capturing():
+            if not captured:
                 _workspaces[key] = ws
     return ws
 
@@ -284,9 +299,9 @@ def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=No
     """Causal attention of the rotated queries [tokens, q heads, dim] over the cache: [tokens, q
     heads, dim].  scale: 1 / sqrt(dim) by default.  window: how many of the latest tokens a row
     sees (0: all).  lse: an f32 [tokens, q heads] tensor for the logarithm of the softmax's sum.
-    workspace: a uint8 tensor of mmq_kv_workspace_bytes(dim) bytes, its first 16384 zero, for calls
-    that may overlap others of the same stream (a captured graph replayed elsewhere); by default
-    the package keeps one for each stream."""
+    workspace: a uint8 tensor of mmq_kv_workspace_bytes(dim) bytes, its first 16384 zero, that no call
+    that may overlap this one uses.  By default the package keeps one for each stream, and a captured call
+    has one of the graph's own, zeroed by a node of the graph that a workspace given here saves."""
     dt, dev, qs, qshape = q.dtype, cache.device, q.stride(), q.shape
     _here(dev)
     d = _DTYPES.get(dt)

@@ -634,3 +634,65 @@ def test_attention_layer_example(fmt):
     example = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(example)
     assert example.run(fmt, prompts=(90, 33, 5), steps=5, page=32, quiet=True, hidden=512, heads=8, kv_heads=2, dim=64) < 1.3e-4
+
+
+def test_a_capture_on_a_stream_in_use_has_its_own_workspace():
+    """Two graphs captured on a stream that has already run a call share nothing with it or each other: what
+    a call leaves in the stream's workspace does not reach the replays."""
+    from block_quantized_int8_mmq_gb300 import kv
+    c = Case(73, [900, 2100], [1, 2], 8, 2, 128, 64, "bf16")
+    cache, batch = c.upload()
+    q = c.rows(8)
+    qd, side = q.cuda(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mmq.mmq_kv_attend(cache, batch, qd, scale=0.1)
+    side.synchronize()
+    kept = kv._workspaces[(0, side.cuda_stream, 128)]
+    graphs, outs = [], []
+    for i in range(2):
+        out = torch.zeros_like(qd)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            mmq.mmq_kv_attend(cache, batch, qd, scale=0.1, out=out)
+            if i:  # and once more in one graph, the stream named
+                mmq.mmq_kv_attend(cache, batch, qd, scale=0.1, out=out, stream=side)
+        graphs.append(graph)
+        outs.append(out)
+    kept.fill_(255)  # counters that no call has left, partial results that are NaN
+    for i in (0, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        clean()
+        compare_attend(c, outs[i], None, q, 0.1)
+    assert (kept == 255).all()
+    kept[:16384].zero_()
+    with torch.cuda.stream(side):
+        out = mmq.mmq_kv_attend(cache, batch, qd, scale=0.1)
+    clean()
+    compare_attend(c, out, None, q, 0.1)
+
+
+def test_a_capture_of_a_named_stream_has_its_own_workspace():
+    """The same where the captured stream is not the current one but joined to its capture."""
+    from block_quantized_int8_mmq_gb300 import kv
+    c = Case(79, [900, 2100], [1, 2], 8, 2, 128, 64, "bf16")
+    cache, batch = c.upload()
+    q = c.rows(8)
+    qd, side, out = q.cuda(), torch.cuda.Stream(), torch.zeros_like(q, device="cuda")
+    torch.cuda.synchronize()
+    mmq.mmq_kv_attend(cache, batch, qd, scale=0.1, stream=side)
+    side.synchronize()
+    kept = kv._workspaces[(0, side.cuda_stream, 128)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        mmq.mmq_kv_attend(cache, batch, qd, scale=0.1, out=out, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    kept.fill_(255)
+    graph.replay()
+    clean()
+    compare_attend(c, out, None, q, 0.1)
+    assert (kept == 255).all()
+    kept[:16384].zero_()
