@@ -162,16 +162,24 @@ def _here(device):
                          f"torch.cuda.device({device.index})")
 
 
-def _stream_of(device, stream, made):
-    """The raw stream of a call; `made` (tensors allocated here) stay with a stream other than the
-    one they were allocated on."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    if isinstance(stream, torch.cuda.Stream):
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-    return _stream(stream)
+def _stream_of(device, stream):
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor for what a call returns.  On a stream other than the current one it is that stream's memory,
+    which nothing pending elsewhere uses, and given back once the current stream is done with it too."""
+    if stream is None or int(_stream(stream).value or 0) == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    torch.cuda.set_stream(stream if isinstance(stream, torch.cuda.Stream)
+                          else torch.cuda.ExternalStream(int(stream), device=device))
+    try:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    finally:
+        torch.cuda.set_stream(current)
+    t.record_stream(current)
+    return t
 
 
 def _out(t, shape, dtype, cache, what):
@@ -208,20 +216,19 @@ def mmq_kv_append(cache, batch, k, v, q=None, rope=None, q_out=None, stream=None
     if q is None:
         rows = _Rows3(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
         p = ctypes.addressof(rows)
-        st = _lib.mmq_kv_append(cache._p, batch._p, d, p, p + _ROW_BYTES, None, 0, turn, None, _stream_of(dev, stream, ()))
+        st = _lib.mmq_kv_append(cache._p, batch._p, d, p, p + _ROW_BYTES, None, 0, turn, None, _stream_of(dev, stream))
     else:
         qs, qshape = q.stride(), q.shape
         if q.dtype != dt or len(qshape) != 3 or qshape[0] != shape[0] or qshape[2] != shape[2] or q.device != dev or qs[-1] != 1:
             _refuse(q, "q", (shape[0], 0, shape[2]), dt, dev)
-        made = None
         if q_out is None:
-            q_out = made = torch.empty(qshape, dtype=dt, device=dev)
+            q_out = _empty(qshape, dt, dev, stream)
         else:
             _out(q_out, qshape, dt, cache, "q_out")
         rows = _Rows3(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], q.data_ptr(), qs[0], qs[1])
         p = ctypes.addressof(rows)
         st = _lib.mmq_kv_append(cache._p, batch._p, d, p, p + _ROW_BYTES, p + 2 * _ROW_BYTES, qshape[1], turn,
-                                q_out.data_ptr(), _stream_of(dev, stream, (made,)))
+                                q_out.data_ptr(), _stream_of(dev, stream))
     if st != 0:
         raise MMQError("mmq_kv_append", st)
     return q_out if q is not None else None
@@ -235,18 +242,15 @@ def mmq_kv_read(cache, batch, dtype=torch.float32, k_out=None, v_out=None, strea
         raise ValueError(f"{dtype}: float32, bfloat16 and float16 are taken")
     if batch.device != dev:
         _elsewhere("the batch", batch, dev)
-    made = []
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
-        made.append(k_out)
+        k_out = _empty(shape, dtype, dev, stream)
     else:
         _out(k_out, shape, dtype, cache, "k_out")
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
-        made.append(v_out)
+        v_out = _empty(shape, dtype, dev, stream)
     else:
         _out(v_out, shape, dtype, cache, "v_out")
-    st = _lib.mmq_kv_read(cache._p, batch._p, d, k_out.data_ptr(), v_out.data_ptr(), _stream_of(dev, stream, made))
+    st = _lib.mmq_kv_read(cache._p, batch._p, d, k_out.data_ptr(), v_out.data_ptr(), _stream_of(dev, stream))
     if st != 0:
         raise MMQError("mmq_kv_read", st)
     return k_out, v_out
@@ -309,9 +313,8 @@ def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=No
         _refuse(q, "q", (batch.tokens, 0, cache.dim), dt, dev)
     if batch.device != dev:
         _elsewhere("the batch", batch, dev)
-    made = None
     if out is None:
-        out = made = torch.empty(qshape, dtype=dt, device=dev)
+        out = _empty(qshape, dt, dev, stream)
     else:
         _out(out, qshape, dt, cache, "out")
     if lse is not None:
@@ -325,7 +328,7 @@ def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=No
     rows = _Rows(q.data_ptr(), qs[0], qs[1])
     st = _lib.mmq_kv_attend(cache._p, batch._p, d, ctypes.addressof(rows), qshape[1], scale, window, out.data_ptr(),
                             None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                            _stream_of(dev, stream, (made,)))
+                            _stream_of(dev, stream))
     if st != 0:
         raise MMQError("mmq_kv_attend", st)
     return out

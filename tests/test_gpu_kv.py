@@ -696,3 +696,43 @@ def test_a_capture_of_a_named_stream_has_its_own_workspace():
     compare_attend(c, out, None, q, 0.1)
     assert (kept == 255).all()
     kept[:16384].zero_()
+
+
+@pytest.mark.parametrize("call", ["attend", "append", "read"])
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_made_for_another_stream_have_memory_of_their_own(call, raw):
+    """A call on a stream that waits for nothing: what it returns must not lie where the current stream's
+    pending work still reads (memory that was given back there), nor may its memory go to the current stream's
+    next tensor while the call has not run."""
+    c = Case(83, [40, 70], [20, 30], 4, 2, 64, 32, "f32")
+    cache, batch = c.upload()
+    q, k, v = (c.rows(h).cuda() for h in (4, 2, 2))
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    run = {"attend": lambda: mmq.mmq_kv_attend(cache, batch, q, scale=0.1, stream=stream),
+           "append": lambda: mmq.mmq_kv_append(cache, batch, k, v, q=q, stream=stream),
+           "read": lambda: mmq.mmq_kv_read(cache, batch, stream=stream)[0]}[call]
+    first = run()  # (workspaces and modules are there)
+    clean()
+    first = first.clone()
+    shape = first.shape
+    held = torch.full(shape, 3.0, device="cuda")
+    copy = torch.empty_like(held)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # 0.1 s
+    copy.copy_(held)
+    del held
+    run()
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert (copy == 3.0).all()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    out = run()
+    del out  # the call has not run yet
+    mine = torch.full(shape, 5.0, device="cuda")
+    clean()
+    assert (mine == 5.0).all()
+    out = run()
+    side.synchronize()
+    assert torch.equal(out, first)
