@@ -293,10 +293,10 @@ def _workspace(cache, stream):
 
 def _clean_workspaces():
     """A call that gave up may have left counts in its workspace."""
-    torch.cuda.synchronize()
     for ws in _workspaces.values():
+        torch.cuda.synchronize(ws.device)
         ws[:_WS_ZERO].zero_()
-    torch.cuda.synchronize()
+        torch.cuda.synchronize(ws.device)
 
 
 def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=None, workspace=None, stream=None):

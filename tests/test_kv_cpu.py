@@ -190,3 +190,28 @@ def test_a_cache_of_another_device_is_refused(current, monkeypatch):
             with pytest.raises(ValueError, match="current device"):
                 call()
     assert len(fake.calls) == (4 if current == 1 else 0)
+
+
+def test_workspaces_are_zeroed_behind_their_own_device(monkeypatch):
+    """After a call that gave up, every device that has a workspace is waited for, not the current one alone."""
+    log = []
+
+    class Space:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+        def __getitem__(self, part):
+            return self
+
+        def zero_(self):
+            log.append(("zero", self.device.index))
+
+    def synchronize(device=None):
+        log.append(("wait", 0 if device is None else torch.device(device).index))
+
+    monkeypatch.setattr(torch.cuda, "synchronize", synchronize)
+    monkeypatch.setattr(kv, "_workspaces", {(i, 0, 64): Space(i) for i in (1, 0)})
+    kv._clean_workspaces()
+    for i in (0, 1):
+        at = log.index(("zero", i))
+        assert ("wait", i) in log[:at] and ("wait", i) in log[at:]
