@@ -150,7 +150,8 @@ int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtyp
     if (!st && (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256)))
         st = refuse(fn, MMQ_ERR_ALIGN, "out must be 16-byte, lse 4-byte and workspace 256-byte aligned");
     if (!st && !(scale > 0.f && isfinite(scale))) st = refuse(fn, MMQ_ERR_ARG, "scale must be finite and > 0");
-    if (!st && (int64_t)b.seqs * c.heads * b.table_pages * c.blocks > 0x7fffffff)
+    // (the four factors together can pass 2^64)
+    if (!st && b.table_pages > 0 && (int64_t)b.seqs * c.heads > 0x7fffffff / ((int64_t)b.table_pages * c.blocks))
         st = refuse(fn, MMQ_ERR_SHAPE, "seqs * heads * table_pages * page / 32 must be below 2^31");
     if (!st && window < 0) st = refuse(fn, MMQ_ERR_ARG, "window must be >= 0");
     if (!st && workspace_bytes < mmq_kv_workspace_bytes(c.dim))

@@ -215,3 +215,13 @@ def test_workspaces_are_zeroed_behind_their_own_device(monkeypatch):
     for i in (0, 1):
         at = log.index(("zero", i))
         assert ("wait", i) in log[:at] and ("wait", i) in log[at:]
+
+
+@pytest.mark.parametrize("change", [dict(seqs=1 << 24, heads=1 << 14, q_heads=1 << 14, page=32, table_pages=1 << 25),
+                                    dict(seqs=1 << 24, heads=32766, q_heads=32766, page=1 << 20, table_pages=1 << 10),
+                                    dict(seqs=1 << 23, heads=4, page=64, table_pages=4)])
+def test_more_records_than_can_be_numbered_are_refused(change, capfd):
+    """2^63 of them, close to 2^64, 2^28: past and within 64 bits, the last one is taken."""
+    big = change["seqs"] > 1 << 23
+    assert call("attend", table_stride=change["table_pages"], **change) == (SHAPE if big else 0)
+    assert ("2^31" in capfd.readouterr().err) == big
