@@ -80,14 +80,10 @@ __device__ __forceinline__ void turn1(float& x, float& y, float c, float s) {
     y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
     x = a;
 }
-// a unit's columns of the tables at a position; false: not rotated, or past the tables
+// a unit's columns of the tables at a position; false: not rotated
 template <int V>
 __device__ __forceinline__ bool table(const Unit& o, const Rope& r, int pos, float (&c)[V], float (&s)[V]) {
     if (o.pair < 0) return false;
-    if (pos >= r.rows) {
-        atomicOr(&g_kv_cache_error, ERR_RANGE);
-        return false;
-    }
     const long long at = (long long)pos * (r.rotary / 2) + o.pair;
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
@@ -159,6 +155,11 @@ k_kv_append(Cache c, Batch bt, Rows kr, Rows vr, Rows qr, int q_heads, Rope rope
     ptx::grid_dep_launch_dependents();
     Where w;
     if (!find_block(c, bt, w)) return;
+    if (rope.rotary > 0 && w.pos0 + w.i1 > rope.rows) {  // positions past the tables are skipped
+        if (threadIdx.x == 0) atomicOr(&g_kv_cache_error, ERR_RANGE);
+        w.i1 = (int)(max(rope.rows, (long long)w.pos0) - w.pos0);
+        if (w.i1 <= w.i0) return;
+    }
     const int tid = threadIdx.x;
     const Unit o = unit<V>(tid % O, rope);
     if (blockIdx.y >= c.heads) {

@@ -495,7 +495,7 @@ size_t mmq_kv_block_bytes(int64_t dim);
  *   older codes become clamp(rint(c * (d / d')), -127, 127) where d' differs from d;
  *   new codes clamp(rint(x / d'), -127, 127) (IEEE divisions, ties to even; 0 where d' = 0).
  * Bit-exact by that definition.  Rows of the record past the sequence's end keep their bytes;
- * padding rows of q_out are left alone.
+ * padding rows of q_out are left alone.  So are both where a position is past the rotation tables.
  * A record must belong to one sequence of the batch: pages that sequences share are only read.
  * Finite inputs are required: a NaN or an infinity leaves the codes and the scale of its own
  * record (keys or values) unspecified, and a rotated query row its own values.  Errors:

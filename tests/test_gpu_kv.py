@@ -736,3 +736,31 @@ def test_outputs_made_for_another_stream_have_memory_of_their_own(call, raw):
     out = run()
     side.synchronize()
     assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("dtype,rotary", [("f32", 64), ("bf16", 64), ("f16", 40)])
+@pytest.mark.parametrize("news,lens,rows", [([30, 40, 5], [90, 40, 70], 65), ([1, 1, 1], [90, 89, 12], 89),
+                                            ([90, 33, 8], [90, 33, 40], 1), ([3, 2, 2], [90, 64, 33], 32)])
+def test_rows_past_the_rotation_tables_are_skipped(dtype, rotary, news, lens, rows):
+    """The tables end inside a block, at its beginning, before a sequence's new tokens: the rows up to there
+    are appended and turned, the others leave the cache and their row of q_out as they were."""
+    c = Case(89 + rows, lens, news, 12, 2, 64, 32, dtype)
+    q, k, v = (c.rows(h) for h in (12, 2, 2))
+    cos, sin = tables(rows, rotary)
+    cache, batch = c.upload()
+    out = torch.full((c.T, 12, 64), 7.0, dtype=DT[dtype], device="cuda")
+    mmq.mmq_kv_append(cache, batch, k.cuda(), v.cuda(), q=q.cuda(), rope=mmq.Rope(dev(cos), dev(sin)), q_out=out)
+    torch.cuda.synchronize()
+    assert mmq.mmq_get_device_error() == MMQ_ERR_RANGE
+    ref, want = c.data.copy(), np.full(out.shape, 7.0, np.float32)
+    for b, (n, m) in enumerate(zip(lens, news)):
+        first, end = n - m, min(n, rows)
+        for t in range(first, end):
+            r = c.starts[b] + t - first
+            for h in range(12):
+                want[r, h] = kv_ref.rotate(q.float().numpy()[r, h], t, cos, sin, False)
+        if end > first:
+            kv_ref.append(ref, [c.starts[b], c.starts[b] + end - first], [end], c.table[b:b + 1], k.float().numpy(),
+                          v.float().numpy(), 64, (cos, sin, False))
+    assert np.array_equal(cache.data.cpu().numpy(), ref)
+    assert torch.equal(out.cpu(), torch.from_numpy(want).to(DT[dtype]))
