@@ -16,6 +16,13 @@
 // rows (exact but for bits 2^-25 below the row's largest), two for f32 rows (SPLIT), whose
 // weights are split into two f16 terms as well.
 //
+// The tensor core's accumulation rounds towards zero: a sum falls short by about 2^-22.7 of itself for every
+// record added to it.  For f32 rows the products of 16 tokens therefore start at zero and are added in f32, to
+// nearest: 65500 tokens of one sign, 400 to 2000 records a warp, come within 7e-7 to 3e-6 of 64 bits, where one long
+// chain was 9e-5 to 4e-4 off (64 sequences of 1000 to 8191 tokens, 4 rows a head of 64 / 128 / 256: 69 / 104 / 227 ->
+// 72 / 107 / 245 us).  For 16-bit rows the chain stays: 400 records are 6e-5 off, a quarter of f16's own rounding
+// (2^-12), and the additions cost 1 to 8 % (62.9 -> 63.5 us, 24 rows of 128 on long runs 1365 -> 1480).
+//
 // Measured (GB300): 64 sequences of 1000 to 8191 tokens, 4 rows a head, 614 MB of records: 108 us,
 // 5.7 TB/s, 0.84 of the copy rate, with an issue slot used in 0.45 of the cycles and the tensor pipe in
 // 0.14.  One sequence of 131069 tokens, 135 MB: 36 us; a CTA's prologue (lengths, first table entries,
@@ -54,6 +61,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// as mma16816, from zero
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t o;
@@ -436,11 +451,19 @@ k_kv_attend_stream(const Attend a) {
                             const uint2 c0 = umma::i8x4_to_f16x4(__byte_perm(wv[0][j >> 1], wv[1][j >> 1], sel));
                             const uint2 c1 = umma::i8x4_to_f16x4(__byte_perm(wv[2][j >> 1], wv[3][j >> 1], sel));
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float (&to)[4] = acc[hh * (RUN / 2) + j][nt];
+                                if (SPLIT) {  // the small terms first
+                                    float part[4];
+                                    mma16816_first(part, c0.x, c0.y, c1.x, c1.y, pf[SPLIT ? 1 : 0][mt][nt][0],
+                                                   pf[SPLIT ? 1 : 0][mt][nt][1]);
+                                    mma16816(part, c0.x, c0.y, c1.x, c1.y, pf[0][mt][nt][0], pf[0][mt][nt][1]);
 #pragma unroll
-                                for (int e = 0; e < (SPLIT ? 2 : 1); ++e)
-                                    mma16816(acc[hh * (RUN / 2) + j][nt], c0.x, c0.y, c1.x, c1.y, pf[e][mt][nt][0],
-                                             pf[e][mt][nt][1]);
+                                    for (int c = 0; c < 4; ++c) to[c] += part[c];
+                                } else {
+                                    mma16816(to, c0.x, c0.y, c1.x, c1.y, pf[0][mt][nt][0], pf[0][mt][nt][1]);
+                                }
+                            }
                         }
                     }
                 __syncwarp();  // the stage is read
