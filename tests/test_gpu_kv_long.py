@@ -72,3 +72,84 @@ def test_f32_sums_of_long_runs(dim, seqs, new):
                 12 * math.sqrt(n / 3) * 2.0 ** -23 / math.sqrt(12) + UNIT["f32"]
             off = float(((out[b * new + t].double() - want) / want).abs().max())
             assert off <= bound, f"2^{math.log2(off):.1f} off, 2^{math.log2(bound):.1f} allowed"
+
+
+def stream_shape(dim, rows, dtype):
+    """Of the attention stream with at most `rows` query rows a sequence and head: rows of a unit, workers on this
+    GPU, records that a worker has in flight."""
+    unit = 8 if dim == 256 or rows <= 8 else 16 if rows <= 16 or (dim == 128 and dtype == "f32") else 24
+    warps = 6 if dim == 256 else 12 if unit == 8 else 8
+    stages = 4 if dim == 64 else 3 if dim == 128 and unit > 8 else 2
+    return unit, warps * torch.cuda.get_device_properties(0).multi_processor_count, stages
+
+
+# (query heads a key/value head, new tokens): units of 8, 16 and 24 rows, one or several of them a sequence and head
+ROWS = {64: [(4, 1), (4, 4), (8, 3), (4, 11)], 128: [(7, 1), (4, 4), (8, 3), (8, 5)], 256: [(4, 2), (8, 2)]}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim,group,new", [(d, g, n) for d in ROWS for g, n in ROWS[d]])
+@pytest.mark.parametrize("heads,page,window", [(4, 32, 0), (3, 256, 0), (4, 96, 700)])
+def test_workers_go_many_times_round_their_rings(dtype, dim, group, new, heads, page, window):
+    """Ragged sequences with idle slots between them: at least twelve records and three ring turns a worker,
+    ranges that hold whole units, ends of units, pages and windows of the page table.  All rows against 64 bits,
+    with the bound of the other attention tests."""
+    gen = torch.Generator(device="cuda").manual_seed(dim + group + new + page)
+    unit, workers, stages = stream_shape(dim, group * new, dtype)
+    lens, news, records = [], [], 0
+    while records < workers * max(12, 3 * stages):
+        i = len(lens)
+        n = 40 + int(4300 * ((i * 0.6180339887 + 0.1) % 1.0) ** 1.5)
+        m = 0 if i % 7 == 3 else new if i % 3 else 1 + i % new
+        first = max(0, n - m - window + 1) if window else 0
+        records += heads * -(-m * group // unit) * (-(-n // 32) - first // 32)
+        lens.append(n)
+        news.append(m)
+    need = [-(-n // page) for n in lens]
+    data, k, v = make_records(sum(need) + 1, heads, page, dim, gen, -127)
+    order = torch.randperm(sum(need) + 1, device="cuda", generator=gen)
+    table = torch.full((len(lens), max(need)), -3, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    starts = [0]
+    for m in news:
+        starts.append(starts[-1] + m)
+    T, H = starts[-1], heads * group
+    batch = mmq.KVBatch(int32(starts), int32(lens), table, T, new)
+    q = torch.randn((T, H, dim), device="cuda", generator=gen).to(DT[dtype])
+    scale = 1 / math.sqrt(dim)
+    out, lse = torch.full_like(q, float("nan")), torch.full((T, H), float("nan"), device="cuda")
+    mmq.mmq_profile_read(reset=True)
+    before = mmq.mmq_profile_enable(True)
+    mmq.mmq_kv_attend(mmq.KVCache(data), batch, q, scale=scale, window=window, out=out, lse=lse)
+    torch.cuda.synchronize()
+    mmq.mmq_profile_enable(before)
+    assert "k_kv_attend_stream" in mmq.mmq_profile_read(reset=True)
+    assert mmq.mmq_get_device_error() == 0
+    e = 2.0 ** -22 if dtype == "f32" else 2.0 ** -11
+    for b, (n, m) in enumerate(zip(lens, news)):
+        if m == 0:
+            continue
+        pages = table[b, :need[b]].long()
+        kk, vv = (x[:, pages].reshape(heads, -1, dim)[:, :n] for x in (k, v))
+        rows = slice(starts[b], starts[b + 1])
+        x = q[rows].double().view(m, heads, group, dim).transpose(0, 1).reshape(heads, m * group, dim)
+        pos = torch.arange(n - m, n, device="cuda").repeat_interleave(group)[:, None]
+        key = torch.arange(n, device="cuda")[None]
+        seen = (key <= pos) & (key > pos - window) if window else key <= pos
+        s = (x @ kk.transpose(1, 2) * scale).masked_fill(~seen, -math.inf)
+        big = (x.abs() @ kk.abs().transpose(1, 2) * scale).masked_fill(~seen, 0).amax(-1)
+        w = s.softmax(-1)
+
+        def back(t):
+            return t.view(heads, m, group, -1).transpose(0, 1).reshape(m, H, -1)
+
+        want, size, f = back(w @ vv), back(w @ vv.abs()), 2.0 ** -19 * (4 + back(big))
+        bound = UNIT[dtype] * want.abs() + (2.0 ** -25 if dtype == "f16" else 0) + (e + f) * size + \
+            2.0 ** -31 * n * float(vv.abs().max())
+        off = (out[rows].double() - want).abs()
+        assert bool((off <= bound).all()), f"sequence {b}: {float((off / bound).max())} of the bound"
+        ref = back(s.logsumexp(-1)[..., None])[..., 0]
+        assert bool(((lse[rows].double() - ref).abs() <= 2 * f[..., 0] + 2.0 ** -22 * ref.abs()).all())
