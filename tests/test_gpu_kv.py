@@ -764,3 +764,53 @@ def test_rows_past_the_rotation_tables_are_skipped(dtype, rotary, news, lens, ro
                           v.float().numpy(), 64, (cos, sin, False))
     assert np.array_equal(cache.data.cpu().numpy(), ref)
     assert torch.equal(out.cpu(), torch.from_numpy(want).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("what,appended", [("page", (0, 1, 2)), ("length", (0, 2)), ("negative", (0, 2)), ("starts", (2,)),
+                                           ("past tokens", (0, 1)), ("max_new", (2,))])
+def test_what_is_out_of_range_is_all_that_is_skipped(what, new, appended):
+    """Values out of range in device memory, one kind at a time: the sequences that are in order are appended and
+    attended to, rows and records of the others keep what they held; of a wrong page, its own records alone."""
+    c = Case(97, [90, 80, 70], [new] * 3, 4, 2, 64, 32, "f32")
+    cache, batch = c.upload()
+    q, k, v = (c.rows(h) for h in (4, 2, 2))
+    starts, lens, table = c.starts.copy(), list(c.lens), c.table.copy()
+    if what == "page":
+        table[1, 2] = c.pages
+    elif what == "length":
+        lens[1] = table.shape[1] * 32 + 1
+    elif what == "negative":
+        lens[1] = -1
+    elif what == "starts":
+        starts[1] = 3 * new + 5
+    elif what == "past tokens":
+        starts[3] = 3 * new + 1
+    else:
+        starts[1] = 0  # sequence 1 has twice as many
+    batch.starts.copy_(torch.from_numpy(starts))
+    batch.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    batch.table.copy_(torch.from_numpy(table))
+    turned, out, lse = (torch.full(s, 9.0, device="cuda") for s in (q.shape, q.shape, q.shape[:2]))
+    mmq.mmq_kv_append(cache, batch, k.cuda(), v.cuda(), q=q.cuda(), q_out=turned)
+    torch.cuda.synchronize()
+    assert mmq.mmq_get_device_error() == MMQ_ERR_RANGE
+    mmq.mmq_kv_attend(cache, batch, q.cuda(), scale=0.1, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert mmq.mmq_get_device_error() == MMQ_ERR_RANGE
+    ref = np.concatenate([c.data, c.data[:1]])  # one more page takes what the wrong one would
+    at = np.zeros(c.T, bool)
+    for b in appended:
+        kv_ref.append(ref, [starts[b], starts[b + 1]], [lens[b]], table[b:b + 1], k.numpy(), v.numpy(), 64)
+        at[starts[b]:starts[b + 1]] = True
+    ref = ref[:c.pages]
+    assert np.array_equal(cache.data.cpu().numpy(), ref)
+    assert torch.equal(turned[at].cpu(), q[at]) and (turned[~at] == 9.0).all()
+    assert (out[~at] == 9.0).all() and (lse[~at] == 9.0).all()
+    for b in appended:
+        if what == "page" and b == 1:
+            continue
+        one = Case.__new__(Case)
+        one.data, one.starts, one.lens, one.table, one.D, one.dt = ref, [0, new], [lens[b]], table[b:b + 1], 64, "f32"
+        rows = slice(starts[b], starts[b + 1])
+        compare_attend(one, out[rows], lse[rows], q[rows], 0.1)
