@@ -11,6 +11,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "kv.cuh"
 
 namespace mmq {
 
@@ -28,7 +29,6 @@ int launch_status(const char* fn) {
 }
 
 bool tc_available();
-unsigned kv_cache_take_error();
 unsigned kv_stream_take_error();
 unsigned kv_tile_take_error();
 

@@ -36,7 +36,6 @@ __host__ __device__ constexpr int kq_qs_off(int fmt) { return fmt == FMT_Q5_K ? 
 
 // Error bits a kernel may set in its translation unit's device error word.
 constexpr unsigned ERR_TIMEOUT = 1u;
-constexpr unsigned ERR_RANGE = 2u;  // a value in device memory outside its range
 
 __device__ __forceinline__ float f16_bits_to_f32(uint32_t bits16) {
     return __half2float(__ushort_as_half((unsigned short)(bits16 & 0xffffu)));

@@ -7,9 +7,12 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
-#include "ptx.cuh"
+#include "kv_ptx.cuh"
 
 namespace mmq {
+
+constexpr unsigned ERR_RANGE = 2u;  // error bit beside ERR_TIMEOUT: a value in device memory outside its range
+
 namespace kv {
 
 constexpr int BT = 32;                 // tokens per block (one scale per head)
