@@ -422,7 +422,8 @@ int mmq_last_path(void);
  *   int8 kc[32][dim] @0, int8 vc[32][dim] @32*dim, f32 dk @64*dim, f32 dv @64*dim + 4,
  *   8 reserved bytes: 64*dim + 16 bytes (mmq_kv_block_bytes), and the key of token i is
  *   kc[i][:] * dk, its value vc[i][:] * dv.  One contiguous 16-byte-strided record brings a
- *   block's codes and scales in one copy.
+ *   block's codes and scales in one copy.  Scales are finite and never negative, in records
+ *   that a program writes itself too: attention takes that for granted.
  * The cache is [pages][heads][page/32] records.  Token p of sequence b lies in page
  * table[b][p / page], block (p % page) / 32, row p % 32.
  *
@@ -496,6 +497,12 @@ size_t mmq_kv_block_bytes(int64_t dim);
  *   new codes clamp(rint(x / d'), -127, 127) (IEEE divisions, ties to even; 0 where d' = 0).
  * Bit-exact by that definition.  Rows of the record past the sequence's end keep their bytes;
  * padding rows of q_out are left alone.  So are both where a position is past the rotation tables.
+ * What that keeps of normal values, heads of 128, relative error of a block: 0.9 % appended at
+ * once, 1.0 % token by token; where tokens grow from 1 to 8, 1.2 and 2.4 %, as the older codes
+ * are rounded again at each growth.  A block's scale never shrinks while tokens stay in it:
+ * drafted tokens that are rejected and overwritten leave theirs behind (four of eight times the
+ * size: 6 % on the tokens before them).  Appending the block once more from its first token
+ * (rope NULL), with what mmq_kv_read gave before the drafts, takes that back.
  * A record must belong to one sequence of the batch: pages that sequences share are only read.
  * Finite inputs are required: a NaN or an infinity leaves the codes and the scale of its own
  * record (keys or values) unspecified, and a rotated query row its own values.  Errors:

@@ -225,3 +225,64 @@ def test_more_records_than_can_be_numbered_are_refused(change, capfd):
     big = change["seqs"] > 1 << 23
     assert call("attend", table_stride=change["table_pages"], **change) == (SHAPE if big else 0)
     assert ("2^31" in capfd.readouterr().err) == big
+
+
+def grown(steps, dim=128, seed=3):
+    """One block of 32 normal tokens, appended steps[i] at a time, token t times size(t): what was put in, what the
+    cache holds after each step, and the key scales that the block has had."""
+    rng = np.random.default_rng(seed)
+
+    def fill(size):
+        x = (rng.normal(0, 1, (32, 1, dim)) * np.array([size(t) for t in range(32)])[:, None, None]).astype(np.float32)
+        data, table, n, scales = np.zeros((1, 1, 1, kv_ref.rec_bytes(dim)), np.uint8), np.array([[0]]), 0, []
+        for m in steps:
+            kv_ref.append(data, [0, m], [n + m], table, x[n:n + m], x[n:n + m], dim)
+            n += m
+            scales.append(float(kv_ref.split(data[0, 0, 0], dim)[2][0]))
+        return x, kv_ref.values(data, table, 0, n, dim, 0), scales
+
+    return fill
+
+
+def rms(x):
+    return float(np.sqrt(np.mean(np.square(x))))
+
+
+@pytest.mark.parametrize("size", [lambda t: 1.0, lambda t: 1.0 + 7.0 * t / 31])
+def test_what_a_block_rounds_away(size):
+    """A token is rounded under its block's scale, by half a step at most, and once more by half of the new step
+    whenever the scale grows; a rounding's deviation is step / sqrt(12)."""
+    x, got, scales = grown([32])(size)
+    assert np.abs(got - x).max() <= scales[0] / 2 * (1 + 1e-5)
+    assert rms(got - x) <= 1.1 * scales[0] / np.sqrt(12)
+    x, got, scales = grown([1] * 32)(size)
+    for t in range(32):
+        seen = sorted(set(scales[t:]))
+        assert np.abs(got[t] - x[t]).max() <= sum(seen) / 2 * (1 + 1e-5)
+        assert rms(got[t] - x[t]) <= 1.5 * np.sqrt(sum(d * d for d in seen) / 12)
+
+
+def test_rejected_drafts_leave_their_scale_and_a_new_append_of_the_block_takes_it_back():
+    """Four drafts of eight times the size behind 20 tokens, then the sequence goes on from token 20: the block keeps
+    the drafts' scale, and its older tokens are rounded under it.  Appended once more from the block's beginning,
+    with what the cache held before the drafts, they are what they were."""
+    dim, table = 128, np.array([[0]])
+    rng = np.random.default_rng(7)
+    x, drafts, more = (rng.normal(0, s, (n, 1, dim)).astype(np.float32) for n, s in ((20, 1.0), (4, 8.0), (12, 1.0)))
+    data = np.zeros((1, 1, 1, kv_ref.rec_bytes(dim)), np.uint8)
+    kv_ref.append(data, [0, 20], [20], table, x, x, dim)
+    before = [kv_ref.values(data, table, 0, 20, dim, w, np.float32) for w in (0, 1)]
+    small = float(kv_ref.split(data[0, 0, 0], dim)[2][0])
+    kv_ref.append(data, [0, 4], [24], table, drafts, drafts, dim)
+    large = float(kv_ref.split(data[0, 0, 0], dim)[2][0])
+    assert large > 6 * small
+    left = data.copy()
+    kv_ref.append(left, [0, 12], [32], table, more, more, dim)
+    assert float(kv_ref.split(left[0, 0, 0], dim)[2][0]) == np.float32(large)
+    off = kv_ref.values(left, table, 0, 20, dim, 0) - x
+    assert np.abs(off).max() <= (small + large) / 2 * (1 + 1e-5)
+    assert 0.8 * large / np.sqrt(12) <= rms(off) <= 1.2 * large / np.sqrt(12)
+    kv_ref.append(data, [0, 32], [32], table, np.concatenate([before[0], more]), np.concatenate([before[1], more]), dim)
+    scale = float(kv_ref.split(data[0, 0, 0], dim)[2][0])
+    assert scale <= 1.3 * small
+    assert rms(kv_ref.values(data, table, 0, 20, dim, 0) - x) <= 1.5 * np.sqrt((small ** 2 + scale ** 2) / 12)
