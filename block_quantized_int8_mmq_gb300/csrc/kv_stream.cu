@@ -25,10 +25,13 @@
 //
 // Measured (GB300): 64 sequences of 1000 to 8191 tokens, 4 rows a head, 614 MB of records: 108 us,
 // 5.7 TB/s, 0.84 of the copy rate, with an issue slot used in 0.45 of the cycles and the tensor pipe in
-// 0.14.  One sequence of 131069 tokens, 135 MB: 36 us; a CTA's prologue (lengths, first table entries,
-// first records: three dependent trips to memory), its parts' join and the CTAs' are about 15 us of any
-// call, and one of 777 tokens takes 12.2 us.  Past 8 rows the warps' instructions bound it: a record
+// 0.14.  One sequence of 131069 tokens, 135 MB: 36 us; of 777 tokens, f32: 12.8 us, which are a CTA's prologue
+// (lengths, first table entries, first records: three dependent trips to memory), a record's chain, its parts'
+// join and the CTAs'.  The two large calls are 16 to 17 us above their bytes; how much of that is the same
+// prologue and joins was not taken apart.  Past 8 rows the warps' instructions bound it: a record
 // takes a warp 2.6 us at 24 rows of 128 where eight share an SM.
+// Registers: all but 24 rows of 128 (16-bit), 8 and 16 of 128 and 8 of 256 (f32) fit without a spill; those
+// keep 12 to 108 bytes a thread on the stack.
 #include "kv_attend.cuh"
 #include "umma.cuh"
 
@@ -678,14 +681,16 @@ int launch_rows(const Attend& a, int rows, cudaStream_t s) {
 //   128, 16-bit, 24   31.7 / 41.9   28.3 / 42.2   84.5 / 138   56.3 / 87      322 / 584
 //                48   48.1 / 42.2   42.1 / 43.8    123 / 140   86.7 / 94      618 / 584
 //                64   50.0 / 42.4   49.0 / 43.6    149 / 142    120 / 93      912 / 584
-//   128, f32,    48   40.8 / 52.6   41.9 / 60.4    113 / 249    110 / 164     842 / 1199
-//                64   49.1 / 53.7   49.0 / 60.7    143 / 248    137 / 164    1112 / 1201
+//   128, f32,    48   42.8 / 52.8   44.2 / 61.1    128 / 249    120 / 165     954 / 1204
+//                64   52.3 / 54.1   52.1 / 61.0    160 / 251    152 / 165    1249 / 1205
 //    64, 16-bit, 48   31.1 / 35.4   30.1 / 35.1   74.2 / 107   59.4 / 74      428 / 508
 //                64   33.2 / 35.4   35.1 / 34.9   91.7 / 108   81.2 / 74      633 / 508
 //   256, 16-bit, 16   39.0 / 42.5   37.9 / 46.5   99.7 / 166   94.0 / 130     754 / 962
 //                24   46.5 / 43.8   47.1 / 47.0    131 / 174    131 / 131    1111 / 965
-//   256, f32,    32   57.7 / 64.2   67.6 / 79.9    188 / 284    204 / 245    1720 / 2026
-//                48   72.1 / 68.5   92.9 / 84.3    271 / 300    297 / 253    2536 / 2031
+//    64, f32,    48   33.2 / 36.1   34.1 / 41.6   87.2 / 140   73.7 / 108     555 / 823
+//                64   35.9 / 36.4   39.3 / 41.6    109 / 144    103 / 108     826 / 823
+//   256, f32,    32   62.3 / 64.2   71.3 / 79.9    201 / 285    219 / 244    1878 / 2025
+//                48   78.6 / 68.5   98.4 / 83.6    293 / 299    320 / 253    2767 / 2031
 // Where most sequences have fewer rows than the longest one the stream gains, the tiles do not: 8 sequences
 // of 517 to 3001 tokens with 14 to 35 rows of 128 take 30.1 us there, 32.2 in the tiles.
 int kv_stream_rows(int dim, int dtype) {

@@ -25,6 +25,9 @@
 // cycles), and S, maximum, weights and P are a chain that the other tile's products cover in part.  Short
 // prompts pay their units' ends (queries to f16 tiles, an empty pipeline, the output), five tiles' time
 // each: 2048 tokens, 28 heads over 4, 53.4 us where the same work inside a long one would be 26.
+// Registers: the launch's 168 a thread are the compiler's limit, whatever the split gives later; every instance
+// spills, 140 to 268 bytes a thread stored, f32 rows of 128 640 (their flushed output alone is 128 registers
+// beside 64 of S).
 #include "kv_attend.cuh"
 #include "umma.cuh"
 
@@ -104,7 +107,10 @@ constexpr int JOIN = 8;  // parts joined at a time (three levels: up to 512 CTAs
 
 // Units that are short beside a CTA's share are dealt whole instead: the longest first, round after round in
 // turning order (0 .. W - 1, W - 1 .. 0, ..), where the longest of the shares that come of it is at most
-// CUT key tiles above the even share: what cutting costs (a second piece of a unit, a join).
+// CUT key tiles above the even share.  What cutting costs, a second piece of a unit and a join, is seven of the tiles
+// that OVERHEAD was fitted to (128 keys, 16 bits); CUT is fitted too, at 5 / 7 / 9: a 1024-token bf16 prompt 40.3 / 33.0 /
+// 33.0 us, the f32 prompts below 88.0 / 88.2 / 79.9.  Both count tiles of 64 and 32 keys (f32, heads of 256), which
+// take less time, the same; a figure for each was not measured.
 // Measured dealt / cut, us: one prompt of 1024 tokens 33.0 / 39.3, 2048 54.4 / 70.9, 4096 157 / 189, 8192 465 / 507; sixteen
 // of 100 to 900 on 900 to 1200 196 / 236; f32 79.4 / 87.7; where it would leave SMs idle (700 of 3000 with 16 heads of
 // 64: 48 units) 55.8 / 38.7.  Its price where units are cut all the same, with / without the code for it: 1 to 4 us of
