@@ -305,7 +305,7 @@ def mmq_kv_attend(cache, batch, q, scale=None, window: int = 0, out=None, lse=No
     sees (0: all).  lse: an f32 [tokens, q heads] tensor for the logarithm of the softmax's sum.
     workspace: a uint8 tensor of mmq_kv_workspace_bytes(dim) bytes, its first 16384 zero, that no call
     that may overlap this one uses.  By default the package keeps one for each stream, and a captured call
-    has one of the graph's own, zeroed by a node of the graph that a workspace given here saves."""
+    has one of the graph's own, zeroed by a node of the graph (1 us) that a workspace given here saves."""
     dt, dev, qs, qshape = q.dtype, cache.device, q.stride(), q.shape
     _here(dev)
     d = _DTYPES.get(dt)

@@ -814,3 +814,27 @@ def test_what_is_out_of_range_is_all_that_is_skipped(what, new, appended):
         one.data, one.starts, one.lens, one.table, one.D, one.dt = ref, [0, new], [lens[b]], table[b:b + 1], 64, "f32"
         rows = slice(starts[b], starts[b + 1])
         compare_attend(one, out[rows], lse[rows], q[rows], 0.1)
+
+
+def test_outputs_made_in_a_capture_of_a_named_stream():
+    """A call on a stream that is joined to the current one's capture, its output made by the call."""
+    c = Case(101, [900, 70], [1, 2], 8, 2, 128, 64, "f16")
+    cache, batch = c.upload()
+    q = c.rows(8)
+    qd, side = q.cuda(), torch.cuda.Stream()
+    mmq.mmq_kv_attend(cache, batch, qd, scale=0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        first = mmq.mmq_kv_attend(cache, batch, qd, scale=0.1, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        del first
+        out = mmq.mmq_kv_attend(cache, batch, qd, scale=0.1, stream=side.cuda_stream)
+        torch.cuda.current_stream().wait_stream(side)
+        kept = out + 0
+    for _ in range(2):
+        kept.zero_()
+        graph.replay()
+        clean()
+        compare_attend(c, kept, None, q, 0.1)
