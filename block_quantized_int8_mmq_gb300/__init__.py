@@ -30,6 +30,7 @@ EXPORTED = (
     "mmq_debug_small_route", "mmq_debug_expand_tiling", "mmq_gemm_grouped_q6_k", "mmq_debug_small_ksplit",
     "mmq_debug_small_grid",
     "mmq_kv_block_bytes", "mmq_kv_append", "mmq_kv_read", "mmq_kv_workspace_bytes", "mmq_kv_attend",
+    "mmq_project", "mmq_gated", "mmq_project_backward", "mmq_gated_backward",
 )
 
 
@@ -330,13 +331,20 @@ def mmq_linear(x, wq, fmt: str, N: int, xq=None, out=None, stream=None):
 
 _KV = ("KVBatch", "KVCache", "Rope", "mmq_kv_append", "mmq_kv_attend", "mmq_kv_block_bytes", "mmq_kv_read",
        "mmq_kv_workspace_bytes")
+_FFN = ("mmq_gated", "mmq_gated_backward", "mmq_project", "mmq_project_backward")
 
 
 def __getattr__(name):
-    """The key/value cache's names come with their module (which imports torch) when first used."""
+    """The key/value cache's and the feed-forward operators' names come with their modules (which import
+    torch) when first used."""
     if name in _KV:
         from . import kv
         for n in _KV:
             globals()[n] = getattr(kv, n)
+        return globals()[name]
+    if name in _FFN:
+        from . import ffn
+        for n in _FFN:
+            globals()[n] = getattr(ffn, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

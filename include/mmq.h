@@ -553,6 +553,52 @@ int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtyp
                   int64_t q_heads, float scale, int64_t window, void* out, float* lse, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/*
+ * ------------------------------------------- feed-forward operators over quantized weights
+ *
+ * The products of a feed-forward block with what follows them in their epilogues, and the way back
+ * to their inputs.  The rows enter as they are (not quantized), in f32, bf16 or f16 (`dtype`, the type
+ * of x, residual, pre, out and the gradients alike); the weights are the formats above, frozen.
+ *   project:           z = x W^T + bias,  out = act(z) + residual
+ *   gated:             g = x Wg^T + bg,  u = x Wu^T + bu,  out = act(g) u
+ *   project_backward:  dz = dy act'(z),  dx = dz W
+ *   gated_backward:    dg = dh u act'(g),  du = dh act(g),  dx = dg Wg + du Wu
+ * with W the [N][K] values that the blocks stand for.
+ *   fmt: 0 = Q8_0, 1 = Q4_K, 2 = Q5_K, 3 = Q6_K.  M >= 0 rows (0: nothing is done), N and K >= 1,
+ *   K a multiple of 32 (Q8_0) or 256; each below 2^30, products of two below 2^40.
+ *   Weights: 16-byte aligned, as for the contractions.  x: [M][K], every row 16-byte aligned (base and
+ *   x_stride, in elements).  dy, dh, residual: [M][N] with a row stride (in elements) of at least N;
+ *   pre, gate, up, dz, dgate, dup: [M][N] contiguous; out, dx: contiguous; all aligned to their elements.
+ *   Biases: f32 [N], NULL for none.  residual NULL for none; it may be out itself.  No other array
+ *   that is written may overlap one that is read or written.
+ *   pre, gate, up (forward): NULL, or where z, g and u go for the backward pass, rounded to `dtype`; out
+ *   is formed from the unrounded values.  dz, dgate, dup: NULL, or where the gradients of z, g and u go
+ *   (sums of their columns are the biases' gradients; with the rows, those of an adapter).
+ *   pre (backward): NULL is allowed where act is MMQ_ACT_NONE, and it is not read then.
+ * Accuracy: sums, biases, activations and the epilogue are f32; outputs are rounded once.
+ * Finite inputs are required: a NaN or an infinity in a row leaves that row's outputs unspecified, and
+ * no other's.  The order of summation depends on the sizes alone, so repeated calls give the same bits.
+ * Scratch: stream-ordered, as the expanded path's.
+ * Errors: MMQ_ERR_ARG (fmt, dtype, act), MMQ_ERR_SHAPE, MMQ_ERR_K_MULTIPLE, MMQ_ERR_NULL,
+ * MMQ_ERR_ALIGN, MMQ_ERR_SMEM, MMQ_ERR_NOMEM, MMQ_ERR_LAUNCH.
+ */
+
+/* act(z): z;  z / (1 + e^-z);  z Phi(z);  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2;  max(z, 0), its
+ * derivative 0 at 0. */
+enum { MMQ_ACT_NONE = 0, MMQ_ACT_SILU = 1, MMQ_ACT_GELU = 2, MMQ_ACT_GELU_TANH = 3, MMQ_ACT_RELU = 4 };
+
+int mmq_project(int fmt, int dtype, const void* x, int64_t x_stride, int64_t M, const void* wq, int64_t N, int64_t K,
+                const float* bias, int act, const void* residual, int64_t residual_stride, void* pre, void* out,
+                void* stream);
+int mmq_gated(int fmt, int dtype, const void* x, int64_t x_stride, int64_t M, const void* w_gate, const void* w_up,
+              int64_t N, int64_t K, const float* bias_gate, const float* bias_up, int act, void* gate, void* up, void* out,
+              void* stream);
+int mmq_project_backward(int fmt, int dtype, const void* dy, int64_t dy_stride, int64_t M, const void* wq, int64_t N,
+                         int64_t K, int act, const void* pre, void* dz, void* dx, void* stream);
+int mmq_gated_backward(int fmt, int dtype, const void* dh, int64_t dh_stride, int64_t M, const void* w_gate,
+                       const void* w_up, int64_t N, int64_t K, int act, const void* gate, const void* up, void* dgate,
+                       void* dup, void* dx, void* stream);
+
 /* Per-kernel device timing, for tests and benchmarks.  While enabled, every kernel the
  * library launches is bracketed by two CUDA events on its stream.  On a stream being
  * captured into a graph the two records become event-record nodes of the graph (their
