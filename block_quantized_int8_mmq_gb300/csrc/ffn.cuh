@@ -28,6 +28,58 @@ struct Call {
     void* out;
 };
 
+// What the row kernels write: f16 tiles, per step of 64 values and group of 8 rows 1024 bytes.
+struct Rows {
+    const void* x;
+    long long stride;
+    int dtype, act, mats, rows, width, groups;
+    const void* pre[2];
+    void* dz[2];
+    uint8_t* tiles;
+    long long term;  // bytes from the first terms to the second
+    float* up;
+    unsigned* counters;
+    int n_counters;
+};
+
+struct Tile {
+    const uint8_t* w[2];
+    long long w_bytes, row_bytes;  // of a weight matrix, of a row
+    const uint8_t* x;              // the rows' tiles
+    long long x_term;
+    const float* up;
+    float* parts;
+    unsigned* counters;
+    int mats, M, N, K, width;    // width: of the output
+    int groups, mtiles, nt;      // groups of 8 rows, row tiles, rows in a tile (a multiple of 16)
+    int units, steps, chunks;    // steps (64 values of the reduction) and chunks of a unit
+    int rounds, rest;            // rounds of whole units, then `rest` units cut into equal runs of chunks
+    int aligned, slot, rs, xs;   // weight rows begin on 16 bytes; bytes of a chunk's place; ring lengths
+    int dtype, act;
+    const float* bias[2];
+    const void* residual;
+    long long residual_stride;
+    void* pre[2];
+    void* out;
+};
+
+constexpr int W_WARPS = 8, THREADS = (W_WARPS + 2) * 32;
+constexpr int STEP = 64;     // values of the reduction that are multiplied together
+constexpr int CHUNK = 256;   // values of a weight row that are copied together
+constexpr int X_MOST = 8, R_MOST = 8;  // longest rings
+template <bool SPLIT>
+struct Shape {
+    static constexpr int TERMS = SPLIT ? 2 : 1;
+    static constexpr int NT = SPLIT ? 64 : 192;     // rows of x in a tile, at most
+    static constexpr int DB = SPLIT ? 2 : 1;        // accumulator buffers
+    static constexpr int D_COLS = 2 * NT;           // of a buffer: two weight tiles
+    static constexpr int COL_A = DB * D_COLS;       // forward: weights, two stages
+    static constexpr int A_COLS = 64 * TERMS;       // of a stage: two tiles, 32 columns a term
+    static constexpr int A_BYTES = STEP * CHUNK * 2;  // backward: a stage's term in shared memory
+    static_assert(COL_A + 2 * A_COLS <= 512, "TMEM columns");
+};
+constexpr int SMEM_MOST = 232448 - 2048;  // less what is static
+
 __device__ __forceinline__ float load(const void* p, int dtype, long long i) {
     if (dtype == MMQ_F32) return static_cast<const float*>(p)[i];
     if (dtype == MMQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -68,6 +120,8 @@ __device__ __forceinline__ void activate(int act, float z, float& a, float& d) {
 }  // namespace ffn
 
 int ffn_launch(const ffn::Call& c, cudaStream_t s);
-unsigned ffn_take_error();
+int ffn_rows_launch(const ffn::Rows& r, bool back, const char* fn, cudaStream_t s);
+int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s);
+int ffn_backward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s);
 
 }  // namespace mmq

@@ -1,0 +1,24 @@
+// The products of the forward pass: the instances of k_ffn_tile (ffn_tile.cuh) for each format and type.
+#include "ffn_tile.cuh"
+
+namespace mmq {
+namespace {
+
+template <int FMT>
+int launch(const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+    return a.dtype == MMQ_F32 ? ffn::launch_tile<FMT, true, false>(a, smem, ctas, fn, s)
+                              : ffn::launch_tile<FMT, false, false>(a, smem, ctas, fn, s);
+}
+
+}  // namespace
+
+int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, fn, s);
+    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, fn, s);
+    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, fn, s);
+    return launch<FMT_Q6_K>(a, smem, ctas, fn, s);
+}
+
+unsigned ffn_forward_take_error() { return ffn::take_tile_error(); }
+
+}  // namespace mmq

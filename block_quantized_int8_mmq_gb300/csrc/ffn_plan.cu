@@ -1,0 +1,120 @@
+// How a feed-forward call is laid out on the GPU (row tiles, rounds, cuts, rings, scratch memory), and its two
+// launches: the rows as operands, then the products.
+#include "ffn_weights.cuh"
+
+namespace mmq {
+namespace {
+
+using namespace ffn;
+
+constexpr long long up_to(long long n, long long unit) { return (n + unit - 1) / unit * unit; }
+constexpr long long ceil_div(long long n, long long d) { return (n + d - 1) / d; }
+
+// Times in us, for the choice between whole and cut units: a chunk's copies at an SM's share of HBM, its products at
+// the tensor rate; and what cutting costs, parts written and read back (nt x 256 sums each) and a counter's trip.
+struct Cost {
+    double chunk, join;
+};
+Cost cost(const Tile& a, int fmt, bool split, bool back) {
+    const double steps = back ? 1 : CHUNK / STEP;
+    const double copy = steps * STEP * chunk_bytes(fmt) / 44e3;
+    const double products = steps * 8 * (split ? 3 : 1) * (a.nt < 64 ? 64 : a.nt) / 2 / 1900.0;
+    return {copy > products ? copy : products, 2.5 + a.nt * 2048.0 / 44e3};
+}
+
+// Rounds of whole units; or, where the last round leaves too much undone, it and the one before it cut evenly.
+int deal(Tile& a, const Cost& t, int sms) {
+    const long long whole = ceil_div(a.units, sms) * a.chunks;
+    const long long full = a.units % sms == 0 ? a.units / sms : a.units < sms ? 0 : a.units / sms - 1;
+    const long long rest = a.units - full * sms;
+    if (rest > 0) {
+        const double cut = full * a.chunks + (double)ceil_div(rest * a.chunks, sms);
+        if (cut * t.chunk + t.join < whole * t.chunk) {
+            a.rounds = (int)full;
+            a.rest = (int)rest;
+            return (int)(rest * a.chunks < sms ? rest * a.chunks : sms);
+        }
+    }
+    a.rounds = (int)ceil_div(a.units, sms);
+    a.rest = 0;
+    return (int)(a.units < sms ? a.units : sms);
+}
+
+}  // namespace
+
+int ffn_launch(const Call& c, cudaStream_t s) {
+    const bool split = c.dtype == MMQ_F32;
+    const int terms = split ? 2 : 1, nt_most = split ? Shape<true>::NT : Shape<false>::NT;
+    Tile a{};
+    a.w[0] = static_cast<const uint8_t*>(c.w[0]);
+    a.w[1] = static_cast<const uint8_t*>(c.w[1]);
+    a.row_bytes = c.fmt == FMT_Q8_0 ? c.K / QK * Q8_0_BYTES : c.K / QK_K * kq_bytes(c.fmt);
+    a.w_bytes = a.row_bytes * c.N;
+    a.mats = c.mats;
+    a.M = (int)c.M;
+    a.N = (int)c.N;
+    a.K = (int)c.K;
+    a.width = c.backward ? a.K : a.N;
+    a.groups = (int)ceil_div(c.M, 8);
+    a.nt = (int)up_to(ceil_div(c.M, ceil_div(c.M, nt_most)), 16);
+    a.mtiles = (int)ceil_div(c.M, a.nt);
+    a.units = (int)(a.mtiles * ceil_div(a.width, !c.backward && c.mats == 2 ? 128 : 256));
+    a.steps = (int)(c.backward ? c.mats * ceil_div(c.N, STEP) : ceil_div(c.K, STEP));
+    a.chunks = c.backward ? a.steps : (int)ceil_div(c.K, CHUNK);
+    a.aligned = a.row_bytes % 16 == 0;
+    a.slot = slot_bytes(c.fmt, a.aligned);
+    a.dtype = c.dtype;
+    a.act = c.act;
+    for (int g = 0; g < 2; ++g) {
+        a.bias[g] = c.bias[g];
+        a.pre[g] = c.backward ? nullptr : c.pre[g];
+    }
+    a.residual = c.residual;
+    a.residual_stride = c.residual_stride;
+    a.out = c.out;
+    const int ctas = deal(a, cost(a, c.fmt, split, c.backward), device_shape().sms);
+    // shared memory: two chunks' places at least, then up to four steps of rows, then more chunks
+    const int x_bytes = a.nt * 128 * terms, w_bytes = a.slot * (c.backward ? STEP : CHUNK);
+    const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true>::A_BYTES : 0);
+    a.xs = (left - 2 * w_bytes) / x_bytes;
+    a.xs = a.xs > 4 ? 4 : a.xs;
+    a.rs = (left - a.xs * x_bytes) / w_bytes;
+    a.rs = a.rs > R_MOST ? R_MOST : a.rs;
+    const int smem = SMEM_MOST - left + a.xs * x_bytes + a.rs * w_bytes;
+
+    const long long term = (long long)a.steps * a.groups * 1024;
+    const long long counters = up_to(4ll * a.rest, 256), ups = up_to(4 * c.M, 256);
+    const long long parts = a.rest ? 2ll * ctas * 2 * a.nt * 128 * 4 : 0;
+    void* scratch = nullptr;
+    int st = scratch_alloc((size_t)(counters + ups + term * terms + parts), s, &scratch, c.fn);
+    if (st != MMQ_OK) return st;
+    uint8_t* at = static_cast<uint8_t*>(scratch);
+    Rows r{};
+    r.x = c.x;
+    r.stride = c.x_stride;
+    r.dtype = c.dtype;
+    r.act = c.act;
+    r.mats = c.mats;
+    r.rows = a.M;
+    r.width = c.backward ? a.N : a.K;
+    r.groups = a.groups;
+    for (int g = 0; g < 2; ++g) {
+        r.pre[g] = c.backward ? c.pre[g] : nullptr;
+        r.dz[g] = c.dz[g];
+    }
+    r.counters = a.counters = reinterpret_cast<unsigned*>(at);
+    r.n_counters = a.rest;
+    r.up = reinterpret_cast<float*>(at + counters);
+    a.up = r.up;
+    r.tiles = at + counters + ups;
+    r.term = a.x_term = term;
+    a.x = r.tiles;
+    a.parts = reinterpret_cast<float*>(r.tiles + term * terms);
+    st = ffn_rows_launch(r, c.backward, c.fn, s);
+    if (st == MMQ_OK)
+        st = c.backward ? ffn_backward_launch(c.fmt, a, smem, ctas, c.fn, s) : ffn_forward_launch(c.fmt, a, smem, ctas, c.fn, s);
+    scratch_free(scratch, s);  // stream-ordered: after the kernels above
+    return st;
+}
+
+}  // namespace mmq

@@ -1,0 +1,603 @@
+// The products of the feed-forward operators: k_ffn_tile.
+//
+// A unit is 256 weight rows (forward: 128 of gate and the same 128 of up, or 256 in a row; backward: 256
+// columns) by up to NT_MOST rows of x, summed over the whole reduction.  Weights are the M side of the tensor
+// cores' products (two tiles of 128), rows of x the N side, so one row costs what sixteen do, an output's
+// epilogue finds gate and up in one TMEM lane, and a warp stores 32 neighbouring columns at a time.  Roles of a CTA:
+//   weight warps (8)  copy chunks of 256 values of their weight rows by bulk copies into a ring of their own
+//                     and turn them into f16 (ffn_weights.cuh): forward, a thread per weight row, straight
+//                     into TMEM as the A operand; backward, where the reduction runs over weight rows, into shared
+//                     memory as an MN-major A operand (8 x 16-byte core matrices, no transpose).  Then the
+//                     epilogue, a thread per lane;
+//   a loader warp     the rows' tiles, which k_ffn_rows has laid out, one bulk copy a step and term;
+//   an issuer warp    the products, 64 values of the reduction a step.
+// f32 rows (SPLIT): rows and weights in two f16 terms each, three products, and the accumulators move to registers
+// every 256 values of the reduction: the tensor core's additions round towards zero, and over a long sum that
+// would be more than f32 allows.
+//
+// The work is dealt unit by unit in rounds; where the last round would leave too many SMs idle it and the one before
+// are laid end to end instead and cut into equal runs.  A unit that is cut leaves its parts in scratch memory, and the
+// last CTA to arrive adds them in their order: the order of summation depends on the sizes alone.
+#pragma once
+
+#include <type_traits>
+
+#include "ffn_weights.cuh"
+#include "kv.cuh"
+
+namespace mmq {
+namespace ffn {
+
+static __device__ unsigned g_ffn_tile_error;  // of each translation unit its own
+
+constexpr int PERIOD = 4;  // SPLIT: steps between two moves of the accumulators
+
+// The pieces of work of a CTA: (unit, first chunk, end).
+struct Pieces {
+    int r = 0;
+    long long x, x1;
+    __device__ __forceinline__ explicit Pieces(const Tile& a) {
+        const long long all = (long long)a.rest * a.chunks;
+        x = all * blockIdx.x / gridDim.x;
+        x1 = all * (blockIdx.x + 1) / gridDim.x;
+    }
+    __device__ __forceinline__ bool next(const Tile& a, int& unit, int& c0, int& c1) {
+        if (r < a.rounds) {
+            unit = r++ * (int)gridDim.x + (int)blockIdx.x;
+            c0 = 0;
+            c1 = a.chunks;
+            if (unit < a.units - a.rest) return true;
+        }
+        if (x >= x1) return false;
+        const int u = (int)(x / a.chunks);
+        unit = a.units - a.rest + u;
+        c0 = (int)(x - (long long)u * a.chunks);
+        c1 = (int)min((long long)a.chunks, c0 + (x1 - x));
+        x += c1 - c0;
+        return true;
+    }
+};
+// the CTA whose run holds chunk x of the units that are cut
+__device__ __forceinline__ int run_owner(const Tile& a, long long x) {
+    return (int)(((x + 1) * gridDim.x - 1) / ((long long)a.rest * a.chunks));
+}
+
+__device__ __forceinline__ void sync_weight_warps() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
+    if (act == MMQ_ACT_NONE) return;
+#define MMQ_ACT_CASE(A)                   \
+    if (act == A)                         \
+        _Pragma("unroll") for (int i = 0; i < 8; ++i) { \
+            float a, d;                   \
+            activate(A, v[i], a, d);      \
+            v[i] = a;                     \
+        }
+    MMQ_ACT_CASE(MMQ_ACT_SILU)
+    MMQ_ACT_CASE(MMQ_ACT_GELU)
+    MMQ_ACT_CASE(MMQ_ACT_GELU_TANH)
+    MMQ_ACT_CASE(MMQ_ACT_RELU)
+#undef MMQ_ACT_CASE
+}
+
+__device__ __forceinline__ void store8(void* p, int dtype, long long at, long long stride, int count, const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < count) store(p, dtype, at + i * stride, v[i]);
+}
+
+// Eight rows of x, m .. m + count - 1, of the output columns of a lane: z0, z1 are the sums of its two tiles.
+template <bool BACK>
+__device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, int m, int count, float (&z0)[8],
+                                        float (&z1)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float up = i < count ? __ldg(a.up + m + i) : 0.f;
+        z0[i] *= up;
+        z1[i] *= up;
+    }
+    if (!BACK && a.mats == 2) {
+        const int n = pair * 128 + lane_row;
+        if (n >= a.width) return;
+        const long long at = (long long)m * a.width + n;
+        if (a.bias[0]) {
+            const float b = __ldg(a.bias[0] + n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z0[i] += b;
+        }
+        if (a.bias[1]) {
+            const float b = __ldg(a.bias[1] + n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z1[i] += b;
+        }
+        if (a.pre[0]) store8(a.pre[0], a.dtype, at, a.width, count, z0);
+        if (a.pre[1]) store8(a.pre[1], a.dtype, at, a.width, count, z1);
+        activate8(a.act, z0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z0[i] *= z1[i];
+        store8(a.out, a.dtype, at, a.width, count, z0);
+        return;
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        float(&z)[8] = g ? z1 : z0;
+        const int n = pair * 256 + g * 128 + lane_row;
+        if (n >= a.width) continue;
+        const long long at = (long long)m * a.width + n;
+        if (!BACK) {
+            if (a.bias[0]) {
+                const float b = __ldg(a.bias[0] + n);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] += b;
+            }
+            if (a.pre[0]) store8(a.pre[0], a.dtype, at, a.width, count, z);
+            activate8(a.act, z);
+            if (a.residual) {
+                float r[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = i < count ? load(a.residual, a.dtype, (m + i) * a.residual_stride + n) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] += r[i];
+            }
+        }
+        store8(a.out, a.dtype, at, a.width, count, z);
+    }
+}
+
+template <int FMT, bool SPLIT, bool BACK>
+__global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
+    using S = Shape<SPLIT>;
+    constexpr int TERMS = S::TERMS;
+    constexpr int GW = BACK ? 4 : 1, NG = W_WARPS / GW;  // weight warps that share a ring, rings
+    constexpr int CB = chunk_bytes(FMT);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t s_bar[2 * X_MOST + 4 + 4 + NG * R_MOST + (BACK ? NG * R_MOST : 0) + 1];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_last;
+    const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const uint32_t bars = ptx::smem_u32(s_bar);
+    const uint32_t x_full = bars, x_empty = x_full + 8 * X_MOST, a_full = x_empty + 8 * X_MOST, a_empty = a_full + 16;
+    const uint32_t d_full = a_empty + 16, d_empty = d_full + 16, raw_full = d_empty + 16;
+    const uint32_t raw_empty = raw_full + 8 * NG * R_MOST, done = raw_empty + (BACK ? 8 * NG * R_MOST : 0);
+    const int xb = a.nt * 128 * TERMS;  // bytes of a step's rows
+    const uint32_t xs_addr = ptx::smem_u32(smem), as_addr = xs_addr + a.xs * xb;
+    uint8_t* a_smem = smem + a.xs * xb;
+    uint8_t* raw = a_smem + (BACK ? 2 * TERMS * S::A_BYTES : 0);
+    if (tid == 0) {
+        for (int i = 0; i < X_MOST; ++i) {
+            ptx::mbar_init(x_full + 8 * i, 1);
+            ptx::mbar_init(x_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(a_full + 8 * i, W_WARPS);
+            ptx::mbar_init(a_empty + 8 * i, 1);
+            ptx::mbar_init(d_full + 8 * i, 1);
+            ptx::mbar_init(d_empty + 8 * i, W_WARPS);
+        }
+        for (int i = 0; i < NG * R_MOST; ++i) {
+            ptx::mbar_init(raw_full + 8 * i, 1);
+            if (BACK) ptx::mbar_init(raw_empty + 8 * i, GW);
+        }
+        ptx::mbar_init(done, 1);
+        ptx::fence_barrier_init();
+        s_abort = 0;
+    }
+    if (wid == W_WARPS + 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&s_tmem), 512);
+        ptx::tmem_relinquish();
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::grid_dep_launch_dependents();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+    volatile int* abort = &s_abort;
+    unsigned* err = &g_ffn_tile_error;
+    auto step_range = [&](int c0, int c1, int& s0, int& s1) {
+        s0 = BACK ? c0 : c0 * (CHUNK / STEP);
+        s1 = BACK ? c1 : min(a.steps, c1 * (CHUNK / STEP));
+    };
+
+    if (wid < W_WARPS) {
+        // ------------------------------------------------ weights, then the epilogue
+        const int grp = BACK ? wid & 1 : wid;       // ring
+        const bool leader = !BACK || wid < 2;       // the warp that fills it
+        const int g = wid >> 2, lane_row = 32 * (wid & 3) + lane;
+        uint8_t* ring = raw + grp * a.rs * 32 * a.slot + lane * a.slot;
+        const int nsteps = (a.N + STEP - 1) / STEP;  // backward: steps of a matrix
+        // byte offset of this lane's row at a chunk, or -1
+        auto row_at = [&](int pair, int c, int& mat) -> long long {
+            if (BACK) {
+                mat = c >= nsteps;
+                const int n = (c - mat * nsteps) * STEP + 32 * grp + lane;
+                return n < a.N ? n * a.row_bytes + (long long)pair * CB : -1;
+            }
+            mat = a.mats == 2 ? g : 0;
+            const int n = (a.mats == 2 ? pair * 128 : pair * 256 + g * 128) + lane_row;
+            return n < a.N ? n * a.row_bytes + (long long)c * CB : -1;
+        };
+        // ---- the ring: chunks in the order of the pieces
+        Pieces pf(a);
+        int f_unit = 0, f_c = 0, f_c1 = 0, fetched = 0, f_slot = 0;
+        auto fetch = [&]() {
+            if (f_c == f_c1 && !pf.next(a, f_unit, f_c, f_c1)) return;
+            int mat;
+            const int pair = f_unit / a.mtiles;
+            const long long at = row_at(pair, f_c, mat);
+            const uint32_t bar = raw_full + 8 * (grp * R_MOST + f_slot);
+            uint8_t* dst = ring + f_slot * 32 * a.slot;
+            const uint8_t* src = nullptr;
+            int bytes = 0;
+            if (at >= 0) {
+                const int mis = (int)(at & 15);
+                const long long in_row = (long long)(BACK ? pair : f_c) * CB;
+                const int len = (int)min((long long)CB, a.row_bytes - in_row);
+                bytes = (mis + len + 15) & ~15;
+                src = a.w[mat] + (at - mis);
+                const long long past = at - mis + bytes - a.w_bytes;
+                if (past > 0) {  // the matrix's last bytes do not fill 16
+                    bytes -= 16;
+                    for (int i = bytes; i < mis + len; ++i) dst[i] = src[i];
+                }
+            }
+            const int total = __reduce_add_sync(0xffffffffu, bytes);  // (and the bytes above are there)
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, total);
+            __syncwarp();
+            if (bytes > 0) ptx::bulk_load(ptx::smem_u32(dst), src, bytes, bar);
+            ++f_c;
+            ++fetched;
+            if (++f_slot == a.rs) f_slot = 0;
+        };
+        if (leader)
+            for (int i = 0; i < a.rs; ++i) fetch();
+        bool ok = true, waited = false, bad = false;
+        int taken = 0, slot = 0;           // chunks processed, the ring's place
+        uint32_t par = 0;                  // its parity
+        uint32_t n_a = 0, n_d = 0;         // stages, accumulator periods so far
+        float run[SPLIT ? S::NT : 1];      // SPLIT: sums of this thread's lane of tile g
+        auto drain = [&](uint32_t period, bool last) {
+            const uint32_t b = period & 1;
+            if (!umma::warp_wait(d_full + 8 * b, (period >> 1) & 1, abort, err)) return false;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < S::NT / 16; ++c) {
+                if (16 * c >= a.nt) break;
+                uint32_t v[16];
+                ptx::tmem_ld16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + b * S::D_COLS + g * S::NT + 16 * c, v);
+                ptx::tmem_ld_wait(v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) run[SPLIT ? 16 * c + k : 0] += __uint_as_float(v[k]);
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (!last && lane == 0) ptx::mbar_arrive(d_empty + 8 * b);
+            return true;
+        };
+        Pieces pc(a);
+        int unit, c0, c1;
+        while (ok && pc.next(a, unit, c0, c1)) {
+            const int pair = unit / a.mtiles, mt = unit - pair * a.mtiles;
+            int s0, s1;
+            step_range(c0, c1, s0, s1);
+            if (SPLIT)
+#pragma unroll
+                for (int k = 0; k < (SPLIT ? S::NT : 1); ++k) run[k] = 0.f;
+            int in_piece = 0;  // steps of the piece so far
+#pragma unroll 1
+            for (int c = c0; c < c1 && ok; ++c) {
+                int mat;
+                const long long at = row_at(pair, c, mat);
+                const bool valid = at >= 0;
+                const int mis = valid ? (int)(at & 15) : 0;
+                if (!umma::warp_wait(raw_full + 8 * (grp * R_MOST + slot), par, abort, err)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* src = ring + slot * 32 * a.slot;
+                auto one = [&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    const int k0 = (BACK ? pair : c) * CHUNK + j * STEP;
+                    const int blocks = min(2, max(0, (a.K - k0) / QK));
+                    const uint32_t st = n_a & 1;
+                    quarter<FMT, SPLIT, j>(src, mis, a.aligned, blocks, valid, bad,
+                                           [&](int half, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+                        if (half == 0 && ok) ok = umma::warp_wait(a_empty + 8 * st, ((n_a >> 1) & 1) ^ 1, abort, err);
+                        if (!BACK) {
+                            if (half == 0) ptx::tc_fence_after();
+                            const uint32_t t = tmem + ((uint32_t)(32 * (wid & 3)) << 16) + S::COL_A + st * S::A_COLS +
+                                               g * 32 * TERMS + 16 * half;
+                            ptx::tmem_st16(t, hi);
+                            if (SPLIT) ptx::tmem_st16(t + 32, lo);
+                        } else {
+                            const int n = 32 * grp + lane;
+                            uint8_t* p = a_smem + st * TERMS * S::A_BYTES + (n >> 3) * 4096 + (8 * j + 4 * half) * 128 + (n & 7) * 16;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                *reinterpret_cast<uint4*>(p + 128 * i) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                                if (SPLIT)
+                                    *reinterpret_cast<uint4*>(p + S::A_BYTES + 128 * i) =
+                                        make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                            }
+                        }
+                    });
+                    if (!BACK) {
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before();
+                    } else {
+                        ptx::fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(a_full + 8 * st);
+                    ++n_a;
+                    ++in_piece;
+                    if (SPLIT && in_piece % PERIOD == 0 && in_piece > PERIOD) ok = ok && drain(n_d++, false);
+                };
+                if (BACK) {
+                    const int q = wid >> 1;
+                    if (q == 0)
+                        one(std::integral_constant<int, 0>{});
+                    else if (q == 1)
+                        one(std::integral_constant<int, 1>{});
+                    else if (q == 2)
+                        one(std::integral_constant<int, 2>{});
+                    else
+                        one(std::integral_constant<int, 3>{});
+                } else {
+                    one(std::integral_constant<int, 0>{});
+                    if (ok && 4 * c + 1 < a.steps) one(std::integral_constant<int, 1>{});
+                    if (ok && 4 * c + 2 < a.steps) one(std::integral_constant<int, 2>{});
+                    if (ok && 4 * c + 3 < a.steps) one(std::integral_constant<int, 3>{});
+                }
+                // the chunk has been read: its place is free (the fetching warp of a shared ring fills the place
+                // before this one, which the others have most likely left too)
+                __syncwarp();
+                if (BACK) {
+                    if (lane == 0) ptx::mbar_arrive(raw_empty + 8 * (grp * R_MOST + slot));
+                    if (leader && taken > 0) {
+                        const int before = taken - 1;
+                        ok = ok && umma::warp_wait(raw_empty + 8 * (grp * R_MOST + before % a.rs), (before / a.rs) & 1, abort, err);
+                        if (ok) fetch();
+                    }
+                } else {
+                    fetch();
+                }
+                ++taken;
+                if (++slot == a.rs) {
+                    slot = 0;
+                    par ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (!waited) ptx::grid_dep_wait();  // what follows reads and writes the call's rows
+            waited = true;
+            uint32_t buf = 0;
+            if (SPLIT) {
+                // the last period, and the one before it where that has not been drained
+                if (in_piece > PERIOD && in_piece % PERIOD != 0) ok = drain(n_d++, false);
+                buf = n_d & 1;
+                ok = ok && drain(n_d++, true);
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < S::NT / 16; ++c) {
+                    if (16 * c >= a.nt) break;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(run[SPLIT ? 16 * c + k : 0]);
+                    ptx::tmem_st16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + buf * S::D_COLS + g * S::NT + 16 * c, v);
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                sync_weight_warps();
+                ptx::tc_fence_after();
+            } else {
+                ok = umma::warp_wait(d_full, n_d & 1, abort, err);
+                ++n_d;
+                if (!ok) break;
+                ptx::tc_fence_after();
+            }
+            // ---- the output, or this CTA's part of it: the lane's row, half of the tile's columns
+            const bool whole = c0 == 0 && c1 == a.chunks;
+            const int m0 = mt * a.nt, m1 = min(a.M, m0 + a.nt);
+            const uint32_t src = tmem + ((uint32_t)(32 * (wid & 3)) << 16) + buf * S::D_COLS;
+            auto part = [&](int cta, int which, int tile) {
+                return a.parts + ((((long long)cta * 2 + which) * 2 + tile) * a.nt) * 128 + lane_row;
+            };
+            const int b0 = 8 * g;  // the two groups of warps take columns by turns
+#pragma unroll 1
+            for (int b = b0; m0 + b < m1; b += 16) {
+                uint32_t v0[8], v1[8];
+                ptx::tmem_ld8(src + b, v0);
+                ptx::tmem_ld8(src + S::NT + b, v1);
+                ptx::tmem_ld_wait(v0);
+                ptx::tmem_ld_wait(v1);
+                if (whole) {
+                    float z0[8], z1[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        z0[i] = __uint_as_float(v0[i]);
+                        z1[i] = __uint_as_float(v1[i]);
+                    }
+                    finish8<BACK>(a, pair, lane_row, m0 + b, min(8, m1 - m0 - b), z0, z1);
+                } else {
+                    float* p0 = part(blockIdx.x, c0 == 0, 0) + b * 128;
+                    float* p1 = part(blockIdx.x, c0 == 0, 1) + b * 128;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        p0[i * 128] = __uint_as_float(v0[i]);
+                        p1[i * 128] = __uint_as_float(v1[i]);
+                    }
+                }
+                __syncwarp();
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(d_empty + 8 * buf);
+            if (!whole) {
+                const int u = unit - (a.units - a.rest);
+                const int first = run_owner(a, (long long)u * a.chunks), last = run_owner(a, (long long)(u + 1) * a.chunks - 1);
+                sync_weight_warps();  // every warp's part is written; the counter releases and acquires them
+                if (tid == 0) s_last = ptx::atom_inc_acq_rel(a.counters + u) == (unsigned)(last - first);
+                sync_weight_warps();
+                if (s_last) {
+#pragma unroll 1
+                    for (int b = b0; m0 + b < m1; b += 16) {
+                        float z0[8], z1[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z0[i] = z1[i] = 0.f;
+#pragma unroll 2
+                        for (int cta = first; cta <= last; ++cta) {
+                            // a run that begins inside the unit is its CTA's first piece, one that begins with it the last
+                            const int which = cta == first;
+                            const float* p0 = part(cta, which, 0) + b * 128;
+                            const float* p1 = part(cta, which, 1) + b * 128;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                z0[i] += __ldcg(p0 + i * 128);
+                                z1[i] += __ldcg(p1 + i * 128);
+                            }
+                        }
+                        finish8<BACK>(a, pair, lane_row, m0 + b, min(8, m1 - m0 - b), z0, z1);
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if (bad) atomicOr(err, ERR_RANGE);
+        if (!ok && leader) {  // let the copies in flight land before the shared memory goes
+            for (int i = taken; i < fetched; ++i)
+                umma::drain_bar(raw_full + 8 * (grp * R_MOST + i % a.rs), (i / a.rs) & 1, err);
+        }
+    } else if (wid == W_WARPS) {
+        // ------------------------------------------------ the rows' tiles
+        ptx::grid_dep_wait();
+        Pieces pc(a);
+        int unit, c0, c1, st = 0, loaded = 0;
+        uint32_t par = 1;
+        bool ok = true;
+        while (ok && pc.next(a, unit, c0, c1)) {
+            const int mt = unit % a.mtiles, g0 = mt * (a.nt / 8);
+            const uint32_t bytes = min(a.nt / 8, a.groups - g0) * 1024;
+            int s0, s1;
+            step_range(c0, c1, s0, s1);
+            const uint8_t* src = a.x + ((long long)s0 * a.groups + g0) * 1024;
+#pragma unroll 1
+            for (int s = s0; s < s1; ++s, src += (long long)a.groups * 1024) {
+                if (!umma::warp_wait(x_empty + 8 * st, par, abort, err)) {
+                    ok = false;
+                    break;
+                }
+                if (ptx::elect_one()) {
+                    ptx::mbar_arrive_expect_tx(x_full + 8 * st, bytes * TERMS);
+                    ptx::bulk_load(xs_addr + st * xb, src, bytes, x_full + 8 * st);
+                    if (SPLIT) ptx::bulk_load(xs_addr + st * xb + a.nt * 128, src + a.x_term, bytes, x_full + 8 * st);
+                }
+                ++loaded;
+                if (++st == a.xs) {
+                    st = 0;
+                    par ^= 1;
+                }
+            }
+        }
+        if (!ok)
+            for (int i = max(0, loaded - a.xs); i < loaded; ++i) umma::drain_bar(x_full + 8 * (i % a.xs), (i / a.xs) & 1, err);
+    } else {
+        // ------------------------------------------------ the products
+        Pieces pc(a);
+        int unit, c0, c1, xst = 0;
+        uint32_t xpar = 0, n_a = 0, n_d = 0;
+        bool ok = true;
+        const uint32_t idesc = umma::make_idesc(128, a.nt) | (BACK ? 1u << 15 : 0u);
+        const uint32_t term_x = a.nt * 128 >> 4;
+        while (ok && pc.next(a, unit, c0, c1)) {
+            int s0, s1;
+            step_range(c0, c1, s0, s1);
+#pragma unroll 1
+            for (int s = s0; s < s1; ++s) {
+                const int i = s - s0;
+                const bool fresh = SPLIT ? i % PERIOD == 0 : i == 0, last = s + 1 == s1 || (SPLIT && i % PERIOD == PERIOD - 1);
+                const uint32_t buf = SPLIT ? n_d & 1 : 0;
+                const uint32_t st = n_a & 1;
+                if (fresh) ok = umma::warp_wait(d_empty + 8 * buf, (SPLIT ? (n_d >> 1) & 1 : n_d & 1) ^ 1, abort, err);
+                ok = ok && umma::warp_wait(x_full + 8 * xst, xpar, abort, err) &&
+                     umma::warp_wait(a_full + 8 * st, (n_a >> 1) & 1, abort, err);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t x_at = __shfl_sync(0xffffffffu, xs_addr + xst * xb, 0);
+                if (ptx::elect_one()) {
+                    const uint64_t xd = umma::sdesc(x_at, 1024);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const uint32_t d = tmem + buf * S::D_COLS + g * S::NT;
+                        uint32_t acc = fresh ? 0u : 1u;
+                        // the products of small terms first
+#pragma unroll
+                        for (int e = SPLIT ? 2 : 0; e >= 0; --e) {
+                            const int ea = e == 2, ex = e == 1;
+#pragma unroll
+                            for (int kk = 0; kk < STEP / 16; ++kk) {
+                                if (!BACK) {
+                                    ptx::umma_f16_ts(d, tmem + S::COL_A + st * S::A_COLS + (g * TERMS + ea) * 32 + 8 * kk,
+                                                     xd + ex * term_x + 16 * kk, idesc, acc);
+                                } else {
+                                    // 8-column groups 128 B apart (stride offset), 8-row groups 4096 B (leading offset)
+                                    const uint32_t at = as_addr + (st * TERMS + ea) * S::A_BYTES + g * 2048 + kk * 8192;
+                                    const uint64_t ad = (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(4096 >> 4) << 16) |
+                                                        ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+                                    ptx::umma_f16(d, ad, xd + ex * term_x + 16 * kk, idesc, acc);
+                                }
+                                acc = 1u;
+                            }
+                        }
+                    }
+                    ptx::umma_commit(a_empty + 8 * st);
+                    ptx::umma_commit(x_empty + 8 * xst);
+                    if (last) ptx::umma_commit(d_full + 8 * buf);
+                }
+                __syncwarp();
+                ++n_a;
+                if (last) ++n_d;
+                if (++xst == a.xs) {
+                    xst = 0;
+                    xpar ^= 1;
+                }
+            }
+        }
+        if (!ok) {  // let the products in flight end
+            if (ptx::elect_one()) ptx::umma_commit(done);
+            __syncwarp();
+            umma::drain_bar(done, 0, err);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (wid == W_WARPS + 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------------------ host
+template <int FMT, bool SPLIT, bool BACK>
+int launch_tile(const Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+    static SmemAttr attr;
+    auto k = &k_ffn_tile<FMT, SPLIT, BACK>;
+    const int st = ensure_smem(reinterpret_cast<const void*>(k), SMEM_MOST, attr);
+    if (st != MMQ_OK) {
+        report(fn, st, "the tiles' shared memory was refused");
+        return st;
+    }
+    ProfScope ps(BACK ? "k_ffn_tile_back" : "k_ffn_tile", s);
+    return pdl_status(launch_pdl(k, dim3((unsigned)ctas), dim3(THREADS), smem, s, a), fn);
+}
+
+static unsigned take_tile_error() {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_ffn_tile_error, sizeof(v)) != cudaSuccess) return 0;
+    if (v) {
+        const unsigned zero = 0;
+        cudaMemcpyToSymbol(g_ffn_tile_error, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace ffn
+}  // namespace mmq
