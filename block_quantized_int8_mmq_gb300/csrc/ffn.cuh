@@ -43,6 +43,7 @@ struct Rows {
 };
 
 struct Tile {
+    CUtensorMap map[2];            // of the weight matrices, where rows begin on 16 bytes
     const uint8_t* w[2];
     long long w_bytes, row_bytes;  // of a weight matrix, of a row
     const uint8_t* x;              // the rows' tiles
@@ -63,7 +64,7 @@ struct Tile {
     void* out;
 };
 
-constexpr int W_WARPS = 8, THREADS = (W_WARPS + 2) * 32;
+constexpr int W_WARPS = 16, C_WARPS = 1, THREADS = (W_WARPS + C_WARPS + 2) * 32;
 constexpr int STEP = 64;     // values of the reduction that are multiplied together
 constexpr int CHUNK = 256;   // values of a weight row that are copied together
 constexpr int X_MOST = 8, R_MOST = 8;  // longest rings
@@ -78,6 +79,9 @@ struct Shape {
     static constexpr int A_BYTES = STEP * CHUNK * 2;  // backward: a stage's term in shared memory
     static_assert(COL_A + 2 * A_COLS <= 512, "TMEM columns");
 };
+// Rings of weight chunks, 32 rows each: forward, one for each 32 of the 256 weight rows, which two warps share;
+// backward, one for each half of a step's 64 rows and each of the two sets of warps.
+__host__ __device__ constexpr int rings(bool back) { return back ? 4 : 8; }
 constexpr int SMEM_MOST = 232448 - 2048;  // less what is static
 
 __device__ __forceinline__ float load(const void* p, int dtype, long long i) {

@@ -74,14 +74,23 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.out = c.out;
     const int ctas = deal(a, cost(a, c.fmt, split, c.backward), device_shape().sms);
     // shared memory: two chunks' places at least, then up to four steps of rows, then more chunks
-    const int x_bytes = a.nt * 128 * terms, w_bytes = a.slot * (c.backward ? STEP : CHUNK);
+    const int x_bytes = a.nt * 128 * terms, w_bytes = rings(c.backward) * 32 * a.slot;
     const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true>::A_BYTES : 0);
     a.xs = (left - 2 * w_bytes) / x_bytes;
     a.xs = a.xs > 4 ? 4 : a.xs;
     a.rs = (left - a.xs * x_bytes) / w_bytes;
     a.rs = a.rs > R_MOST ? R_MOST : a.rs;
+    if (a.xs < 1 || a.rs < 2) {
+        report(c.fn, MMQ_ERR_SMEM, "the rings do not fit in shared memory");
+        return MMQ_ERR_SMEM;
+    }
     const int smem = SMEM_MOST - left + a.xs * x_bytes + a.rs * w_bytes;
 
+    for (int g = 0; g < c.mats && a.aligned; ++g)
+        if (!make_byte_map(&a.map[g], c.w[g], (uint64_t)a.row_bytes, (uint64_t)c.N, (uint32_t)chunk_bytes(c.fmt), 32, 2)) {
+            report(c.fn, MMQ_ERR_CUDA, "the weights' tensor map was refused");
+            return MMQ_ERR_CUDA;
+        }
     const long long term = (long long)a.steps * a.groups * 1024;
     const long long counters = up_to(4ll * a.rest, 256), ups = up_to(4 * c.M, 256);
     const long long parts = a.rest ? 2ll * ctas * 2 * a.nt * 128 * 4 : 0;

@@ -4,8 +4,9 @@
 // columns) by up to NT_MOST rows of x, summed over the whole reduction.  Weights are the M side of the tensor
 // cores' products (two tiles of 128), rows of x the N side, so one row costs what sixteen do, an output's
 // epilogue finds gate and up in one TMEM lane, and a warp stores 32 neighbouring columns at a time.  Roles of a CTA:
-//   weight warps (8)  copy chunks of 256 values of their weight rows by bulk copies into a ring of their own
-//                     and turn them into f16 (ffn_weights.cuh): forward, a thread per weight row, straight
+//   a copy warp       chunks of 256 values of the weight rows into rings, as TMA boxes of 32 rows; where rows do not
+//                     begin on 16 bytes the weight warps copy them themselves;
+//   weight warps (16) turn them into f16 (ffn_weights.cuh): forward, a thread per weight row, straight
 //                     into TMEM as the A operand; backward, where the reduction runs over weight rows, into shared
 //                     memory as an MN-major A operand (8 x 16-byte core matrices, no transpose).  Then the
 //                     epilogue, a thread per lane;
@@ -62,7 +63,18 @@ __device__ __forceinline__ int run_owner(const Tile& a, long long x) {
     return (int)(((x + 1) * gridDim.x - 1) / ((long long)a.rest * a.chunks));
 }
 
-__device__ __forceinline__ void sync_weight_warps() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// 16 bytes to shared memory, the first `bytes` of them from src, the others zero; an arrival at a barrier once this
+// thread's copies so far have landed.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void sync_weight_warps() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 __device__ __forceinline__ void activate8(int act, float (&v)[8]) {
     if (act == MMQ_ACT_NONE) return;
@@ -145,22 +157,23 @@ __device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, i
 }
 
 template <int FMT, bool SPLIT, bool BACK>
-__global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
+__global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__ Tile a) {
     using S = Shape<SPLIT>;
     constexpr int TERMS = S::TERMS;
-    constexpr int GW = BACK ? 4 : 1, NG = W_WARPS / GW;  // weight warps that share a ring, rings
+    constexpr int NG = rings(BACK), GW = W_WARPS / NG;  // rings, weight warps that share one
     constexpr int CB = chunk_bytes(FMT);
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[2 * X_MOST + 4 + 4 + NG * R_MOST + (BACK ? NG * R_MOST : 0) + 1];
+    __shared__ __align__(8) uint64_t s_bar[2 * X_MOST + 4 + 4 + 2 * NG * R_MOST + 1];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last;
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = ptx::smem_u32(s_bar);
     const uint32_t x_full = bars, x_empty = x_full + 8 * X_MOST, a_full = x_empty + 8 * X_MOST, a_empty = a_full + 16;
     const uint32_t d_full = a_empty + 16, d_empty = d_full + 16, raw_full = d_empty + 16;
-    const uint32_t raw_empty = raw_full + 8 * NG * R_MOST, done = raw_empty + (BACK ? 8 * NG * R_MOST : 0);
+    const uint32_t raw_empty = raw_full + 8 * NG * R_MOST, done = raw_empty + 8 * NG * R_MOST;
     const int xb = a.nt * 128 * TERMS;  // bytes of a step's rows
     const uint32_t xs_addr = ptx::smem_u32(smem), as_addr = xs_addr + a.xs * xb;
+    const uint32_t raw_addr = as_addr + (BACK ? 2 * TERMS * S::A_BYTES : 0);
     uint8_t* a_smem = smem + a.xs * xb;
     uint8_t* raw = a_smem + (BACK ? 2 * TERMS * S::A_BYTES : 0);
     if (tid == 0) {
@@ -169,20 +182,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
             ptx::mbar_init(x_empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(a_full + 8 * i, W_WARPS);
+            ptx::mbar_init(a_full + 8 * i, W_WARPS / 2);
             ptx::mbar_init(a_empty + 8 * i, 1);
             ptx::mbar_init(d_full + 8 * i, 1);
             ptx::mbar_init(d_empty + 8 * i, W_WARPS);
         }
         for (int i = 0; i < NG * R_MOST; ++i) {
-            ptx::mbar_init(raw_full + 8 * i, 1);
-            if (BACK) ptx::mbar_init(raw_empty + 8 * i, GW);
+            ptx::mbar_init(raw_full + 8 * i, a.aligned ? 1 : 32 * GW);
+            ptx::mbar_init(raw_empty + 8 * i, GW);
         }
         ptx::mbar_init(done, 1);
         ptx::fence_barrier_init();
         s_abort = 0;
     }
-    if (wid == W_WARPS + 1) {
+    if (wid == W_WARPS + C_WARPS + 1) {
         ptx::tmem_alloc(ptx::smem_u32(&s_tmem), 512);
         ptx::tmem_relinquish();
     }
@@ -199,70 +212,77 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
 
     if (wid < W_WARPS) {
         // ------------------------------------------------ weights, then the epilogue
-        const int grp = BACK ? wid & 1 : wid;       // ring
-        const bool leader = !BACK || wid < 2;       // the warp that fills it
-        const int g = wid >> 2, lane_row = 32 * (wid & 3) + lane;
+        // Two sets of eight warps take the steps by turns, each with a stage of its own.
+        const int e = wid >> 3;                                   // set and stage
+        const int g = (wid >> 2) & 1, lane_row = 32 * (wid & 3) + lane;  // forward: weight tile and row of it
+        const int grp = BACK ? 2 * e + (wid & 1) : wid & 7;       // ring; backward: of 32 of a step's 64 weight rows
+        const int q = (wid & 7) >> 1;                             // backward: the quarter of the 256 columns
         uint8_t* ring = raw + grp * a.rs * 32 * a.slot + lane * a.slot;
         const int nsteps = (a.N + STEP - 1) / STEP;  // backward: steps of a matrix
         // byte offset of this lane's row at a chunk, or -1
         auto row_at = [&](int pair, int c, int& mat) -> long long {
             if (BACK) {
                 mat = c >= nsteps;
-                const int n = (c - mat * nsteps) * STEP + 32 * grp + lane;
+                const int n = (c - mat * nsteps) * STEP + 32 * (wid & 1) + lane;
                 return n < a.N ? n * a.row_bytes + (long long)pair * CB : -1;
             }
             mat = a.mats == 2 ? g : 0;
             const int n = (a.mats == 2 ? pair * 128 : pair * 256 + g * 128) + lane_row;
             return n < a.N ? n * a.row_bytes + (long long)c * CB : -1;
         };
-        // ---- the ring: chunks in the order of the pieces
+        // the chunks of a piece that are this ring's: all; backward, those of its set
+        auto first_of = [&](int c) { return BACK ? c + ((c ^ e) & 1) : c; };
+        constexpr int NEXT = BACK ? 2 : 1;
+        // ---- rows that do not begin on 16 bytes: each warp of a ring copies its share of them, eight lanes a row, whole
+        // 16-byte units (bulk copies of single rows take 24 to 46 cycles each, whatever is in flight)
+        constexpr bool ROWS = FMT == FMT_Q8_0 || FMT == FMT_Q6_K;
         Pieces pf(a);
-        int f_unit = 0, f_c = 0, f_c1 = 0, fetched = 0, f_slot = 0;
+        int f_unit = 0, f_c = 0, f_c1 = 0, f_slot = 0;
+        const int f_row = (BACK ? 8 * q : 16 * e) + (lane >> 3);
         auto fetch = [&]() {
-            if (f_c == f_c1 && !pf.next(a, f_unit, f_c, f_c1)) return;
-            int mat;
-            const int pair = f_unit / a.mtiles;
-            const long long at = row_at(pair, f_c, mat);
-            const uint32_t bar = raw_full + 8 * (grp * R_MOST + f_slot);
-            uint8_t* dst = ring + f_slot * 32 * a.slot;
-            const uint8_t* src = nullptr;
-            int bytes = 0;
-            if (at >= 0) {
-                const int mis = (int)(at & 15);
-                const long long in_row = (long long)(BACK ? pair : f_c) * CB;
-                const int len = (int)min((long long)CB, a.row_bytes - in_row);
-                bytes = (mis + len + 15) & ~15;
-                src = a.w[mat] + (at - mis);
-                const long long past = at - mis + bytes - a.w_bytes;
-                if (past > 0) {  // the matrix's last bytes do not fill 16
-                    bytes -= 16;
-                    for (int i = bytes; i < mis + len; ++i) dst[i] = src[i];
-                }
+            while (f_c >= f_c1) {
+                if (!pf.next(a, f_unit, f_c, f_c1)) return;
+                f_c = first_of(f_c);
             }
-            const int total = __reduce_add_sync(0xffffffffu, bytes);  // (and the bytes above are there)
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, total);
-            __syncwarp();
-            if (bytes > 0) ptx::bulk_load(ptx::smem_u32(dst), src, bytes, bar);
-            ++f_c;
-            ++fetched;
+            const int pair = f_unit / a.mtiles, mat = BACK ? f_c >= nsteps : a.mats == 2 ? g : 0;
+            const int n0 = f_row + (BACK ? (f_c - mat * nsteps) * STEP + 32 * (wid & 1)
+                                         : (a.mats == 2 ? pair * 128 : pair * 256 + g * 128) + 32 * (wid & 3));
+            const long long in_row = (long long)(BACK ? pair : f_c) * CB;
+            const int len = (int)min((long long)CB, a.row_bytes - in_row), sub = 16 * (lane & 7);
+            const uint32_t dst = raw_addr + ((grp * a.rs + f_slot) * 32 + f_row) * a.slot + sub;
+            long long o = n0 * a.row_bytes + in_row;
+#pragma unroll
+            for (int t = 0; t < (BACK ? 2 : 4); ++t, o += 4 * a.row_bytes) {
+                const int mis = (int)(o & 15), need = n0 + 4 * t < a.N ? mis + len : 0;
+                const uint8_t* src = a.w[mat] + (o - mis) + sub;
+                const long long end = a.w_bytes - (o - mis) - sub;  // bytes of the matrix from here
+#pragma unroll
+                for (int k = 0; k < slot_bytes(FMT, false); k += 128)
+                    if (sub + k < need) cp_async16(dst + 4 * t * a.slot + k, src + k, end - k < 16 ? (int)(end - k) : 16);
+            }
+            cp_async_arrive(raw_full + 8 * (grp * R_MOST + f_slot));
+            f_c += NEXT;
             if (++f_slot == a.rs) f_slot = 0;
         };
-        if (leader)
+        if (ROWS && !a.aligned)
             for (int i = 0; i < a.rs; ++i) fetch();
         bool ok = true, waited = false, bad = false;
-        int taken = 0, slot = 0;           // chunks processed, the ring's place
+        int taken = 0;                     // chunks read
+        Check check;
+        int slot = 0;                      // the ring's place
         uint32_t par = 0;                  // its parity
         uint32_t n_a = 0, n_d = 0;         // stages, accumulator periods so far
-        float run[SPLIT ? S::NT : 1];      // SPLIT: sums of this thread's lane of tile g
+        constexpr int RUN = SPLIT ? S::NT / 2 : 1;
+        float run[RUN];                    // SPLIT: sums of this thread's lane of tile g, half of its columns
         auto drain = [&](uint32_t period, bool last) {
             const uint32_t b = period & 1;
             if (!umma::warp_wait(d_full + 8 * b, (period >> 1) & 1, abort, err)) return false;
             ptx::tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < S::NT / 16; ++c) {
-                if (16 * c >= a.nt) break;
+            for (int c = 0; c < RUN / 16; ++c) {
+                if (e * RUN + 16 * c >= a.nt) break;
                 uint32_t v[16];
-                ptx::tmem_ld16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + b * S::D_COLS + g * S::NT + 16 * c, v);
+                ptx::tmem_ld16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + b * S::D_COLS + g * S::NT + e * RUN + 16 * c, v);
                 ptx::tmem_ld_wait(v);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) run[SPLIT ? 16 * c + k : 0] += __uint_as_float(v[k]);
@@ -280,10 +300,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
             step_range(c0, c1, s0, s1);
             if (SPLIT)
 #pragma unroll
-                for (int k = 0; k < (SPLIT ? S::NT : 1); ++k) run[k] = 0.f;
-            int in_piece = 0;  // steps of the piece so far
+                for (int k = 0; k < RUN; ++k) run[k] = 0.f;
+            int drained = 0, mine = 0;  // SPLIT: periods moved to registers; steps that this set has taken
 #pragma unroll 1
-            for (int c = c0; c < c1 && ok; ++c) {
+            for (int c = first_of(c0); c < c1 && ok; c += NEXT) {
                 int mat;
                 const long long at = row_at(pair, c, mat);
                 const bool valid = at >= 0;
@@ -293,23 +313,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
                     break;
                 }
                 const uint8_t* src = ring + slot * 32 * a.slot;
-                auto one = [&](auto J) {
-                    constexpr int j = decltype(J)::value;
+                auto one = [&](int j) {
                     const int k0 = (BACK ? pair : c) * CHUNK + j * STEP;
                     const int blocks = min(2, max(0, (a.K - k0) / QK));
-                    const uint32_t st = n_a & 1;
-                    quarter<FMT, SPLIT, j>(src, mis, a.aligned, blocks, valid, bad,
-                                           [&](int half, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
-                        if (half == 0 && ok) ok = umma::warp_wait(a_empty + 8 * st, ((n_a >> 1) & 1) ^ 1, abort, err);
+                    quarter<FMT, SPLIT>(src, j, mis, a.aligned, blocks, !BACK || valid, check,
+                                        [&](int half, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+                        if (half == 0 && ok) ok = umma::warp_wait(a_empty + 8 * e, (n_a & 1) ^ 1, abort, err);
                         if (!BACK) {
                             if (half == 0) ptx::tc_fence_after();
-                            const uint32_t t = tmem + ((uint32_t)(32 * (wid & 3)) << 16) + S::COL_A + st * S::A_COLS +
+                            const uint32_t t = tmem + ((uint32_t)(32 * (wid & 3)) << 16) + S::COL_A + e * S::A_COLS +
                                                g * 32 * TERMS + 16 * half;
                             ptx::tmem_st16(t, hi);
                             if (SPLIT) ptx::tmem_st16(t + 32, lo);
                         } else {
-                            const int n = 32 * grp + lane;
-                            uint8_t* p = a_smem + st * TERMS * S::A_BYTES + (n >> 3) * 4096 + (8 * j + 4 * half) * 128 + (n & 7) * 16;
+                            const int n = 32 * (wid & 1) + lane;
+                            uint8_t* p = a_smem + e * TERMS * S::A_BYTES + (n >> 3) * 4096 + (8 * j + 4 * half) * 128 + (n & 7) * 16;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 *reinterpret_cast<uint4*>(p + 128 * i) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
@@ -326,63 +344,72 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
                         ptx::fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(a_full + 8 * st);
+                    if (lane == 0) ptx::mbar_arrive(a_full + 8 * e);
                     ++n_a;
-                    ++in_piece;
-                    if (SPLIT && in_piece % PERIOD == 0 && in_piece > PERIOD) ok = ok && drain(n_d++, false);
+                    ++mine;
                 };
                 if (BACK) {
-                    const int q = wid >> 1;
-                    if (q == 0)
-                        one(std::integral_constant<int, 0>{});
-                    else if (q == 1)
-                        one(std::integral_constant<int, 1>{});
-                    else if (q == 2)
-                        one(std::integral_constant<int, 2>{});
-                    else
-                        one(std::integral_constant<int, 3>{});
-                } else {
-                    one(std::integral_constant<int, 0>{});
-                    if (ok && 4 * c + 1 < a.steps) one(std::integral_constant<int, 1>{});
-                    if (ok && 4 * c + 2 < a.steps) one(std::integral_constant<int, 2>{});
-                    if (ok && 4 * c + 3 < a.steps) one(std::integral_constant<int, 3>{});
-                }
-                // the chunk has been read: its place is free (the fetching warp of a shared ring fills the place
-                // before this one, which the others have most likely left too)
-                __syncwarp();
-                if (BACK) {
-                    if (lane == 0) ptx::mbar_arrive(raw_empty + 8 * (grp * R_MOST + slot));
-                    if (leader && taken > 0) {
-                        const int before = taken - 1;
-                        ok = ok && umma::warp_wait(raw_empty + 8 * (grp * R_MOST + before % a.rs), (before / a.rs) & 1, abort, err);
-                        if (ok) fetch();
+                    if (FMT == FMT_Q8_0) {
+                        if (q == 0) one(0);
+                        if (q == 1) one(1);
+                        if (q == 2) one(2);
+                        if (q == 3) one(3);
+                    } else {
+                        one(q);
+                    }
+                } else if (FMT == FMT_Q8_0) {
+                    if (e == 0) {
+                        one(0);
+                        if (ok && 4 * c + 2 < a.steps) one(2);
+                    } else {
+                        if (4 * c + 1 < a.steps) one(1);
+                        if (ok && 4 * c + 3 < a.steps) one(3);
                     }
                 } else {
-                    fetch();
+#pragma unroll 1
+                    for (int j = e; j < 4 && ok; j += 2) one(j);
                 }
-                ++taken;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(raw_empty + 8 * (grp * R_MOST + slot));  // the chunk has been read
+                if (ROWS && !a.aligned) {
+                    // the place before this one: the ring's other warps have most likely left it too
+                    const int before = taken - 1;
+                    if (taken > 0 && ok)
+                        ok = umma::warp_wait(raw_empty + 8 * (grp * R_MOST + before % a.rs), (before / a.rs) & 1, abort, err);
+                    if (taken > 0 && ok) fetch();
+                    ++taken;
+                }
                 if (++slot == a.rs) {
                     slot = 0;
                     par ^= 1;
                 }
+                // SPLIT: a period (two steps of each set) behind
+                if (SPLIT && mine >= PERIOD / 2 * (drained + 2)) {
+                    ok = ok && drain(n_d++, false);
+                    ++drained;
+                }
             }
+            int any;
+            bad |= check.bad() && (BACK || row_at(pair, 0, any) >= 0);  // (lanes past the last row hold anything)
+            check = Check();
             if (!ok) break;
             if (!waited) ptx::grid_dep_wait();  // what follows reads and writes the call's rows
             waited = true;
             uint32_t buf = 0;
             if (SPLIT) {
-                // the last period, and the one before it where that has not been drained
-                if (in_piece > PERIOD && in_piece % PERIOD != 0) ok = drain(n_d++, false);
+                // the periods that are left: the last stays in its buffer's hands
+                for (; ok && drained + 1 < (s1 - s0 + PERIOD - 1) / PERIOD; ++drained) ok = drain(n_d++, false);
+                if (!ok) break;
                 buf = n_d & 1;
                 ok = ok && drain(n_d++, true);
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < S::NT / 16; ++c) {
-                    if (16 * c >= a.nt) break;
+                for (int c = 0; c < RUN / 16; ++c) {
+                    if (e * RUN + 16 * c >= a.nt) break;
                     uint32_t v[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(run[SPLIT ? 16 * c + k : 0]);
-                    ptx::tmem_st16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + buf * S::D_COLS + g * S::NT + 16 * c, v);
+                    ptx::tmem_st16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + buf * S::D_COLS + g * S::NT + e * RUN + 16 * c, v);
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
@@ -401,9 +428,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
             auto part = [&](int cta, int which, int tile) {
                 return a.parts + ((((long long)cta * 2 + which) * 2 + tile) * a.nt) * 128 + lane_row;
             };
-            const int b0 = 8 * g;  // the two groups of warps take columns by turns
+            const int b0 = 8 * (wid >> 2);  // the four warps of a lane take columns by turns
 #pragma unroll 1
-            for (int b = b0; m0 + b < m1; b += 16) {
+            for (int b = b0; m0 + b < m1; b += 32) {
                 uint32_t v0[8], v1[8];
                 ptx::tmem_ld8(src + b, v0);
                 ptx::tmem_ld8(src + S::NT + b, v1);
@@ -439,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
                 sync_weight_warps();
                 if (s_last) {
 #pragma unroll 1
-                    for (int b = b0; m0 + b < m1; b += 16) {
+                    for (int b = b0; m0 + b < m1; b += 32) {
                         float z0[8], z1[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) z0[i] = z1[i] = 0.f;
@@ -462,11 +489,52 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
             }
         }
         if (bad) atomicOr(err, ERR_RANGE);
-        if (!ok && leader) {  // let the copies in flight land before the shared memory goes
-            for (int i = taken; i < fetched; ++i)
-                umma::drain_bar(raw_full + 8 * (grp * R_MOST + i % a.rs), (i / a.rs) & 1, err);
+        if (ROWS) cp_async_wait_all();
+    } else if (wid < W_WARPS + C_WARPS) {
+        // ------------------------------------------------ weight chunks as boxes of 32 rows
+        Pieces pc(a);
+        int unit, c0, c1, slot[BACK ? 2 : 1] = {};  // the ring's place (of each set)
+        uint32_t par[BACK ? 2 : 1];
+        par[0] = par[BACK ? 1 : 0] = 1;
+        bool ok = a.aligned;
+        int asked[NG] = {};  // boxes of each ring
+        const int nsteps = (a.N + STEP - 1) / STEP;
+        while (ok && pc.next(a, unit, c0, c1)) {
+            const int pair = unit / a.mtiles;
+#pragma unroll 1
+            for (int c = c0; c < c1 && ok; ++c) {
+                const int e = BACK ? c & 1 : 0, k = BACK ? e : 0;
+                const int mat0 = BACK ? c >= nsteps : 0, x = (BACK ? pair : c) * (CB / 2);
+                const int n0 = BACK ? (c - mat0 * nsteps) * STEP : a.mats == 2 ? pair * 128 : pair * 256;
+#pragma unroll 1
+                for (int i = 0; i < (BACK ? 2 : NG); ++i) {
+                    const int r = BACK ? 2 * e + i : i, place = (BACK && k ? slot[BACK ? 1 : 0] : slot[0]);
+                    ok = umma::warp_wait(raw_empty + 8 * (r * R_MOST + place), BACK && k ? par[BACK ? 1 : 0] : par[0], abort, err);
+                    if (!ok) break;
+                    const bool up = BACK ? mat0 : a.mats == 2 && i >= 4;
+                    if (ptx::elect_one()) {
+                        const uint32_t bar = raw_full + 8 * (r * R_MOST + place);
+                        ptx::mbar_arrive_expect_tx(bar, 32 * CB);
+                        ptx::tma_load_2d(raw_addr + (r * a.rs + place) * 32 * CB, &a.map[up], bar, x,
+                                         n0 + 32 * (BACK || a.mats == 1 ? i : i & 3));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) asked[j] += j == r;
+                }
+                int& s = BACK && k ? slot[BACK ? 1 : 0] : slot[0];
+                if (++s == a.rs) {
+                    s = 0;
+                    (BACK && k ? par[BACK ? 1 : 0] : par[0]) ^= 1;
+                }
+            }
         }
-    } else if (wid == W_WARPS) {
+        if (!ok && a.aligned)  // let the boxes in flight land before the shared memory goes
+            for (int r = 0; r < NG; ++r)
+                for (int i = 0; i < a.rs; ++i)
+                    if (const int n = (asked[r] - i + a.rs - 1) / a.rs; asked[r] > i)
+                        umma::drain_bar(raw_full + 8 * (r * R_MOST + i), (n - 1) & 1, err);
+    } else if (wid == W_WARPS + C_WARPS) {
         // ------------------------------------------------ the rows' tiles
         ptx::grid_dep_wait();
         Pieces pc(a);
@@ -503,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
         // ------------------------------------------------ the products
         Pieces pc(a);
         int unit, c0, c1, xst = 0;
-        uint32_t xpar = 0, n_a = 0, n_d = 0;
+        uint32_t xpar = 0, n_a[2] = {0, 0}, n_d = 0;
         bool ok = true;
         const uint32_t idesc = umma::make_idesc(128, a.nt) | (BACK ? 1u << 15 : 0u);
         const uint32_t term_x = a.nt * 128 >> 4;
@@ -515,10 +583,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
                 const int i = s - s0;
                 const bool fresh = SPLIT ? i % PERIOD == 0 : i == 0, last = s + 1 == s1 || (SPLIT && i % PERIOD == PERIOD - 1);
                 const uint32_t buf = SPLIT ? n_d & 1 : 0;
-                const uint32_t st = n_a & 1;
+                const uint32_t st = s & 1;  // (a chunk of four steps begins on an even one)
                 if (fresh) ok = umma::warp_wait(d_empty + 8 * buf, (SPLIT ? (n_d >> 1) & 1 : n_d & 1) ^ 1, abort, err);
                 ok = ok && umma::warp_wait(x_full + 8 * xst, xpar, abort, err) &&
-                     umma::warp_wait(a_full + 8 * st, (n_a >> 1) & 1, abort, err);
+                     umma::warp_wait(a_full + 8 * st, (st ? n_a[1] : n_a[0]) & 1, abort, err);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t x_at = __shfl_sync(0xffffffffu, xs_addr + xst * xb, 0);
@@ -553,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
                     if (last) ptx::umma_commit(d_full + 8 * buf);
                 }
                 __syncwarp();
-                ++n_a;
+                st ? ++n_a[1] : ++n_a[0];
                 if (last) ++n_d;
                 if (++xst == a.xs) {
                     xst = 0;
@@ -569,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const Tile a) {
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (wid == W_WARPS + 1) {
+    if (wid == W_WARPS + C_WARPS + 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }

@@ -3,7 +3,7 @@
 // taken off again), times the block's scale, less its minimum.
 //
 // Weights enter the product times 2^8: f16 is then normal from 2^-22 up, and whatever a weight is formed
-// from, |scale| times the largest code and the minimum, has to stay below 255 (`bad` otherwise).
+// from, |scale| times the largest code and the minimum, has to stay below 255 (Check).
 // For 16-bit rows the scale and the minimum are rounded to f16 first and the weight once more, 2^-11 each: no more
 // than the rows' own type loses, and four instructions for two weights.  For f32 rows the weight is formed in
 // f32 and split in two f16 terms (2^-22).
@@ -24,38 +24,46 @@ __host__ __device__ constexpr int slot_bytes(int fmt, bool aligned) {
 }
 constexpr float W_UP = 256.f, W_MOST = 65504.f;
 
-// A linear map of codes, s q + m.
-struct Lin {
-    __half2 s2, m2;
-    float s, m;
-    __device__ __forceinline__ Lin(float s_, float m_, float most, bool valid, bool& bad) {
-        s = valid ? s_ : 0.f;  // rows that are not there: whatever is in their place counts for nothing
-        m = valid ? m_ : 0.f;
-        bad |= !(fabsf(s) * most + fabsf(m) <= W_MOST);
-        s2 = __float2half2_rn(s);
-        m2 = __float2half2_rn(m);
+__device__ __forceinline__ uint32_t h2(__half2 h) { return umma::h2_bits(h); }
+__device__ __forceinline__ __half2 low2(__half2 h) { return __lows2half2(h, h); }
+__device__ __forceinline__ __half2 high2(__half2 h) { return __highs2half2(h, h); }
+
+// What became of the range: NaN or an infinity once a scale was too large.
+struct Check {
+    float f = 0.f;
+    __half2 h = __half2{__half_raw{0}, __half_raw{0}};
+    __device__ __forceinline__ void add(__half2 s, __half2 m, float most) {
+        const __half2 t = __hfma2(__habs2(s), __float2half2_rn(most), __habs2(m));
+        h = __hfma2(t, __float2half2_rn(0.f), h);  // an infinity times 0 stays in the sum
     }
+    __device__ __forceinline__ void add(float s, float m, float most) {
+        if (!(fabsf(s) * most + fabsf(m) <= W_MOST)) f = 1.f;
+    }
+    __device__ __forceinline__ bool bad() const { return f != 0.f || !__hbeq2(h, __float2half2_rn(0.f)); }
 };
 
-__device__ __forceinline__ uint32_t h2(__half2 h) { return umma::h2_bits(h); }
-
-// Four codes (one per byte) to two pairs of f16: hi, and for SPLIT what hi leaves in lo.
-template <bool SPLIT, bool MIN>
-__device__ __forceinline__ void four(uint32_t codes, uint32_t bias, const Lin& l, uint32_t* hi, uint32_t* lo) {
+// Four codes (one per byte) to two pairs of f16, s q + m: 16-bit rows.
+template <bool MIN>
+__device__ __forceinline__ void four(uint32_t codes, uint32_t bias, __half2 s, __half2 m, uint32_t* hi) {
     const __half2 b = umma::bits_h2(bias);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const __half2 q = __hsub2(umma::bits_h2(__byte_perm(codes, 0x64646464u, i ? 0x4342 : 0x4140)), b);
-        if (!SPLIT) {
-            hi[i] = h2(MIN ? __hfma2(q, l.s2, l.m2) : __hmul2(q, l.s2));
-        } else {
-            const float2 f = __half22float2(q);
-            const float a = MIN ? fmaf(f.x, l.s, l.m) : f.x * l.s, c = MIN ? fmaf(f.y, l.s, l.m) : f.y * l.s;
-            const __half2 h = __floats2half2_rn(a, c);
-            const float2 back = __half22float2(h);
-            hi[i] = h2(h);
-            lo[i] = h2(__floats2half2_rn(a - back.x, c - back.y));
-        }
+        hi[i] = h2(MIN ? __hfma2(q, s, m) : __hmul2(q, s));
+    }
+}
+// The same for f32 rows: hi, and what it leaves in lo.
+template <bool MIN>
+__device__ __forceinline__ void four(uint32_t codes, uint32_t bias, float s, float m, uint32_t* hi, uint32_t* lo) {
+    const __half2 b = umma::bits_h2(bias);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 f = __half22float2(__hsub2(umma::bits_h2(__byte_perm(codes, 0x64646464u, i ? 0x4342 : 0x4140)), b));
+        const float a = MIN ? fmaf(f.x, s, m) : f.x * s, c = MIN ? fmaf(f.y, s, m) : f.y * s;
+        const __half2 h = __floats2half2_rn(a, c);
+        const float2 back = __half22float2(h);
+        hi[i] = h2(h);
+        lo[i] = h2(__floats2half2_rn(a - back.x, c - back.y));
     }
 }
 
@@ -80,11 +88,14 @@ __device__ __forceinline__ void read_run(const uint8_t* p, int off, uint32_t (&o
 }
 
 // Values 64 J .. 64 J + 63 of the chunk at `slot` (mis: bytes before its first, 0 .. 14).  emit(half, hi, lo)
-// takes 32 values at a time as 16 pairs.  blocks: Q8_0's 32-value blocks that exist here (0 .. 2), the others are zero.
-template <int FMT, bool SPLIT, int J, class Emit>
-__device__ __forceinline__ void quarter(const uint8_t* slot, int mis, bool aligned, int blocks, bool valid, bool& bad,
-                                        Emit&& emit) {
+// takes 32 values at a time as 16 pairs.  blocks: Q8_0's 32-value blocks that exist here (0 .. 2), the others are
+// zero.  valid: whether there is such a row; where not, zeros come out of whatever is in its place.  J is a constant
+// for Q8_0 (its blocks of 34 bytes lie at another word offset in each quarter).
+template <int FMT, bool SPLIT, class Emit>
+__device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, bool aligned, int blocks, bool valid,
+                                        Check& check, Emit&& emit) {
     uint32_t hi[16], lo[16];
+    const __half2 up2 = __float2half2_rn(W_UP);
     if (FMT == FMT_Q8_0) {
         uint32_t w[17];
         if (aligned) {
@@ -99,33 +110,58 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int mis, bool align
         } else {
             read_run<17>(slot, 68 * J + mis, w);
         }
+        uint32_t dd = __byte_perm(w[0], w[8], 0x7610);  // the two blocks' scales
+        dd &= (valid && blocks > 0 ? 0xffffu : 0u) | (valid && blocks > 1 ? 0xffff0000u : 0u);
+        const __half2 d2 = __hmul2(umma::bits_h2(dd), up2);
+        if (!SPLIT) check.add(d2, d2, 127.f);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const Lin l(f16_bits_to_f32(b ? w[8] >> 16 : w[0]) * W_UP, 0.f, 128.f, valid && b < blocks, bad);
+            const float s = f16_bits_to_f32(b ? dd >> 16 : dd) * W_UP;
+            if (SPLIT) check.add(s, 0.f, 128.f);
+            const __half2 s2 = b ? high2(d2) : low2(d2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t c = b ? w[9 + i] : __funnelshift_r(w[i], w[i + 1], 16);
-                four<SPLIT, false>(c ^ 0x80808080u, 0x64806480u, l, hi + 2 * i, lo + 2 * i);
+                const uint32_t c = (b ? w[9 + i] : __funnelshift_r(w[i], w[i + 1], 16)) ^ 0x80808080u;
+                if (SPLIT)
+                    four<false>(c, 0x64806480u, s, 0.f, hi + 2 * i, lo + 2 * i);
+                else
+                    four<false>(c, 0x64806480u, s2, s2, hi + 2 * i);
             }
             emit(b, hi, lo);
         }
     } else if (FMT == FMT_Q6_K) {
-        constexpr int H = J >> 1, T = 2 * (J & 1);
+        const int H = J >> 1, T = 2 * (J & 1);
         uint32_t ql[16], qh[8], sc[1];
         read_run<16>(slot, 64 * H + mis, ql);
         read_run<8>(slot, 128 + 32 * H + mis, qh);
         read_run<1>(slot, 192 + 4 * J + mis, sc);
-        const float d = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(slot + 208 + mis)) * W_UP;
+        const uint32_t dd = valid ? *reinterpret_cast<const uint16_t*>(slot + 208 + mis) * 0x10001u : 0u;
+        const float d = f16_bits_to_f32(dd) * W_UP;
+        __half2 sp[2];
+        if (!SPLIT) {
+            const __half2 d2 = __hmul2(umma::bits_h2(dd), up2), bias = umma::bits_h2(0x64806480u);
+            const uint32_t u = sc[0] ^ 0x80808080u;
+            sp[0] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias), d2);
+            sp[1] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias), d2);
+            check.add(sp[0], __float2half2_rn(0.f), 32.f);
+            check.add(sp[1], __float2half2_rn(0.f), 32.f);
+        }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+            const int turn = 4 - 2 * (T + b);  // the two high bits of each byte to bits 4 and 5
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const Lin l(d * (float)(int8_t)(sc[0] >> (16 * b + 8 * g)), 0.f, 32.f, valid, bad);
+                const float s = d * (float)(int8_t)(sc[0] >> (16 * b + 8 * g));
+                const __half2 s2 = g ? high2(sp[b]) : low2(sp[b]);
+                if (SPLIT) check.add(s, 0.f, 32.f);
 #pragma unroll
                 for (int i = 4 * g; i < 4 * g + 4; ++i) {
-                    const uint32_t low = (ql[8 * b + i] >> (2 * T)) & 0x0f0f0f0fu;
-                    const uint32_t top = T + b >= 2 ? qh[i] >> (2 * (T + b) - 4) : qh[i] << (4 - 2 * (T + b));
-                    four<SPLIT, false>(low | (top & 0x30303030u), 0x64206420u, l, hi + 2 * i, lo + 2 * i);
+                    const uint32_t c = ((ql[8 * b + i] >> (2 * T)) & 0x0f0f0f0fu) |
+                                       (__funnelshift_l(qh[i], qh[i], turn) & 0x30303030u);
+                    if (SPLIT)
+                        four<false>(c, 0x64206420u, s, 0.f, hi + 2 * i, lo + 2 * i);
+                    else
+                        four<false>(c, 0x64206420u, s2, s2, hi + 2 * i);
                 }
             }
             emit(b, hi, lo);
@@ -146,20 +182,40 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int mis, bool align
                 qh[4 * i] = v.x, qh[4 * i + 1] = v.y, qh[4 * i + 2] = v.z, qh[4 * i + 3] = v.w;
             }
         }
-        const float d = f16_bits_to_f32(head.x) * W_UP, dmin = f16_bits_to_f32(head.x >> 16) * -W_UP;
+        // sub-scales and minimums 2J, 2J + 1 (q4_k_scale_min for two at a time), in the low two bytes
+        uint32_t sc, mn;
+        if (J < 2) {
+            sc = head.y & 0x3f3f3f3fu;
+            mn = head.z & 0x3f3f3f3fu;
+        } else {
+            sc = (head.w & 0x0f0f0f0fu) | ((head.y >> 2) & 0x30303030u);
+            mn = ((head.w >> 4) & 0x0f0f0f0fu) | ((head.z >> 2) & 0x30303030u);
+        }
+        sc >>= 16 * (J & 1);
+        mn >>= 16 * (J & 1);
+        constexpr float MOST = FMT == FMT_Q5_K ? 31.f : 15.f;
+        const uint32_t dd = valid ? head.x : 0u;
+        __half2 s2{}, m2{};
+        if (!SPLIT) {
+            const __half2 d2 = __hmul2(umma::bits_h2(dd), __floats2half2_rn(W_UP, -W_UP)), bias = umma::bits_h2(0x64006400u);
+            s2 = __hmul2(__hsub2(umma::bits_h2(__byte_perm(sc, 0x64646464u, 0x4140)), bias), low2(d2));
+            m2 = __hmul2(__hsub2(umma::bits_h2(__byte_perm(mn, 0x64646464u, 0x4140)), bias), high2(d2));
+            check.add(s2, m2, MOST);
+        }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            int sc, mn;
-            q4_k_scale_min(head.y, head.z, head.w, 2 * J + b, sc, mn);
-            const Lin l(d * (float)sc, dmin * (float)mn, FMT == FMT_Q5_K ? 31.f : 15.f, valid, bad);
+            const float s = f16_bits_to_f32(dd) * W_UP * (float)((sc >> (8 * b)) & 63);
+            const float m = f16_bits_to_f32(dd >> 16) * -W_UP * (float)((mn >> (8 * b)) & 63);
+            if (SPLIT) check.add(s, m, MOST);
+            const __half2 sb = b ? high2(s2) : low2(s2), mb = b ? high2(m2) : low2(m2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t c = (b ? q[i] >> 4 : q[i]) & 0x0f0f0f0fu;
-                if (FMT == FMT_Q5_K) {
-                    constexpr int S = 2 * J;
-                    c |= (S + b >= 4 ? qh[i] >> (S + b - 4) : qh[i] << (4 - S - b)) & 0x10101010u;
-                }
-                four<SPLIT, true>(c, 0x64006400u, l, hi + 2 * i, lo + 2 * i);
+                if (FMT == FMT_Q5_K) c |= __funnelshift_l(qh[i], qh[i], 4 - 2 * J - b) & 0x10101010u;
+                if (SPLIT)
+                    four<true>(c, 0x64006400u, s, m, hi + 2 * i, lo + 2 * i);
+                else
+                    four<true>(c, 0x64006400u, sb, mb, hi + 2 * i);
             }
             emit(b, hi, lo);
         }
