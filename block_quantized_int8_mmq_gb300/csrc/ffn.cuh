@@ -64,10 +64,10 @@ struct Tile {
     void* out;
 };
 
-constexpr int W_WARPS = 16, C_WARPS = 1, THREADS = (W_WARPS + C_WARPS + 2) * 32;
+constexpr int W_WARPS = 16, C_WARPS = 1, I_WARPS = 2, THREADS = (W_WARPS + C_WARPS + 1 + I_WARPS) * 32;
 constexpr int STEP = 64;     // values of the reduction that are multiplied together
 constexpr int CHUNK = 256;   // values of a weight row that are copied together
-constexpr int X_MOST = 8, R_MOST = 8;  // longest rings
+constexpr int RING = 8, R_MOST = 8;  // barriers of steps; longest ring of weight chunks
 template <bool SPLIT>
 struct Shape {
     static constexpr int TERMS = SPLIT ? 2 : 1;

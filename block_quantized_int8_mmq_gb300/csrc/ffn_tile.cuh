@@ -11,7 +11,7 @@
 //                     memory as an MN-major A operand (8 x 16-byte core matrices, no transpose).  Then the
 //                     epilogue, a thread per lane;
 //   a loader warp     the rows' tiles, which k_ffn_rows has laid out, one bulk copy a step and term;
-//   an issuer warp    the products, 64 values of the reduction a step.
+//   issuer warps (2)  the products of a weight tile each, 64 values of the reduction a step.
 // f32 rows (SPLIT): rows and weights in two f16 terms each, three products, and the accumulators move to registers
 // every 256 values of the reduction: the tensor core's additions round towards zero, and over a long sum that
 // would be more than f32 allows.
@@ -163,35 +163,34 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
     constexpr int NG = rings(BACK), GW = W_WARPS / NG;  // rings, weight warps that share one
     constexpr int CB = chunk_bytes(FMT);
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[2 * X_MOST + 4 + 4 + 2 * NG * R_MOST + 1];
+    __shared__ __align__(8) uint64_t s_bar[2 * RING + 4 + 2 * NG * R_MOST + 2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last;
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = ptx::smem_u32(s_bar);
-    const uint32_t x_full = bars, x_empty = x_full + 8 * X_MOST, a_full = x_empty + 8 * X_MOST, a_empty = a_full + 16;
-    const uint32_t d_full = a_empty + 16, d_empty = d_full + 16, raw_full = d_empty + 16;
-    const uint32_t raw_empty = raw_full + 8 * NG * R_MOST, done = raw_empty + 8 * NG * R_MOST;
+    // Steps are counted through all pieces: full (the rows' tile and the set's weights are there) and empty (its products
+    // are done) of step n at n % RING.
+    const uint32_t full = bars, empty = full + 8 * RING, d_full = empty + 8 * RING, d_empty = d_full + 16;
+    const uint32_t raw_full = d_empty + 16, raw_empty = raw_full + 8 * NG * R_MOST, done = raw_empty + 8 * NG * R_MOST;
     const int xb = a.nt * 128 * TERMS;  // bytes of a step's rows
     const uint32_t xs_addr = ptx::smem_u32(smem), as_addr = xs_addr + a.xs * xb;
     const uint32_t raw_addr = as_addr + (BACK ? 2 * TERMS * S::A_BYTES : 0);
     uint8_t* a_smem = smem + a.xs * xb;
     uint8_t* raw = a_smem + (BACK ? 2 * TERMS * S::A_BYTES : 0);
     if (tid == 0) {
-        for (int i = 0; i < X_MOST; ++i) {
-            ptx::mbar_init(x_full + 8 * i, 1);
-            ptx::mbar_init(x_empty + 8 * i, 1);
+        for (int i = 0; i < RING; ++i) {
+            ptx::mbar_init(full + 8 * i, W_WARPS / 2 + 1);
+            ptx::mbar_init(empty + 8 * i, I_WARPS);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(a_full + 8 * i, W_WARPS / 2);
-            ptx::mbar_init(a_empty + 8 * i, 1);
-            ptx::mbar_init(d_full + 8 * i, 1);
+            ptx::mbar_init(d_full + 8 * i, I_WARPS);
             ptx::mbar_init(d_empty + 8 * i, W_WARPS);
+            ptx::mbar_init(done + 8 * i, 1);
         }
         for (int i = 0; i < NG * R_MOST; ++i) {
             ptx::mbar_init(raw_full + 8 * i, a.aligned ? 1 : 32 * GW);
             ptx::mbar_init(raw_empty + 8 * i, GW);
         }
-        ptx::mbar_init(done, 1);
         ptx::fence_barrier_init();
         s_abort = 0;
     }
@@ -271,7 +270,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
         Check check;
         int slot = 0;                      // the ring's place
         uint32_t par = 0;                  // its parity
-        uint32_t n_a = 0, n_d = 0;         // stages, accumulator periods so far
+        uint32_t n_d = 0;                  // accumulator periods so far
+        int base = 0, before = -1;         // steps of the pieces before, this set's last step
         constexpr int RUN = SPLIT ? S::NT / 2 : 1;
         float run[RUN];                    // SPLIT: sums of this thread's lane of tile g, half of its columns
         auto drain = [&](uint32_t period, bool last) {
@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     const int blocks = min(2, max(0, (a.K - k0) / QK));
                     quarter<FMT, SPLIT>(src, j, mis, a.aligned, blocks, !BACK || valid, check,
                                         [&](int half, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
-                        if (half == 0 && ok) ok = umma::warp_wait(a_empty + 8 * e, (n_a & 1) ^ 1, abort, err);
+                        if (half == 0 && ok && before >= 0)
+                            ok = umma::warp_wait(empty + 8 * (before % RING), (before / RING) & 1, abort, err);
                         if (!BACK) {
                             if (half == 0) ptx::tc_fence_after();
                             const uint32_t t = tmem + ((uint32_t)(32 * (wid & 3)) << 16) + S::COL_A + e * S::A_COLS +
@@ -344,8 +345,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                         ptx::fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(a_full + 8 * e);
-                    ++n_a;
+                    before = base + (BACK ? c - c0 : 4 * (c - c0) + j);
+                    if (lane == 0) ptx::mbar_arrive(full + 8 * (before % RING));
                     ++mine;
                 };
                 if (BACK) {
@@ -373,9 +374,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 if (lane == 0) ptx::mbar_arrive(raw_empty + 8 * (grp * R_MOST + slot));  // the chunk has been read
                 if (ROWS && !a.aligned) {
                     // the place before this one: the ring's other warps have most likely left it too
-                    const int before = taken - 1;
+                    const int prev = taken - 1;
                     if (taken > 0 && ok)
-                        ok = umma::warp_wait(raw_empty + 8 * (grp * R_MOST + before % a.rs), (before / a.rs) & 1, abort, err);
+                        ok = umma::warp_wait(raw_empty + 8 * (grp * R_MOST + prev % a.rs), (prev / a.rs) & 1, abort, err);
                     if (taken > 0 && ok) fetch();
                     ++taken;
                 }
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     ++drained;
                 }
             }
+            base += s1 - s0;
             int any;
             bad |= check.bad() && (BACK || row_at(pair, 0, any) >= 0);  // (lanes past the last row hold anything)
             check = Check();
@@ -538,8 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
         // ------------------------------------------------ the rows' tiles
         ptx::grid_dep_wait();
         Pieces pc(a);
-        int unit, c0, c1, st = 0, loaded = 0;
-        uint32_t par = 1;
+        int unit, c0, c1, st = 0, n = 0;
         bool ok = true;
         while (ok && pc.next(a, unit, c0, c1)) {
             const int mt = unit % a.mtiles, g0 = mt * (a.nt / 8);
@@ -548,91 +549,89 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
             step_range(c0, c1, s0, s1);
             const uint8_t* src = a.x + ((long long)s0 * a.groups + g0) * 1024;
 #pragma unroll 1
-            for (int s = s0; s < s1; ++s, src += (long long)a.groups * 1024) {
-                if (!umma::warp_wait(x_empty + 8 * st, par, abort, err)) {
+            for (int s = s0; s < s1; ++s, ++n, src += (long long)a.groups * 1024) {
+                const int free = n - a.xs;  // the step whose products have read this place
+                if (free >= 0 && !umma::warp_wait(empty + 8 * (free % RING), (free / RING) & 1, abort, err)) {
                     ok = false;
                     break;
                 }
                 if (ptx::elect_one()) {
-                    ptx::mbar_arrive_expect_tx(x_full + 8 * st, bytes * TERMS);
-                    ptx::bulk_load(xs_addr + st * xb, src, bytes, x_full + 8 * st);
-                    if (SPLIT) ptx::bulk_load(xs_addr + st * xb + a.nt * 128, src + a.x_term, bytes, x_full + 8 * st);
+                    const uint32_t bar = full + 8 * (n % RING);
+                    ptx::mbar_arrive_expect_tx(bar, bytes * TERMS);
+                    ptx::bulk_load(xs_addr + st * xb, src, bytes, bar);
+                    if (SPLIT) ptx::bulk_load(xs_addr + st * xb + a.nt * 128, src + a.x_term, bytes, bar);
                 }
-                ++loaded;
-                if (++st == a.xs) {
-                    st = 0;
-                    par ^= 1;
-                }
+                __syncwarp();
+                if (++st == a.xs) st = 0;
             }
         }
-        if (!ok)
-            for (int i = max(0, loaded - a.xs); i < loaded; ++i) umma::drain_bar(x_full + 8 * (i % a.xs), (i / a.xs) & 1, err);
+        if (!ok) {
+            // let the copies in flight land before the shared memory goes (a step's barrier counts the weights too, which may
+            // never come: the copies are given the time of a wait)
+            const uint64_t t0 = ptx::globaltimer_ns();
+            while (ptx::globaltimer_ns() - t0 < 1000000ull) {
+            }
+        }
     } else {
-        // ------------------------------------------------ the products
+        // ------------------------------------------------ the products, a warp for each weight tile
+        // The tensor core's queue is short, so what a warp does between two steps counts (measured with one warp for both
+        // tiles and barriers of their own for rows and weights: 450 cycles of waits and loops beside 750 of products at
+        // nt = 192, with weights and rows never late).  Products issue from uniform registers in an elected lane.
+        const int g = wid - (W_WARPS + C_WARPS + 1);
         Pieces pc(a);
         int unit, c0, c1, xst = 0;
-        uint32_t xpar = 0, n_a[2] = {0, 0}, n_d = 0;
+        uint32_t n = 0, n_d = 0;
         bool ok = true;
         const uint32_t idesc = umma::make_idesc(128, a.nt) | (BACK ? 1u << 15 : 0u);
         const uint32_t term_x = a.nt * 128 >> 4;
+        // 8-column groups 128 B apart (stride offset), 8-row groups 4096 B (leading offset)
+        const uint64_t a_desc = (uint64_t)(((as_addr + g * 2048) & 0x3FFFFu) >> 4) | ((uint64_t)(4096 >> 4) << 16) |
+                                ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
         while (ok && pc.next(a, unit, c0, c1)) {
             int s0, s1;
             step_range(c0, c1, s0, s1);
 #pragma unroll 1
-            for (int s = s0; s < s1; ++s) {
+            for (int s = s0; s < s1; ++s, ++n) {
                 const int i = s - s0;
                 const bool fresh = SPLIT ? i % PERIOD == 0 : i == 0, last = s + 1 == s1 || (SPLIT && i % PERIOD == PERIOD - 1);
                 const uint32_t buf = SPLIT ? n_d & 1 : 0;
                 const uint32_t st = s & 1;  // (a chunk of four steps begins on an even one)
                 if (fresh) ok = umma::warp_wait(d_empty + 8 * buf, (SPLIT ? (n_d >> 1) & 1 : n_d & 1) ^ 1, abort, err);
-                ok = ok && umma::warp_wait(x_full + 8 * xst, xpar, abort, err) &&
-                     umma::warp_wait(a_full + 8 * st, (st ? n_a[1] : n_a[0]) & 1, abort, err);
+                ok = ok && umma::warp_wait(full + 8 * (n % RING), (n / RING) & 1, abort, err);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t x_at = __shfl_sync(0xffffffffu, xs_addr + xst * xb, 0);
                 if (ptx::elect_one()) {
                     const uint64_t xd = umma::sdesc(x_at, 1024);
+                    const uint32_t d = tmem + buf * S::D_COLS + g * S::NT;
+                    uint32_t acc = fresh ? 0u : 1u;
+                    // the products of small terms first
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const uint32_t d = tmem + buf * S::D_COLS + g * S::NT;
-                        uint32_t acc = fresh ? 0u : 1u;
-                        // the products of small terms first
+                    for (int e = SPLIT ? 2 : 0; e >= 0; --e) {
+                        const int ea = e == 2, ex = e == 1;
 #pragma unroll
-                        for (int e = SPLIT ? 2 : 0; e >= 0; --e) {
-                            const int ea = e == 2, ex = e == 1;
-#pragma unroll
-                            for (int kk = 0; kk < STEP / 16; ++kk) {
-                                if (!BACK) {
-                                    ptx::umma_f16_ts(d, tmem + S::COL_A + st * S::A_COLS + (g * TERMS + ea) * 32 + 8 * kk,
-                                                     xd + ex * term_x + 16 * kk, idesc, acc);
-                                } else {
-                                    // 8-column groups 128 B apart (stride offset), 8-row groups 4096 B (leading offset)
-                                    const uint32_t at = as_addr + (st * TERMS + ea) * S::A_BYTES + g * 2048 + kk * 8192;
-                                    const uint64_t ad = (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(4096 >> 4) << 16) |
-                                                        ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-                                    ptx::umma_f16(d, ad, xd + ex * term_x + 16 * kk, idesc, acc);
-                                }
-                                acc = 1u;
-                            }
+                        for (int kk = 0; kk < STEP / 16; ++kk) {
+                            if (!BACK)
+                                ptx::umma_f16_ts(d, tmem + S::COL_A + st * S::A_COLS + (g * TERMS + ea) * 32 + 8 * kk,
+                                                 xd + ex * term_x + 16 * kk, idesc, acc);
+                            else
+                                ptx::umma_f16(d, a_desc + (uint32_t)((st * TERMS + ea) * (S::A_BYTES >> 4) + kk * 512),
+                                              xd + ex * term_x + 16 * kk, idesc, acc);
+                            acc = 1u;
                         }
                     }
-                    ptx::umma_commit(a_empty + 8 * st);
-                    ptx::umma_commit(x_empty + 8 * xst);
+                    ptx::umma_commit(empty + 8 * (n % RING));
                     if (last) ptx::umma_commit(d_full + 8 * buf);
                 }
                 __syncwarp();
-                st ? ++n_a[1] : ++n_a[0];
                 if (last) ++n_d;
-                if (++xst == a.xs) {
-                    xst = 0;
-                    xpar ^= 1;
-                }
+                if (++xst == a.xs) xst = 0;
             }
         }
         if (!ok) {  // let the products in flight end
-            if (ptx::elect_one()) ptx::umma_commit(done);
+            if (ptx::elect_one()) ptx::umma_commit(done + 8 * g);
             __syncwarp();
-            umma::drain_bar(done, 0, err);
+            umma::drain_bar(done + 8 * g, 0, err);
         }
     }
     ptx::tc_fence_before();
