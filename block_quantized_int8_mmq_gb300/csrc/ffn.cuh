@@ -84,21 +84,14 @@ struct Shape {
 __host__ __device__ constexpr int rings(bool back) { return back ? 4 : 8; }
 constexpr int SMEM_MOST = 232448 - 2048;  // less what is static
 
-__device__ __forceinline__ float load(const void* p, int dtype, long long i) {
-    if (dtype == MMQ_F32) return static_cast<const float*>(p)[i];
-    if (dtype == MMQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    return __half2float(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void store(void* p, int dtype, long long i, float v) {
-    if (dtype == MMQ_F32)
-        static_cast<float*>(p)[i] = v;
-    else if (dtype == MMQ_BF16)
-        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
+__device__ __forceinline__ float get_one(const float* p) { return *p; }
+__device__ __forceinline__ float get_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float get_one(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ void put_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put_one(__half* p, float v) { *p = __float2half_rn(v); }
 
-// act(z) and act'(z).  A NaN stays one.
+// act(z) and act'(z).  A NaN stays one.  (The quotients are 1 / (1 + e) with two ulp, and 0 above 2^126.)
 __device__ __forceinline__ void activate(int act, float z, float& a, float& d) {
     if (act == MMQ_ACT_NONE) {
         a = z;
@@ -107,7 +100,7 @@ __device__ __forceinline__ void activate(int act, float z, float& a, float& d) {
         a = z < 0.f ? 0.f : z;
         d = z > 0.f ? 1.f : 0.f;
     } else if (act == MMQ_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
+        const float s = __fdividef(1.f, 1.f + expf(-z));
         a = z * s;
         d = s * (1.f + z * (1.f - s));
     } else if (act == MMQ_ACT_GELU) {
@@ -115,7 +108,7 @@ __device__ __forceinline__ void activate(int act, float z, float& a, float& d) {
         a = z * s;
         d = s + z * 0.39894228040143268f * expf(-0.5f * z * z);
     } else {  // gelu, by tanh: (1 + tanh(t)) / 2 = 1 / (1 + exp(-2 t))
-        const float z2 = z * z, s = 1.f / (1.f + expf(-1.5957691216057308f * z * (1.f + 0.044715f * z2)));
+        const float z2 = z * z, s = __fdividef(1.f, 1.f + expf(-1.5957691216057308f * z * (1.f + 0.044715f * z2)));
         a = z * s;
         d = s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z2);
     }

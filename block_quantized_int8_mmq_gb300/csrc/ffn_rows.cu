@@ -111,19 +111,30 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
     for (int c = runs + threadIdx.x; c < min(places, HELD * THREADS); c += THREADS) put(r, m, c >> 3, c & 7, none, s.down);
 }
 
+// Eight values from an address that is aligned to its elements, as one load where it is aligned to 16 bytes.
 template <typename T>
-__device__ __forceinline__ float one(const void* p, long long i);
-template <>
-__device__ __forceinline__ float one<float>(const void* p, long long i) {
-    return static_cast<const float*>(p)[i];
+__device__ __forceinline__ void get8(const T* p, int left, bool vector, float (&v)[8]) {
+    if (vector && left >= 8) {
+        load8(p, v);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < left ? get_one(p + k) : 0.f;
 }
-template <>
-__device__ __forceinline__ float one<__nv_bfloat16>(const void* p, long long i) {
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-template <>
-__device__ __forceinline__ float one<__half>(const void* p, long long i) {
-    return __half2float(static_cast<const __half*>(p)[i]);
+template <typename T>
+__device__ __forceinline__ void put8(T* p, int left, bool vector, const float (&v)[8]) {
+    if (vector && left >= 8) {
+        if (sizeof(T) == 2) {
+            kv::store_run<T, 8>(p, v);
+        } else {
+            kv::Elem<T>::store4(p, make_float4(v[0], v[1], v[2], v[3]));
+            kv::Elem<T>::store4(p + 4, make_float4(v[4], v[5], v[6], v[7]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < left) put_one(p + k, v[k]);
 }
 
 template <typename T, int THREADS>
@@ -135,39 +146,43 @@ __global__ void __launch_bounds__(THREADS) k_ffn_gradients(const Rows r) {
     const int m = blockIdx.x, N = r.width, steps = (N + 63) / 64;
     const long long at = (long long)m * N;
     const T* x = static_cast<const T*>(r.x) + m * r.stride;
+    const T* pre[2] = {static_cast<const T*>(r.pre[0]) + at, static_cast<const T*>(r.pre[1]) + at};
+    T* dz[2] = {static_cast<T*>(r.dz[0]) + at, static_cast<T*>(r.dz[1]) + at};
+    auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    const bool vx = aligned(x), v0 = aligned(pre[0]), v1 = aligned(pre[1]), w0 = aligned(dz[0]), w1 = aligned(dz[1]);
     // the gradients of values n .. n + 7, 0 past the row
     auto form = [&](int n, float (&g)[8], float (&u)[8]) {
+        const int left = N - n;
+        get8(x + n, left, vx, g);
+        if (!r.pre[0]) return;
+        float z[8], y[8];
+        get8(pre[0] + n, left, v0, z);
+        if (r.mats == 2) get8(pre[1] + n, left, v1, y);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            g[k] = u[k] = 0.f;
-            if (n + k >= N) continue;
-            g[k] = one<T>(x, n + k);
-            if (!r.pre[0]) continue;
             float a, d;
-            activate(r.act, one<T>(r.pre[0], at + n + k), a, d);
+            activate(r.act, z[k], a, d);
             u[k] = g[k] * a;
             g[k] *= d;
-            if (r.mats == 2) g[k] *= one<T>(r.pre[1], at + n + k);
+            if (r.mats == 2) g[k] *= y[k];
         }
     };
     float amax = 0.f, g[8], u[8];
-    for (int c = threadIdx.x; c < steps * 8; c += THREADS) {
+#pragma unroll 2
+    for (int c = threadIdx.x; c < (N + 7) / 8; c += THREADS) {
         form(8 * c, g, u);
 #pragma unroll
         for (int k = 0; k < 8; ++k) amax = fmaxf(amax, r.mats == 2 ? fmaxf(fabsf(g[k]), fabsf(u[k])) : fabsf(g[k]));
     }
     const Scale s = row_scale(max_cta<THREADS>(amax, s_max));
     if (threadIdx.x == 0) r.up[m] = s.up;
+#pragma unroll 2
     for (int c = threadIdx.x; c < steps * 8; c += THREADS) {
         form(8 * c, g, u);
         put(r, m, c >> 3, c & 7, g, s.down);
         if (r.mats == 2) put(r, m, steps + (c >> 3), c & 7, u, s.down);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (8 * c + k >= N) continue;
-            if (r.dz[0]) store(r.dz[0], r.dtype, at + 8 * c + k, g[k]);
-            if (r.dz[1]) store(r.dz[1], r.dtype, at + 8 * c + k, u[k]);
-        }
+        if (r.dz[0]) put8(dz[0] + 8 * c, N - 8 * c, w0, g);
+        if (r.dz[1]) put8(dz[1] + 8 * c, N - 8 * c, w1, u);
     }
 }
 

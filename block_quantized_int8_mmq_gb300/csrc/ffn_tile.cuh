@@ -76,58 +76,79 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 
 __device__ __forceinline__ void sync_weight_warps() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
-__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
-    if (act == MMQ_ACT_NONE) return;
-#define MMQ_ACT_CASE(A)                   \
-    if (act == A)                         \
-        _Pragma("unroll") for (int i = 0; i < 8; ++i) { \
-            float a, d;                   \
-            activate(A, v[i], a, d);      \
-            v[i] = a;                     \
-        }
-    MMQ_ACT_CASE(MMQ_ACT_SILU)
-    MMQ_ACT_CASE(MMQ_ACT_GELU)
-    MMQ_ACT_CASE(MMQ_ACT_GELU_TANH)
-    MMQ_ACT_CASE(MMQ_ACT_RELU)
-#undef MMQ_ACT_CASE
-}
-
-__device__ __forceinline__ void store8(void* p, int dtype, long long at, long long stride, int count, const float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < count) store(p, dtype, at + i * stride, v[i]);
-}
-
-// Eight rows of x, m .. m + count - 1, of the output columns of a lane: z0, z1 are the sums of its two tiles.
-template <bool BACK>
-__device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, int m, int count, float (&z0)[8],
-                                        float (&z1)[8]) {
+template <int ACT>
+__device__ __forceinline__ void activate8(float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float up = i < count ? __ldg(a.up + m + i) : 0.f;
-        z0[i] *= up;
-        z1[i] *= up;
+        float a, d;
+        activate(ACT, v[i], a, d);
+        v[i] = a;
     }
+}
+__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
+    if (act == MMQ_ACT_SILU) activate8<MMQ_ACT_SILU>(v);
+    if (act == MMQ_ACT_GELU) activate8<MMQ_ACT_GELU>(v);
+    if (act == MMQ_ACT_GELU_TANH) activate8<MMQ_ACT_GELU_TANH>(v);
+    if (act == MMQ_ACT_RELU) activate8<MMQ_ACT_RELU>(v);
+}
+
+// Eight rows of x (m .. m + count - 1) of an output column: stored with `stride` elements between them.
+template <typename T>
+__device__ __forceinline__ void store8(void* p, long long at, long long stride, int count, const float (&v)[8]) {
+    T* q = static_cast<T*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i < count) put_one(q, v[i]);
+        q += stride;
+    }
+}
+
+// What an output column needs beside its sums, asked for before they are there.
+struct Beside {
+    float up[8], r[2][8];
+};
+template <typename T, bool BACK>
+__device__ __forceinline__ void beside8(const Tile& a, int pair, int lane_row, int m, int count, Beside& w) {
+    if (count == 8) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(a.up + m)), v = __ldg(reinterpret_cast<const float4*>(a.up + m + 4));
+        w.up[0] = u.x, w.up[1] = u.y, w.up[2] = u.z, w.up[3] = u.w, w.up[4] = v.x, w.up[5] = v.y, w.up[6] = v.z, w.up[7] = v.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w.up[i] = i < count ? __ldg(a.up + m + i) : 0.f;
+    }
+    if (BACK || !a.residual) return;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int n = pair * 256 + g * 128 + lane_row;
+        const T* q = static_cast<const T*>(a.residual) + m * a.residual_stride + n;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w.r[g][i] = i < count && n < a.width ? get_one(q) : 0.f;
+            q += a.residual_stride;
+        }
+    }
+}
+
+// The outputs of a lane's columns: z0, z1 are the sums of its two tiles.
+template <typename T, bool BACK>
+__device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, int m, int count, const Beside& w,
+                                        float (&z0)[8], float (&z1)[8]) {
     if (!BACK && a.mats == 2) {
         const int n = pair * 128 + lane_row;
         if (n >= a.width) return;
         const long long at = (long long)m * a.width + n;
-        if (a.bias[0]) {
-            const float b = __ldg(a.bias[0] + n);
+        const float b0 = a.bias[0] ? __ldg(a.bias[0] + n) : 0.f, b1 = a.bias[1] ? __ldg(a.bias[1] + n) : 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z0[i] += b;
+        for (int i = 0; i < 8; ++i) {
+            z0[i] = fmaf(z0[i], w.up[i], b0);
+            z1[i] = fmaf(z1[i], w.up[i], b1);
         }
-        if (a.bias[1]) {
-            const float b = __ldg(a.bias[1] + n);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z1[i] += b;
-        }
-        if (a.pre[0]) store8(a.pre[0], a.dtype, at, a.width, count, z0);
-        if (a.pre[1]) store8(a.pre[1], a.dtype, at, a.width, count, z1);
+        if (a.pre[0]) store8<T>(a.pre[0], at, a.width, count, z0);
+        if (a.pre[1]) store8<T>(a.pre[1], at, a.width, count, z1);
         activate8(a.act, z0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z0[i] *= z1[i];
-        store8(a.out, a.dtype, at, a.width, count, z0);
+        store8<T>(a.out, at, a.width, count, z0);
         return;
     }
 #pragma unroll
@@ -136,23 +157,17 @@ __device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, i
         const int n = pair * 256 + g * 128 + lane_row;
         if (n >= a.width) continue;
         const long long at = (long long)m * a.width + n;
+        const float b = !BACK && a.bias[0] ? __ldg(a.bias[0] + n) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = fmaf(z[i], w.up[i], b);
         if (!BACK) {
-            if (a.bias[0]) {
-                const float b = __ldg(a.bias[0] + n);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] += b;
-            }
-            if (a.pre[0]) store8(a.pre[0], a.dtype, at, a.width, count, z);
+            if (a.pre[0]) store8<T>(a.pre[0], at, a.width, count, z);
             activate8(a.act, z);
-            if (a.residual) {
-                float r[8];
+            if (a.residual)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r[i] = i < count ? load(a.residual, a.dtype, (m + i) * a.residual_stride + n) : 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] += r[i];
-            }
+                for (int i = 0; i < 8; ++i) z[i] += w.r[g][i];
         }
-        store8(a.out, a.dtype, at, a.width, count, z);
+        store8<T>(a.out, at, a.width, count, z);
     }
 }
 
@@ -431,22 +446,43 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 return a.parts + ((((long long)cta * 2 + which) * 2 + tile) * a.nt) * 128 + lane_row;
             };
             const int b0 = 8 * (wid >> 2);  // the four warps of a lane take columns by turns
+            auto output = [&](auto type) {
+                using T = decltype(type);
 #pragma unroll 1
-            for (int b = b0; m0 + b < m1; b += 32) {
-                uint32_t v0[8], v1[8];
-                ptx::tmem_ld8(src + b, v0);
-                ptx::tmem_ld8(src + S::NT + b, v1);
-                ptx::tmem_ld_wait(v0);
-                ptx::tmem_ld_wait(v1);
-                if (whole) {
+                for (int b = b0; m0 + b < m1; b += 32) {
+                    const int count = min(8, m1 - m0 - b);
+                    Beside w;
+                    beside8<T, BACK>(a, pair, lane_row, m0 + b, count, w);
+                    uint32_t v0[8], v1[8];
+                    ptx::tmem_ld8(src + b, v0);
+                    ptx::tmem_ld8(src + S::NT + b, v1);
+                    ptx::tmem_ld_wait(v0);
+                    ptx::tmem_ld_wait(v1);
                     float z0[8], z1[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         z0[i] = __uint_as_float(v0[i]);
                         z1[i] = __uint_as_float(v1[i]);
                     }
-                    finish8<BACK>(a, pair, lane_row, m0 + b, min(8, m1 - m0 - b), z0, z1);
-                } else {
+                    finish8<T, BACK>(a, pair, lane_row, m0 + b, count, w, z0, z1);
+                    __syncwarp();
+                }
+            };
+            if (whole) {
+                if (SPLIT)
+                    output(float{});
+                else if (a.dtype == MMQ_BF16)
+                    output(__nv_bfloat16{});
+                else
+                    output(__half{});
+            } else {
+#pragma unroll 1
+                for (int b = b0; m0 + b < m1; b += 32) {
+                    uint32_t v0[8], v1[8];
+                    ptx::tmem_ld8(src + b, v0);
+                    ptx::tmem_ld8(src + S::NT + b, v1);
+                    ptx::tmem_ld_wait(v0);
+                    ptx::tmem_ld_wait(v1);
                     float* p0 = part(blockIdx.x, c0 == 0, 0) + b * 128;
                     float* p1 = part(blockIdx.x, c0 == 0, 1) + b * 128;
 #pragma unroll
@@ -455,7 +491,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                         p1[i * 128] = __uint_as_float(v1[i]);
                     }
                 }
-                __syncwarp();
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -466,9 +501,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 sync_weight_warps();  // every warp's part is written; the counter releases and acquires them
                 if (tid == 0) s_last = ptx::atom_inc_acq_rel(a.counters + u) == (unsigned)(last - first);
                 sync_weight_warps();
-                if (s_last) {
+                auto join = [&](auto type) {
+                    using T = decltype(type);
 #pragma unroll 1
                     for (int b = b0; m0 + b < m1; b += 32) {
+                        const int count = min(8, m1 - m0 - b);
+                        Beside w;
+                        beside8<T, BACK>(a, pair, lane_row, m0 + b, count, w);
                         float z0[8], z1[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) z0[i] = z1[i] = 0.f;
@@ -478,15 +517,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                             const int which = cta == first;
                             const float* p0 = part(cta, which, 0) + b * 128;
                             const float* p1 = part(cta, which, 1) + b * 128;
+                            float x0[8], x1[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                z0[i] += __ldcg(p0 + i * 128);
-                                z1[i] += __ldcg(p1 + i * 128);
+                                x0[i] = __ldcg(p0 + i * 128);
+                                x1[i] = __ldcg(p1 + i * 128);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                z0[i] += x0[i];
+                                z1[i] += x1[i];
                             }
                         }
-                        finish8<BACK>(a, pair, lane_row, m0 + b, min(8, m1 - m0 - b), z0, z1);
+                        finish8<T, BACK>(a, pair, lane_row, m0 + b, count, w, z0, z1);
                         __syncwarp();
                     }
+                };
+                if (s_last) {
+                    if (SPLIT)
+                        join(float{});
+                    else if (a.dtype == MMQ_BF16)
+                        join(__nv_bfloat16{});
+                    else
+                        join(__half{});
                 }
             }
         }
