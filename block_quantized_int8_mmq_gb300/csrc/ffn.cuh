@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace mmq {
@@ -91,27 +93,49 @@ __device__ __forceinline__ void put_one(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put_one(__half* p, float v) { *p = __float2half_rn(v); }
 
-// act(z) and act'(z).  A NaN stays one.  (The quotients are 1 / (1 + e) with two ulp, and 0 above 2^126.)
-__device__ __forceinline__ void activate(int act, float z, float& a, float& d) {
-    if (act == MMQ_ACT_NONE) {
+// e^x.  FAST: 2^(x log2 e) with the argument rounded to f32: 2^-23 of it off, which is nothing beside a 16-bit value.
+template <bool FAST>
+__device__ __forceinline__ float exponential(float x) {
+    return FAST ? __expf(x) : expf(x);
+}
+
+// act(z) and act'(z).  A NaN stays one.  The quotients are 1 / (1 + e) with two ulp, and 0 where e is above 2^126.
+template <int ACT, bool FAST>
+__device__ __forceinline__ void activate(float z, float& a, float& d) {
+    if (ACT == MMQ_ACT_NONE) {
         a = z;
         d = 1.f;
-    } else if (act == MMQ_ACT_RELU) {
+    } else if (ACT == MMQ_ACT_RELU) {
         a = z < 0.f ? 0.f : z;
         d = z > 0.f ? 1.f : 0.f;
-    } else if (act == MMQ_ACT_SILU) {
-        const float s = __fdividef(1.f, 1.f + expf(-z));
+    } else if (ACT == MMQ_ACT_SILU) {
+        const float s = __fdividef(1.f, 1.f + exponential<FAST>(-z));
         a = z * s;
         d = s * (1.f + z * (1.f - s));
-    } else if (act == MMQ_ACT_GELU) {
+    } else if (ACT == MMQ_ACT_GELU) {
         const float s = 0.5f * erfcf(-0.70710678118654752f * z);
         a = z * s;
-        d = s + z * 0.39894228040143268f * expf(-0.5f * z * z);
+        d = s + z * 0.39894228040143268f * exponential<FAST>(-0.5f * z * z);
     } else {  // gelu, by tanh: (1 + tanh(t)) / 2 = 1 / (1 + exp(-2 t))
-        const float z2 = z * z, s = __fdividef(1.f, 1.f + expf(-1.5957691216057308f * z * (1.f + 0.044715f * z2)));
+        const float z2 = z * z;
+        const float s = __fdividef(1.f, 1.f + exponential<FAST>(-1.5957691216057308f * z * (1.f + 0.044715f * z2)));
         a = z * s;
         d = s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z2);
     }
+}
+// f(integral_constant of the activation): one branch for a loop of them
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+    if (act == MMQ_ACT_SILU)
+        f(std::integral_constant<int, MMQ_ACT_SILU>{});
+    else if (act == MMQ_ACT_GELU)
+        f(std::integral_constant<int, MMQ_ACT_GELU>{});
+    else if (act == MMQ_ACT_GELU_TANH)
+        f(std::integral_constant<int, MMQ_ACT_GELU_TANH>{});
+    else if (act == MMQ_ACT_RELU)
+        f(std::integral_constant<int, MMQ_ACT_RELU>{});
+    else
+        f(std::integral_constant<int, MMQ_ACT_NONE>{});
 }
 
 }  // namespace ffn

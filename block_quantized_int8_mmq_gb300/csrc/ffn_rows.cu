@@ -5,7 +5,7 @@
 // but what lies 2^-38 below it, and written as f16 (bf16 rows exactly, f16 rows as they are but for the
 // scaling; f32 rows in two terms) in the order in which the tensor cores read them: per 64 values and 8 rows 1024
 // bytes, eight core matrices of 8 rows x 16 bytes.  `up` takes the scaling back, and the 2^8 of the weights.
-// HBM-bound; a CTA per row, the row read twice (the second time from L1 or L2) where it does not fit in registers.
+// HBM-bound.  f16 rows are operands as they are: no scaling, so they are cut at will.
 #include "ffn.cuh"
 #include "kv.cuh"
 #include "umma.cuh"
@@ -53,7 +53,7 @@ __device__ __forceinline__ void put(const Rows& r, int m, int step, int chunk, c
 }
 
 __device__ __forceinline__ void clear_counters(const Rows& r) {
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < r.n_counters; i += blockDim.x) r.counters[i] = 0u;
 }
 
@@ -67,48 +67,67 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
     }
 }
 
-constexpr int HELD = 4;  // runs of 8 values a thread keeps
+// A CTA lays out eight rows (a group), or one of them where there are few: a thread takes runs of eight values of
+// one row; with eight rows, neighbouring threads those of one place, whose 16 bytes lie side by side in a tile.
+constexpr int HELD = 5;  // runs a thread keeps between looking for the largest value and writing
 
-template <typename T, int THREADS>
+template <typename T, int ROWS, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
-    __shared__ float s_max[THREADS / 32];
+    constexpr int LANES = THREADS / ROWS;  // threads of a row
+    constexpr bool SCALED = !std::is_same<T, __half>::value;
+    __shared__ float s_max[THREADS / 32][ROWS];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch_dependents();
     clear_counters(r);
-    const int m = blockIdx.x, runs = r.width / 8, places = (r.width + 63) / 64 * 8;  // K is a multiple of 32
+    const int m = blockIdx.x * ROWS + threadIdx.x % ROWS, first = threadIdx.x / ROWS + blockIdx.y * LANES;
+    const int step = LANES * gridDim.y;                                 // (f16 rows are shared by several CTAs)
+    const int runs = m < r.rows ? r.width / 8 : 0;                      // K is a multiple of 32
+    const int places = m < r.rows ? (r.width + 63) / 64 * 8 : 0;        // whole steps: zeros past K
     const T* x = static_cast<const T*>(r.x) + m * r.stride;
-    float held[HELD][8], amax = 0.f;
+    float held[HELD][8], down = 1.f;
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-        const int c = threadIdx.x + i * THREADS;
+        const int c = first + i * step;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) held[i][k] = 0.f;
         if (c < runs) load8(x + 8ll * c, held[i]);
     }
+    if (SCALED) {
+        float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < HELD; ++i)
-        if (threadIdx.x + i * THREADS < runs)
+        for (int i = 0; i < HELD; ++i)
 #pragma unroll
             for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(held[i][k]));
-    for (int c = threadIdx.x + HELD * THREADS; c < runs; c += THREADS) {
-        float v[8];
-        load8(x + 8ll * c, v);
+#pragma unroll 4
+        for (int c = first + HELD * step; c < runs; c += step) {
+            float v[8];
+            load8(x + 8ll * c, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
+            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
+        }
+#pragma unroll
+        for (int o = ROWS; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (threadIdx.x % 32 < ROWS) s_max[threadIdx.x / 32][threadIdx.x % ROWS] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) amax = fmaxf(amax, s_max[i][threadIdx.x % ROWS]);
+        const Scale s = row_scale(amax);
+        if (threadIdx.x < ROWS && m < r.rows) r.up[m] = s.up;
+        down = s.down;
+    } else if (blockIdx.y == 0 && threadIdx.x < ROWS && m < r.rows) {
+        r.up[m] = 1.f / 256.f;  // the weights' 2^8
     }
-    const Scale s = row_scale(max_cta<THREADS>(amax, s_max));
-    if (threadIdx.x == 0) r.up[m] = s.up;
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-        const int c = threadIdx.x + i * THREADS;
-        if (c < runs) put(r, m, c >> 3, c & 7, held[i], s.down);
+        const int c = first + i * step;
+        if (c < places) put(r, m, c >> 3, c & 7, held[i], down);
     }
-    for (int c = threadIdx.x + HELD * THREADS; c < places; c += THREADS) {
+#pragma unroll 4
+    for (int c = first + HELD * step; c < places; c += step) {
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (c < runs) load8(x + 8ll * c, v);
-        put(r, m, c >> 3, c & 7, v, s.down);
+        put(r, m, c >> 3, c & 7, v, down);
     }
-    // the last step's places past K, where all runs are held
-    const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int c = runs + threadIdx.x; c < min(places, HELD * THREADS); c += THREADS) put(r, m, c >> 3, c & 7, none, s.down);
 }
 
 // Eight values from an address that is aligned to its elements, as one load where it is aligned to 16 bytes.
@@ -146,53 +165,69 @@ __global__ void __launch_bounds__(THREADS) k_ffn_gradients(const Rows r) {
     const int m = blockIdx.x, N = r.width, steps = (N + 63) / 64;
     const long long at = (long long)m * N;
     const T* x = static_cast<const T*>(r.x) + m * r.stride;
-    const T* pre[2] = {static_cast<const T*>(r.pre[0]) + at, static_cast<const T*>(r.pre[1]) + at};
-    T* dz[2] = {static_cast<T*>(r.dz[0]) + at, static_cast<T*>(r.dz[1]) + at};
+    const T* pre[2] = {nullptr, nullptr};
+    T* dz[2] = {nullptr, nullptr};
+    for (int g = 0; g < 2; ++g) {
+        if (r.pre[g]) pre[g] = static_cast<const T*>(r.pre[g]) + at;
+        if (r.dz[g]) dz[g] = static_cast<T*>(r.dz[g]) + at;
+    }
     auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
     const bool vx = aligned(x), v0 = aligned(pre[0]), v1 = aligned(pre[1]), w0 = aligned(dz[0]), w1 = aligned(dz[1]);
-    // the gradients of values n .. n + 7, 0 past the row
-    auto form = [&](int n, float (&g)[8], float (&u)[8]) {
-        const int left = N - n;
-        get8(x + n, left, vx, g);
-        if (!r.pre[0]) return;
-        float z[8], y[8];
-        get8(pre[0] + n, left, v0, z);
-        if (r.mats == 2) get8(pre[1] + n, left, v1, y);
+    with_act(r.pre[0] ? r.act : MMQ_ACT_NONE, [&](auto A) {
+        // the gradients of values n .. n + 7, 0 past the row
+        auto form = [&](int n, auto fast, float (&g)[8], float (&u)[8]) {
+            const int left = N - n;
+            float z[8], y[8];
+            get8(x + n, left, vx, g);
+            if (r.pre[0]) get8(pre[0] + n, left, v0, z);
+            if (r.mats == 2) get8(pre[1] + n, left, v1, y);
+            if (!r.pre[0]) return;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float a, d;
-            activate(r.act, z[k], a, d);
-            u[k] = g[k] * a;
-            g[k] *= d;
-            if (r.mats == 2) g[k] *= y[k];
+            for (int k = 0; k < 8; ++k) {
+                float a, d;
+                activate<decltype(A)::value, decltype(fast)::value>(z[k], a, d);
+                u[k] = g[k] * a;
+                g[k] *= d;
+                if (r.mats == 2) g[k] *= y[k];
+            }
+        };
+        float amax = 0.f, g[8], u[8];
+#pragma unroll 1
+        for (int c = threadIdx.x; c < (N + 7) / 8; c += THREADS) {
+            form(8 * c, std::true_type{}, g, u);  // (the largest value's exponent is all that is wanted)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, r.mats == 2 ? fmaxf(fabsf(g[k]), fabsf(u[k])) : fabsf(g[k]));
         }
-    };
-    float amax = 0.f, g[8], u[8];
-#pragma unroll 2
-    for (int c = threadIdx.x; c < (N + 7) / 8; c += THREADS) {
-        form(8 * c, g, u);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, r.mats == 2 ? fmaxf(fabsf(g[k]), fabsf(u[k])) : fabsf(g[k]));
-    }
-    const Scale s = row_scale(max_cta<THREADS>(amax, s_max));
-    if (threadIdx.x == 0) r.up[m] = s.up;
-#pragma unroll 2
-    for (int c = threadIdx.x; c < steps * 8; c += THREADS) {
-        form(8 * c, g, u);
-        put(r, m, c >> 3, c & 7, g, s.down);
-        if (r.mats == 2) put(r, m, steps + (c >> 3), c & 7, u, s.down);
-        if (r.dz[0]) put8(dz[0] + 8 * c, N - 8 * c, w0, g);
-        if (r.dz[1]) put8(dz[1] + 8 * c, N - 8 * c, w1, u);
-    }
+        const Scale s = row_scale(max_cta<THREADS>(amax, s_max));
+        if (threadIdx.x == 0) r.up[m] = s.up;
+#pragma unroll 1
+        for (int c = threadIdx.x; c < steps * 8; c += THREADS) {
+            form(8 * c, std::integral_constant<bool, sizeof(T) == 2>{}, g, u);
+            put(r, m, c >> 3, c & 7, g, s.down);
+            if (r.mats == 2) put(r, m, steps + (c >> 3), c & 7, u, s.down);
+            if (r.dz[0]) put8(dz[0] + 8 * c, N - 8 * c, w0, g);
+            if (r.dz[1]) put8(dz[1] + 8 * c, N - 8 * c, w1, u);
+        }
+    });
 }
 
 template <typename T>
 int launch(const Rows& r, bool back, const char* fn, cudaStream_t s) {
     ProfScope ps(back ? "k_ffn_gradients" : "k_ffn_rows", s);
-    constexpr int T0 = 256;
-    const dim3 grid((unsigned)r.rows);
-    return pdl_status(back ? launch_pdl(&k_ffn_gradients<T, T0>, grid, dim3(T0), 0, s, r)
-                           : launch_pdl(&k_ffn_rows<T, T0>, grid, dim3(T0), 0, s, r),
+    if (back) return pdl_status(launch_pdl(&k_ffn_gradients<T, 256>, dim3((unsigned)r.rows), dim3(256), 0, s, r), fn);
+    // eight rows a CTA where that makes a CTA for every other SM at least
+    const int sms = device_shape().sms;
+    const bool many = r.rows >= 4 * sms;
+    const int ctas = many ? r.groups : r.rows;
+    int cuts = 1;
+    if (std::is_same<T, __half>::value) {
+        const int runs = r.width / 8, each = (many ? 64 : 512) * HELD;  // runs of a row that one CTA holds
+        cuts = 4 * sms / ctas < 1 ? 1 : 4 * sms / ctas;
+        cuts = cuts < (runs + each - 1) / each ? cuts : (runs + each - 1) / each;
+    }
+    const dim3 grid((unsigned)ctas, (unsigned)cuts);
+    return pdl_status(many ? launch_pdl(&k_ffn_rows<T, 8, 512>, grid, dim3(512), 0, s, r)
+                           : launch_pdl(&k_ffn_rows<T, 1, 512>, grid, dim3(512), 0, s, r),
                       fn);
 }
 

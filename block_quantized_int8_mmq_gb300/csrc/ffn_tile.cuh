@@ -21,8 +21,6 @@
 // last CTA to arrive adds them in their order: the order of summation depends on the sizes alone.
 #pragma once
 
-#include <type_traits>
-
 #include "ffn_weights.cuh"
 #include "kv.cuh"
 
@@ -76,20 +74,17 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 
 __device__ __forceinline__ void sync_weight_warps() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
-template <int ACT>
-__device__ __forceinline__ void activate8(float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float a, d;
-        activate(ACT, v[i], a, d);
-        v[i] = a;
-    }
-}
+template <bool FAST>
 __device__ __forceinline__ void activate8(int act, float (&v)[8]) {
-    if (act == MMQ_ACT_SILU) activate8<MMQ_ACT_SILU>(v);
-    if (act == MMQ_ACT_GELU) activate8<MMQ_ACT_GELU>(v);
-    if (act == MMQ_ACT_GELU_TANH) activate8<MMQ_ACT_GELU_TANH>(v);
-    if (act == MMQ_ACT_RELU) activate8<MMQ_ACT_RELU>(v);
+    if (act == MMQ_ACT_NONE) return;
+    with_act(act, [&](auto A) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float a, d;
+            activate<decltype(A)::value, FAST>(v[i], a, d);
+            v[i] = a;
+        }
+    });
 }
 
 // Eight rows of x (m .. m + count - 1) of an output column: stored with `stride` elements between them.
@@ -145,7 +140,7 @@ __device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, i
         }
         if (a.pre[0]) store8<T>(a.pre[0], at, a.width, count, z0);
         if (a.pre[1]) store8<T>(a.pre[1], at, a.width, count, z1);
-        activate8(a.act, z0);
+        activate8<sizeof(T) == 2>(a.act, z0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z0[i] *= z1[i];
         store8<T>(a.out, at, a.width, count, z0);
@@ -162,7 +157,7 @@ __device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, i
         for (int i = 0; i < 8; ++i) z[i] = fmaf(z[i], w.up[i], b);
         if (!BACK) {
             if (a.pre[0]) store8<T>(a.pre[0], at, a.width, count, z);
-            activate8(a.act, z);
+            activate8<sizeof(T) == 2>(a.act, z);
             if (a.residual)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z[i] += w.r[g][i];
