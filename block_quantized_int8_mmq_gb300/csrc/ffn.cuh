@@ -54,8 +54,9 @@ struct Tile {
     float* parts;
     unsigned* counters;
     int mats, M, N, K, width;    // width: of the output
+    int sub;                     // 64-value pieces of the reduction in a step
     int groups, mtiles, nt;      // groups of 8 rows, row tiles, rows in a tile (a multiple of 16)
-    int units, steps, chunks;    // steps (64 values of the reduction) and chunks of a unit
+    int units, steps, chunks;    // steps (64 or 128 values of the reduction) and chunks of a unit
     int rounds, rest;            // rounds of whole units, then `rest` units cut into equal runs of chunks
     int aligned, slot, rs, xs;   // weight rows begin on 16 bytes; bytes of a chunk's place; ring lengths
     int dtype, act;
@@ -70,14 +71,16 @@ constexpr int W_WARPS = 16, C_WARPS = 1, I_WARPS = 2, THREADS = (W_WARPS + C_WAR
 constexpr int STEP = 64;     // values of the reduction that are multiplied together
 constexpr int CHUNK = 256;   // values of a weight row that are copied together
 constexpr int RING = 8, R_MOST = 8;  // barriers of steps; longest ring of weight chunks
-template <bool SPLIT>
+// SUB: 64-value pieces of the reduction in a step.  Two where TMEM has the room (16-bit rows, forward, up to 128 rows
+// a tile): a step costs its warps some 600 cycles of waits and loops, which few rows' products do not cover.
+template <bool SPLIT, int SUB = 1>
 struct Shape {
     static constexpr int TERMS = SPLIT ? 2 : 1;
-    static constexpr int NT = SPLIT ? 64 : 192;     // rows of x in a tile, at most
+    static constexpr int NT = SPLIT ? 64 : SUB == 2 ? 128 : 192;  // rows of x in a tile, at most
     static constexpr int DB = SPLIT ? 2 : 1;        // accumulator buffers
     static constexpr int D_COLS = 2 * NT;           // of a buffer: two weight tiles
     static constexpr int COL_A = DB * D_COLS;       // forward: weights, two stages
-    static constexpr int A_COLS = 64 * TERMS;       // of a stage: two tiles, 32 columns a term
+    static constexpr int A_COLS = 64 * TERMS * SUB; // of a stage: two tiles, 32 columns a term and piece
     static constexpr int A_BYTES = STEP * CHUNK * 2;  // backward: a stage's term in shared memory
     static_assert(COL_A + 2 * A_COLS <= 512, "TMEM columns");
 };

@@ -6,8 +6,8 @@ namespace {
 
 template <int FMT>
 int launch(const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    return a.dtype == MMQ_F32 ? ffn::launch_tile<FMT, true, true>(a, smem, ctas, fn, s)
-                              : ffn::launch_tile<FMT, false, true>(a, smem, ctas, fn, s);
+    return a.dtype == MMQ_F32 ? ffn::launch_tile<FMT, true, true, 1>(a, smem, ctas, fn, s)
+                              : ffn::launch_tile<FMT, false, true, 1>(a, smem, ctas, fn, s);
 }
 
 }  // namespace

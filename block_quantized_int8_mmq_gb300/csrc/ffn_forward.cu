@@ -6,8 +6,9 @@ namespace {
 
 template <int FMT>
 int launch(const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    return a.dtype == MMQ_F32 ? ffn::launch_tile<FMT, true, false>(a, smem, ctas, fn, s)
-                              : ffn::launch_tile<FMT, false, false>(a, smem, ctas, fn, s);
+    if (a.dtype == MMQ_F32) return ffn::launch_tile<FMT, true, false, 1>(a, smem, ctas, fn, s);
+    return a.sub == 2 ? ffn::launch_tile<FMT, false, false, 2>(a, smem, ctas, fn, s)
+                      : ffn::launch_tile<FMT, false, false, 1>(a, smem, ctas, fn, s);
 }
 
 }  // namespace

@@ -59,7 +59,9 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.nt = (int)up_to(ceil_div(c.M, ceil_div(c.M, nt_most)), 16);
     a.mtiles = (int)ceil_div(c.M, a.nt);
     a.units = (int)(a.mtiles * ceil_div(a.width, !c.backward && c.mats == 2 ? 128 : 256));
-    a.steps = (int)(c.backward ? c.mats * ceil_div(c.N, STEP) : ceil_div(c.K, STEP));
+    a.sub = !c.backward && !split && a.nt <= Shape<false, 2>::NT && c.K % (2 * STEP) == 0 ? 2 : 1;
+    const int pieces = (int)(c.backward ? c.mats * ceil_div(c.N, STEP) : ceil_div(c.K, STEP));  // of 64 values
+    a.steps = pieces / a.sub;
     a.chunks = c.backward ? a.steps : (int)ceil_div(c.K, CHUNK);
     a.aligned = a.row_bytes % 16 == 0;
     a.slot = slot_bytes(c.fmt, a.aligned);
@@ -74,7 +76,7 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.out = c.out;
     const int ctas = deal(a, cost(a, c.fmt, split, c.backward), device_shape().sms);
     // shared memory: two chunks' places at least, then up to four steps of rows, then more chunks
-    const int x_bytes = a.nt * 128 * terms, w_bytes = rings(c.backward) * 32 * a.slot;
+    const int x_bytes = a.nt * 128 * terms * a.sub, w_bytes = rings(c.backward) * 32 * a.slot;
     const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true>::A_BYTES : 0);
     a.xs = (left - 2 * w_bytes) / x_bytes;
     a.xs = a.xs > 4 ? 4 : a.xs;
@@ -91,7 +93,7 @@ int ffn_launch(const Call& c, cudaStream_t s) {
             report(c.fn, MMQ_ERR_CUDA, "the weights' tensor map was refused");
             return MMQ_ERR_CUDA;
         }
-    const long long term = (long long)a.steps * a.groups * 1024;
+    const long long term = (long long)pieces * a.groups * 1024;
     const long long counters = up_to(4ll * a.rest, 256), ups = up_to(4 * c.M, 256);
     const long long parts = a.rest ? 2ll * ctas * 2 * a.nt * 128 * 4 : 0;
     void* scratch = nullptr;

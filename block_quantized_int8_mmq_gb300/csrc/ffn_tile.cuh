@@ -166,9 +166,10 @@ __device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, i
     }
 }
 
-template <int FMT, bool SPLIT, bool BACK>
+template <int FMT, bool SPLIT, bool BACK, int SUB>
 __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__ Tile a) {
-    using S = Shape<SPLIT>;
+    using S = Shape<SPLIT, SUB>;
+    constexpr int PER = CHUNK / STEP / SUB;  // forward: steps of a chunk
     constexpr int TERMS = S::TERMS;
     constexpr int NG = rings(BACK), GW = W_WARPS / NG;  // rings, weight warps that share one
     constexpr int CB = chunk_bytes(FMT);
@@ -182,28 +183,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
     // are done) of step n at n % RING.
     const uint32_t full = bars, empty = full + 8 * RING, d_full = empty + 8 * RING, d_empty = d_full + 16;
     const uint32_t raw_full = d_empty + 16, raw_empty = raw_full + 8 * NG * R_MOST, done = raw_empty + 8 * NG * R_MOST;
-    const int xb = a.nt * 128 * TERMS;  // bytes of a step's rows
+    const int xb = a.nt * 128 * TERMS * SUB;  // bytes of a step's rows
     const uint32_t xs_addr = ptx::smem_u32(smem), as_addr = xs_addr + a.xs * xb;
     const uint32_t raw_addr = as_addr + (BACK ? 2 * TERMS * S::A_BYTES : 0);
     uint8_t* a_smem = smem + a.xs * xb;
     uint8_t* raw = a_smem + (BACK ? 2 * TERMS * S::A_BYTES : 0);
-    if (tid == 0) {
-        for (int i = 0; i < RING; ++i) {
-            ptx::mbar_init(full + 8 * i, W_WARPS / 2 + 1);
-            ptx::mbar_init(empty + 8 * i, I_WARPS);
-        }
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(d_full + 8 * i, I_WARPS);
-            ptx::mbar_init(d_empty + 8 * i, W_WARPS);
-            ptx::mbar_init(done + 8 * i, 1);
-        }
-        for (int i = 0; i < NG * R_MOST; ++i) {
-            ptx::mbar_init(raw_full + 8 * i, a.aligned ? 1 : 32 * GW);
-            ptx::mbar_init(raw_empty + 8 * i, GW);
-        }
-        ptx::fence_barrier_init();
-        s_abort = 0;
+    if (tid < RING) {
+        ptx::mbar_init(full + 8 * tid, W_WARPS / 2 + 1);
+        ptx::mbar_init(empty + 8 * tid, I_WARPS);
+    } else if (tid < RING + 2) {
+        const int i = tid - RING;
+        ptx::mbar_init(d_full + 8 * i, I_WARPS);
+        ptx::mbar_init(d_empty + 8 * i, W_WARPS);
+        ptx::mbar_init(done + 8 * i, 1);
+        if (a.aligned && i < a.mats) ptx::tma_prefetch_desc(&a.map[i]);
+        if (i == 0) s_abort = 0;
+    } else if (tid >= 32 && tid < 32 + NG * R_MOST) {
+        const int i = tid - 32;
+        ptx::mbar_init(raw_full + 8 * i, a.aligned ? 1 : 32 * GW);
+        ptx::mbar_init(raw_empty + 8 * i, GW);
     }
+    ptx::fence_barrier_init();
     if (wid == W_WARPS + C_WARPS + 1) {
         ptx::tmem_alloc(ptx::smem_u32(&s_tmem), 512);
         ptx::tmem_relinquish();
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
     volatile int* abort = &s_abort;
     unsigned* err = &g_ffn_tile_error;
     auto step_range = [&](int c0, int c1, int& s0, int& s1) {
-        s0 = BACK ? c0 : c0 * (CHUNK / STEP);
-        s1 = BACK ? c1 : min(a.steps, c1 * (CHUNK / STEP));
+        s0 = BACK ? c0 : c0 * PER;
+        s1 = BACK ? c1 : min(a.steps, c1 * PER);
     };
 
     if (wid < W_WARPS) {
@@ -323,17 +323,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     break;
                 }
                 const uint8_t* src = ring + slot * 32 * a.slot;
-                auto one = [&](int j) {
+                // the quarter j: piece `sub` of this set's step
+                auto one = [&](int j, int sub) {
                     const int k0 = (BACK ? pair : c) * CHUNK + j * STEP;
                     const int blocks = min(2, max(0, (a.K - k0) / QK));
                     quarter<FMT, SPLIT>(src, j, mis, a.aligned, blocks, !BACK || valid, check,
                                         [&](int half, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
-                        if (half == 0 && ok && before >= 0)
+                        if (half == 0 && sub == 0 && ok && before >= 0)
                             ok = umma::warp_wait(empty + 8 * (before % RING), (before / RING) & 1, abort, err);
                         if (!BACK) {
                             if (half == 0) ptx::tc_fence_after();
                             const uint32_t t = tmem + ((uint32_t)(32 * (wid & 3)) << 16) + S::COL_A + e * S::A_COLS +
-                                               g * 32 * TERMS + 16 * half;
+                                               (g * SUB + sub) * 32 * TERMS + 16 * half;
                             ptx::tmem_st16(t, hi);
                             if (SPLIT) ptx::tmem_st16(t + 32, lo);
                         } else {
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                             }
                         }
                     });
+                    if (sub + 1 < SUB) return;
                     if (!BACK) {
                         ptx::tmem_st_wait();
                         ptx::tc_fence_before();
@@ -355,30 +357,39 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                         ptx::fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    before = base + (BACK ? c - c0 : 4 * (c - c0) + j);
+                    before = base + (BACK ? c - c0 : PER * (c - c0) + (SUB == 2 ? e : j));
                     if (lane == 0) ptx::mbar_arrive(full + 8 * (before % RING));
                     ++mine;
                 };
                 if (BACK) {
                     if (FMT == FMT_Q8_0) {
-                        if (q == 0) one(0);
-                        if (q == 1) one(1);
-                        if (q == 2) one(2);
-                        if (q == 3) one(3);
+                        if (q == 0) one(0, 0);
+                        if (q == 1) one(1, 0);
+                        if (q == 2) one(2, 0);
+                        if (q == 3) one(3, 0);
                     } else {
-                        one(q);
+                        one(q, 0);
                     }
                 } else if (FMT == FMT_Q8_0) {
+                    // the set's quarters: e and e + 2, or 2 e and 2 e + 1
                     if (e == 0) {
-                        one(0);
-                        if (ok && 4 * c + 2 < a.steps) one(2);
+                        one(0, 0);
+                        if (SUB == 2)
+                            one(1, 1);
+                        else if (ok && 4 * c + 2 < a.steps)
+                            one(2, 0);
+                    } else if (SUB == 2) {
+                        if (2 * c + 1 < a.steps) {
+                            one(2, 0);
+                            one(3, 1);
+                        }
                     } else {
-                        if (4 * c + 1 < a.steps) one(1);
-                        if (ok && 4 * c + 3 < a.steps) one(3);
+                        if (4 * c + 1 < a.steps) one(1, 0);
+                        if (ok && 4 * c + 3 < a.steps) one(3, 0);
                     }
                 } else {
 #pragma unroll 1
-                    for (int j = e; j < 4 && ok; j += 2) one(j);
+                    for (int i = 0; i < 2 && ok; ++i) SUB == 2 ? one(2 * e + i, i) : one(e + 2 * i, 0);
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(raw_empty + 8 * (grp * R_MOST + slot));  // the chunk has been read
@@ -595,9 +606,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
             const uint32_t bytes = min(a.nt / 8, a.groups - g0) * 1024;
             int s0, s1;
             step_range(c0, c1, s0, s1);
-            const uint8_t* src = a.x + ((long long)s0 * a.groups + g0) * 1024;
+            const uint8_t* src = a.x + ((long long)s0 * SUB * a.groups + g0) * 1024;
 #pragma unroll 1
-            for (int s = s0; s < s1; ++s, ++n, src += (long long)a.groups * 1024) {
+            for (int s = s0; s < s1; ++s, ++n, src += (long long)SUB * a.groups * 1024) {
                 const int free = n - a.xs;  // the step whose products have read this place
                 if (free >= 0 && !umma::warp_wait(empty + 8 * (free % RING), (free / RING) & 1, abort, err)) {
                     ok = false;
@@ -605,8 +616,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 }
                 if (ptx::elect_one()) {
                     const uint32_t bar = full + 8 * (n % RING);
-                    ptx::mbar_arrive_expect_tx(bar, bytes * TERMS);
+                    ptx::mbar_arrive_expect_tx(bar, bytes * TERMS * SUB);
                     ptx::bulk_load(xs_addr + st * xb, src, bytes, bar);
+                    if (SUB == 2) ptx::bulk_load(xs_addr + st * xb + a.nt * 128, src + (long long)a.groups * 1024, bytes, bar);
                     if (SPLIT) ptx::bulk_load(xs_addr + st * xb + a.nt * 128, src + a.x_term, bytes, bar);
                 }
                 __syncwarp();
@@ -643,7 +655,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 const int i = s - s0;
                 const bool fresh = SPLIT ? i % PERIOD == 0 : i == 0, last = s + 1 == s1 || (SPLIT && i % PERIOD == PERIOD - 1);
                 const uint32_t buf = SPLIT ? n_d & 1 : 0;
-                const uint32_t st = s & 1;  // (a chunk of four steps begins on an even one)
+                const uint32_t st = s & 1;  // (a chunk of two or four steps begins on an even one)
                 if (fresh) ok = umma::warp_wait(d_empty + 8 * buf, (SPLIT ? (n_d >> 1) & 1 : n_d & 1) ^ 1, abort, err);
                 ok = ok && umma::warp_wait(full + 8 * (n % RING), (n / RING) & 1, abort, err);
                 if (!ok) break;
@@ -658,10 +670,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     for (int e = SPLIT ? 2 : 0; e >= 0; --e) {
                         const int ea = e == 2, ex = e == 1;
 #pragma unroll
-                        for (int kk = 0; kk < STEP / 16; ++kk) {
+                        for (int kk = 0; kk < SUB * STEP / 16; ++kk) {
                             if (!BACK)
-                                ptx::umma_f16_ts(d, tmem + S::COL_A + st * S::A_COLS + (g * TERMS + ea) * 32 + 8 * kk,
-                                                 xd + ex * term_x + 16 * kk, idesc, acc);
+                                ptx::umma_f16_ts(d, tmem + S::COL_A + st * S::A_COLS + (g * SUB * TERMS + ea) * 32 + 8 * kk,
+                                                 xd + (ex + kk / 4) * term_x + 16 * (kk % 4), idesc, acc);
                             else
                                 ptx::umma_f16(d, a_desc + (uint32_t)((st * TERMS + ea) * (S::A_BYTES >> 4) + kk * 512),
                                               xd + ex * term_x + 16 * kk, idesc, acc);
@@ -691,10 +703,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
 }
 
 // ------------------------------------------------------------------------------------------ host
-template <int FMT, bool SPLIT, bool BACK>
+template <int FMT, bool SPLIT, bool BACK, int SUB>
 int launch_tile(const Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
     static SmemAttr attr;
-    auto k = &k_ffn_tile<FMT, SPLIT, BACK>;
+    auto k = &k_ffn_tile<FMT, SPLIT, BACK, SUB>;
     const int st = ensure_smem(reinterpret_cast<const void*>(k), SMEM_MOST, attr);
     if (st != MMQ_OK) {
         report(fn, st, "the tiles' shared memory was refused");
