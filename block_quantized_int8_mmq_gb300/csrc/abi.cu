@@ -33,6 +33,7 @@ unsigned kv_stream_take_error();
 unsigned kv_tile_take_error();
 unsigned ffn_forward_take_error();
 unsigned ffn_backward_take_error();
+unsigned ffn_stream_take_error();
 
 DeviceShape device_shape() {
     static std::atomic<int> sms[MAX_DEVICES], smem[MAX_DEVICES], l2[MAX_DEVICES];
@@ -504,7 +505,7 @@ int mmq_get_device_error(void* stream) {
     }
     const unsigned bits = tc_take_error() | tcx_take_error() | small_take_error() | kv_cache_take_error() |
                           kv_stream_take_error() | kv_tile_take_error() | ffn_forward_take_error() |
-                          ffn_backward_take_error();
+                          ffn_backward_take_error() | ffn_stream_take_error();
     return (bits & ERR_TIMEOUT) ? MMQ_ERR_TIMEOUT : (bits & ERR_RANGE) ? MMQ_ERR_RANGE : MMQ_OK;
 }
 

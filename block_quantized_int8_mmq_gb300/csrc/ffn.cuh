@@ -39,6 +39,7 @@ struct Rows {
     void* dz[2];
     uint8_t* tiles;
     long long term;  // bytes from the first terms to the second
+    uint8_t* sums;   // where the sums of 32-value blocks go (k_ffn_stream), or nullptr
     float* up;
     unsigned* counters;
     int n_counters;
@@ -66,6 +67,27 @@ struct Tile {
     void* pre[2];
     void* out;
 };
+
+// The products of few rows (k_ffn_stream).
+struct Stream {
+    CUtensorMap map[2];            // of the weight matrices, where rows begin on 16 bytes
+    const uint8_t* w[2];
+    long long w_bytes, row_bytes;  // of a weight matrix, of a row
+    const uint8_t* x;              // the rows' tiles
+    long long x_term;
+    const uint8_t* sums;           // Q4_K, Q5_K: the blocks' sums
+    const float* up;
+    int mats, M, N, K, chunks, xgroups;  // xgroups: of 8 rows
+    int groups, splits;            // of a CTA: runs of 16 weight rows, shares of the reduction
+    int aligned, slot, rs;         // bytes of a chunk's row in shared memory, places of a warp's ring
+    int dtype, act;
+    const float* bias[2];
+    const void* residual;
+    long long residual_stride;
+    void* pre[2];
+    void* out;
+};
+constexpr int STREAM_ROWS = 16, STREAM_WARPS = 16, STREAM_SLAB = 16;  // rows of x at most, warps, weight rows of a warp
 
 constexpr int W_WARPS = 16, C_WARPS = 1, I_WARPS = 2, THREADS = (W_WARPS + C_WARPS + 1 + I_WARPS) * 32;
 constexpr int STEP = 64;     // values of the reduction that are multiplied together
@@ -147,5 +169,6 @@ int ffn_launch(const ffn::Call& c, cudaStream_t s);
 int ffn_rows_launch(const ffn::Rows& r, bool back, const char* fn, cudaStream_t s);
 int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s);
 int ffn_backward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s);
+int ffn_stream_launch(int fmt, const ffn::Stream& a, int smem, int ctas, const char* fn, cudaStream_t s);
 
 }  // namespace mmq

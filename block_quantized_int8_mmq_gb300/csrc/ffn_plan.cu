@@ -40,9 +40,96 @@ int deal(Tile& a, const Cost& t, int sms) {
     return (int)(a.units < sms ? a.units : sms);
 }
 
+// The row kernel's side of a call.
+Rows rows_of(const Call& c, int groups) {
+    Rows r{};
+    r.x = c.x;
+    r.stride = c.x_stride;
+    r.dtype = c.dtype;
+    r.act = c.act;
+    r.mats = c.mats;
+    r.rows = (int)c.M;
+    r.width = (int)(c.backward ? c.N : c.K);
+    r.groups = groups;
+    for (int g = 0; g < 2; ++g) {
+        r.pre[g] = c.backward ? c.pre[g] : nullptr;
+        r.dz[g] = c.dz[g];
+    }
+    return r;
+}
+
+bool weight_maps(const Call& c, CUtensorMap* map, long long row_bytes, int box_rows) {
+    for (int g = 0; g < c.mats; ++g)
+        if (!make_byte_map(&map[g], c.w[g], (uint64_t)row_bytes, (uint64_t)c.N, (uint32_t)chunk_bytes(c.fmt), box_rows, 2)) {
+            report(c.fn, MMQ_ERR_CUDA, "the weights' tensor map was refused");
+            return false;
+        }
+    return true;
+}
+
+// Few rows, forward: the weights as a stream.
+int stream(const Call& c, cudaStream_t s) {
+    const int terms = c.dtype == MMQ_F32 ? 2 : 1;
+    Stream a{};
+    a.row_bytes = c.fmt == FMT_Q8_0 ? c.K / QK * Q8_0_BYTES : c.K / QK_K * kq_bytes(c.fmt);
+    a.w_bytes = a.row_bytes * c.N;
+    a.mats = c.mats;
+    a.M = (int)c.M;
+    a.N = (int)c.N;
+    a.K = (int)c.K;
+    a.chunks = (int)ceil_div(c.K, CHUNK);
+    a.xgroups = (int)ceil_div(c.M, 8);
+    a.aligned = a.row_bytes % 16 == 0;
+    a.slot = slot_bytes(c.fmt, a.aligned);
+    a.dtype = c.dtype;
+    a.act = c.act;
+    for (int g = 0; g < 2; ++g) {
+        a.w[g] = static_cast<const uint8_t*>(c.w[g]);
+        a.bias[g] = c.bias[g];
+        a.pre[g] = c.pre[g];
+    }
+    a.residual = c.residual;
+    a.residual_stride = c.residual_stride;
+    a.out = c.out;
+    // Column runs of a CTA and shares of the reduction: the fewest chunks in a row, a wave's start counted as two.
+    const long long runs = ceil_div(c.N, STREAM_SLAB), sms = device_shape().sms;
+    long long best = 0, ctas = 0;
+    for (int per = 1; per * c.mats <= STREAM_WARPS; ++per) {
+        const int splits = STREAM_WARPS / (per * c.mats);
+        const long long n = ceil_div(runs, per), time = ceil_div(n, sms) * (ceil_div(a.chunks, splits) + 2);
+        if (best && time >= best) continue;
+        best = time;
+        ctas = n;
+        a.groups = per * c.mats;
+        a.splits = splits;
+    }
+    a.rs = 200 * 1024 / (STREAM_WARPS * STREAM_SLAB * a.slot);  // (what is left of the SM's memory caches rows of x)
+    a.rs = a.rs > R_MOST ? R_MOST : a.rs;
+    const int smem = STREAM_WARPS * STREAM_SLAB * a.slot * a.rs;
+    if (a.aligned && !weight_maps(c, a.map, a.row_bytes, STREAM_SLAB)) return MMQ_ERR_CUDA;
+
+    const long long term = ceil_div(c.K, STEP) * a.xgroups * 1024, sums = is_kquant(c.fmt) ? (long long)a.chunks * a.xgroups * 256 : 0;
+    void* scratch = nullptr;
+    int st = scratch_alloc((size_t)(256 + term * terms + sums), s, &scratch, c.fn);
+    if (st != MMQ_OK) return st;
+    uint8_t* at = static_cast<uint8_t*>(scratch);
+    Rows r = rows_of(c, a.xgroups);
+    r.up = reinterpret_cast<float*>(at);
+    a.up = r.up;
+    r.tiles = at + 256;
+    a.x = r.tiles;
+    r.term = a.x_term = term;
+    if (sums) a.sums = r.sums = r.tiles + term * terms;
+    st = ffn_rows_launch(r, false, c.fn, s);
+    if (st == MMQ_OK) st = ffn_stream_launch(c.fmt, a, smem, (int)ctas, c.fn, s);
+    scratch_free(scratch, s);  // stream-ordered: after the kernels above
+    return st;
+}
+
 }  // namespace
 
 int ffn_launch(const Call& c, cudaStream_t s) {
+    if (!c.backward && c.M <= STREAM_ROWS) return stream(c, s);
     const bool split = c.dtype == MMQ_F32;
     const int terms = split ? 2 : 1, nt_most = split ? Shape<true>::NT : Shape<false>::NT;
     Tile a{};
@@ -88,11 +175,7 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     }
     const int smem = SMEM_MOST - left + a.xs * x_bytes + a.rs * w_bytes;
 
-    for (int g = 0; g < c.mats && a.aligned; ++g)
-        if (!make_byte_map(&a.map[g], c.w[g], (uint64_t)a.row_bytes, (uint64_t)c.N, (uint32_t)chunk_bytes(c.fmt), 32, 2)) {
-            report(c.fn, MMQ_ERR_CUDA, "the weights' tensor map was refused");
-            return MMQ_ERR_CUDA;
-        }
+    if (a.aligned && !weight_maps(c, a.map, a.row_bytes, 32)) return MMQ_ERR_CUDA;
     const long long term = (long long)pieces * a.groups * 1024;
     const long long counters = up_to(4ll * a.rest, 256), ups = up_to(4 * c.M, 256);
     const long long parts = a.rest ? 2ll * ctas * 2 * a.nt * 128 * 4 : 0;
@@ -100,19 +183,7 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     int st = scratch_alloc((size_t)(counters + ups + term * terms + parts), s, &scratch, c.fn);
     if (st != MMQ_OK) return st;
     uint8_t* at = static_cast<uint8_t*>(scratch);
-    Rows r{};
-    r.x = c.x;
-    r.stride = c.x_stride;
-    r.dtype = c.dtype;
-    r.act = c.act;
-    r.mats = c.mats;
-    r.rows = a.M;
-    r.width = c.backward ? a.N : a.K;
-    r.groups = a.groups;
-    for (int g = 0; g < 2; ++g) {
-        r.pre[g] = c.backward ? c.pre[g] : nullptr;
-        r.dz[g] = c.dz[g];
-    }
+    Rows r = rows_of(c, a.groups);
     r.counters = a.counters = reinterpret_cast<unsigned*>(at);
     r.n_counters = a.rest;
     r.up = reinterpret_cast<float*>(at + counters);

@@ -52,6 +52,21 @@ __device__ __forceinline__ void put(const Rows& r, int m, int step, int chunk, c
     if (r.dtype == MMQ_F32) *reinterpret_cast<uint4*>(p + r.term) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
+// The sum of a block of 32 values, held by four neighbouring threads, in two f16 terms, times 2^-6 so that they fit:
+// in the order in which k_ffn_stream's product takes them, per 256 values and eight rows 256 bytes.
+__device__ __forceinline__ void put_sum(const Rows& r, int m, int run, const float (&v)[8], float down) {
+    float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (run & 3) return;
+    s *= down * 0x1p-6f;
+    const int block = run >> 2, j = block & 7;
+    uint8_t* p = r.sums + (((long long)(block >> 3) * r.groups + (m >> 3)) * 32 + (m & 7) * 4 + (j >> 1)) * 8 + (j & 1) * 2;
+    const __half hi = __float2half_rn(s);
+    *reinterpret_cast<__half*>(p) = hi;
+    *reinterpret_cast<__half*>(p + 4) = __float2half_rn(s - __half2float(hi));
+}
+
 __device__ __forceinline__ void clear_counters(const Rows& r) {
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < r.n_counters; i += blockDim.x) r.counters[i] = 0u;
@@ -120,13 +135,17 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
         const int c = first + i * step;
-        if (c < places) put(r, m, c >> 3, c & 7, held[i], down);
+        if (c < places) {
+            put(r, m, c >> 3, c & 7, held[i], down);
+            if (ROWS == 1 && r.sums) put_sum(r, m, c, held[i], down);  // (whole warps: K is a multiple of 256 then)
+        }
     }
 #pragma unroll 4
     for (int c = first + HELD * step; c < places; c += step) {
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (c < runs) load8(x + 8ll * c, v);
         put(r, m, c >> 3, c & 7, v, down);
+        if (ROWS == 1 && r.sums) put_sum(r, m, c, v, down);
     }
 }
 

@@ -1,0 +1,400 @@
+// The forward products of a few rows (up to 16): k_ffn_stream.
+//
+// Bound: HBM, the weights once.  A warp takes 16 weight rows and a run of 256-value chunks, which it streams
+// through a ring of its own (TMA boxes of 16 rows; rows that do not begin on 16 bytes by asynchronous copies) and
+// multiplies with m16n8k16 products: weights on the M side, rows of x, as k_ffn_rows has laid them out, on the N
+// side.  The codes enter as they are, exact in f16 (Q4_K and Q5_K as subnormals, code x 2^-24, with no instruction beyond
+// the bytes' placing; Q6_K and Q8_0 less their centre), and every block's sum is scaled in f32, so f32 rows take two
+// terms of x but one of the weights.  The order of the values within a block is free as long as both sides
+// share it: a thread's share of a block's codes are the bytes it reads at once.  Q4_K's and Q5_K's minimums multiply
+// the blocks' sums of x (16 values of the reduction: eight sums in two terms): one product a chunk.
+// The products leave the tensor core every 32 values (16 for Q6_K).
+//
+// A CTA is `groups` runs of 16 weight rows (gate and up of the same columns are two) times `splits` shares of the
+// reduction, added up in shared memory in their order.
+#include "ffn_weights.cuh"
+#include "kv.cuh"
+
+namespace mmq {
+namespace {
+
+using namespace ffn;
+
+__device__ unsigned g_ffn_stream_error;
+
+constexpr int WARPS = STREAM_WARPS, SLAB = STREAM_SLAB;
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A word at an even byte offset.
+__device__ __forceinline__ uint32_t word_at(const uint8_t* p, int off) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p + (off & ~3));
+    return __funnelshift_r(w[0], w[1], (off & 2) * 8);
+}
+
+// Two codes of a word as f16: bytes 0, 1 (i = 0) or 2, 3; as subnormals, or less a centre.
+__device__ __forceinline__ uint32_t small(uint32_t codes, int i) { return __byte_perm(codes, 0u, i ? 0x4342 : 0x4140); }
+__device__ __forceinline__ uint32_t centred(uint32_t codes, int i, uint32_t bias) {
+    return h2(__hsub2(umma::bits_h2(__byte_perm(codes, 0x64646464u, i ? 0x4342 : 0x4140)), umma::bits_h2(bias)));
+}
+
+template <int FMT, int NT, int TERMS>
+__global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_constant__ Stream a) {
+    constexpr int CB = chunk_bytes(FMT);
+    constexpr bool MINS = is_kquant(FMT), ROWS = !MINS;  // ROWS: rows may be off 16 bytes
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t s_bar[WARPS * R_MOST];
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int g = lane >> 2, t = lane & 3;
+    const int group = wid / a.splits, split = wid - group * a.splits;
+    const bool works = group < a.groups;
+    const uint32_t bars = ptx::smem_u32(s_bar) + 8 * wid * R_MOST;
+    if (lane < a.rs) ptx::mbar_init(bars + 8 * lane, a.aligned ? 1 : 32);
+    if (tid == 0) s_abort = 0;
+    ptx::fence_barrier_init();
+    __syncthreads();
+    ptx::grid_dep_launch_dependents();
+    volatile int* abort = &s_abort;
+    unsigned* err = &g_ffn_stream_error;
+
+    // this warp's rows and chunks
+    const int per = a.mats == 2 ? a.groups / 2 : a.groups;       // column runs of a CTA
+    const int mat = a.mats == 2 && group >= per ? 1 : 0;
+    const int n0 = (blockIdx.x * per + group - mat * per) * SLAB;
+    const int c0 = works && n0 < a.N ? (int)((long long)a.chunks * split / a.splits) : 0;
+    const int c1 = works && n0 < a.N ? (int)((long long)a.chunks * (split + 1) / a.splits) : 0;
+    const int stage = SLAB * a.slot;
+    uint8_t* ring = smem + wid * a.rs * stage;
+    int asked = c0, put = 0;
+    auto fetch = [&]() {
+        if (asked >= c1) return;
+        const uint32_t bar = bars + 8 * put, dst = ptx::smem_u32(ring) + put * stage;
+        if (!ROWS || a.aligned) {
+            if (ptx::elect_one()) {
+                ptx::mbar_arrive_expect_tx(bar, SLAB * CB);
+                ptx::tma_load_2d(dst, &a.map[mat], bar, asked * (CB / 2), n0);
+            }
+            __syncwarp();
+        } else {
+            const int sub = 16 * (lane & 7), r0 = lane >> 3;
+            const long long in_row = (long long)asked * CB;
+            const int len = (int)min((long long)CB, a.row_bytes - in_row);
+            long long o = (n0 + r0) * a.row_bytes + in_row;
+#pragma unroll
+            for (int r = 0; r < SLAB; r += 4, o += 4 * a.row_bytes) {
+                const int mis = (int)(o & 15), need = n0 + r0 + r < a.N ? mis + len : 0;
+                const uint8_t* src = a.w[mat] + (o - mis) + sub;
+                const long long end = a.w_bytes - (o - mis) - sub;  // bytes of the matrix from here
+#pragma unroll
+                for (int k = 0; k < slot_bytes(FMT, false); k += 128)
+                    if (sub + k < need) cp_async16(dst + (r0 + r) * a.slot + sub + k, src + k, end - k < 16 ? (int)(end - k) : 16);
+            }
+            cp_async_arrive(bar);
+        }
+        ++asked;
+        if (++put == a.rs) put = 0;
+    };
+    for (int i = 0; i < a.rs; ++i) fetch();
+
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    ptx::grid_dep_wait();  // the rows are laid out
+    const uint8_t* xt = a.x + (FMT == FMT_Q6_K ? (t >> 1) * 128 + g * 16 + (t & 1) * 8 : t * 128 + g * 16);
+    const long long xstep = (long long)a.xgroups * 1024;
+    // one block of 32 values of x for this lane: [term], 16 bytes (Q6_K: two of 8, of its two halves)
+    auto load_x = [&](int block, uint4 (&v)[NT][TERMS]) {
+        const uint8_t* p = xt + (block >> 1) * xstep + (block & 1) * 512;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) {
+                const uint8_t* q = p + n * 1024 + e * a.x_term;
+                if (FMT == FMT_Q6_K) {
+                    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(q)), hi = __ldg(reinterpret_cast<const uint2*>(q + 256));
+                    v[n][e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                } else {
+                    v[n][e] = __ldg(reinterpret_cast<const uint4*>(q));
+                }
+            }
+    };
+    // D of a block from its two products (Q6_K: of one 16-value half)
+    auto block_sum = [&](const uint32_t (&a0)[4], const uint32_t (&a1)[4], const uint4 (&v)[TERMS], float (&d)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = 0.f;
+#pragma unroll
+        for (int e = TERMS - 1; e >= 0; --e) {  // the small terms first
+            mma(d, a0, v[e].x, v[e].y);
+            mma(d, a1, v[e].z, v[e].w);
+        }
+    };
+
+    int st = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    uint4 xv[2][NT][TERMS];
+    const int nblocks = a.K / QK;
+    if (c0 < c1) load_x(8 * c0, xv[0]);
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+        if (!umma::warp_wait(bars + 8 * st, par, abort, err)) {
+            ok = false;
+            break;
+        }
+        const uint8_t* rows[2] = {ring + st * stage + g * a.slot, ring + st * stage + (g + 8) * a.slot};
+        int mis[2] = {0, 0};
+        if (ROWS && !a.aligned)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) mis[r] = (int)(((n0 + g + 8 * r) * a.row_bytes + (long long)c * CB) & 15);
+        const int last = min(8 * c + 8, nblocks);  // Q8_0: the last chunk may be short
+        if (MINS) {
+            uint4 head[2];
+            uint32_t sc[2][2], mn[2][2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                head[r] = *reinterpret_cast<const uint4*>(rows[r]);
+                sc[r][0] = head[r].y & 0x3f3f3f3fu;
+                mn[r][0] = head[r].z & 0x3f3f3f3fu;
+                sc[r][1] = (head[r].w & 0x0f0f0f0fu) | ((head[r].y >> 2) & 0x30303030u);
+                mn[r][1] = ((head[r].w >> 4) & 0x0f0f0f0fu) | ((head[r].z >> 2) & 0x30303030u);
+            }
+            float part[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
+            uint2 qh[2];
+            if (FMT == FMT_Q5_K)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) qh[r] = *reinterpret_cast<const uint2*>(rows[r] + 16 + 8 * t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint2 q[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) q[r] = *reinterpret_cast<const uint2*>(rows[r] + kq_qs_off(FMT) + 32 * j + 8 * t);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int block = 2 * j + b;
+                    if (8 * c + block + 1 < 8 * c1) load_x(8 * c + block + 1, xv[(block + 1) & 1]);
+                    uint32_t a0[4], a1[4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t lo = (b ? q[r].x >> 4 : q[r].x) & 0x0f0f0f0fu, hi = (b ? q[r].y >> 4 : q[r].y) & 0x0f0f0f0fu;
+                        if (FMT == FMT_Q5_K) {
+                            lo |= (block >= 4 ? qh[r].x >> (block - 4) : qh[r].x << (4 - block)) & 0x10101010u;
+                            hi |= (block >= 4 ? qh[r].y >> (block - 4) : qh[r].y << (4 - block)) & 0x10101010u;
+                        }
+                        a0[r] = small(lo, 0), a0[2 + r] = small(lo, 1);
+                        a1[r] = small(hi, 0), a1[2 + r] = small(hi, 1);
+                    }
+                    const float s0 = (float)((sc[0][block >> 2] >> (8 * (block & 3))) & 63u);
+                    const float s1 = (float)((sc[1][block >> 2] >> (8 * (block & 3))) & 63u);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float d[4];
+                        block_sum(a0, a1, xv[block & 1][n], d);
+                        part[n][0] = fmaf(s0, d[0], part[n][0]);
+                        part[n][1] = fmaf(s0, d[1], part[n][1]);
+                        part[n][2] = fmaf(s1, d[2], part[n][2]);
+                        part[n][3] = fmaf(s1, d[3], part[n][3]);
+                    }
+                }
+            }
+            // minimums times the blocks' sums of x (which are stored times 2^-6)
+            uint32_t m[4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) m[r] = m[2 + r] = __byte_perm(mn[r][t >> 1], 0u, t & 1 ? 0x4342 : 0x4140);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint2 x = __ldg(reinterpret_cast<const uint2*>(a.sums + (((long long)c * a.xgroups + n) * 32 + lane) * 8));
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma(d, m, x.x, x.y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t dd = head[i >> 1].x;
+                    acc[n][i] = fmaf(f16_bits_to_f32(dd) * 0x1p24f, part[n][i],
+                                     fmaf(f16_bits_to_f32(dd >> 16) * -0x1p30f, d[i], acc[n][i]));
+                }
+            }
+        } else if (FMT == FMT_Q8_0) {
+#pragma unroll
+            for (int block = 0; block < 8; ++block) {
+                if (8 * c + block >= last) break;
+                if (8 * c + block + 1 < min(8 * c1, nblocks)) load_x(8 * c + block + 1, xv[(block + 1) & 1]);
+                uint32_t a0[4], a1[4];
+                float s[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int at = 34 * block + mis[r];
+                    const uint32_t* w = reinterpret_cast<const uint32_t*>(rows[r] + ((at + 2 + 8 * t) & ~3));
+                    const int sh = (at + 2) & 2 ? 16 : 0;
+                    const uint32_t w0 = w[0], w1 = w[1], w2 = sh ? w[2] : 0u;
+                    const uint32_t lo = __funnelshift_r(w0, w1, sh) ^ 0x80808080u, hi = __funnelshift_r(w1, w2, sh) ^ 0x80808080u;
+                    a0[r] = centred(lo, 0, 0x64806480u), a0[2 + r] = centred(lo, 1, 0x64806480u);
+                    a1[r] = centred(hi, 0, 0x64806480u), a1[2 + r] = centred(hi, 1, 0x64806480u);
+                    s[r] = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(rows[r] + at));
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float d[4];
+                    block_sum(a0, a1, xv[block & 1][n], d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s[i >> 1], d[i], acc[n][i]);
+                }
+            }
+        } else {
+            float part[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
+            float d[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) d[r] = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(rows[r] + 208 + mis[r]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t ql[2][4], qh[2][2], sc[2][2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ql[r][i] = word_at(rows[r], 64 * h + 16 * i + 4 * t + mis[r]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        qh[r][i] = word_at(rows[r], 128 + 32 * h + 16 * i + 4 * t + mis[r]);
+                        sc[r][i] = word_at(rows[r], 192 + 8 * h + 4 * i + mis[r]);
+                    }
+                }
+#pragma unroll
+                for (int T = 0; T < 4; ++T) {
+                    const int block = 4 * h + T;
+                    if (8 * c + block + 1 < 8 * c1) load_x(8 * c + block + 1, xv[(block + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // a 16-value half of the block
+                        uint32_t w[4];
+                        float s[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t low = (ql[r][2 * (T & 1) + i] >> (4 * (T >> 1))) & 0x0f0f0f0fu;
+                            const uint32_t top = (T >= 2 ? qh[r][i] >> (2 * T - 4) : qh[r][i] << (4 - 2 * T)) & 0x30303030u;
+                            w[r] = centred(low | top, 0, 0x64206420u), w[2 + r] = centred(low | top, 1, 0x64206420u);
+                            s[r] = (float)(int8_t)(sc[r][T >> 1] >> (16 * (T & 1) + 8 * i));
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float e4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int e = TERMS - 1; e >= 0; --e) {
+                                const uint4 v = xv[block & 1][n][e];
+                                mma(e4, w, i ? v.z : v.x, i ? v.w : v.y);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) part[n][k] = fmaf(s[k >> 1], e4[k], part[n][k]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(d[i >> 1], part[n][i], acc[n][i]);
+        }
+        __syncwarp();  // the chunk has been read
+        fetch();
+        if (++st == a.rs) {
+            st = 0;
+            par ^= 1;
+        }
+    }
+    if (ROWS) cp_async_wait_all();
+    if (!ok && (!ROWS || a.aligned))  // let the boxes in flight land before the shared memory goes
+        for (int i = 0; i < a.rs; ++i) {
+            const int n = asked - c0;
+            if (n > i) umma::drain_bar(bars + 8 * i, ((n - i + a.rs - 1) / a.rs - 1) & 1, err);
+        }
+    // ---- the shares of the reduction in their order, then the outputs: 16 columns side by side
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);  // [warp][8 NT rows of x][16 columns]
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[(wid * 8 * NT + 8 * n + 2 * t + (i & 1)) * SLAB + g + 8 * (i >> 1)] = acc[n][i];
+    __syncthreads();
+    if (*abort) return;
+    auto output = [&](auto type) {
+        using T = decltype(type);
+        for (int i = tid; i < per * a.M * SLAB; i += 32 * WARPS) {
+            const int k = i % SLAB, m = i / SLAB % a.M, run = i / SLAB / a.M;
+            const int n = (blockIdx.x * per + run) * SLAB + k;
+            if (n >= a.N) continue;
+            const long long at = (long long)m * a.N + n;
+            const float up = __ldg(a.up + m) * 256.f;  // (times the weights' 2^8, which these weights have not)
+            float z[2] = {0.f, 0.f};
+            for (int w = 0; w < a.mats; ++w) {
+                for (int s = 0; s < a.splits; ++s) z[w] += sums[(((w * per + run) * a.splits + s) * 8 * NT + m) * SLAB + k];
+                z[w] = fmaf(z[w], up, a.bias[w] ? __ldg(a.bias[w] + n) : 0.f);
+                if (a.pre[w]) put_one(static_cast<T*>(a.pre[w]) + at, z[w]);
+            }
+            float y = 0.f;
+            with_act(a.act, [&](auto A) {
+                float d;
+                activate<decltype(A)::value, sizeof(T) == 2>(z[0], y, d);
+            });
+            if (a.mats == 2) y *= z[1];
+            if (a.residual) y += get_one(static_cast<const T*>(a.residual) + m * a.residual_stride + n);
+            put_one(static_cast<T*>(a.out) + at, y);
+        }
+    };
+    if (TERMS == 2)
+        output(float{});
+    else if (a.dtype == MMQ_BF16)
+        output(__nv_bfloat16{});
+    else
+        output(__half{});
+}
+
+template <int FMT, int NT, int TERMS>
+int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+    static SmemAttr attr;
+    auto k = &k_ffn_stream<FMT, NT, TERMS>;
+    const int st = ensure_smem(reinterpret_cast<const void*>(k), SMEM_MOST, attr);
+    if (st != MMQ_OK) {
+        report(fn, st, "the stream's shared memory was refused");
+        return st;
+    }
+    ProfScope ps("k_ffn_stream", s);
+    return pdl_status(launch_pdl(k, dim3((unsigned)ctas), dim3(32 * WARPS), smem, s, a), fn);
+}
+
+template <int FMT>
+int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+    if (a.dtype == MMQ_F32) return a.xgroups == 1 ? launch<FMT, 1, 2>(a, smem, ctas, fn, s) : launch<FMT, 2, 2>(a, smem, ctas, fn, s);
+    return a.xgroups == 1 ? launch<FMT, 1, 1>(a, smem, ctas, fn, s) : launch<FMT, 2, 1>(a, smem, ctas, fn, s);
+}
+
+}  // namespace
+
+int ffn_stream_launch(int fmt, const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, fn, s);
+    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, fn, s);
+    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, fn, s);
+    return launch<FMT_Q6_K>(a, smem, ctas, fn, s);
+}
+
+unsigned ffn_stream_take_error() {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_ffn_stream_error, sizeof(v)) != cudaSuccess) return 0;
+    if (v) {
+        const unsigned zero = 0;
+        cudaMemcpyToSymbol(g_ffn_stream_error, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace mmq

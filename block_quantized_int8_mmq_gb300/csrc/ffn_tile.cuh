@@ -61,17 +61,6 @@ __device__ __forceinline__ int run_owner(const Tile& a, long long x) {
     return (int)(((x + 1) * gridDim.x - 1) / ((long long)a.rest * a.chunks));
 }
 
-// 16 bytes to shared memory, the first `bytes` of them from src, the others zero; an arrival at a barrier once this
-// thread's copies so far have landed.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 __device__ __forceinline__ void sync_weight_warps() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 template <bool FAST>

@@ -22,6 +22,17 @@ __host__ __device__ constexpr int chunk_bytes(int fmt) { return fmt == FMT_Q8_0 
 __host__ __device__ constexpr int slot_bytes(int fmt, bool aligned) {
     return fmt == FMT_Q8_0 ? (aligned ? 272 : 304) : fmt == FMT_Q6_K ? 240 : kq_bytes(fmt);
 }
+// 16 bytes to shared memory, the first `bytes` of them from src, the others zero; an arrival at a barrier once this
+// thread's copies so far have landed.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 constexpr float W_UP = 256.f, W_MOST = 65504.f;
 
 __device__ __forceinline__ uint32_t h2(__half2 h) { return umma::h2_bits(h); }
