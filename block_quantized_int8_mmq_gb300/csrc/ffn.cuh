@@ -79,7 +79,7 @@ struct Stream {
     const float* up;
     int mats, M, N, K, chunks, xgroups;  // xgroups: of 8 rows
     int groups, splits;            // of a CTA: runs of 16 weight rows, shares of the reduction
-    int aligned, slot, rs;         // bytes of a chunk's row in shared memory, places of a warp's ring
+    int aligned, slot, rs, held;   // bytes of a chunk's row in shared memory, places of a warp's ring, whether x is held there too
     int dtype, act;
     const float* bias[2];
     const void* residual;

@@ -103,9 +103,13 @@ int stream(const Call& c, cudaStream_t s) {
         a.groups = per * c.mats;
         a.splits = splits;
     }
-    a.rs = 200 * 1024 / (STREAM_WARPS * STREAM_SLAB * a.slot);  // (what is left of the SM's memory caches rows of x)
+    // shared memory: all of x where two places of every ring are left beside it (else the SM's cache has the rest)
+    const int place = STREAM_WARPS * STREAM_SLAB * a.slot;
+    const long long x_bytes = ceil_div(c.K, STEP) * a.xgroups * 1024 * terms;
+    a.held = x_bytes <= SMEM_MOST - 2 * place;
+    a.rs = (int)((a.held ? SMEM_MOST - x_bytes : 200 * 1024) / place);
     a.rs = a.rs > R_MOST ? R_MOST : a.rs;
-    const int smem = STREAM_WARPS * STREAM_SLAB * a.slot * a.rs;
+    const int smem = place * a.rs + (a.held ? (int)x_bytes : 0);
     if (a.aligned && !weight_maps(c, a.map, a.row_bytes, STREAM_SLAB)) return MMQ_ERR_CUDA;
 
     const long long term = ceil_div(c.K, STEP) * a.xgroups * 1024, sums = is_kquant(c.fmt) ? (long long)a.chunks * a.xgroups * 256 : 0;

@@ -30,6 +30,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_fresh(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // A word at an even byte offset.
 __device__ __forceinline__ uint32_t word_at(const uint8_t* p, int off) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(p + (off & ~3));
@@ -42,12 +48,12 @@ __device__ __forceinline__ uint32_t centred(uint32_t codes, int i, uint32_t bias
     return h2(__hsub2(umma::bits_h2(__byte_perm(codes, 0x64646464u, i ? 0x4342 : 0x4140)), umma::bits_h2(bias)));
 }
 
-template <int FMT, int NT, int TERMS>
+template <int FMT, int NT, int TERMS, bool HELD>
 __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_constant__ Stream a) {
     constexpr int CB = chunk_bytes(FMT);
     constexpr bool MINS = is_kquant(FMT), ROWS = !MINS;  // ROWS: rows may be off 16 bytes
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[WARPS * R_MOST];
+    __shared__ __align__(8) uint64_t s_bar[WARPS * R_MOST + 1];
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int g = lane >> 2, t = lane & 3;
@@ -55,7 +61,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     const bool works = group < a.groups;
     const uint32_t bars = ptx::smem_u32(s_bar) + 8 * wid * R_MOST;
     if (lane < a.rs) ptx::mbar_init(bars + 8 * lane, a.aligned ? 1 : 32);
-    if (tid == 0) s_abort = 0;
+    const uint32_t x_bar = ptx::smem_u32(s_bar) + 8 * WARPS * R_MOST;
+    if (tid == 0) {
+        s_abort = 0;
+        ptx::mbar_init(x_bar, 1);
+    }
     ptx::fence_barrier_init();
     __syncthreads();
     ptx::grid_dep_launch_dependents();
@@ -107,31 +117,65 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     ptx::grid_dep_wait();  // the rows are laid out
-    const uint8_t* xt = a.x + (FMT == FMT_Q6_K ? (t >> 1) * 128 + g * 16 + (t & 1) * 8 : t * 128 + g * 16);
-    const long long xstep = (long long)a.xgroups * 1024;
-    // one block of 32 values of x for this lane: [term], 16 bytes (Q6_K: two of 8, of its two halves)
-    auto load_x = [&](int block, uint4 (&v)[NT][TERMS]) {
-        const uint8_t* p = xt + (block >> 1) * xstep + (block & 1) * 512;
+    // HELD: all of the rows' tiles in shared memory, after the rings, by one warp's bulk copies (a step of 64 values each)
+    const int x_steps = (a.K + STEP - 1) / STEP;
+    uint8_t* x_held = smem + WARPS * a.rs * stage;
+    if (HELD) {
+        const int bytes = NT * 1024;
+        if (wid == 0) {
+            if (lane == 0) ptx::mbar_arrive_expect_tx(x_bar, x_steps * bytes * TERMS);
+            __syncwarp();
+            const int run = (x_steps + 31) / 32, i0 = min(x_steps, lane * run), i1 = min(x_steps, i0 + run);
+            if (i1 > i0)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                for (int e = 0; e < TERMS; ++e)
+                    ptx::bulk_load(ptx::smem_u32(x_held) + (e * x_steps + i0) * bytes, a.x + e * a.x_term + (long long)i0 * bytes,
+                                   (i1 - i0) * bytes, x_bar);
+        }
+    }
+    // x for this lane, AHEAD blocks of 32 values at a time and as many ahead of their use: 16 bytes a block and term (Q6_K:
+    // two of 8, of its two halves).  Measured one block ahead, from L2: most of a decode's cycles waited for it.
+    constexpr int AHEAD = HELD ? 1 : 4 / (NT * TERMS);
+    const int x_lane = FMT == FMT_Q6_K ? (t >> 1) * 128 + g * 16 + (t & 1) * 8 : t * 128 + g * 16;
+    const uint8_t* xt = HELD ? x_held + x_lane : a.x + x_lane;
+    const long long x_term = HELD ? (long long)x_steps * NT * 1024 : a.x_term;
+    const int b_end = min(8 * c1, a.K / QK);
+    const int lane_rows = g < a.M ? g + 8 < a.M ? 2 : 1 : 0;  // rows of x that this lane reads: g, g + 8
+    uint4 xv[2][AHEAD][NT][TERMS];
 #pragma unroll
-            for (int e = 0; e < TERMS; ++e) {
-                const uint8_t* q = p + n * 1024 + e * a.x_term;
-                if (FMT == FMT_Q6_K) {
-                    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(q)), hi = __ldg(reinterpret_cast<const uint2*>(q + 256));
-                    v[n][e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                } else {
-                    v[n][e] = __ldg(reinterpret_cast<const uint4*>(q));
+    for (int i = 0; i < 2 * AHEAD * NT * TERMS; ++i) (&xv[0][0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    auto load_x = [&](int block, uint4 (&v)[AHEAD][NT][TERMS]) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (block + i >= b_end || lane_rows == 0) break;
+            const uint8_t* p = xt + (long long)((block + i) >> 1) * (NT * 1024) + ((block + i) & 1) * 512;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n >= lane_rows) break;
+#pragma unroll
+                for (int e = 0; e < TERMS; ++e) {
+                    const uint8_t* q = p + n * 1024 + e * x_term;
+                    if (FMT == FMT_Q6_K) {
+                        const uint2* w = reinterpret_cast<const uint2*>(q);
+                        const uint2 lo = HELD ? w[0] : __ldg(w), hi = HELD ? w[32] : __ldg(w + 32);
+                        v[i][n][e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    } else {
+                        const uint4* w = reinterpret_cast<const uint4*>(q);
+                        v[i][n][e] = HELD ? *w : __ldg(w);
+                    }
                 }
             }
+        }
+    };
+    // before block `block` (0 .. 7) of chunk c: the next batch is asked for where one begins
+    auto next_x = [&](int c, int block) {
+        if (block % AHEAD == 0) load_x(8 * c + block + AHEAD, xv[(block / AHEAD + 1) & 1]);
     };
     // D of a block from its two products (Q6_K: of one 16-value half)
     auto block_sum = [&](const uint32_t (&a0)[4], const uint32_t (&a1)[4], const uint4 (&v)[TERMS], float (&d)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = 0.f;
-#pragma unroll
         for (int e = TERMS - 1; e >= 0; --e) {  // the small terms first
-            mma(d, a0, v[e].x, v[e].y);
+            e == TERMS - 1 ? mma_fresh(d, a0, v[e].x, v[e].y) : mma(d, a0, v[e].x, v[e].y);
             mma(d, a1, v[e].z, v[e].w);
         }
     };
@@ -139,11 +183,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     int st = 0;
     uint32_t par = 0;
     bool ok = true;
-    uint4 xv[2][NT][TERMS];
-    const int nblocks = a.K / QK;
-    if (c0 < c1) load_x(8 * c0, xv[0]);
+    if (HELD) ok = umma::warp_wait(x_bar, 0, abort, err);
+    if (ok) load_x(8 * c0, xv[0]);
 #pragma unroll 1
-    for (int c = c0; c < c1; ++c) {
+    for (int c = c0; c < c1 && ok; ++c) {
         if (!umma::warp_wait(bars + 8 * st, par, abort, err)) {
             ok = false;
             break;
@@ -153,8 +196,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
         if (ROWS && !a.aligned)
 #pragma unroll
             for (int r = 0; r < 2; ++r) mis[r] = (int)(((n0 + g + 8 * r) * a.row_bytes + (long long)c * CB) & 15);
-        const int last = min(8 * c + 8, nblocks);  // Q8_0: the last chunk may be short
+        const int last = min(8 * c + 8, b_end);  // Q8_0: the last chunk may be short
         if (MINS) {
+            uint2 xs[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                xs[n] = __ldg(reinterpret_cast<const uint2*>(a.sums + (((long long)c * a.xgroups + n) * 32 + lane) * 8));
             uint4 head[2];
             uint32_t sc[2][2], mn[2][2];
 #pragma unroll
@@ -182,7 +229,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const int block = 2 * j + b;
-                    if (8 * c + block + 1 < 8 * c1) load_x(8 * c + block + 1, xv[(block + 1) & 1]);
+                    next_x(c, block);
                     uint32_t a0[4], a1[4];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
@@ -199,7 +246,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float d[4];
-                        block_sum(a0, a1, xv[block & 1][n], d);
+                        block_sum(a0, a1, xv[(block / AHEAD) & 1][block % AHEAD][n], d);
                         part[n][0] = fmaf(s0, d[0], part[n][0]);
                         part[n][1] = fmaf(s0, d[1], part[n][1]);
                         part[n][2] = fmaf(s1, d[2], part[n][2]);
@@ -213,9 +260,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             for (int r = 0; r < 2; ++r) m[r] = m[2 + r] = __byte_perm(mn[r][t >> 1], 0u, t & 1 ? 0x4342 : 0x4140);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const uint2 x = __ldg(reinterpret_cast<const uint2*>(a.sums + (((long long)c * a.xgroups + n) * 32 + lane) * 8));
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma(d, m, x.x, x.y);
+                float d[4];
+                mma_fresh(d, m, xs[n].x, xs[n].y);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t dd = head[i >> 1].x;
@@ -227,7 +273,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
             for (int block = 0; block < 8; ++block) {
                 if (8 * c + block >= last) break;
-                if (8 * c + block + 1 < min(8 * c1, nblocks)) load_x(8 * c + block + 1, xv[(block + 1) & 1]);
+                next_x(c, block);
                 uint32_t a0[4], a1[4];
                 float s[2];
 #pragma unroll
@@ -244,7 +290,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float d[4];
-                    block_sum(a0, a1, xv[block & 1][n], d);
+                    block_sum(a0, a1, xv[(block / AHEAD) & 1][block % AHEAD][n], d);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s[i >> 1], d[i], acc[n][i]);
                 }
@@ -274,7 +320,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
                 for (int T = 0; T < 4; ++T) {
                     const int block = 4 * h + T;
-                    if (8 * c + block + 1 < 8 * c1) load_x(8 * c + block + 1, xv[(block + 1) & 1]);
+                    next_x(c, block);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {  // a 16-value half of the block
                         uint32_t w[4];
@@ -288,11 +334,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            float e4[4] = {0.f, 0.f, 0.f, 0.f};
+                            float e4[4];
 #pragma unroll
                             for (int e = TERMS - 1; e >= 0; --e) {
-                                const uint4 v = xv[block & 1][n][e];
-                                mma(e4, w, i ? v.z : v.x, i ? v.w : v.y);
+                                const uint4 v = xv[(block / AHEAD) & 1][block % AHEAD][n][e];
+                                const uint32_t b0 = i ? v.z : v.x, b1 = i ? v.w : v.y;
+                                e == TERMS - 1 ? mma_fresh(e4, w, b0, b1) : mma(e4, w, b0, b1);
                             }
 #pragma unroll
                             for (int k = 0; k < 4; ++k) part[n][k] = fmaf(s[k >> 1], e4[k], part[n][k]);
@@ -313,6 +360,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
         }
     }
     if (ROWS) cp_async_wait_all();
+    if (HELD && !ok && wid == 0) umma::drain_bar(x_bar, 0, err);
     if (!ok && (!ROWS || a.aligned))  // let the boxes in flight land before the shared memory goes
         for (int i = 0; i < a.rs; ++i) {
             const int n = asked - c0;
@@ -359,10 +407,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
         output(__half{});
 }
 
-template <int FMT, int NT, int TERMS>
+template <int FMT, int NT, int TERMS, bool HELD>
 int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
     static SmemAttr attr;
-    auto k = &k_ffn_stream<FMT, NT, TERMS>;
+    auto k = &k_ffn_stream<FMT, NT, TERMS, HELD>;
     const int st = ensure_smem(reinterpret_cast<const void*>(k), SMEM_MOST, attr);
     if (st != MMQ_OK) {
         report(fn, st, "the stream's shared memory was refused");
@@ -370,6 +418,11 @@ int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) 
     }
     ProfScope ps("k_ffn_stream", s);
     return pdl_status(launch_pdl(k, dim3((unsigned)ctas), dim3(32 * WARPS), smem, s, a), fn);
+}
+
+template <int FMT, int NT, int TERMS>
+int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+    return a.held ? launch<FMT, NT, TERMS, true>(a, smem, ctas, fn, s) : launch<FMT, NT, TERMS, false>(a, smem, ctas, fn, s);
 }
 
 template <int FMT>
