@@ -48,7 +48,7 @@ struct Rows {
 struct Tile {
     CUtensorMap map[2];            // of the weight matrices, where rows begin on 16 bytes
     const uint8_t* w[2];
-    long long w_bytes, row_bytes;  // of a weight matrix, of a row
+    long long row_bytes;           // of a weight row
     const uint8_t* x;              // the rows' tiles
     long long x_term;
     const float* up;
@@ -72,7 +72,7 @@ struct Tile {
 struct Stream {
     CUtensorMap map[2];            // of the weight matrices, where rows begin on 16 bytes
     const uint8_t* w[2];
-    long long w_bytes, row_bytes;  // of a weight matrix, of a row
+    long long row_bytes;           // of a weight row
     const uint8_t* x;              // the rows' tiles
     long long x_term;
     const uint8_t* sums;           // Q4_K, Q5_K: the blocks' sums

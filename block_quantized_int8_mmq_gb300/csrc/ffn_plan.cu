@@ -72,7 +72,6 @@ int stream(const Call& c, cudaStream_t s) {
     const int terms = c.dtype == MMQ_F32 ? 2 : 1;
     Stream a{};
     a.row_bytes = c.fmt == FMT_Q8_0 ? c.K / QK * Q8_0_BYTES : c.K / QK_K * kq_bytes(c.fmt);
-    a.w_bytes = a.row_bytes * c.N;
     a.mats = c.mats;
     a.M = (int)c.M;
     a.N = (int)c.N;
@@ -140,7 +139,6 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.w[0] = static_cast<const uint8_t*>(c.w[0]);
     a.w[1] = static_cast<const uint8_t*>(c.w[1]);
     a.row_bytes = c.fmt == FMT_Q8_0 ? c.K / QK * Q8_0_BYTES : c.K / QK_K * kq_bytes(c.fmt);
-    a.w_bytes = a.row_bytes * c.N;
     a.mats = c.mats;
     a.M = (int)c.M;
     a.N = (int)c.N;

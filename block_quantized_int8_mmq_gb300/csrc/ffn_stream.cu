@@ -39,7 +39,7 @@ __device__ __forceinline__ void mma_fresh(float (&d)[4], const uint32_t (&a)[4],
 // A word at an even byte offset.
 __device__ __forceinline__ uint32_t word_at(const uint8_t* p, int off) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(p + (off & ~3));
-    return __funnelshift_r(w[0], w[1], (off & 2) * 8);
+    return off & 2 ? __funnelshift_r(w[0], w[1], 16) : w[0];
 }
 
 // Two codes of a word as f16: bytes 0, 1 (i = 0) or 2, 3; as subnormals, or less a centre.
@@ -91,18 +91,17 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             }
             __syncwarp();
         } else {
-            const int sub = 16 * (lane & 7), r0 = lane >> 3;
-            const long long in_row = (long long)asked * CB;
-            const int len = (int)min((long long)CB, a.row_bytes - in_row);
-            long long o = (n0 + r0) * a.row_bytes + in_row;
+            const int sub = 16 * (lane & 7), r0 = lane >> 3, in_row = asked * CB, len = min(CB, (int)a.row_bytes - in_row);
+            const uint8_t* p = a.w[mat] + (n0 + r0) * a.row_bytes + in_row;
+            // the matrix's last bytes do not fill 16: a copy there takes what there is
+            const bool tail = in_row + len == (int)a.row_bytes;
 #pragma unroll
-            for (int r = 0; r < SLAB; r += 4, o += 4 * a.row_bytes) {
-                const int mis = (int)(o & 15), need = n0 + r0 + r < a.N ? mis + len : 0;
-                const uint8_t* src = a.w[mat] + (o - mis) + sub;
-                const long long end = a.w_bytes - (o - mis) - sub;  // bytes of the matrix from here
+            for (int r = 0; r < SLAB; r += 4, p += 4 * a.row_bytes) {
+                const int mis = (int)(reinterpret_cast<uintptr_t>(p) & 15), need = n0 + r0 + r < a.N ? mis + len - sub : 0;
+                const uint8_t* src = p - mis + sub;
 #pragma unroll
                 for (int k = 0; k < slot_bytes(FMT, false); k += 128)
-                    if (sub + k < need) cp_async16(dst + (r0 + r) * a.slot + sub + k, src + k, end - k < 16 ? (int)(end - k) : 16);
+                    if (k < need) cp_async16(dst + (r0 + r) * a.slot + sub + k, src + k, tail ? min(16, need - k) : 16);
             }
             cp_async_arrive(bar);
         }
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
         int mis[2] = {0, 0};
         if (ROWS && !a.aligned)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) mis[r] = (int)(((n0 + g + 8 * r) * a.row_bytes + (long long)c * CB) & 15);
+            for (int r = 0; r < 2; ++r) mis[r] = (int)(((uint32_t)(n0 + g + 8 * r) * (uint32_t)a.row_bytes + (uint32_t)c * CB) & 15u);
         const int last = min(8 * c + 8, b_end);  // Q8_0: the last chunk may be short
         if (MINS) {
             uint2 xs[NT];

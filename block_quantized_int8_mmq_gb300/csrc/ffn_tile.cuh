@@ -155,6 +155,10 @@ __device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, i
     }
 }
 
+// Forward, one piece a step: the steps of a chunk take its quarters in the order 0, 2, 1, 3, so that a set's two are
+// side by side (Q6_K's share their bytes); Q8_0, whose last chunk may be short, as they come.
+__host__ __device__ constexpr int step_of(int fmt, int q) { return fmt == FMT_Q8_0 || q == 0 || q == 3 ? q : 3 - q; }
+
 template <int FMT, bool SPLIT, bool BACK, int SUB>
 __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__ Tile a) {
     using S = Shape<SPLIT, SUB>;
@@ -245,18 +249,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
             const int pair = f_unit / a.mtiles, mat = BACK ? f_c >= nsteps : a.mats == 2 ? g : 0;
             const int n0 = f_row + (BACK ? (f_c - mat * nsteps) * STEP + 32 * (wid & 1)
                                          : (a.mats == 2 ? pair * 128 : pair * 256 + g * 128) + 32 * (wid & 3));
-            const long long in_row = (long long)(BACK ? pair : f_c) * CB;
-            const int len = (int)min((long long)CB, a.row_bytes - in_row), sub = 16 * (lane & 7);
+            const int in_row = (BACK ? pair : f_c) * CB, len = min(CB, (int)a.row_bytes - in_row), sub = 16 * (lane & 7);
             const uint32_t dst = raw_addr + ((grp * a.rs + f_slot) * 32 + f_row) * a.slot + sub;
-            long long o = n0 * a.row_bytes + in_row;
+            const uint8_t* p = a.w[mat] + n0 * a.row_bytes + in_row;
+            // the matrix's last bytes do not fill 16: a copy there takes what there is
+            const bool tail = in_row + len == (int)a.row_bytes;
 #pragma unroll
-            for (int t = 0; t < (BACK ? 2 : 4); ++t, o += 4 * a.row_bytes) {
-                const int mis = (int)(o & 15), need = n0 + 4 * t < a.N ? mis + len : 0;
-                const uint8_t* src = a.w[mat] + (o - mis) + sub;
-                const long long end = a.w_bytes - (o - mis) - sub;  // bytes of the matrix from here
+            for (int t = 0; t < (BACK ? 2 : 4); ++t, p += 4 * a.row_bytes) {
+                const int mis = (int)(reinterpret_cast<uintptr_t>(p) & 15), need = n0 + 4 * t < a.N ? mis + len - sub : 0;
+                const uint8_t* src = p - mis + sub;
 #pragma unroll
                 for (int k = 0; k < slot_bytes(FMT, false); k += 128)
-                    if (sub + k < need) cp_async16(dst + 4 * t * a.slot + k, src + k, end - k < 16 ? (int)(end - k) : 16);
+                    if (k < need) cp_async16(dst + 4 * t * a.slot + k, src + k, tail ? min(16, need - k) : 16);
             }
             cp_async_arrive(raw_full + 8 * (grp * R_MOST + f_slot));
             f_c += NEXT;
@@ -313,11 +317,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 }
                 const uint8_t* src = ring + slot * 32 * a.slot;
                 // the quarter j: piece `sub` of this set's step
+                Q6Half q6;
+                if (FMT == FMT_Q6_K && !BACK) q6.load(src, e, mis, true);
                 auto one = [&](int j, int sub) {
                     const int k0 = (BACK ? pair : c) * CHUNK + j * STEP;
                     const int blocks = min(2, max(0, (a.K - k0) / QK));
-                    quarter<FMT, SPLIT>(src, j, mis, a.aligned, blocks, !BACK || valid, check,
-                                        [&](int half, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+                    auto put = [&](int half, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
                         if (half == 0 && sub == 0 && ok && before >= 0)
                             ok = umma::warp_wait(empty + 8 * (before % RING), (before / RING) & 1, abort, err);
                         if (!BACK) {
@@ -337,7 +342,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                                         make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
                             }
                         }
-                    });
+                    };
+                    if (FMT == FMT_Q6_K && !BACK)
+                        quarter_q6<SPLIT>(q6, j & 1, check, put);
+                    else
+                        quarter<FMT, SPLIT>(src, j, mis, a.aligned, blocks, !BACK || valid, check, put);
                     if (sub + 1 < SUB) return;
                     if (!BACK) {
                         ptx::tmem_st_wait();
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                         ptx::fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    before = base + (BACK ? c - c0 : PER * (c - c0) + (SUB == 2 ? e : j));
+                    before = base + (BACK ? c - c0 : PER * (c - c0) + (SUB == 2 ? e : step_of(FMT, j)));
                     if (lane == 0) ptx::mbar_arrive(full + 8 * (before % RING));
                     ++mine;
                 };
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     }
                 } else {
 #pragma unroll 1
-                    for (int i = 0; i < 2 && ok; ++i) SUB == 2 ? one(2 * e + i, i) : one(e + 2 * i, 0);
+                    for (int i = 0; i < 2 && ok; ++i) one(2 * e + i, SUB == 2 ? i : 0);
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(raw_empty + 8 * (grp * R_MOST + slot));  // the chunk has been read
@@ -595,9 +604,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
             const uint32_t bytes = min(a.nt / 8, a.groups - g0) * 1024;
             int s0, s1;
             step_range(c0, c1, s0, s1);
-            const uint8_t* src = a.x + ((long long)s0 * SUB * a.groups + g0) * 1024;
 #pragma unroll 1
-            for (int s = s0; s < s1; ++s, ++n, src += (long long)SUB * a.groups * 1024) {
+            for (int s = s0; s < s1; ++s, ++n) {
+                const int piece = !BACK && SUB == 1 ? (s & ~3) + step_of(FMT, s & 3) : s * SUB;
+                const uint8_t* src = a.x + ((long long)piece * a.groups + g0) * 1024;
                 const int free = n - a.xs;  // the step whose products have read this place
                 if (free >= 0 && !umma::warp_wait(empty + 8 * (free % RING), (free / RING) & 1, abort, err)) {
                     ok = false;

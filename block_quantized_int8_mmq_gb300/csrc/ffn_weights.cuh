@@ -98,6 +98,53 @@ __device__ __forceinline__ void read_run(const uint8_t* p, int off, uint32_t (&o
     for (int i = 0; i < W; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], sh);
 }
 
+// Half of a Q6_K chunk, 128 values, as it is read: two quarters share its bytes.
+struct Q6Half {
+    uint32_t ql[16], qh[8], sc[2], d;
+    __device__ __forceinline__ void load(const uint8_t* slot, int H, int mis, bool valid) {
+        read_run<16>(slot, 64 * H + mis, ql);
+        read_run<8>(slot, 128 + 32 * H + mis, qh);
+        read_run<2>(slot, 192 + 8 * H + mis, sc);
+        d = valid ? *reinterpret_cast<const uint16_t*>(slot + 208 + mis) * 0x10001u : 0u;
+    }
+};
+// Its first (P = 0) or second quarter: emit(half, hi, lo) as below.
+template <bool SPLIT, class Emit>
+__device__ __forceinline__ void quarter_q6(const Q6Half& w, int P, Check& check, Emit&& emit) {
+    uint32_t hi[16], lo[16];
+    const uint32_t sc = P ? w.sc[1] : w.sc[0];
+    const float d = f16_bits_to_f32(w.d) * W_UP;
+    __half2 sp[2];
+    if (!SPLIT) {
+        const __half2 d2 = __hmul2(umma::bits_h2(w.d), __float2half2_rn(W_UP)), bias = umma::bits_h2(0x64806480u);
+        const uint32_t u = sc ^ 0x80808080u;
+        sp[0] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias), d2);
+        sp[1] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias), d2);
+        check.add(sp[0], __float2half2_rn(0.f), 32.f);
+        check.add(sp[1], __float2half2_rn(0.f), 32.f);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int turn = 4 - 2 * (2 * P + b);  // the two high bits of each byte to bits 4 and 5
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const float s = d * (float)(int8_t)(sc >> (16 * b + 8 * g));
+            const __half2 s2 = g ? high2(sp[b]) : low2(sp[b]);
+            if (SPLIT) check.add(s, 0.f, 32.f);
+#pragma unroll
+            for (int i = 4 * g; i < 4 * g + 4; ++i) {
+                const uint32_t c = ((w.ql[8 * b + i] >> (4 * P)) & 0x0f0f0f0fu) |
+                                   (__funnelshift_l(w.qh[i], w.qh[i], turn) & 0x30303030u);
+                if (SPLIT)
+                    four<false>(c, 0x64206420u, s, 0.f, hi + 2 * i, lo + 2 * i);
+                else
+                    four<false>(c, 0x64206420u, s2, s2, hi + 2 * i);
+            }
+        }
+        emit(b, hi, lo);
+    }
+}
+
 // Values 64 J .. 64 J + 63 of the chunk at `slot` (mis: bytes before its first, 0 .. 14).  emit(half, hi, lo)
 // takes 32 values at a time as 16 pairs.  blocks: Q8_0's 32-value blocks that exist here (0 .. 2), the others are
 // zero.  valid: whether there is such a row; where not, zeros come out of whatever is in its place.  J is a constant
@@ -141,42 +188,9 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
             emit(b, hi, lo);
         }
     } else if (FMT == FMT_Q6_K) {
-        const int H = J >> 1, T = 2 * (J & 1);
-        uint32_t ql[16], qh[8], sc[1];
-        read_run<16>(slot, 64 * H + mis, ql);
-        read_run<8>(slot, 128 + 32 * H + mis, qh);
-        read_run<1>(slot, 192 + 4 * J + mis, sc);
-        const uint32_t dd = valid ? *reinterpret_cast<const uint16_t*>(slot + 208 + mis) * 0x10001u : 0u;
-        const float d = f16_bits_to_f32(dd) * W_UP;
-        __half2 sp[2];
-        if (!SPLIT) {
-            const __half2 d2 = __hmul2(umma::bits_h2(dd), up2), bias = umma::bits_h2(0x64806480u);
-            const uint32_t u = sc[0] ^ 0x80808080u;
-            sp[0] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias), d2);
-            sp[1] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias), d2);
-            check.add(sp[0], __float2half2_rn(0.f), 32.f);
-            check.add(sp[1], __float2half2_rn(0.f), 32.f);
-        }
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int turn = 4 - 2 * (T + b);  // the two high bits of each byte to bits 4 and 5
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float s = d * (float)(int8_t)(sc[0] >> (16 * b + 8 * g));
-                const __half2 s2 = g ? high2(sp[b]) : low2(sp[b]);
-                if (SPLIT) check.add(s, 0.f, 32.f);
-#pragma unroll
-                for (int i = 4 * g; i < 4 * g + 4; ++i) {
-                    const uint32_t c = ((ql[8 * b + i] >> (2 * T)) & 0x0f0f0f0fu) |
-                                       (__funnelshift_l(qh[i], qh[i], turn) & 0x30303030u);
-                    if (SPLIT)
-                        four<false>(c, 0x64206420u, s, 0.f, hi + 2 * i, lo + 2 * i);
-                    else
-                        four<false>(c, 0x64206420u, s2, s2, hi + 2 * i);
-                }
-            }
-            emit(b, hi, lo);
-        }
+        Q6Half w;
+        w.load(slot, J >> 1, mis, valid);
+        quarter_q6<SPLIT>(w, J & 1, check, emit);
     } else {
         const uint4 head = *reinterpret_cast<const uint4*>(slot);
         uint32_t q[8], qh[8];
