@@ -95,16 +95,16 @@ constexpr int CHUNK = 256;   // values of a weight row that are copied together
 constexpr int RING = 8, R_MOST = 8;  // barriers of steps; longest ring of weight chunks
 // SUB: 64-value pieces of the reduction in a step.  Two where TMEM has the room (16-bit rows, forward, up to 128 rows
 // a tile): a step costs its warps some 600 cycles of waits and loops, which few rows' products do not cover.
-template <bool SPLIT, int SUB = 1>
+template <bool SPLIT, bool BACK, int SUB = 1>
 struct Shape {
     static constexpr int TERMS = SPLIT ? 2 : 1;
     static constexpr int NT = SPLIT ? 64 : SUB == 2 ? 128 : 192;  // rows of x in a tile, at most
-    static constexpr int DB = SPLIT ? 2 : 1;        // accumulator buffers
-    static constexpr int D_COLS = 2 * NT;           // of a buffer: two weight tiles
-    static constexpr int COL_A = DB * D_COLS;       // forward: weights, two stages
-    static constexpr int A_COLS = 64 * TERMS * SUB; // of a stage: two tiles, 32 columns a term and piece
+    static constexpr int DB = SPLIT ? 2 : 1;          // accumulator buffers
+    static constexpr int D_COLS = 2 * NT;             // of a buffer: two weight tiles
+    static constexpr int COL_A = DB * D_COLS;         // forward: weights, two stages
+    static constexpr int A_COLS = 64 * TERMS * SUB;   // of a stage: two tiles, 32 columns a term and piece
     static constexpr int A_BYTES = STEP * CHUNK * 2;  // backward: a stage's term in shared memory
-    static_assert(COL_A + 2 * A_COLS <= 512, "TMEM columns");
+    static_assert(COL_A + (BACK ? 0 : 2 * A_COLS) <= 512, "TMEM columns");
 };
 // Rings of weight chunks, 32 rows each: forward, one for each 32 of the 256 weight rows, which two warps share;
 // backward, one for each half of a step's 64 rows and each of the two sets of warps.

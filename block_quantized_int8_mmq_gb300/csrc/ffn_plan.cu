@@ -10,16 +10,17 @@ using namespace ffn;
 constexpr long long up_to(long long n, long long unit) { return (n + unit - 1) / unit * unit; }
 constexpr long long ceil_div(long long n, long long d) { return (n + d - 1) / d; }
 
-// Times in us, for the choice between whole and cut units: a chunk's copies at an SM's share of HBM, its products at
-// the tensor rate; and what cutting costs, parts written and read back (nt x 256 sums each) and a counter's trip.
+// Times in us, for the choice between whole and cut units.  A chunk: its products at the tensor rate, or its weights'
+// way to f16 where that takes longer (measured a 64-value step of 256 weight rows: 16-bit rows 0.55, backward 0.4, of Q6_K 0.9, f32
+// rows 1.1).  What cutting costs: parts of nt x 256 sums written and read back, and a counter's trip (measured at 192 rows 14).
 struct Cost {
     double chunk, join;
 };
 Cost cost(const Tile& a, int fmt, bool split, bool back) {
-    const double steps = back ? 1 : CHUNK / STEP;
-    const double copy = steps * STEP * chunk_bytes(fmt) / 44e3;
-    const double products = steps * 8 * (split ? 3 : 1) * (a.nt < 64 ? 64 : a.nt) / 2 / 1900.0;
-    return {copy > products ? copy : products, 2.5 + a.nt * 2048.0 / 44e3};
+    const double pieces = back ? 1 : CHUNK / STEP;
+    const double weights = split ? 1.1 : fmt == FMT_Q6_K ? 0.9 : back ? 0.4 : 0.55;
+    const double products = 8 * (split ? 3 : 1) * (a.nt < 64 ? 64 : a.nt) / 2 / 1900.0;
+    return {pieces * (weights > products ? weights : products), 3.0 + a.nt * 0.06};
 }
 
 // Rounds of whole units; or, where the last round leaves too much undone, it and the one before it cut evenly.
@@ -29,7 +30,7 @@ int deal(Tile& a, const Cost& t, int sms) {
     const long long rest = a.units - full * sms;
     if (rest > 0) {
         const double cut = full * a.chunks + (double)ceil_div(rest * a.chunks, sms);
-        if (cut * t.chunk + t.join < whole * t.chunk) {
+        if (cut * t.chunk + t.join < 0.93 * whole * t.chunk) {
             a.rounds = (int)full;
             a.rest = (int)rest;
             return (int)(rest * a.chunks < sms ? rest * a.chunks : sms);
@@ -134,7 +135,7 @@ int stream(const Call& c, cudaStream_t s) {
 int ffn_launch(const Call& c, cudaStream_t s) {
     if (!c.backward && c.M <= STREAM_ROWS) return stream(c, s);
     const bool split = c.dtype == MMQ_F32;
-    const int terms = split ? 2 : 1, nt_most = split ? Shape<true>::NT : Shape<false>::NT;
+    const int terms = split ? 2 : 1, nt_most = !split ? Shape<false, false>::NT : c.backward ? Shape<true, true>::NT : Shape<true, false>::NT;
     Tile a{};
     a.w[0] = static_cast<const uint8_t*>(c.w[0]);
     a.w[1] = static_cast<const uint8_t*>(c.w[1]);
@@ -148,7 +149,7 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.nt = (int)up_to(ceil_div(c.M, ceil_div(c.M, nt_most)), 16);
     a.mtiles = (int)ceil_div(c.M, a.nt);
     a.units = (int)(a.mtiles * ceil_div(a.width, !c.backward && c.mats == 2 ? 128 : 256));
-    a.sub = !c.backward && !split && a.nt <= Shape<false, 2>::NT && c.K % (2 * STEP) == 0 ? 2 : 1;
+    a.sub = !c.backward && !split && a.nt <= Shape<false, false, 2>::NT && c.K % (2 * STEP) == 0 ? 2 : 1;
     const int pieces = (int)(c.backward ? c.mats * ceil_div(c.N, STEP) : ceil_div(c.K, STEP));  // of 64 values
     a.steps = pieces / a.sub;
     a.chunks = c.backward ? a.steps : (int)ceil_div(c.K, CHUNK);
@@ -164,11 +165,12 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.residual_stride = c.residual_stride;
     a.out = c.out;
     const int ctas = deal(a, cost(a, c.fmt, split, c.backward), device_shape().sms);
-    // shared memory: two chunks' places at least, then up to four steps of rows, then more chunks
+    // shared memory: two chunks' places and two steps of rows at least where they fit, four places, four steps, more places
     const int x_bytes = a.nt * 128 * terms * a.sub, w_bytes = rings(c.backward) * 32 * a.slot;
-    const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true>::A_BYTES : 0);
-    a.xs = (left - 2 * w_bytes) / x_bytes;
-    a.xs = a.xs > 4 ? 4 : a.xs;
+    const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true, true>::A_BYTES : 0);
+    auto steps_left = [&](int places) { return (left - places * w_bytes) / x_bytes; };
+    a.rs = steps_left(4) >= 2 ? 4 : steps_left(3) >= 2 ? 3 : 2;
+    a.xs = steps_left(a.rs) < 4 ? steps_left(a.rs) : 4;
     a.rs = (left - a.xs * x_bytes) / w_bytes;
     a.rs = a.rs > R_MOST ? R_MOST : a.rs;
     if (a.xs < 1 || a.rs < 2) {

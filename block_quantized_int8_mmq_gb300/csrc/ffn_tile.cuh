@@ -161,7 +161,7 @@ __host__ __device__ constexpr int step_of(int fmt, int q) { return fmt == FMT_Q8
 
 template <int FMT, bool SPLIT, bool BACK, int SUB>
 __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__ Tile a) {
-    using S = Shape<SPLIT, SUB>;
+    using S = Shape<SPLIT, BACK, SUB>;
     constexpr int PER = CHUNK / STEP / SUB;  // forward: steps of a chunk
     constexpr int TERMS = S::TERMS;
     constexpr int NG = rings(BACK), GW = W_WARPS / NG;  // rings, weight warps that share one
@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
         constexpr int RUN = SPLIT ? S::NT / 2 : 1;
         float run[RUN];                    // SPLIT: sums of this thread's lane of tile g, half of its columns
         auto drain = [&](uint32_t period, bool last) {
-            const uint32_t b = period & 1;
-            if (!umma::warp_wait(d_full + 8 * b, (period >> 1) & 1, abort, err)) return false;
+            const uint32_t b = S::DB == 2 ? period & 1 : 0;
+            if (!umma::warp_wait(d_full + 8 * b, (S::DB == 2 ? period >> 1 : period) & 1, abort, err)) return false;
             ptx::tc_fence_after();
 #pragma unroll
             for (int c = 0; c < RUN / 16; ++c) {
@@ -311,6 +311,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 const long long at = row_at(pair, c, mat);
                 const bool valid = at >= 0;
                 const int mis = valid ? (int)(at & 15) : 0;
+                if (ROWS && !a.aligned && taken > 0) {
+                    // the place before this one is filled again as soon as the ring's other warps have left it too
+                    const int prev = taken - 1;
+                    ok = umma::warp_wait(raw_empty + 8 * (grp * R_MOST + prev % a.rs), (prev / a.rs) & 1, abort, err);
+                    if (!ok) break;
+                    fetch();
+                }
                 if (!umma::warp_wait(raw_full + 8 * (grp * R_MOST + slot), par, abort, err)) {
                     ok = false;
                     break;
@@ -358,6 +365,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     before = base + (BACK ? c - c0 : PER * (c - c0) + (SUB == 2 ? e : step_of(FMT, j)));
                     if (lane == 0) ptx::mbar_arrive(full + 8 * (before % RING));
                     ++mine;
+                    // SPLIT: a period (two steps of each set) behind; with one buffer behind a period's first step, which its
+                    // products wait with
+                    if (SPLIT && mine >= PERIOD / 2 * (drained + S::DB) + (S::DB == 1)) {
+                        ok = ok && drain(n_d++, false);
+                        ++drained;
+                    }
                 };
                 if (BACK) {
                     if (FMT == FMT_Q8_0) {
@@ -391,22 +404,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(raw_empty + 8 * (grp * R_MOST + slot));  // the chunk has been read
-                if (ROWS && !a.aligned) {
-                    // the place before this one: the ring's other warps have most likely left it too
-                    const int prev = taken - 1;
-                    if (taken > 0 && ok)
-                        ok = umma::warp_wait(raw_empty + 8 * (grp * R_MOST + prev % a.rs), (prev / a.rs) & 1, abort, err);
-                    if (taken > 0 && ok) fetch();
-                    ++taken;
-                }
+                ++taken;
                 if (++slot == a.rs) {
                     slot = 0;
                     par ^= 1;
-                }
-                // SPLIT: a period (two steps of each set) behind
-                if (SPLIT && mine >= PERIOD / 2 * (drained + 2)) {
-                    ok = ok && drain(n_d++, false);
-                    ++drained;
                 }
             }
             base += s1 - s0;
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 // the periods that are left: the last stays in its buffer's hands
                 for (; ok && drained + 1 < (s1 - s0 + PERIOD - 1) / PERIOD; ++drained) ok = drain(n_d++, false);
                 if (!ok) break;
-                buf = n_d & 1;
+                buf = S::DB == 2 ? n_d & 1 : 0;
                 ok = ok && drain(n_d++, true);
                 if (!ok) break;
 #pragma unroll
@@ -653,9 +654,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
             for (int s = s0; s < s1; ++s, ++n) {
                 const int i = s - s0;
                 const bool fresh = SPLIT ? i % PERIOD == 0 : i == 0, last = s + 1 == s1 || (SPLIT && i % PERIOD == PERIOD - 1);
-                const uint32_t buf = SPLIT ? n_d & 1 : 0;
+                const uint32_t buf = S::DB == 2 ? n_d & 1 : 0;
                 const uint32_t st = s & 1;  // (a chunk of two or four steps begins on an even one)
-                if (fresh) ok = umma::warp_wait(d_empty + 8 * buf, (SPLIT ? (n_d >> 1) & 1 : n_d & 1) ^ 1, abort, err);
+                if (fresh) ok = umma::warp_wait(d_empty + 8 * buf, ((S::DB == 2 ? n_d >> 1 : n_d) & 1) ^ 1, abort, err);
                 ok = ok && umma::warp_wait(full + 8 * (n % RING), (n / RING) & 1, abort, err);
                 if (!ok) break;
                 ptx::tc_fence_after();

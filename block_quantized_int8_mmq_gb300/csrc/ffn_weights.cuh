@@ -63,18 +63,36 @@ __device__ __forceinline__ void four(uint32_t codes, uint32_t bias, __half2 s, _
         hi[i] = h2(MIN ? __hfma2(q, s, m) : __hmul2(q, s));
     }
 }
-// The same for f32 rows: hi, and what it leaves in lo.
+// The same for f32 rows: hi, and what it leaves in lo.  With a minimum in f32; without one in f16 alone: s = s1 + s2
+// (f16 each), hi = q s1 rounded, what that leaves is a product's remainder and an f16 value itself, and q s2 joins it.
+struct Scale2 {
+    float s, m;
+    __half2 s1, s2;
+    __device__ __forceinline__ Scale2(float s_, float m_, bool min) : s(s_), m(m_) {
+        if (min) return;
+        s1 = __float2half2_rn(s_);
+        s2 = __float2half2_rn(s_ - __low2float(s1));
+    }
+};
 template <bool MIN>
-__device__ __forceinline__ void four(uint32_t codes, uint32_t bias, float s, float m, uint32_t* hi, uint32_t* lo) {
+__device__ __forceinline__ void four(uint32_t codes, uint32_t bias, const Scale2& l, uint32_t* hi, uint32_t* lo) {
     const __half2 b = umma::bits_h2(bias);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float2 f = __half22float2(__hsub2(umma::bits_h2(__byte_perm(codes, 0x64646464u, i ? 0x4342 : 0x4140)), b));
-        const float a = MIN ? fmaf(f.x, s, m) : f.x * s, c = MIN ? fmaf(f.y, s, m) : f.y * s;
-        const __half2 h = __floats2half2_rn(a, c);
+        const __half2 q = __hsub2(umma::bits_h2(__byte_perm(codes, 0x64646464u, i ? 0x4342 : 0x4140)), b);
+        if (!MIN) {
+            const __half2 h = __hmul2(q, l.s1);
+            hi[i] = h2(h);
+            lo[i] = h2(__hfma2(q, l.s2, __hfma2(q, l.s1, __hneg2(h))));
+            continue;
+        }
+        const float2 f = __half22float2(q);
+        const unsigned long long w = ptx::fma_f32x2(ptx::f2_bits(f.x, f.y), ptx::f2_bits(l.s, l.s), ptx::f2_bits(l.m, l.m));
+        const __half2 h = __floats2half2_rn(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
         const float2 back = __half22float2(h);
+        const unsigned long long r = ptx::add_f32x2(w, ptx::f2_bits(-back.x, -back.y));
         hi[i] = h2(h);
-        lo[i] = h2(__floats2half2_rn(a - back.x, c - back.y));
+        lo[i] = h2(__floats2half2_rn(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32))));
     }
 }
 
@@ -131,12 +149,13 @@ __device__ __forceinline__ void quarter_q6(const Q6Half& w, int P, Check& check,
             const float s = d * (float)(int8_t)(sc >> (16 * b + 8 * g));
             const __half2 s2 = g ? high2(sp[b]) : low2(sp[b]);
             if (SPLIT) check.add(s, 0.f, 32.f);
+            const Scale2 w2(s, 0.f, false);
 #pragma unroll
             for (int i = 4 * g; i < 4 * g + 4; ++i) {
                 const uint32_t c = ((w.ql[8 * b + i] >> (4 * P)) & 0x0f0f0f0fu) |
                                    (__funnelshift_l(w.qh[i], w.qh[i], turn) & 0x30303030u);
                 if (SPLIT)
-                    four<false>(c, 0x64206420u, s, 0.f, hi + 2 * i, lo + 2 * i);
+                    four<false>(c, 0x64206420u, w2, hi + 2 * i, lo + 2 * i);
                 else
                     four<false>(c, 0x64206420u, s2, s2, hi + 2 * i);
             }
@@ -176,12 +195,13 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
         for (int b = 0; b < 2; ++b) {
             const float s = f16_bits_to_f32(b ? dd >> 16 : dd) * W_UP;
             if (SPLIT) check.add(s, 0.f, 128.f);
+            const Scale2 w2(s, 0.f, false);
             const __half2 s2 = b ? high2(d2) : low2(d2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t c = (b ? w[9 + i] : __funnelshift_r(w[i], w[i + 1], 16)) ^ 0x80808080u;
                 if (SPLIT)
-                    four<false>(c, 0x64806480u, s, 0.f, hi + 2 * i, lo + 2 * i);
+                    four<false>(c, 0x64806480u, w2, hi + 2 * i, lo + 2 * i);
                 else
                     four<false>(c, 0x64806480u, s2, s2, hi + 2 * i);
             }
@@ -232,13 +252,14 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
             const float s = f16_bits_to_f32(dd) * W_UP * (float)((sc >> (8 * b)) & 63);
             const float m = f16_bits_to_f32(dd >> 16) * -W_UP * (float)((mn >> (8 * b)) & 63);
             if (SPLIT) check.add(s, m, MOST);
+            const Scale2 w2(s, m, true);
             const __half2 sb = b ? high2(s2) : low2(s2), mb = b ? high2(m2) : low2(m2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t c = (b ? q[i] >> 4 : q[i]) & 0x0f0f0f0fu;
                 if (FMT == FMT_Q5_K) c |= __funnelshift_l(qh[i], qh[i], 4 - 2 * J - b) & 0x10101010u;
                 if (SPLIT)
-                    four<true>(c, 0x64006400u, s, m, hi + 2 * i, lo + 2 * i);
+                    four<true>(c, 0x64006400u, w2, hi + 2 * i, lo + 2 * i);
                 else
                     four<true>(c, 0x64006400u, sb, mb, hi + 2 * i);
             }
