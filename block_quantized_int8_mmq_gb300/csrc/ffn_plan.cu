@@ -135,7 +135,7 @@ int stream(const Call& c, cudaStream_t s) {
 int ffn_launch(const Call& c, cudaStream_t s) {
     if (!c.backward && c.M <= STREAM_ROWS) return stream(c, s);
     const bool split = c.dtype == MMQ_F32;
-    const int terms = split ? 2 : 1, nt_most = !split ? Shape<false, false>::NT : c.backward ? Shape<true, true>::NT : Shape<true, false>::NT;
+    const int terms = split ? 2 : 1;
     Tile a{};
     a.w[0] = static_cast<const uint8_t*>(c.w[0]);
     a.w[1] = static_cast<const uint8_t*>(c.w[1]);
@@ -146,6 +146,13 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.K = (int)c.K;
     a.width = c.backward ? a.K : a.N;
     a.groups = (int)ceil_div(c.M, 8);
+    a.aligned = a.row_bytes % 16 == 0;
+    a.slot = slot_bytes(c.fmt, a.aligned);
+    // rows of a tile: the most, but for two steps of them in shared memory beside two places of the rings
+    const int w_bytes = rings(c.backward) * 32 * a.slot;
+    const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true, true>::A_BYTES : 0);
+    int nt_most = split ? Shape<true, false>::NT : Shape<false, false>::NT;
+    while ((left - 2 * w_bytes) / (nt_most * 128 * terms) < 2) nt_most -= 16;
     a.nt = (int)up_to(ceil_div(c.M, ceil_div(c.M, nt_most)), 16);
     a.mtiles = (int)ceil_div(c.M, a.nt);
     a.units = (int)(a.mtiles * ceil_div(a.width, !c.backward && c.mats == 2 ? 128 : 256));
@@ -153,8 +160,6 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     const int pieces = (int)(c.backward ? c.mats * ceil_div(c.N, STEP) : ceil_div(c.K, STEP));  // of 64 values
     a.steps = pieces / a.sub;
     a.chunks = c.backward ? a.steps : (int)ceil_div(c.K, CHUNK);
-    a.aligned = a.row_bytes % 16 == 0;
-    a.slot = slot_bytes(c.fmt, a.aligned);
     a.dtype = c.dtype;
     a.act = c.act;
     for (int g = 0; g < 2; ++g) {
@@ -165,9 +170,8 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.residual_stride = c.residual_stride;
     a.out = c.out;
     const int ctas = deal(a, cost(a, c.fmt, split, c.backward), device_shape().sms);
-    // shared memory: two chunks' places and two steps of rows at least where they fit, four places, four steps, more places
-    const int x_bytes = a.nt * 128 * terms * a.sub, w_bytes = rings(c.backward) * 32 * a.slot;
-    const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true, true>::A_BYTES : 0);
+    // shared memory: two chunks' places and two steps of rows at least, then four places, four steps, more places
+    const int x_bytes = a.nt * 128 * terms * a.sub;
     auto steps_left = [&](int places) { return (left - places * w_bytes) / x_bytes; };
     a.rs = steps_left(4) >= 2 ? 4 : steps_left(3) >= 2 ? 3 : 2;
     a.xs = steps_left(a.rs) < 4 ? steps_left(a.rs) : 4;
