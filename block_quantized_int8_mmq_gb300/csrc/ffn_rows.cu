@@ -4,7 +4,7 @@
 // A row is scaled by a power of two that brings its largest magnitude into [2^13, 2^14), so that f16 holds all
 // but what lies 2^-38 below it, and written as f16 (bf16 rows exactly, f16 rows as they are but for the
 // scaling; f32 rows in two terms) in the order in which the tensor cores read them: per 64 values and 8 rows 1024
-// bytes, eight core matrices of 8 rows x 16 bytes.  `up` takes the scaling back, and the 2^8 of the weights.
+// bytes, a row 128 of them, its 16-byte pieces exchanged by the row's number (piece c at c ^ row: 128-byte swizzle).  `up` takes the scaling back, and the 2^8 of the weights.
 // HBM-bound.  f16 rows are operands as they are: no scaling, so they are cut at will.
 #include "ffn.cuh"
 #include "kv.cuh"
@@ -38,7 +38,7 @@ __device__ __forceinline__ float max_cta(float v, float* scratch) {
 
 // Eight values of a row to their place(s).
 __device__ __forceinline__ void put(const Rows& r, int m, int step, int chunk, const float (&v)[8], float down) {
-    uint8_t* p = r.tiles + ((long long)step * r.groups + (m >> 3)) * 1024 + chunk * 128 + (m & 7) * 16;
+    uint8_t* p = r.tiles + ((long long)step * r.groups + (m >> 3)) * 1024 + (m & 7) * 128 + ((chunk ^ (m & 7)) << 4);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -82,22 +82,18 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
     }
 }
 
-// A CTA lays out eight rows (a group), or one of them where there are few: a thread takes runs of eight values of
-// one row; with eight rows, neighbouring threads those of one place, whose 16 bytes lie side by side in a tile.
+// A CTA per row (f16 rows: several), a thread per run of eight values; eight neighbouring threads write a line.
 constexpr int HELD = 5;  // runs a thread keeps between looking for the largest value and writing
 
-template <typename T, int ROWS, int THREADS>
+template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
-    constexpr int LANES = THREADS / ROWS;  // threads of a row
     constexpr bool SCALED = !std::is_same<T, __half>::value;
-    __shared__ float s_max[THREADS / 32][ROWS];
+    __shared__ float s_max[THREADS / 32];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch_dependents();
     clear_counters(r);
-    const int m = blockIdx.x * ROWS + threadIdx.x % ROWS, first = threadIdx.x / ROWS + blockIdx.y * LANES;
-    const int step = LANES * gridDim.y;                                 // (f16 rows are shared by several CTAs)
-    const int runs = m < r.rows ? r.width / 8 : 0;                      // K is a multiple of 32
-    const int places = m < r.rows ? (r.width + 63) / 64 * 8 : 0;        // whole steps: zeros past K
+    const int m = blockIdx.x, first = threadIdx.x + blockIdx.y * THREADS, step = THREADS * gridDim.y;
+    const int runs = r.width / 8, places = (r.width + 63) / 64 * 8;  // K is a multiple of 32; whole steps: zeros past K
     const T* x = static_cast<const T*>(r.x) + m * r.stride;
     float held[HELD][8], down = 1.f;
 #pragma unroll
@@ -120,16 +116,10 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
         }
-#pragma unroll
-        for (int o = ROWS; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (threadIdx.x % 32 < ROWS) s_max[threadIdx.x / 32][threadIdx.x % ROWS] = amax;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < THREADS / 32; ++i) amax = fmaxf(amax, s_max[i][threadIdx.x % ROWS]);
-        const Scale s = row_scale(amax);
-        if (threadIdx.x < ROWS && m < r.rows) r.up[m] = s.up;
+        const Scale s = row_scale(max_cta<THREADS>(amax, s_max));
+        if (threadIdx.x == 0) r.up[m] = s.up;
         down = s.down;
-    } else if (blockIdx.y == 0 && threadIdx.x < ROWS && m < r.rows) {
+    } else if (blockIdx.y == 0 && threadIdx.x == 0) {
         r.up[m] = 1.f / 256.f;  // the weights' 2^8
     }
 #pragma unroll
@@ -137,7 +127,7 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
         const int c = first + i * step;
         if (c < places) {
             put(r, m, c >> 3, c & 7, held[i], down);
-            if (ROWS == 1 && r.sums) put_sum(r, m, c, held[i], down);  // (whole warps: K is a multiple of 256 then)
+            if (r.sums) put_sum(r, m, c, held[i], down);  // (whole warps: K is a multiple of 256 then)
         }
     }
 #pragma unroll 4
@@ -145,7 +135,7 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (c < runs) load8(x + 8ll * c, v);
         put(r, m, c >> 3, c & 7, v, down);
-        if (ROWS == 1 && r.sums) put_sum(r, m, c, v, down);
+        if (r.sums) put_sum(r, m, c, v, down);
     }
 }
 
@@ -267,20 +257,10 @@ int launch(const Rows& r, bool back, const char* fn, cudaStream_t s) {
         if (r.width <= 4096) return gradients<T, 256, true>(r, keep, fn, s);
         return keep <= KEEP_MOST ? gradients<T, 1024, true>(r, keep, fn, s) : gradients<T, 256, false>(r, 0, fn, s);
     }
-    // eight rows a CTA where that makes a CTA for every other SM at least
-    const int sms = device_shape().sms;
-    const bool many = r.rows >= 4 * sms;
-    const int ctas = many ? r.groups : r.rows;
-    int cuts = 1;
-    if (std::is_same<T, __half>::value) {
-        const int runs = r.width / 8, each = (many ? 64 : 512) * HELD;  // runs of a row that one CTA holds
-        cuts = 16 * sms / ctas < 1 ? 1 : 16 * sms / ctas;
-        cuts = cuts < (runs + each - 1) / each ? cuts : (runs + each - 1) / each;
-    }
-    const dim3 grid((unsigned)ctas, (unsigned)cuts);
-    return pdl_status(many ? launch_pdl(&k_ffn_rows<T, 8, 512>, grid, dim3(512), 0, s, r)
-                           : launch_pdl(&k_ffn_rows<T, 1, 512>, grid, dim3(512), 0, s, r),
-                      fn);
+    // f16 rows: CTAs enough for every SM's threads, as long as each has what its threads hold
+    const int each = 512 * HELD, runs = r.width / 8, want = 4 * device_shape().sms / r.rows + 1;
+    const int most = (runs + each - 1) / each, cuts = std::is_same<T, __half>::value ? (want < most ? want : most) : 1;
+    return pdl_status(launch_pdl(&k_ffn_rows<T, 512>, dim3((unsigned)r.rows, (unsigned)cuts), dim3(512), 0, s, r), fn);
 }
 
 }  // namespace

@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     // x for this lane, AHEAD blocks of 32 values at a time and as many ahead of their use: 16 bytes a block and term (Q6_K:
     // two of 8, of its two halves).  Measured one block ahead, from L2: most of a decode's cycles waited for it.
     constexpr int AHEAD = HELD ? 1 : 4 / (NT * TERMS);
-    const int x_lane = FMT == FMT_Q6_K ? (t >> 1) * 128 + g * 16 + (t & 1) * 8 : t * 128 + g * 16;
-    const uint8_t* xt = HELD ? x_held + x_lane : a.x + x_lane;
+    const int x_lane = FMT == FMT_Q6_K ? g * 128 + (((t >> 1) ^ g) << 4) + (t & 1) * 8 : g * 128 + ((t ^ g) << 4);
+    const uint8_t* xt = HELD ? x_held : a.x;
     const long long x_term = HELD ? (long long)x_steps * NT * 1024 : a.x_term;
     const int b_end = min(8 * c1, a.K / QK);
     const int lane_rows = g < a.M ? g + 8 < a.M ? 2 : 1 : 0;  // rows of x that this lane reads: g, g + 8
@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             if (block + i >= b_end || lane_rows == 0) break;
-            const uint8_t* p = xt + (long long)((block + i) >> 1) * (NT * 1024) + ((block + i) & 1) * 512;
+            const int at = x_lane ^ ((block + i) & 1) * 64;  // (pieces 4 .. 7 of a step)
+            const uint8_t* p = xt + (long long)((block + i) >> 1) * (NT * 1024);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 if (n >= lane_rows) break;
@@ -155,11 +156,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
                 for (int e = 0; e < TERMS; ++e) {
                     const uint8_t* q = p + n * 1024 + e * x_term;
                     if (FMT == FMT_Q6_K) {
-                        const uint2* w = reinterpret_cast<const uint2*>(q);
-                        const uint2 lo = HELD ? w[0] : __ldg(w), hi = HELD ? w[32] : __ldg(w + 32);
+                        const uint2 *w0 = reinterpret_cast<const uint2*>(q + at), *w1 = reinterpret_cast<const uint2*>(q + (at ^ 32));
+                        const uint2 lo = HELD ? *w0 : __ldg(w0), hi = HELD ? *w1 : __ldg(w1);
                         v[i][n][e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     } else {
-                        const uint4* w = reinterpret_cast<const uint4*>(q);
+                        const uint4* w = reinterpret_cast<const uint4*>(q + at);
                         v[i][n][e] = HELD ? *w : __ldg(w);
                     }
                 }

@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 ptx::tc_fence_after();
                 const uint32_t x_at = __shfl_sync(0xffffffffu, xs_addr + xst * xb, 0);
                 if (ptx::elect_one()) {
-                    const uint64_t xd = umma::sdesc(x_at, 1024);
+                    const uint64_t xd = umma::sdesc(x_at, 1024) | (2ull << 61);  // 128-byte swizzle
                     const uint32_t d = tmem + buf * S::D_COLS + g * S::NT;
                     uint32_t acc = fresh ? 0u : 1u;
                     // the products of small terms first
@@ -673,10 +673,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                         for (int kk = 0; kk < SUB * STEP / 16; ++kk) {
                             if (!BACK)
                                 ptx::umma_f16_ts(d, tmem + S::COL_A + st * S::A_COLS + (g * SUB * TERMS + ea) * 32 + 8 * kk,
-                                                 xd + (ex + kk / 4) * term_x + 16 * (kk % 4), idesc, acc);
+                                                 xd + (ex + kk / 4) * term_x + 2 * (kk % 4), idesc, acc);
                             else
                                 ptx::umma_f16(d, a_desc + (uint32_t)((st * TERMS + ea) * (S::A_BYTES >> 4) + kk * 512),
-                                              xd + ex * term_x + 16 * kk, idesc, acc);
+                                              xd + ex * term_x + 2 * kk, idesc, acc);
                             acc = 1u;
                         }
                     }
