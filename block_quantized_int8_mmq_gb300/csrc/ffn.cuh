@@ -166,9 +166,10 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }  // namespace ffn
 
 int ffn_launch(const ffn::Call& c, cudaStream_t s);
-int ffn_rows_launch(const ffn::Rows& r, bool back, const char* fn, cudaStream_t s);
-int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s);
-int ffn_backward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s);
-int ffn_stream_launch(int fmt, const ffn::Stream& a, int smem, int ctas, const char* fn, cudaStream_t s);
+// go: false asks for the shared memory that the kernel needs and launches nothing, so that a refusal comes before any launch
+int ffn_rows_launch(const ffn::Rows& r, bool back, bool go, const char* fn, cudaStream_t s);
+int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s);
+int ffn_backward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s);
+int ffn_stream_launch(int fmt, const ffn::Stream& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s);
 
 }  // namespace mmq

@@ -5,18 +5,18 @@ namespace mmq {
 namespace {
 
 template <int FMT>
-int launch(const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    return a.dtype == MMQ_F32 ? ffn::launch_tile<FMT, true, true, 1>(a, smem, ctas, fn, s)
-                              : ffn::launch_tile<FMT, false, true, 1>(a, smem, ctas, fn, s);
+int launch(const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    return a.dtype == MMQ_F32 ? ffn::launch_tile<FMT, true, true, 1>(a, smem, ctas, go, fn, s)
+                              : ffn::launch_tile<FMT, false, true, 1>(a, smem, ctas, go, fn, s);
 }
 
 }  // namespace
 
-int ffn_backward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, fn, s);
-    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, fn, s);
-    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, fn, s);
-    return launch<FMT_Q6_K>(a, smem, ctas, fn, s);
+int ffn_backward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, go, fn, s);
+    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, go, fn, s);
+    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, go, fn, s);
+    return launch<FMT_Q6_K>(a, smem, ctas, go, fn, s);
 }
 
 unsigned ffn_backward_take_error() { return ffn::take_tile_error(); }

@@ -5,19 +5,19 @@ namespace mmq {
 namespace {
 
 template <int FMT>
-int launch(const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    if (a.dtype == MMQ_F32) return ffn::launch_tile<FMT, true, false, 1>(a, smem, ctas, fn, s);
-    return a.sub == 2 ? ffn::launch_tile<FMT, false, false, 2>(a, smem, ctas, fn, s)
-                      : ffn::launch_tile<FMT, false, false, 1>(a, smem, ctas, fn, s);
+int launch(const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    if (a.dtype == MMQ_F32) return ffn::launch_tile<FMT, true, false, 1>(a, smem, ctas, go, fn, s);
+    return a.sub == 2 ? ffn::launch_tile<FMT, false, false, 2>(a, smem, ctas, go, fn, s)
+                      : ffn::launch_tile<FMT, false, false, 1>(a, smem, ctas, go, fn, s);
 }
 
 }  // namespace
 
-int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, fn, s);
-    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, fn, s);
-    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, fn, s);
-    return launch<FMT_Q6_K>(a, smem, ctas, fn, s);
+int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, go, fn, s);
+    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, go, fn, s);
+    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, go, fn, s);
+    return launch<FMT_Q6_K>(a, smem, ctas, go, fn, s);
 }
 
 unsigned ffn_forward_take_error() { return ffn::take_tile_error(); }

@@ -41,6 +41,21 @@ int deal(Tile& a, const Cost& t, int sms) {
     return (int)(a.units < sms ? a.units : sms);
 }
 
+// scratch_alloc, but under capture the graph's own memory without the library's pool, which cannot be made there: so a
+// program's first call may be a captured one.
+int scratch_of(size_t bytes, cudaStream_t s, void** p, const char* fn) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &status) != cudaSuccess || status == cudaStreamCaptureStatusNone) {
+        cudaGetLastError();
+        return scratch_alloc(bytes, s, p, fn);
+    }
+    if (cudaMallocAsync(p, bytes, s) == cudaSuccess) return MMQ_OK;
+    cudaGetLastError();
+    *p = nullptr;
+    report(fn, MMQ_ERR_NOMEM, "scratch allocation failed");
+    return MMQ_ERR_NOMEM;
+}
+
 // The row kernel's side of a call.
 Rows rows_of(const Call& c, int groups) {
     Rows r{};
@@ -79,7 +94,7 @@ int stream(const Call& c, cudaStream_t s) {
     a.K = (int)c.K;
     a.chunks = (int)ceil_div(c.K, CHUNK);
     a.xgroups = (int)ceil_div(c.M, 8);
-    a.aligned = a.row_bytes % 16 == 0;
+    a.aligned = c.fmt != FMT_Q6_K && a.row_bytes % 16 == 0;  // (whose chunks of 210 bytes are not, wherever rows begin)
     a.slot = slot_bytes(c.fmt, a.aligned);
     a.dtype = c.dtype;
     a.act = c.act;
@@ -113,19 +128,20 @@ int stream(const Call& c, cudaStream_t s) {
     if (a.aligned && !weight_maps(c, a.map, a.row_bytes, STREAM_SLAB)) return MMQ_ERR_CUDA;
 
     const long long term = ceil_div(c.K, STEP) * a.xgroups * 1024, sums = is_kquant(c.fmt) ? (long long)a.chunks * a.xgroups * 256 : 0;
+    Rows r = rows_of(c, a.xgroups);
+    int st = ffn_stream_launch(c.fmt, a, smem, (int)ctas, false, c.fn, s);
     void* scratch = nullptr;
-    int st = scratch_alloc((size_t)(256 + term * terms + sums), s, &scratch, c.fn);
+    if (!st) st = scratch_of((size_t)(256 + term * terms + sums), s, &scratch, c.fn);
     if (st != MMQ_OK) return st;
     uint8_t* at = static_cast<uint8_t*>(scratch);
-    Rows r = rows_of(c, a.xgroups);
     r.up = reinterpret_cast<float*>(at);
     a.up = r.up;
     r.tiles = at + 256;
     a.x = r.tiles;
     r.term = a.x_term = term;
     if (sums) a.sums = r.sums = r.tiles + term * terms;
-    st = ffn_rows_launch(r, false, c.fn, s);
-    if (st == MMQ_OK) st = ffn_stream_launch(c.fmt, a, smem, (int)ctas, c.fn, s);
+    st = ffn_rows_launch(r, false, true, c.fn, s);
+    if (st == MMQ_OK) st = ffn_stream_launch(c.fmt, a, smem, (int)ctas, true, c.fn, s);
     scratch_free(scratch, s);  // stream-ordered: after the kernels above
     return st;
 }
@@ -146,7 +162,7 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.K = (int)c.K;
     a.width = c.backward ? a.K : a.N;
     a.groups = (int)ceil_div(c.M, 8);
-    a.aligned = a.row_bytes % 16 == 0;
+    a.aligned = c.fmt != FMT_Q6_K && a.row_bytes % 16 == 0;  // (whose chunks of 210 bytes are not, wherever rows begin)
     a.slot = slot_bytes(c.fmt, a.aligned);
     // rows of a tile: the most, but for two steps of them in shared memory beside two places of the rings
     const int w_bytes = rings(c.backward) * 32 * a.slot;
@@ -187,11 +203,14 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     const long long term = (long long)pieces * a.groups * 1024;
     const long long counters = up_to(4ll * a.rest, 256), ups = up_to(4 * c.M, 256);
     const long long parts = a.rest ? 2ll * ctas * 2 * a.nt * 128 * 4 : 0;
+    Rows r = rows_of(c, a.groups);
+    auto products = c.backward ? ffn_backward_launch : ffn_forward_launch;
+    int st = products(c.fmt, a, smem, ctas, false, c.fn, s);
+    if (!st) st = ffn_rows_launch(r, c.backward, false, c.fn, s);
     void* scratch = nullptr;
-    int st = scratch_alloc((size_t)(counters + ups + term * terms + parts), s, &scratch, c.fn);
+    if (!st) st = scratch_of((size_t)(counters + ups + term * terms + parts), s, &scratch, c.fn);
     if (st != MMQ_OK) return st;
     uint8_t* at = static_cast<uint8_t*>(scratch);
-    Rows r = rows_of(c, a.groups);
     r.counters = a.counters = reinterpret_cast<unsigned*>(at);
     r.n_counters = a.rest;
     r.up = reinterpret_cast<float*>(at + counters);
@@ -200,9 +219,8 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     r.term = a.x_term = term;
     a.x = r.tiles;
     a.parts = reinterpret_cast<float*>(r.tiles + term * terms);
-    st = ffn_rows_launch(r, c.backward, c.fn, s);
-    if (st == MMQ_OK)
-        st = c.backward ? ffn_backward_launch(c.fmt, a, smem, ctas, c.fn, s) : ffn_forward_launch(c.fmt, a, smem, ctas, c.fn, s);
+    st = ffn_rows_launch(r, c.backward, true, c.fn, s);
+    if (st == MMQ_OK) st = products(c.fmt, a, smem, ctas, true, c.fn, s);
     scratch_free(scratch, s);  // stream-ordered: after the kernels above
     return st;
 }

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(THREADS) k_ffn_gradients(const Rows r) {
 constexpr int KEEP_MOST = 200 * 1024;
 
 template <typename T, int THREADS, bool KEEP>
-int gradients(const Rows& r, int smem, const char* fn, cudaStream_t s) {
+int gradients(const Rows& r, int smem, bool go, const char* fn, cudaStream_t s) {
     static SmemAttr attr;
     auto k = &k_ffn_gradients<T, THREADS, KEEP>;
     if (smem > 48 * 1024)
@@ -246,29 +246,38 @@ int gradients(const Rows& r, int smem, const char* fn, cudaStream_t s) {
             report(fn, st, "the gradients' shared memory was refused");
             return st;
         }
+    if (!go) return MMQ_OK;
+    ProfScope ps("k_ffn_gradients", s);
     return pdl_status(launch_pdl(k, dim3((unsigned)r.rows), dim3(THREADS), smem, s, r), fn);
 }
 
+template <typename T, int THREADS>
+int rows(const Rows& r, const char* fn, cudaStream_t s) {
+    // f16 rows: CTAs enough for every SM's threads, as long as each has what its threads hold
+    const int each = THREADS * HELD, runs = r.width / 8, want = 4 * device_shape().sms / r.rows + 1;
+    const int most = (runs + each - 1) / each, cuts = std::is_same<T, __half>::value ? (want < most ? want : most) : 1;
+    ProfScope ps("k_ffn_rows", s);
+    return pdl_status(launch_pdl(&k_ffn_rows<T, THREADS>, dim3((unsigned)r.rows, (unsigned)cuts), dim3(THREADS), 0, s, r), fn);
+}
+
 template <typename T>
-int launch(const Rows& r, bool back, const char* fn, cudaStream_t s) {
-    ProfScope ps(back ? "k_ffn_gradients" : "k_ffn_rows", s);
+int launch(const Rows& r, bool back, bool go, const char* fn, cudaStream_t s) {
     if (back) {
         const int keep = (r.width + STEP - 1) / STEP * STEP * 4 * r.mats;
-        if (r.width <= 4096) return gradients<T, 256, true>(r, keep, fn, s);
-        return keep <= KEEP_MOST ? gradients<T, 1024, true>(r, keep, fn, s) : gradients<T, 256, false>(r, 0, fn, s);
+        if (r.width <= 4096) return gradients<T, 256, true>(r, keep, go, fn, s);
+        return keep <= KEEP_MOST ? gradients<T, 1024, true>(r, keep, go, fn, s) : gradients<T, 256, false>(r, 0, go, fn, s);
     }
-    // f16 rows: CTAs enough for every SM's threads, as long as each has what its threads hold
-    const int each = 512 * HELD, runs = r.width / 8, want = 4 * device_shape().sms / r.rows + 1;
-    const int most = (runs + each - 1) / each, cuts = std::is_same<T, __half>::value ? (want < most ? want : most) : 1;
-    return pdl_status(launch_pdl(&k_ffn_rows<T, 512>, dim3((unsigned)r.rows, (unsigned)cuts), dim3(512), 0, s, r), fn);
+    if (!go) return MMQ_OK;
+    // a narrow row in small CTAs where there are many; one row's latency in a large one
+    return r.rows >= 2 * device_shape().sms && r.width <= 8 * 128 * HELD ? rows<T, 128>(r, fn, s) : rows<T, 512>(r, fn, s);
 }
 
 }  // namespace
 
-int ffn_rows_launch(const Rows& r, bool back, const char* fn, cudaStream_t s) {
-    if (r.dtype == MMQ_F32) return launch<float>(r, back, fn, s);
-    if (r.dtype == MMQ_BF16) return launch<__nv_bfloat16>(r, back, fn, s);
-    return launch<__half>(r, back, fn, s);
+int ffn_rows_launch(const Rows& r, bool back, bool go, const char* fn, cudaStream_t s) {
+    if (r.dtype == MMQ_F32) return launch<float>(r, back, go, fn, s);
+    if (r.dtype == MMQ_BF16) return launch<__nv_bfloat16>(r, back, go, fn, s);
+    return launch<__half>(r, back, go, fn, s);
 }
 
 }  // namespace mmq

@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 }
 
 template <int FMT, int NT, int TERMS, bool HELD>
-int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+int launch(const Stream& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
     static SmemAttr attr;
     auto k = &k_ffn_stream<FMT, NT, TERMS, HELD>;
     const int st = ensure_smem(reinterpret_cast<const void*>(k), SMEM_MOST, attr);
@@ -416,28 +416,29 @@ int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) 
         report(fn, st, "the stream's shared memory was refused");
         return st;
     }
+    if (!go) return MMQ_OK;
     ProfScope ps("k_ffn_stream", s);
     return pdl_status(launch_pdl(k, dim3((unsigned)ctas), dim3(32 * WARPS), smem, s, a), fn);
 }
 
 template <int FMT, int NT, int TERMS>
-int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    return a.held ? launch<FMT, NT, TERMS, true>(a, smem, ctas, fn, s) : launch<FMT, NT, TERMS, false>(a, smem, ctas, fn, s);
+int launch(const Stream& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    return a.held ? launch<FMT, NT, TERMS, true>(a, smem, ctas, go, fn, s) : launch<FMT, NT, TERMS, false>(a, smem, ctas, go, fn, s);
 }
 
 template <int FMT>
-int launch(const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    if (a.dtype == MMQ_F32) return a.xgroups == 1 ? launch<FMT, 1, 2>(a, smem, ctas, fn, s) : launch<FMT, 2, 2>(a, smem, ctas, fn, s);
-    return a.xgroups == 1 ? launch<FMT, 1, 1>(a, smem, ctas, fn, s) : launch<FMT, 2, 1>(a, smem, ctas, fn, s);
+int launch(const Stream& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    if (a.dtype == MMQ_F32) return a.xgroups == 1 ? launch<FMT, 1, 2>(a, smem, ctas, go, fn, s) : launch<FMT, 2, 2>(a, smem, ctas, go, fn, s);
+    return a.xgroups == 1 ? launch<FMT, 1, 1>(a, smem, ctas, go, fn, s) : launch<FMT, 2, 1>(a, smem, ctas, go, fn, s);
 }
 
 }  // namespace
 
-int ffn_stream_launch(int fmt, const Stream& a, int smem, int ctas, const char* fn, cudaStream_t s) {
-    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, fn, s);
-    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, fn, s);
-    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, fn, s);
-    return launch<FMT_Q6_K>(a, smem, ctas, fn, s);
+int ffn_stream_launch(int fmt, const Stream& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    if (fmt == FMT_Q8_0) return launch<FMT_Q8_0>(a, smem, ctas, go, fn, s);
+    if (fmt == FMT_Q4_K) return launch<FMT_Q4_K>(a, smem, ctas, go, fn, s);
+    if (fmt == FMT_Q5_K) return launch<FMT_Q5_K>(a, smem, ctas, go, fn, s);
+    return launch<FMT_Q6_K>(a, smem, ctas, go, fn, s);
 }
 
 unsigned ffn_stream_take_error() {

@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
 
 // ------------------------------------------------------------------------------------------ host
 template <int FMT, bool SPLIT, bool BACK, int SUB>
-int launch_tile(const Tile& a, int smem, int ctas, const char* fn, cudaStream_t s) {
+int launch_tile(const Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
     static SmemAttr attr;
     auto k = &k_ffn_tile<FMT, SPLIT, BACK, SUB>;
     const int st = ensure_smem(reinterpret_cast<const void*>(k), SMEM_MOST, attr);
@@ -712,6 +712,7 @@ int launch_tile(const Tile& a, int smem, int ctas, const char* fn, cudaStream_t 
         report(fn, st, "the tiles' shared memory was refused");
         return st;
     }
+    if (!go) return MMQ_OK;
     ProfScope ps(BACK ? "k_ffn_tile_back" : "k_ffn_tile", s);
     return pdl_status(launch_pdl(k, dim3((unsigned)ctas), dim3(THREADS), smem, s, a), fn);
 }

@@ -567,3 +567,111 @@ def test_python_refusals():
     with pytest.raises(mmq.MMQError):
         mmq.mmq_project(rows(1, 3, K + 8, "bf16")[:, 4:4 + K], w, "q4_k", N)
     clean()
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_a_refused_call_writes_nothing(M, capfd):
+    """Shared memory that is refused: MMQ_ERR_SMEM before anything is launched, the gradients' outputs included."""
+    N, K = 4200, 256
+    w = Weights("q4_k", 1, 20, K)
+    wide = torch.zeros((N, K // 256 * 144), dtype=torch.uint8, device="cuda")
+    x, dy = rows(1, M, K, "f32"), rows(2, M, N, "f32")
+    out, dz, dx = (torch.full(s, 7.0, device="cuda") for s in ((M, 20), (M, N), (M, K)))
+    mmq.mmq_debug_refuse_smem(True)
+    try:
+        for call in (lambda: mmq.mmq_project(x, w.bytes, "q4_k", 20, out=out),
+                     lambda: mmq.mmq_project_backward(dy, wide, "q4_k", K, act="relu", pre=dy, dz=dz, dx=dx)):
+            with pytest.raises(mmq.MMQError) as e:
+                call()
+            assert e.value.status == -5
+    finally:
+        mmq.mmq_debug_refuse_smem(False)
+    clean()
+    assert all(bool((t == 7).all()) for t in (out, dz, dx))
+    assert "refused" in capfd.readouterr().err
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weights_out_of_range_are_reported(fmt, dtype):
+    """Magnitudes past 255: the error word says so; other columns keep their values.  Up to 16 rows take any weights."""
+    N, K, at = 150, 512, {"q6_k": 208}.get(fmt, 0)
+    w = Weights(fmt, 3, N, K)
+    raw = w.bytes.view(N, -1, ffn_ref.BYTES[fmt]).clone()
+    raw[70, 1, at:at + 2] = torch.tensor(np.frombuffer(np.float16(60000.0).tobytes(), np.uint8).copy(), device="cuda")
+    if fmt in ("q4_k", "q5_k"):
+        raw[70, 1, 4:8] |= 16  # (sub-scales that are not all 0)
+    raw = raw.view(N, -1)
+    x, keep = rows(4, 40, K, dtype), [n for n in range(N) if n != 70]
+    good = mmq.mmq_project(x, w.bytes, fmt, N)
+    clean()
+    bad = mmq.mmq_project(x, raw, fmt, N)
+    torch.cuda.synchronize()
+    assert mmq.mmq_get_device_error() == -11
+    assert torch.equal(good[:, keep], bad[:, keep])
+    dy = rows(5, 40, N, dtype)
+    mmq.mmq_project_backward(dy, raw, fmt, K)
+    torch.cuda.synchronize()
+    assert mmq.mmq_get_device_error() == -11
+    big = ffn_ref.values(fmt, raw.cpu().numpy())
+    if dtype == "f32":
+        few = mmq.mmq_project(x[:5], raw, fmt, N)
+        clean()
+        want = x[:5].double() @ torch.from_numpy(big[0]).cuda().T
+        size = x[:5].double().abs() @ torch.from_numpy(big[1]).cuda().T
+        assert bool(((few.double() - want).abs() <= 2.0 ** -16 * size).all())
+
+
+@pytest.mark.parametrize("M", [2, 16, 17, 130])
+def test_a_first_call_inside_a_capture(M):
+    """Nothing has to run before a capture: in a process of its own, the first call of each operator is a captured one."""
+    import subprocess
+    import sys
+    code = f"""
+import torch, synth, block_quantized_int8_mmq_gb300 as mmq
+M, N, K = {M}, 512, 768
+w = [torch.from_numpy(synth.weights("q4_k", i, N, K)).cuda() for i in (1, 2)]
+x = torch.randn((M, K), device="cuda", dtype=torch.bfloat16)
+gate, up = (torch.empty((M, N), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    h = mmq.mmq_gated(x, w[0], w[1], "q4_k", N, gate=gate, up=up)
+    dx = mmq.mmq_gated_backward(h, gate, up, w[0], w[1], "q4_k", K)
+g.replay()
+torch.cuda.synchronize()
+a = mmq.mmq_gated(x, w[0], w[1], "q4_k", N)
+b = mmq.mmq_gated_backward(a, gate, up, w[0], w[1], "q4_k", K)
+assert torch.equal(a, h) and torch.equal(b, dx) and mmq.mmq_get_device_error() == 0
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M", [1, 5, 8, 9, 16])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_few_rows_over_long_and_short_sums(fmt, dtype, M):
+    """The stream of weights: x held in shared memory or not, one share of the reduction or sixteen, ragged columns."""
+    for N, K in ((33, 256), (500, 4096), (2500, 1024), (40, 18944)):
+        project(fmt, dtype, M, N, K, act="silu", bias=True, residual=True, seed=K + M)
+    gated(fmt, dtype, M, 2450, 768, seed=M)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("N", [4090, 4100, 26000])
+def test_wide_gradients(dtype, N):
+    """Rows of gradients in small CTAs, in large ones, and too wide to be kept between their two looks."""
+    backward("q8_0", dtype, 21, N, 64, 2, keep=True, seed=N)
+    backward("q8_0", dtype, 3, N, 64, 1, act="gelu", keep=True, seed=N)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [2, 30, 140])
+def test_q6_k_rows_that_begin_on_16_bytes(dtype, M):
+    """2048 and 4096 values: rows of a multiple of 16 bytes whose chunks of 210 are not."""
+    for K in (2048, 4096):
+        project("q6_k", dtype, M, 150, K, seed=K)
+        backward("q6_k", dtype, M, 150, K, 2, seed=K)
