@@ -4,10 +4,12 @@
 namespace mmq {
 namespace {
 
+// (Q8_0's scales are f16 values: nothing but its weights is rounded as it is)
 template <int FMT>
 int launch(const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
-    return a.dtype == MMQ_F32 ? ffn::launch_tile<FMT, true, true, 1>(a, smem, ctas, go, fn, s)
-                              : ffn::launch_tile<FMT, false, true, 1>(a, smem, ctas, go, fn, s);
+    if (a.dtype == MMQ_F32) return ffn::launch_tile<FMT, true, true, 1, false>(a, smem, ctas, go, fn, s);
+    return a.dtype == MMQ_F16 ? ffn::launch_tile<FMT, false, true, 1, FMT != FMT_Q8_0>(a, smem, ctas, go, fn, s)
+                              : ffn::launch_tile<FMT, false, true, 1, false>(a, smem, ctas, go, fn, s);
 }
 
 }  // namespace

@@ -4,11 +4,16 @@
 namespace mmq {
 namespace {
 
+// (Q8_0's scales are f16 values: nothing but its weights is rounded as it is)
+template <int FMT, int SUB>
+int launch16(const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
+    return a.dtype == MMQ_F16 ? ffn::launch_tile<FMT, false, false, SUB, FMT != FMT_Q8_0>(a, smem, ctas, go, fn, s)
+                              : ffn::launch_tile<FMT, false, false, SUB, false>(a, smem, ctas, go, fn, s);
+}
 template <int FMT>
 int launch(const ffn::Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
-    if (a.dtype == MMQ_F32) return ffn::launch_tile<FMT, true, false, 1>(a, smem, ctas, go, fn, s);
-    return a.sub == 2 ? ffn::launch_tile<FMT, false, false, 2>(a, smem, ctas, go, fn, s)
-                      : ffn::launch_tile<FMT, false, false, 1>(a, smem, ctas, go, fn, s);
+    if (a.dtype == MMQ_F32) return ffn::launch_tile<FMT, true, false, 1, false>(a, smem, ctas, go, fn, s);
+    return a.sub == 2 ? launch16<FMT, 2>(a, smem, ctas, go, fn, s) : launch16<FMT, 1>(a, smem, ctas, go, fn, s);
 }
 
 }  // namespace

@@ -159,7 +159,7 @@ __device__ __forceinline__ void finish8(const Tile& a, int pair, int lane_row, i
 // side by side (Q6_K's share their bytes); Q8_0, whose last chunk may be short, as they come.
 __host__ __device__ constexpr int step_of(int fmt, int q) { return fmt == FMT_Q8_0 || q == 0 || q == 3 ? q : 3 - q; }
 
-template <int FMT, bool SPLIT, bool BACK, int SUB>
+template <int FMT, bool SPLIT, bool BACK, int SUB, bool FINE>
 __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__ Tile a) {
     using S = Shape<SPLIT, BACK, SUB>;
     constexpr int PER = CHUNK / STEP / SUB;  // forward: steps of a chunk
@@ -351,9 +351,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                         }
                     };
                     if (FMT == FMT_Q6_K && !BACK)
-                        quarter_q6<SPLIT>(q6, j & 1, check, put);
+                        quarter_q6<SPLIT, FINE>(q6, j & 1, check, put);
                     else
-                        quarter<FMT, SPLIT>(src, j, mis, a.aligned, blocks, !BACK || valid, check, put);
+                        quarter<FMT, SPLIT, FINE>(src, j, mis, a.aligned, blocks, !BACK || valid, check, put);
                     if (sub + 1 < SUB) return;
                     if (!BACK) {
                         ptx::tmem_st_wait();
@@ -703,10 +703,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
 }
 
 // ------------------------------------------------------------------------------------------ host
-template <int FMT, bool SPLIT, bool BACK, int SUB>
+template <int FMT, bool SPLIT, bool BACK, int SUB, bool FINE>
 int launch_tile(const Tile& a, int smem, int ctas, bool go, const char* fn, cudaStream_t s) {
     static SmemAttr attr;
-    auto k = &k_ffn_tile<FMT, SPLIT, BACK, SUB>;
+    auto k = &k_ffn_tile<FMT, SPLIT, BACK, SUB, FINE>;
     const int st = ensure_smem(reinterpret_cast<const void*>(k), SMEM_MOST, attr);
     if (st != MMQ_OK) {
         report(fn, st, "the tiles' shared memory was refused");

@@ -4,9 +4,9 @@
 //
 // Weights enter the product times 2^8: f16 is then normal from 2^-22 up, and whatever a weight is formed
 // from, |scale| times the largest code and the minimum, has to stay below 255 (Check).
-// For 16-bit rows the scale and the minimum are rounded to f16 first and the weight once more, 2^-11 each: no more
-// than the rows' own type loses, and four instructions for two weights.  For f32 rows the weight is formed in
-// f32 and split in two f16 terms (2^-22).
+// For bf16 rows the scale and the minimum are rounded to f16 first and the weight once more, 2^-11 each: little beside
+// what the rows' own type loses (2^-8), and four instructions for two weights.  For f16 rows only the weight is (Fine).
+// For f32 rows the weight is formed in f32 and split in two f16 terms (2^-22).
 #pragma once
 
 #include "ffn.cuh"
@@ -53,7 +53,35 @@ struct Check {
     __device__ __forceinline__ bool bad() const { return f != 0.f || !__hbeq2(h, __float2half2_rn(0.f)); }
 };
 
-// Four codes (one per byte) to two pairs of f16, s q + m: 16-bit rows.
+// f16 rows: s q - m with no rounding but the weight's own (2^-11, 2.1e-4 of the weights' norm; scale and minimum rounded
+// too, as bf16 rows have them, come to 6.6e-4, three times what f16 outputs lose).  The minimum is c scales and a
+// remainder of half of one, the codes are centred on c, which their placing takes off anyway, and the scale is two
+// terms: s1 (q - c) + (s2 (q - c) + r).
+struct Fine {
+    __half2 s1, s2, r;
+    uint32_t bias;
+    __device__ __forceinline__ Fine(float s, float m, float centre) {
+        float c = centre, rest = 0.f;
+        if (centre == 0.f) {  // a minimum
+            c = fmaxf(-1000.f, fminf(1000.f, rintf(__fdividef(m, s))));
+            rest = fmaf(c, s, -m);
+        }
+        s1 = __float2half2_rn(s);
+        s2 = __float2half2_rn(s - __low2float(s1));
+        r = __float2half2_rn(rest);
+        bias = h2(__float2half2_rn(1024.f + c));
+    }
+};
+__device__ __forceinline__ void four(uint32_t codes, const Fine& l, uint32_t* hi) {
+    const __half2 b = umma::bits_h2(l.bias);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __half2 q = __hsub2(umma::bits_h2(__byte_perm(codes, 0x64646464u, i ? 0x4342 : 0x4140)), b);
+        hi[i] = h2(__hfma2(q, l.s1, __hfma2(q, l.s2, l.r)));
+    }
+}
+
+// Four codes (one per byte) to two pairs of f16, s q + m: bf16 rows.
 template <bool MIN>
 __device__ __forceinline__ void four(uint32_t codes, uint32_t bias, __half2 s, __half2 m, uint32_t* hi) {
     const __half2 b = umma::bits_h2(bias);
@@ -127,13 +155,13 @@ struct Q6Half {
     }
 };
 // Its first (P = 0) or second quarter: emit(half, hi, lo) as below.
-template <bool SPLIT, class Emit>
+template <bool SPLIT, bool FINE, class Emit>
 __device__ __forceinline__ void quarter_q6(const Q6Half& w, int P, Check& check, Emit&& emit) {
     uint32_t hi[16], lo[16];
     const uint32_t sc = P ? w.sc[1] : w.sc[0];
     const float d = f16_bits_to_f32(w.d) * W_UP;
     __half2 sp[2];
-    if (!SPLIT) {
+    if (!SPLIT && !FINE) {
         const __half2 d2 = __hmul2(umma::bits_h2(w.d), __float2half2_rn(W_UP)), bias = umma::bits_h2(0x64806480u);
         const uint32_t u = sc ^ 0x80808080u;
         sp[0] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias), d2);
@@ -148,14 +176,17 @@ __device__ __forceinline__ void quarter_q6(const Q6Half& w, int P, Check& check,
         for (int g = 0; g < 2; ++g) {
             const float s = d * (float)(int8_t)(sc >> (16 * b + 8 * g));
             const __half2 s2 = g ? high2(sp[b]) : low2(sp[b]);
-            if (SPLIT) check.add(s, 0.f, 32.f);
+            if (SPLIT || FINE) check.add(s, 0.f, 32.f);
             const Scale2 w2(s, 0.f, false);
+            const Fine fine(s, 0.f, 32.f);
 #pragma unroll
             for (int i = 4 * g; i < 4 * g + 4; ++i) {
                 const uint32_t c = ((w.ql[8 * b + i] >> (4 * P)) & 0x0f0f0f0fu) |
                                    (__funnelshift_l(w.qh[i], w.qh[i], turn) & 0x30303030u);
                 if (SPLIT)
                     four<false>(c, 0x64206420u, w2, hi + 2 * i, lo + 2 * i);
+                else if (FINE)
+                    four(c, fine, hi + 2 * i);
                 else
                     four<false>(c, 0x64206420u, s2, s2, hi + 2 * i);
             }
@@ -168,7 +199,7 @@ __device__ __forceinline__ void quarter_q6(const Q6Half& w, int P, Check& check,
 // takes 32 values at a time as 16 pairs.  blocks: Q8_0's 32-value blocks that exist here (0 .. 2), the others are
 // zero.  valid: whether there is such a row; where not, zeros come out of whatever is in its place.  J is a constant
 // for Q8_0 (its blocks of 34 bytes lie at another word offset in each quarter).
-template <int FMT, bool SPLIT, class Emit>
+template <int FMT, bool SPLIT, bool FINE, class Emit>
 __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, bool aligned, int blocks, bool valid,
                                         Check& check, Emit&& emit) {
     uint32_t hi[16], lo[16];
@@ -210,7 +241,7 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
     } else if (FMT == FMT_Q6_K) {
         Q6Half w;
         w.load(slot, J >> 1, mis, valid);
-        quarter_q6<SPLIT>(w, J & 1, check, emit);
+        quarter_q6<SPLIT, FINE>(w, J & 1, check, emit);
     } else {
         const uint4 head = *reinterpret_cast<const uint4*>(slot);
         uint32_t q[8], qh[8];
@@ -241,7 +272,7 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
         constexpr float MOST = FMT == FMT_Q5_K ? 31.f : 15.f;
         const uint32_t dd = valid ? head.x : 0u;
         __half2 s2{}, m2{};
-        if (!SPLIT) {
+        if (!SPLIT && !FINE) {
             const __half2 d2 = __hmul2(umma::bits_h2(dd), __floats2half2_rn(W_UP, -W_UP)), bias = umma::bits_h2(0x64006400u);
             s2 = __hmul2(__hsub2(umma::bits_h2(__byte_perm(sc, 0x64646464u, 0x4140)), bias), low2(d2));
             m2 = __hmul2(__hsub2(umma::bits_h2(__byte_perm(mn, 0x64646464u, 0x4140)), bias), high2(d2));
@@ -251,8 +282,9 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
         for (int b = 0; b < 2; ++b) {
             const float s = f16_bits_to_f32(dd) * W_UP * (float)((sc >> (8 * b)) & 63);
             const float m = f16_bits_to_f32(dd >> 16) * -W_UP * (float)((mn >> (8 * b)) & 63);
-            if (SPLIT) check.add(s, m, MOST);
+            if (SPLIT || FINE) check.add(s, m, MOST);
             const Scale2 w2(s, m, true);
+            const Fine fine(s, -m, 0.f);
             const __half2 sb = b ? high2(s2) : low2(s2), mb = b ? high2(m2) : low2(m2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -260,6 +292,8 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
                 if (FMT == FMT_Q5_K) c |= __funnelshift_l(qh[i], qh[i], 4 - 2 * J - b) & 0x10101010u;
                 if (SPLIT)
                     four<true>(c, 0x64006400u, w2, hi + 2 * i, lo + 2 * i);
+                else if (FINE)
+                    four(c, fine, hi + 2 * i);
                 else
                     four<true>(c, 0x64006400u, sb, mb, hi + 2 * i);
             }
