@@ -575,7 +575,17 @@ int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtyp
  *   is formed from the unrounded values.  dz, dgate, dup: NULL, or where the gradients of z, g and u go
  *   (sums of their columns are the biases' gradients; with the rows, those of an adapter).
  *   pre (backward): NULL is allowed where act is MMQ_ACT_NONE, and it is not read then.
- * Accuracy: sums, biases, activations and the epilogue are f32; outputs are rounded once.
+ * Accuracy: sums, biases, activations and the epilogue are f32; outputs are rounded once.  Rows take part as f16 values
+ * times a power of two of each row (f32 rows in two terms, 2^-22): exactly, but for what lies 2^38 below the row's
+ * largest value; gradients that an activation has formed are rounded to f16 so (2^-11) where the type has 16 bits.
+ *   project, gated, up to 16 rows: codes exactly, blocks' sums scaled in f32.
+ *   more rows, and backward: weights as f16 values times 2^8, for f32 rows in two terms (2^-22, those below 2^-22 to
+ *   2^-33).  f16 rows: each rounded once, 2^-11 at most (2.1e-4 of a projection's norm, as the outputs' own rounding);
+ *   bf16 rows: the block's scale and minimum too (6e-4 of the norm at most, the outputs' rounding is 1.7e-3).  What a
+ *   weight is formed from, |scale| x the largest code + |minimum|, has to be below 255: else the device error word is set
+ *   (MMQ_ERR_RANGE) and the outputs of that weight row (backward: all) are unspecified.
+ *   Sums of 16-bit rows stay in the tensor cores, which round towards zero: 2^-22 of the sum at most for every 16 values; f32
+ *   rows' leave them every 256 values (up to 16 rows: every 32).
  * Finite inputs are required: a NaN or an infinity in a row leaves that row's outputs unspecified, and
  * no other's.  The order of summation depends on the sizes alone, so repeated calls give the same bits.
  * Scratch: stream-ordered, as the expanded path's.
@@ -620,7 +630,8 @@ int mmq_profile_read(mmq_kernel_time* out, int capacity, int reset);
 /* Synchronizes `stream`, then reads and clears the device error word of every kernel
  * in the library.  Returns MMQ_OK, MMQ_ERR_TIMEOUT (a bounded wait ran out),
  * MMQ_ERR_RANGE (a length, start, page number or position that a key/value cache call read
- * from device memory was outside its range) or MMQ_ERR_CUDA (the synchronize itself failed). */
+ * from device memory was outside its range, or a weight of a feed-forward call was) or MMQ_ERR_CUDA (the
+ * synchronize itself failed). */
 int mmq_get_device_error(void* stream);
 
 #ifdef __cplusplus

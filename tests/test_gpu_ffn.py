@@ -675,3 +675,32 @@ def test_q6_k_rows_that_begin_on_16_bytes(dtype, M):
     for K in (2048, 4096):
         project("q6_k", dtype, M, 150, K, seed=K)
         backward("q6_k", dtype, M, 150, K, 2, seed=K)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_feed_forward_example(dtype):
+    """The example runs and its gradients are right: a dozen roundings of the rows' type (half a step each, a few to a stage)
+    and of the weights on the way, 24 half steps of bf16 in all; f32 as the tensor cores' products leave it, and torch's
+    own f32 products of the adapter."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    errors = example.run(tokens=90, steps=3, dtype=DT[dtype], quiet=True, hidden=512, inner=768)
+    assert len(errors) == 5 and max(errors) <= (2.0 ** -16 if dtype == "f32" else 24 * 2.0 ** -8)
+
+
+def test_profiler_names():
+    w = Weights("q4_k", 1, 64, 256)
+    prev = mmq.mmq_profile_enable(True)
+    try:
+        for M in (4, 40):
+            mmq.mmq_project(rows(1, M, 256, "f16"), w.bytes, "q4_k", 64)
+        mmq.mmq_project_backward(rows(1, 4, 64, "f16"), w.bytes, "q4_k", 256)
+        torch.cuda.synchronize()
+        names = mmq.mmq_profile_read(reset=True)
+    finally:
+        mmq.mmq_profile_enable(prev)
+    assert {"k_ffn_rows", "k_ffn_stream", "k_ffn_tile", "k_ffn_gradients", "k_ffn_tile_back"} <= set(names)
