@@ -73,7 +73,9 @@ struct Stream {
     CUtensorMap map[2];            // of the weight matrices, where rows begin on 16 bytes
     const uint8_t* w[2];
     long long row_bytes;           // of a weight row
-    const uint8_t* x;              // the rows' tiles
+    const void* rows;              // x where it is held in shared memory, else
+    long long rows_stride;
+    const uint8_t* x;              // its tiles
     long long x_term;
     const uint8_t* sums;           // Q4_K, Q5_K: the blocks' sums
     const float* up;

@@ -120,14 +120,17 @@ int stream(const Call& c, cudaStream_t s) {
     }
     // shared memory: all of x where two places of every ring are left beside it (else the SM's cache has the rest)
     const int place = STREAM_WARPS * STREAM_SLAB * a.slot;
-    const long long x_bytes = ceil_div(c.K, STEP) * a.xgroups * 1024 * terms;
+    const long long term = ceil_div(c.K, STEP) * a.xgroups * 1024, sums = is_kquant(c.fmt) ? (long long)a.chunks * a.xgroups * 256 : 0;
+    const long long x_bytes = ceil_div(c.K, STEP) * c.M * 128 * terms + sums;  // held: the rows that there are
     a.held = x_bytes <= SMEM_MOST - 2 * place;
     a.rs = (int)((a.held ? SMEM_MOST - x_bytes : 200 * 1024) / place);
     a.rs = a.rs > R_MOST ? R_MOST : a.rs;
     const int smem = place * a.rs + (a.held ? (int)x_bytes : 0);
     if (a.aligned && !weight_maps(c, a.map, a.row_bytes, STREAM_SLAB)) return MMQ_ERR_CUDA;
 
-    const long long term = ceil_div(c.K, STEP) * a.xgroups * 1024, sums = is_kquant(c.fmt) ? (long long)a.chunks * a.xgroups * 256 : 0;
+    a.rows = c.x;
+    a.rows_stride = c.x_stride;
+    if (a.held) return ffn_stream_launch(c.fmt, a, smem, (int)ctas, true, c.fn, s);
     Rows r = rows_of(c, a.xgroups);
     int st = ffn_stream_launch(c.fmt, a, smem, (int)ctas, false, c.fn, s);
     void* scratch = nullptr;

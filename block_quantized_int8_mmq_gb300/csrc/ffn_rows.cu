@@ -6,23 +6,12 @@
 // scaling; f32 rows in two terms) in the order in which the tensor cores read them: per 64 values and 8 rows 1024
 // bytes, a row 128 of them, its 16-byte pieces exchanged by the row's number (piece c at c ^ row: 128-byte swizzle).  `up` takes the scaling back, and the 2^8 of the weights.
 // HBM-bound.  f16 rows are operands as they are: no scaling, so they are cut at will.
-#include "ffn.cuh"
-#include "kv.cuh"
-#include "umma.cuh"
+#include "ffn_rows.cuh"
 
 namespace mmq {
 namespace {
 
 using namespace ffn;
-
-struct Scale {
-    float down, up;
-};
-__device__ __forceinline__ Scale row_scale(float amax) {
-    // biased exponent; NaN and infinity count as the largest
-    const int e = max(22, min(254, (int)((__float_as_uint(amax) >> 23) & 255)));
-    return {__uint_as_float((uint32_t)(267 - e) << 23), __uint_as_float((uint32_t)(e - 21) << 23)};
-}
 
 template <int THREADS>
 __device__ __forceinline__ float max_cta(float v, float* scratch) {
@@ -36,50 +25,9 @@ __device__ __forceinline__ float max_cta(float v, float* scratch) {
     return v;
 }
 
-// Eight values of a row to their place(s).
-__device__ __forceinline__ void put(const Rows& r, int m, int step, int chunk, const float (&v)[8], float down) {
-    uint8_t* p = r.tiles + ((long long)step * r.groups + (m >> 3)) * 1024 + (m & 7) * 128 + ((chunk ^ (m & 7)) << 4);
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i] * down, b = v[2 * i + 1] * down;
-        const __half2 h = __floats2half2_rn(a, b);
-        const float2 back = __half22float2(h);
-        hi[i] = umma::h2_bits(h);
-        lo[i] = umma::h2_bits(__floats2half2_rn(a - back.x, b - back.y));
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if (r.dtype == MMQ_F32) *reinterpret_cast<uint4*>(p + r.term) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-}
-
-// The sum of a block of 32 values, held by four neighbouring threads, in two f16 terms, times 2^-6 so that they fit:
-// in the order in which k_ffn_stream's product takes them, per 256 values and eight rows 256 bytes.
-__device__ __forceinline__ void put_sum(const Rows& r, int m, int run, const float (&v)[8], float down) {
-    float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    if (run & 3) return;
-    s *= down * 0x1p-6f;
-    const int block = run >> 2, j = block & 7;
-    uint8_t* p = r.sums + (((long long)(block >> 3) * r.groups + (m >> 3)) * 32 + (m & 7) * 4 + (j >> 1)) * 8 + (j & 1) * 2;
-    const __half hi = __float2half_rn(s);
-    *reinterpret_cast<__half*>(p) = hi;
-    *reinterpret_cast<__half*>(p + 4) = __float2half_rn(s - __half2float(hi));
-}
-
 __device__ __forceinline__ void clear_counters(const Rows& r) {
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < r.n_counters; i += blockDim.x) r.counters[i] = 0u;
-}
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-    if (sizeof(T) == 2) {
-        kv::load_run<T, 8>(p, v);
-    } else {
-        const float4 a = kv::Elem<T>::load4(p), b = kv::Elem<T>::load4(p + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
 }
 
 // A CTA per row (f16 rows: several), a thread per run of eight values; eight neighbouring threads write a line.
@@ -127,7 +75,7 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
         const int c = first + i * step;
         if (c < places) {
             put(r, m, c >> 3, c & 7, held[i], down);
-            if (r.sums) put_sum(r, m, c, held[i], down);  // (whole warps: K is a multiple of 256 then)
+            if (r.sums) put_sum(r.sums, r.groups, m, c, held[i], down);  // (whole warps: K is a multiple of 256 then)
         }
     }
 #pragma unroll 4
@@ -135,7 +83,7 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (c < runs) load8(x + 8ll * c, v);
         put(r, m, c >> 3, c & 7, v, down);
-        if (r.sums) put_sum(r, m, c, v, down);
+        if (r.sums) put_sum(r.sums, r.groups, m, c, v, down);
     }
 }
 

@@ -12,8 +12,8 @@
 //
 // A CTA is `groups` runs of 16 weight rows (gate and up of the same columns are two) times `splits` shares of the
 // reduction, added up in shared memory in their order.
+#include "ffn_rows.cuh"
 #include "ffn_weights.cuh"
-#include "kv.cuh"
 
 namespace mmq {
 namespace {
@@ -53,19 +53,17 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     constexpr int CB = chunk_bytes(FMT);
     constexpr bool MINS = is_kquant(FMT), ROWS = !MINS;  // ROWS: rows may be off 16 bytes
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[WARPS * R_MOST + 1];
+    __shared__ __align__(8) uint64_t s_bar[WARPS * R_MOST];
     __shared__ int s_abort;
+    __shared__ unsigned s_top[STREAM_ROWS];  // HELD: bits of the rows' largest magnitudes
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int g = lane >> 2, t = lane & 3;
     const int group = wid / a.splits, split = wid - group * a.splits;
     const bool works = group < a.groups;
     const uint32_t bars = ptx::smem_u32(s_bar) + 8 * wid * R_MOST;
     if (lane < a.rs) ptx::mbar_init(bars + 8 * lane, a.aligned ? 1 : 32);
-    const uint32_t x_bar = ptx::smem_u32(s_bar) + 8 * WARPS * R_MOST;
-    if (tid == 0) {
-        s_abort = 0;
-        ptx::mbar_init(x_bar, 1);
-    }
+    if (tid == 0) s_abort = 0;
+    if (tid < STREAM_ROWS) s_top[tid] = 0u;
     ptx::fence_barrier_init();
     __syncthreads();
     ptx::grid_dep_launch_dependents();
@@ -80,10 +78,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     const int c1 = works && n0 < a.N ? (int)((long long)a.chunks * (split + 1) / a.splits) : 0;
     const int stage = SLAB * a.slot;
     uint8_t* ring = smem + wid * a.rs * stage;
-    int asked = c0, put = 0;
+    int asked = c0, f_slot = 0;
     auto fetch = [&]() {
         if (asked >= c1) return;
-        const uint32_t bar = bars + 8 * put, dst = ptx::smem_u32(ring) + put * stage;
+        const uint32_t bar = bars + 8 * f_slot, dst = ptx::smem_u32(ring) + f_slot * stage;
         if (!ROWS || a.aligned) {
             if (ptx::elect_one()) {
                 ptx::mbar_arrive_expect_tx(bar, SLAB * CB);
@@ -106,7 +104,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             cp_async_arrive(bar);
         }
         ++asked;
-        if (++put == a.rs) put = 0;
+        if (++f_slot == a.rs) f_slot = 0;
     };
     for (int i = 0; i < a.rs; ++i) fetch();
 
@@ -116,28 +114,57 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     ptx::grid_dep_wait();  // the rows are laid out
-    // HELD: all of the rows' tiles in shared memory, after the rings, by one warp's bulk copies (a step of 64 values each)
+    // HELD: all of x in shared memory, after the rings, laid out here while the first weights are on their way; so there
+    // is no other kernel and no memory beside
     const int x_steps = (a.K + STEP - 1) / STEP;
     uint8_t* x_held = smem + WARPS * a.rs * stage;
+    const int x_step = HELD ? a.M * 128 : NT * 1024;  // bytes of a step's rows (held: only those that there are)
+    const long long x_term = HELD ? (long long)x_steps * x_step : a.x_term;
+    uint8_t* held_sums = x_held + x_term * TERMS;
     if (HELD) {
-        const int bytes = NT * 1024;
-        if (wid == 0) {
-            if (lane == 0) ptx::mbar_arrive_expect_tx(x_bar, x_steps * bytes * TERMS);
-            __syncwarp();
-            const int run = (x_steps + 31) / 32, i0 = min(x_steps, lane * run), i1 = min(x_steps, i0 + run);
-            if (i1 > i0)
+        const int runs = a.K / 8, places = x_steps * 8;
+        auto lay_out = [&](auto type) {
+            using T = decltype(type);
+            constexpr bool SCALED = !std::is_same<T, __half>::value;
+            const T* x = static_cast<const T*>(a.rows);
+            if (SCALED) {
+                for (int m = 0; m < a.M; ++m) {
+                    float top = 0.f;
+                    for (int c = tid; c < runs; c += 32 * WARPS) {
+                        float v[8];
+                        load8(x + m * a.rows_stride + 8ll * c, v);
 #pragma unroll
-                for (int e = 0; e < TERMS; ++e)
-                    ptx::bulk_load(ptx::smem_u32(x_held) + (e * x_steps + i0) * bytes, a.x + e * a.x_term + (long long)i0 * bytes,
-                                   (i1 - i0) * bytes, x_bar);
-        }
+                        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
+                    }
+                    const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // (magnitudes order as their bits)
+                    if (lane == 0 && bits) atomicMax(&s_top[m], bits);
+                }
+                __syncthreads();
+            }
+            for (int m = 0; m < a.M; ++m) {
+                const float down = SCALED ? row_scale(__uint_as_float(s_top[m])).down : 1.f;
+                for (int c = tid; c < places; c += 32 * WARPS) {
+                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (c < runs) load8(x + m * a.rows_stride + 8ll * c, v);
+                    put_at(x_held + (c >> 3) * x_step + m * 128 + (((c ^ m) & 7) << 4), x_term, TERMS == 2, v, down);
+                    if (MINS) put_sum(held_sums, NT, m, c, v, down);  // (whole warps: K is a multiple of 256 then)
+                }
+            }
+            __syncthreads();
+        };
+        if (TERMS == 2)
+            lay_out(float{});
+        else if (a.dtype == MMQ_BF16)
+            lay_out(__nv_bfloat16{});
+        else
+            lay_out(__half{});
     }
+    const uint8_t* x_sums = HELD ? held_sums : a.sums;
     // x for this lane, AHEAD blocks of 32 values at a time and as many ahead of their use: 16 bytes a block and term (Q6_K:
     // two of 8, of its two halves).  Measured one block ahead, from L2: most of a decode's cycles waited for it.
     constexpr int AHEAD = HELD ? 1 : 4 / (NT * TERMS);
     const int x_lane = FMT == FMT_Q6_K ? g * 128 + (((t >> 1) ^ g) << 4) + (t & 1) * 8 : g * 128 + ((t ^ g) << 4);
     const uint8_t* xt = HELD ? x_held : a.x;
-    const long long x_term = HELD ? (long long)x_steps * NT * 1024 : a.x_term;
     const int b_end = min(8 * c1, a.K / QK);
     const int lane_rows = g < a.M ? g + 8 < a.M ? 2 : 1 : 0;  // rows of x that this lane reads: g, g + 8
     uint4 xv[2][AHEAD][NT][TERMS];
@@ -148,7 +175,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
         for (int i = 0; i < AHEAD; ++i) {
             if (block + i >= b_end || lane_rows == 0) break;
             const int at = x_lane ^ ((block + i) & 1) * 64;  // (pieces 4 .. 7 of a step)
-            const uint8_t* p = xt + (long long)((block + i) >> 1) * (NT * 1024);
+            const uint8_t* p = xt + (long long)((block + i) >> 1) * x_step;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 if (n >= lane_rows) break;
@@ -183,8 +210,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     int st = 0;
     uint32_t par = 0;
     bool ok = true;
-    if (HELD) ok = umma::warp_wait(x_bar, 0, abort, err);
-    if (ok) load_x(8 * c0, xv[0]);
+    load_x(8 * c0, xv[0]);
 #pragma unroll 1
     for (int c = c0; c < c1 && ok; ++c) {
         if (!umma::warp_wait(bars + 8 * st, par, abort, err)) {
@@ -201,7 +227,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             uint2 xs[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                xs[n] = __ldg(reinterpret_cast<const uint2*>(a.sums + (((long long)c * a.xgroups + n) * 32 + lane) * 8));
+                xs[n] = *reinterpret_cast<const uint2*>(x_sums + (((long long)c * NT + n) * 32 + lane) * 8);
             uint4 head[2];
             uint32_t sc[2][2], mn[2][2];
 #pragma unroll
@@ -360,7 +386,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
         }
     }
     if (ROWS) cp_async_wait_all();
-    if (HELD && !ok && wid == 0) umma::drain_bar(x_bar, 0, err);
     if (!ok && (!ROWS || a.aligned))  // let the boxes in flight land before the shared memory goes
         for (int i = 0; i < a.rs; ++i) {
             const int n = asked - c0;
@@ -382,7 +407,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             const int n = (blockIdx.x * per + run) * SLAB + k;
             if (n >= a.N) continue;
             const long long at = (long long)m * a.N + n;
-            const float up = __ldg(a.up + m) * 256.f;  // (times the weights' 2^8, which these weights have not)
+            // (the weights' 2^8, which `up` takes back, these weights have not)
+            const float up = (!HELD ? __ldg(a.up + m) : TERMS == 1 && a.dtype == MMQ_F16 ? 1.f / 256.f : row_scale(__uint_as_float(s_top[m])).up) * 256.f;
             float z[2] = {0.f, 0.f};
             for (int w = 0; w < a.mats; ++w) {
                 for (int s = 0; s < a.splits; ++s) z[w] += sums[(((w * per + run) * a.splits + s) * 8 * NT + m) * SLAB + k];
