@@ -10,35 +10,55 @@ using namespace ffn;
 constexpr long long up_to(long long n, long long unit) { return (n + unit - 1) / unit * unit; }
 constexpr long long ceil_div(long long n, long long d) { return (n + d - 1) / d; }
 
-// Times in us, for the choice between whole and cut units.  A chunk: its products at the tensor rate, or its weights'
-// way to f16 where that takes longer (measured a 64-value step of 256 weight rows: 16-bit rows 0.55, backward 0.4, of Q6_K 0.9, f32
-// rows 1.1).  What cutting costs: parts of nt x 256 sums written and read back, and a counter's trip (measured at 192 rows 14).
-struct Cost {
-    double chunk, join;
+// How the products of many rows are dealt out: rows of a tile; rounds of whole units, then `rest` units laid end to end
+// and cut into `ctas` equal runs of chunks.
+struct Deal {
+    int nt = 0, mtiles = 0, units = 0, rounds = 0, rest = 0, ctas = 0;
+    double us = 0;
 };
-Cost cost(const Tile& a, int fmt, bool split, bool back) {
-    const double pieces = back ? 1 : CHUNK / STEP;
-    const double weights = split ? 1.1 : fmt == FMT_Q6_K ? 0.9 : back ? 0.4 : 0.55;
-    const double products = 8 * (split ? 3 : 1) * (a.nt < 64 ? 64 : a.nt) / 2 / 1900.0;
-    return {pieces * (weights > products ? weights : products), 3.0 + a.nt * 0.06};
-}
 
-// Rounds of whole units; or, where the last round leaves too much undone, it and the one before it cut evenly.
-int deal(Tile& a, const Cost& t, int sms) {
-    const long long whole = ceil_div(a.units, sms) * a.chunks;
-    const long long full = a.units % sms == 0 ? a.units / sms : a.units < sms ? 0 : a.units / sms - 1;
-    const long long rest = a.units - full * sms;
-    if (rest > 0) {
-        const double cut = full * a.chunks + (double)ceil_div(rest * a.chunks, sms);
-        if (cut * t.chunk + t.join < 0.93 * whole * t.chunk) {
-            a.rounds = (int)full;
-            a.rest = (int)rest;
-            return (int)(rest * a.chunks < sms ? rest * a.chunks : sms);
+// The cheapest deal by times measured on GB300 (us).  A chunk: its products at the tensor rate, or its weights' way to f16
+// where that takes longer (a 64-value step of 256 weight rows: 16-bit rows 0.55, backward 0.4, of Q6_K 0.9, f32 rows
+// 1.1).  A unit's output 1.5 and 0.02 for each row of x.  What cutting costs: a counter's trip, 3, and a part written and
+// `parts` read back by the last to arrive, 0.02 for each row and part (525 x 469 x 9472 in 25 parts a unit: 85 of 106 us).
+// Smaller tiles are more units, which share fewer parts each but turn the same weights to f16 on more SMs.
+Deal deal(long long M, long long pairs, int chunks, double pieces, int nt_most, int fmt, bool split, bool back, int sms) {
+    Deal best;
+    const double weights = split ? 1.1 : fmt == FMT_Q6_K ? 0.9 : back ? 0.4 : 0.55;
+    const long long least = ceil_div(M, nt_most);
+    for (long long k = least; k < least + 12 && k <= ceil_div(M, 16); ++k) {
+        Deal d;
+        d.nt = (int)up_to(ceil_div(M, k), 16);
+        d.mtiles = (int)ceil_div(M, d.nt);
+        if (d.mtiles != k) continue;  // (another tile's size again)
+        const long long units = d.mtiles * pairs;
+        d.units = (int)units;
+        const double products = 8 * (split ? 3 : 1) * (d.nt < 64 ? 64 : d.nt) / 2 / 1900.0;
+        const double chunk = pieces * (weights > products ? weights : products), output = 1.5 + 0.02 * d.nt;
+        auto take = [&](long long rounds, long long rest, long long ctas, double us) {
+            if (best.ctas && us >= best.us) return;
+            d.rounds = (int)rounds;
+            d.rest = (int)rest;
+            d.ctas = (int)ctas;
+            d.us = us;
+            best = d;
+        };
+        const long long whole = ceil_div(units, sms);
+        take(whole, 0, units < sms ? units : sms, whole * (chunks * chunk + output));
+        if (units % sms == 0) continue;
+        // what does not fill the SMs, with the round before it, is cut
+        const long long full = units < sms ? 0 : units / sms - 1, rest = units - full * sms;
+        for (int p = 1; p <= 24; ++p) {
+            long long ctas = units > sms || rest * p > sms ? sms : rest * p;
+            if (ctas > rest * chunks) ctas = rest * chunks;
+            const double parts = 1.0 + (double)ctas / (double)rest;
+            const double us = full * (chunks * chunk + output) + (double)ceil_div(rest * chunks, ctas) * chunk + output + 3.0 +
+                              0.02 * d.nt * (1.0 + parts);
+            if (ctas != rest) take(full, rest, ctas, us);
+            if (ctas == sms || ctas == rest * chunks) break;
         }
     }
-    a.rounds = (int)ceil_div(a.units, sms);
-    a.rest = 0;
-    return (int)(a.units < sms ? a.units : sms);
+    return best;
 }
 
 // scratch_alloc, but under capture the graph's own memory without the library's pool, which cannot be made there: so a
@@ -172,13 +192,18 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     const int left = SMEM_MOST - (c.backward ? 2 * terms * Shape<true, true>::A_BYTES : 0);
     int nt_most = split ? Shape<true, false>::NT : Shape<false, false>::NT;
     while ((left - 2 * w_bytes) / (nt_most * 128 * terms) < 2) nt_most -= 16;
-    a.nt = (int)up_to(ceil_div(c.M, ceil_div(c.M, nt_most)), 16);
-    a.mtiles = (int)ceil_div(c.M, a.nt);
-    a.units = (int)(a.mtiles * ceil_div(a.width, !c.backward && c.mats == 2 ? 128 : 256));
-    a.sub = !c.backward && !split && a.nt <= Shape<false, false, 2>::NT && c.K % (2 * STEP) == 0 ? 2 : 1;
     const int pieces = (int)(c.backward ? c.mats * ceil_div(c.N, STEP) : ceil_div(c.K, STEP));  // of 64 values
+    a.chunks = c.backward ? pieces : (int)ceil_div(c.K, CHUNK);
+    const Deal d = deal(c.M, ceil_div(a.width, !c.backward && c.mats == 2 ? 128 : 256), a.chunks, c.backward ? 1 : CHUNK / STEP,
+                        nt_most, c.fmt, split, c.backward, device_shape().sms);
+    a.nt = d.nt;
+    a.mtiles = d.mtiles;
+    a.units = d.units;
+    a.rounds = d.rounds;
+    a.rest = d.rest;
+    const int ctas = d.ctas;
+    a.sub = !c.backward && !split && a.nt <= Shape<false, false, 2>::NT && c.K % (2 * STEP) == 0 ? 2 : 1;
     a.steps = pieces / a.sub;
-    a.chunks = c.backward ? a.steps : (int)ceil_div(c.K, CHUNK);
     a.dtype = c.dtype;
     a.act = c.act;
     for (int g = 0; g < 2; ++g) {
@@ -188,7 +213,6 @@ int ffn_launch(const Call& c, cudaStream_t s) {
     a.residual = c.residual;
     a.residual_stride = c.residual_stride;
     a.out = c.out;
-    const int ctas = deal(a, cost(a, c.fmt, split, c.backward), device_shape().sms);
     // shared memory: two chunks' places and two steps of rows at least, then four places, four steps, more places
     const int x_bytes = a.nt * 128 * terms * a.sub;
     auto steps_left = [&](int places) { return (left - places * w_bytes) / x_bytes; };
