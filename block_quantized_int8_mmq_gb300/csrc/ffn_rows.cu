@@ -31,6 +31,7 @@ __device__ __forceinline__ void clear_counters(const Rows& r) {
 }
 
 // A CTA per row (f16 rows: several), a thread per run of eight values; eight neighbouring threads write a line.
+constexpr int GRADIENT_THREADS = 256;
 constexpr int HELD = 5;  // runs a thread keeps between looking for the largest value and writing
 
 template <typename T, int THREADS>
@@ -87,15 +88,22 @@ __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
     }
 }
 
-// Eight values from an address that is aligned to its elements, as one load where it is aligned to 16 bytes.
+// Eight values as they lie, from an address that is aligned to its elements, as one load where it is aligned to 16 bytes.
 template <typename T>
-__device__ __forceinline__ void get8(const T* p, int left, bool vector, float (&v)[8]) {
+struct Run {
+    alignas(16) T v[8];
+};
+template <typename T>
+__device__ __forceinline__ void get8(const T* p, int left, bool vector, Run<T>& r) {
     if (vector && left >= 8) {
-        load8(p, v);
+        const uint4* q = reinterpret_cast<const uint4*>(p);
+        uint4* to = reinterpret_cast<uint4*>(r.v);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) to[i] = q[i];
         return;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < left ? get_one(p + k) : 0.f;
+    for (int k = 0; k < 8; ++k) r.v[k] = k < left ? p[k] : T(0.f);
 }
 template <typename T>
 __device__ __forceinline__ void put8(T* p, int left, bool vector, const float (&v)[8]) {
@@ -113,17 +121,40 @@ __device__ __forceinline__ void put8(T* p, int left, bool vector, const float (&
         if (k < left) put_one(p + k, v[k]);
 }
 
-// A CTA per row.  KEEP: the gradients stay in shared memory between looking for the largest and writing (f32, 8 bytes a value
-// of the gated block); rows that are too wide for that are formed twice.  Measured on 2048 rows of 18944, gated: formed
-// twice 198 us, kept 152.
-template <typename T, int THREADS, bool KEEP>
-__global__ void __launch_bounds__(THREADS) k_ffn_gradients(const Rows r) {
+// The largest of a cluster of CTAS, which every one of them reads where its own stands: no peer's memory is touched once
+// the second barrier is behind, so that a CTA may end.
+template <int CTAS>
+__device__ __forceinline__ float max_cluster(float v, float* s_all) {
+    if (CTAS == 1) return v;
+    const uint32_t here = ptx::smem_u32(s_all + blockIdx.x % CTAS);
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // every peer has begun
+    if (threadIdx.x < CTAS) {
+        uint32_t there;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
+    }
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < CTAS; ++i) v = fmaxf(v, s_all[i]);
+    return v;
+}
+
+// CTAS CTAs per row, a cluster, each its share of whole steps.  KEEP: the gradients stay in shared memory between looking for
+// the largest and writing (f32, 8 bytes a value of the gated block); rows that are too wide for that are formed twice.
+// Four CTAs on an SM, so that one's loads go on while another waits for its row's largest.  Measured on 2048 bf16 rows of
+// 18944, gated, 543 MB: formed twice 198 us, kept by one CTA a row 152, by a cluster of four 151, with the next run's loads
+// under way while one is formed 123 (4.4 TB/s; its bound is what is in flight: at five CTAs of 48 registers it spills, 265).
+template <typename T, bool KEEP, int CTAS>
+__global__ void __launch_bounds__(GRADIENT_THREADS) k_ffn_gradients(const Rows r) {
+    constexpr int THREADS = GRADIENT_THREADS;
     extern __shared__ __align__(16) float s_keep[];
-    __shared__ float s_max[THREADS / 32];
+    __shared__ float s_max[THREADS / 32], s_all[CTAS];
+    if (CTAS > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     ptx::grid_dep_wait();
     ptx::grid_dep_launch_dependents();
     clear_counters(r);
-    const int m = blockIdx.x, N = r.width, steps = (N + 63) / 64;
+    const int m = blockIdx.x / CTAS, N = r.width, steps = (N + 63) / 64, share = (steps + CTAS - 1) / CTAS;
+    const int first = blockIdx.x % CTAS * share, last = min(steps, first + share);
     const long long at = (long long)m * N;
     const T* x = static_cast<const T*>(r.x) + m * r.stride;
     const T* pre[2] = {nullptr, nullptr};
@@ -135,45 +166,56 @@ __global__ void __launch_bounds__(THREADS) k_ffn_gradients(const Rows r) {
     auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
     const bool vx = aligned(x), v0 = aligned(pre[0]), v1 = aligned(pre[1]), w0 = aligned(dz[0]), w1 = aligned(dz[1]);
     with_act(r.pre[0] ? r.act : MMQ_ACT_NONE, [&](auto A) {
-        // the gradients of values n .. n + 7, 0 past the row
-        auto form = [&](int n, auto fast, float (&g)[8], float (&u)[8]) {
-            const int left = N - n;
-            float z[8], y[8];
-            get8(x + n, left, vx, g);
-            if (r.pre[0]) get8(pre[0] + n, left, v0, z);
-            if (r.mats == 2) get8(pre[1] + n, left, v1, y);
-            if (!r.pre[0]) return;
+        struct Values {
+            Run<T> x, pre, up;
+        };
+        auto load = [&](int n, Values& in) {
+            get8(x + n, N - n, vx, in.x);
+            if (r.pre[0]) get8(pre[0] + n, N - n, v0, in.pre);
+            if (r.mats == 2) get8(pre[1] + n, N - n, v1, in.up);
+        };
+        // the gradients of a run, 0 past the row
+        auto form = [&](const Values& in, auto fast, float (&g)[8], float (&u)[8]) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
+                g[k] = (float)in.x.v[k];
+                if (!r.pre[0]) continue;
                 float a, d;
-                activate<decltype(A)::value, decltype(fast)::value>(z[k], a, d);
+                activate<decltype(A)::value, decltype(fast)::value>((float)in.pre.v[k], a, d);
                 u[k] = g[k] * a;
                 g[k] *= d;
-                if (r.mats == 2) g[k] *= y[k];
+                if (r.mats == 2) g[k] *= (float)in.up.v[k];
             }
         };
         float amax = 0.f, g[8], u[8];
-        float* keep_u = s_keep + steps * STEP;
+        float* keep_u = s_keep + share * STEP;
+        Values in, next;  // the next run's loads are under way while one is formed
+        if (first * 8 + (int)threadIdx.x < last * 8) load(8 * (first * 8 + threadIdx.x), in);
 #pragma unroll 1
-        for (int c = threadIdx.x; c < steps * 8; c += THREADS) {
+        for (int c = first * 8 + threadIdx.x; c < last * 8; c += THREADS) {
+            const int kept = 8 * (c - first * 8);
+            if (c + THREADS < last * 8) load(8 * (c + THREADS), next);
             // (where the row is formed again the largest value's exponent is all that is wanted)
-            form(8 * c, std::integral_constant<bool, !KEEP || sizeof(T) == 2>{}, g, u);
+            form(in, std::integral_constant<bool, !KEEP || sizeof(T) == 2>{}, g, u);
+            in = next;
 #pragma unroll
             for (int k = 0; k < 8; ++k) amax = fmaxf(amax, r.mats == 2 ? fmaxf(fabsf(g[k]), fabsf(u[k])) : fabsf(g[k]));
             if (KEEP) {
-                put8(s_keep + 8 * c, 8, true, g);
-                if (r.mats == 2) put8(keep_u + 8 * c, 8, true, u);
+                put8(s_keep + kept, 8, true, g);
+                if (r.mats == 2) put8(keep_u + kept, 8, true, u);
             }
         }
-        const Scale s = row_scale(max_cta<THREADS>(amax, s_max));
-        if (threadIdx.x == 0) r.up[m] = s.up;
+        const Scale s = row_scale(max_cluster<CTAS>(max_cta<THREADS>(amax, s_max), s_all));
+        if (first == 0 && threadIdx.x == 0) r.up[m] = s.up;
 #pragma unroll 1
-        for (int c = threadIdx.x; c < steps * 8; c += THREADS) {
+        for (int c = first * 8 + threadIdx.x; c < last * 8; c += THREADS) {
+            const int kept = 8 * (c - first * 8);
             if (KEEP) {
-                load8(s_keep + 8 * c, g);
-                if (r.mats == 2) load8(keep_u + 8 * c, u);
+                load8(s_keep + kept, g);
+                if (r.mats == 2) load8(keep_u + kept, u);
             } else {
-                form(8 * c, std::integral_constant<bool, sizeof(T) == 2>{}, g, u);
+                load(8 * c, in);
+                form(in, std::integral_constant<bool, sizeof(T) == 2>{}, g, u);
             }
             put(r, m, c >> 3, c & 7, g, s.down);
             if (r.mats == 2) put(r, m, steps + (c >> 3), c & 7, u, s.down);
@@ -183,12 +225,12 @@ __global__ void __launch_bounds__(THREADS) k_ffn_gradients(const Rows r) {
     });
 }
 
-constexpr int KEEP_MOST = 200 * 1024;
+constexpr int KEEP_MOST = 50 * 1024;  // of a CTA, so that four share an SM
 
-template <typename T, int THREADS, bool KEEP>
+template <typename T, bool KEEP, int CTAS>
 int gradients(const Rows& r, int smem, bool go, const char* fn, cudaStream_t s) {
     static SmemAttr attr;
-    auto k = &k_ffn_gradients<T, THREADS, KEEP>;
+    auto k = &k_ffn_gradients<T, KEEP, CTAS>;
     if (smem > 48 * 1024)
         if (const int st = ensure_smem(reinterpret_cast<const void*>(k), KEEP_MOST, attr)) {
             report(fn, st, "the gradients' shared memory was refused");
@@ -196,7 +238,19 @@ int gradients(const Rows& r, int smem, bool go, const char* fn, cudaStream_t s) 
         }
     if (!go) return MMQ_OK;
     ProfScope ps("k_ffn_gradients", s);
-    return pdl_status(launch_pdl(k, dim3((unsigned)r.rows), dim3(THREADS), smem, s, r), fn);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(r.rows * CTAS));
+    cfg.blockDim = dim3(GRADIENT_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim = {CTAS, 1, 1};
+    cfg.attrs = attrs;
+    cfg.numAttrs = CTAS > 1 ? 2 : 1;
+    return pdl_status(cudaLaunchKernelEx(&cfg, k, r), fn);
 }
 
 template <typename T, int THREADS>
@@ -211,9 +265,11 @@ int rows(const Rows& r, const char* fn, cudaStream_t s) {
 template <typename T>
 int launch(const Rows& r, bool back, bool go, const char* fn, cudaStream_t s) {
     if (back) {
-        const int keep = (r.width + STEP - 1) / STEP * STEP * 4 * r.mats;
-        if (r.width <= 4096) return gradients<T, 256, true>(r, keep, go, fn, s);
-        return keep <= KEEP_MOST ? gradients<T, 1024, true>(r, keep, go, fn, s) : gradients<T, 256, false>(r, 0, go, fn, s);
+        constexpr int CTAS = 4;
+        const int steps = (r.width + STEP - 1) / STEP, keep = STEP * 4 * r.mats;
+        if (r.width <= 4096) return gradients<T, true, 1>(r, steps * keep, go, fn, s);
+        const int each = (steps + CTAS - 1) / CTAS * keep;
+        return each <= KEEP_MOST ? gradients<T, true, CTAS>(r, each, go, fn, s) : gradients<T, false, CTAS>(r, 0, go, fn, s);
     }
     if (!go) return MMQ_OK;
     // a narrow row in small CTAs where there are many; one row's latency in a large one
