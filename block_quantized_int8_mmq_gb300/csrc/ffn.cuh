@@ -81,6 +81,7 @@ struct Stream {
     const float* up;
     int mats, M, N, K, chunks, xgroups;  // xgroups: of 8 rows
     int groups, splits;            // of a CTA: runs of 16 weight rows, shares of the reduction
+    int cluster;                   // CTAs that share the same runs' reduction
     int aligned, slot, rs, held;   // bytes of a chunk's row in shared memory, places of a warp's ring, whether x is held there too
     int dtype, act;
     const float* bias[2];

@@ -126,18 +126,22 @@ int stream(const Call& c, cudaStream_t s) {
     a.residual = c.residual;
     a.residual_stride = c.residual_stride;
     a.out = c.out;
-    // Column runs of a CTA and shares of the reduction: the fewest chunks in a row, a wave's start counted as two.
+    // Column runs of a CTA, shares of the reduction in it, CTAs that share one: the fewest chunks in a row, a wave's start
+    // counted as two and the cluster's meeting as one.  (Clusters of four and eight leave some of a GPC's SMs out.)
     const long long runs = ceil_div(c.N, STREAM_SLAB), sms = device_shape().sms;
     long long best = 0, ctas = 0;
-    for (int per = 1; per * c.mats <= STREAM_WARPS; ++per) {
-        const int splits = STREAM_WARPS / (per * c.mats);
-        const long long n = ceil_div(runs, per), time = ceil_div(n, sms) * (ceil_div(a.chunks, splits) + 2);
-        if (best && time >= best) continue;
-        best = time;
-        ctas = n;
-        a.groups = per * c.mats;
-        a.splits = splits;
-    }
+    for (int cluster = 1; cluster <= 8; cluster *= 2)
+        for (int per = 1; per * c.mats <= STREAM_WARPS; ++per) {
+            const int splits = STREAM_WARPS / (per * c.mats);
+            const long long n = ceil_div(runs, per) * cluster, fit = cluster > 2 ? sms * 5 / 6 : sms;
+            const long long time = ceil_div(n, fit) * (ceil_div(a.chunks, splits * cluster) + 2 + (cluster > 1));
+            if (best && time >= best) continue;
+            best = time;
+            ctas = n;
+            a.groups = per * c.mats;
+            a.splits = splits;
+            a.cluster = cluster;
+        }
     // shared memory: all of x where two places of every ring are left beside it (else the SM's cache has the rest)
     const int place = STREAM_WARPS * STREAM_SLAB * a.slot;
     const long long term = ceil_div(c.K, STEP) * a.xgroups * 1024, sums = is_kquant(c.fmt) ? (long long)a.chunks * a.xgroups * 256 : 0;

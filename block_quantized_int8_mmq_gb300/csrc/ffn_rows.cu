@@ -238,19 +238,7 @@ int gradients(const Rows& r, int smem, bool go, const char* fn, cudaStream_t s) 
         }
     if (!go) return MMQ_OK;
     ProfScope ps("k_ffn_gradients", s);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(r.rows * CTAS));
-    cfg.blockDim = dim3(GRADIENT_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attrs[2];
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim = {CTAS, 1, 1};
-    cfg.attrs = attrs;
-    cfg.numAttrs = CTAS > 1 ? 2 : 1;
-    return pdl_status(cudaLaunchKernelEx(&cfg, k, r), fn);
+    return pdl_status(ffn_cluster_launch(k, r.rows * CTAS, GRADIENT_THREADS, CTAS, smem, s, r), fn);
 }
 
 template <typename T, int THREADS>

@@ -7,6 +7,27 @@
 #include "umma.cuh"
 
 namespace mmq {
+// A launch as launch_pdl's, its CTAs in clusters (1: none), of which `ctas` is a multiple.
+template <class Args>
+cudaError_t ffn_cluster_launch(void (*kernel)(Args), int ctas, int threads, int cluster, int smem, cudaStream_t s,
+                               const std::remove_const_t<Args>& args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 namespace ffn {
 
 struct Scale {

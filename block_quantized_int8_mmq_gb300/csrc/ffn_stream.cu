@@ -11,7 +11,9 @@
 // The products leave the tensor core every 32 values (16 for Q6_K).
 //
 // A CTA is `groups` runs of 16 weight rows (gate and up of the same columns are two) times `splits` shares of the
-// reduction, added up in shared memory in their order.
+// reduction, added up in shared memory in their order.  Few columns and a long reduction: a cluster of CTAs shares it, and
+// each adds up its part of the outputs from all of them (9 x 3584 x 18944 of Q6_K 34.7 -> 28.4 us in pairs, on 150 SMs
+// instead of 112; 3 x 333 x 13824 of Q4_K 16 -> 9.8 in fours).
 #include "ffn_rows.cuh"
 #include "ffn_weights.cuh"
 
@@ -34,6 +36,18 @@ __device__ __forceinline__ void mma_fresh(float (&d)[4], const uint32_t (&a)[4],
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// What stands in the shared memory of the cluster's CTA `rank` where p does in this one's.
+__device__ __forceinline__ float peer_value(const float* p, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
 }
 
 // A word at an even byte offset.
@@ -73,9 +87,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     // this warp's rows and chunks
     const int per = a.mats == 2 ? a.groups / 2 : a.groups;       // column runs of a CTA
     const int mat = a.mats == 2 && group >= per ? 1 : 0;
-    const int n0 = (blockIdx.x * per + group - mat * per) * SLAB;
-    const int c0 = works && n0 < a.N ? (int)((long long)a.chunks * split / a.splits) : 0;
-    const int c1 = works && n0 < a.N ? (int)((long long)a.chunks * (split + 1) / a.splits) : 0;
+    const int rank = blockIdx.x % a.cluster, run0 = blockIdx.x / a.cluster * per, shares = a.cluster * a.splits;
+    const int n0 = (run0 + group - mat * per) * SLAB, share = rank * a.splits + split;
+    const int c0 = works && n0 < a.N ? (int)((long long)a.chunks * share / shares) : 0;
+    const int c1 = works && n0 < a.N ? (int)((long long)a.chunks * (share + 1) / shares) : 0;
     const int stage = SLAB * a.slot;
     uint8_t* ring = smem + wid * a.rs * stage;
     int asked = c0, f_slot = 0;
@@ -122,7 +137,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     const long long x_term = HELD ? (long long)x_steps * x_step : a.x_term;
     uint8_t* held_sums = x_held + x_term * TERMS;
     if (HELD) {
+        // a cluster's CTA: its chunks' share of the rows, whose largest is of the whole
         const int runs = a.K / 8, places = x_steps * 8;
+        const int from = (int)((long long)a.chunks * rank / a.cluster) * 32, to = min(places, (int)((long long)a.chunks * (rank + 1) / a.cluster) * 32);
         auto lay_out = [&](auto type) {
             using T = decltype(type);
             constexpr bool SCALED = !std::is_same<T, __half>::value;
@@ -130,6 +147,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             if (SCALED) {
                 for (int m = 0; m < a.M; ++m) {
                     float top = 0.f;
+#pragma unroll 4
                     for (int c = tid; c < runs; c += 32 * WARPS) {
                         float v[8];
                         load8(x + m * a.rows_stride + 8ll * c, v);
@@ -143,7 +161,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             }
             for (int m = 0; m < a.M; ++m) {
                 const float down = SCALED ? row_scale(__uint_as_float(s_top[m])).down : 1.f;
-                for (int c = tid; c < places; c += 32 * WARPS) {
+                for (int c = from + tid; c < to; c += 32 * WARPS) {
                     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     if (c < runs) load8(x + m * a.rows_stride + 8ll * c, v);
                     put_at(x_held + (c >> 3) * x_step + m * 128 + (((c ^ m) & 7) << 4), x_term, TERMS == 2, v, down);
@@ -399,20 +417,28 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
 #pragma unroll
         for (int i = 0; i < 4; ++i) sums[(wid * 8 * NT + 8 * n + 2 * t + (i & 1)) * SLAB + g + 8 * (i >> 1)] = acc[n][i];
     __syncthreads();
-    if (*abort) return;
+    if (a.cluster > 1) cluster_sync();  // (a CTA that gave up comes here too)
+    // the sum of a run's shares at row m and column k
+    auto total = [&](int group, int m, int k) {
+        float z = 0.f;
+        for (int c = 0; c < a.cluster; ++c) {
+            const float* p = sums + (group * a.splits * 8 * NT + m) * SLAB + k;
+            for (int s = 0; s < a.splits; ++s, p += 8 * NT * SLAB) z += a.cluster > 1 ? peer_value(p, c) : *p;
+        }
+        return z;
+    };
     auto output = [&](auto type) {
         using T = decltype(type);
-        for (int i = tid; i < per * a.M * SLAB; i += 32 * WARPS) {
+        for (int i = rank * 32 * WARPS + tid; i < per * a.M * SLAB; i += a.cluster * 32 * WARPS) {
             const int k = i % SLAB, m = i / SLAB % a.M, run = i / SLAB / a.M;
-            const int n = (blockIdx.x * per + run) * SLAB + k;
+            const int n = (run0 + run) * SLAB + k;
             if (n >= a.N) continue;
             const long long at = (long long)m * a.N + n;
             // (the weights' 2^8, which `up` takes back, these weights have not)
             const float up = (!HELD ? __ldg(a.up + m) : TERMS == 1 && a.dtype == MMQ_F16 ? 1.f / 256.f : row_scale(__uint_as_float(s_top[m])).up) * 256.f;
             float z[2] = {0.f, 0.f};
             for (int w = 0; w < a.mats; ++w) {
-                for (int s = 0; s < a.splits; ++s) z[w] += sums[(((w * per + run) * a.splits + s) * 8 * NT + m) * SLAB + k];
-                z[w] = fmaf(z[w], up, a.bias[w] ? __ldg(a.bias[w] + n) : 0.f);
+                z[w] = fmaf(total(w * per + run, m, k), up, a.bias[w] ? __ldg(a.bias[w] + n) : 0.f);
                 if (a.pre[w]) put_one(static_cast<T*>(a.pre[w]) + at, z[w]);
             }
             float y = 0.f;
@@ -425,12 +451,15 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             put_one(static_cast<T*>(a.out) + at, y);
         }
     };
-    if (TERMS == 2)
-        output(float{});
-    else if (a.dtype == MMQ_BF16)
-        output(__nv_bfloat16{});
-    else
-        output(__half{});
+    if (*abort == 0) {
+        if (TERMS == 2)
+            output(float{});
+        else if (a.dtype == MMQ_BF16)
+            output(__nv_bfloat16{});
+        else
+            output(__half{});
+    }
+    if (a.cluster > 1) cluster_sync();  // its sums have been read
 }
 
 template <int FMT, int NT, int TERMS, bool HELD>
@@ -444,7 +473,7 @@ int launch(const Stream& a, int smem, int ctas, bool go, const char* fn, cudaStr
     }
     if (!go) return MMQ_OK;
     ProfScope ps("k_ffn_stream", s);
-    return pdl_status(launch_pdl(k, dim3((unsigned)ctas), dim3(32 * WARPS), smem, s, a), fn);
+    return pdl_status(ffn_cluster_launch(k, ctas, 32 * WARPS, a.cluster, smem, s, a), fn);
 }
 
 template <int FMT, int NT, int TERMS>

@@ -660,6 +660,16 @@ def test_few_rows_over_long_and_short_sums(fmt, dtype, M):
     gated(fmt, dtype, M, 2450, 768, seed=M)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,K", [(20, 18944), (333, 13824), (1300, 13824), (3584, 9472)])
+def test_few_columns_of_a_long_reduction(fmt, dtype, N, K):
+    """Few rows: the reduction in one, two, four and eight CTAs; rows held in shared memory and rows that are not."""
+    for M in (1, 11):
+        project(fmt, dtype, M, N, K, seed=N + M)
+    gated(fmt, dtype, 2, N // 4, K, seed=N)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 @pytest.mark.parametrize("N", [4090, 4100, 26000])
 def test_wide_gradients(dtype, N):
