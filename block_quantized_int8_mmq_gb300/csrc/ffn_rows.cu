@@ -1,11 +1,13 @@
 // The rows of a feed-forward call as operands of its product: k_ffn_rows (x as it is) and k_ffn_gradients
 // (dz = dy act'(z); for the gated block dg = dh u act'(g) and du = dh act(g), side by side).
 //
+// Bound: HBM.  k_ffn_rows 2048 bf16 rows of 18944 values, 155 MB, 28 us (5.5 TB/s); k_ffn_gradients below.
+//
 // A row is scaled by a power of two that brings its largest magnitude into [2^13, 2^14), so that f16 holds all
 // but what lies 2^-38 below it, and written as f16 (bf16 rows exactly, f16 rows as they are but for the
 // scaling; f32 rows in two terms) in the order in which the tensor cores read them: per 64 values and 8 rows 1024
-// bytes, a row 128 of them, its 16-byte pieces exchanged by the row's number (piece c at c ^ row: 128-byte swizzle).  `up` takes the scaling back, and the 2^8 of the weights.
-// HBM-bound.  f16 rows are operands as they are: no scaling, so they are cut at will.
+// bytes, a row 128 of them, its 16-byte pieces exchanged by the row's number (piece c at c ^ row: 128-byte swizzle).  `up` takes
+// the scaling back, and the 2^8 of the weights.  f16 rows are operands as they are: no scaling, so they are cut at will.
 #include "ffn_rows.cuh"
 
 namespace mmq {

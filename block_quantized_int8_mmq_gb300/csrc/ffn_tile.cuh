@@ -13,8 +13,12 @@
 //   a loader warp     the rows' tiles, which k_ffn_rows has laid out, one bulk copy a step and term;
 //   issuer warps (2)  the products of a weight tile each, 64 values of the reduction a step.
 // f32 rows (SPLIT): rows and weights in two f16 terms each, three products, and the accumulators move to registers
-// every 256 values of the reduction: the tensor core's additions round towards zero, and over a long sum that
+// every 128 values of the reduction: the tensor core's additions round towards zero, and over a long sum that
 // would be more than f32 allows.
+//
+// Bound: the tensor cores at 192 rows (a 64-value step 0.50 us of 0.59; gated 2048 x 18944 x 3584 of Q4_K, bf16, 360 us, 1.54
+// PFLOP/s, 0.8 of the library's plain product), the weights' way to f16 at few rows (0.55 us a step, Q6_K 0.9, f32 rows 1.1)
+// and for Q5_K and Q6_K at all; backward 0.65 us a step, both operands read from shared memory (2048 rows 386 us, 1.44 PFLOP/s).
 //
 // The work is dealt unit by unit in rounds; where the last round would leave too many SMs idle it and the one before
 // are laid end to end instead and cut into equal runs.  A unit that is cut leaves its parts in scratch memory, and the
@@ -29,7 +33,9 @@ namespace ffn {
 
 static __device__ unsigned g_ffn_tile_error;  // of each translation unit its own
 
-constexpr int PERIOD = 4;  // SPLIT: steps between two moves of the accumulators
+// SPLIT: steps between two moves of the accumulators.  Measured two against four: 8.4e-7 -> 3.8e-7 of a projection's norm,
+// 66 -> 69 us (517 x 3584 x 3584 of Q5_K).
+constexpr int PERIOD = 2;
 
 // The pieces of work of a CTA: (unit, first chunk, end).
 struct Pieces {
@@ -365,9 +371,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     before = base + (BACK ? c - c0 : PER * (c - c0) + (SUB == 2 ? e : step_of(FMT, j)));
                     if (lane == 0) ptx::mbar_arrive(full + 8 * (before % RING));
                     ++mine;
-                    // SPLIT: a period (two steps of each set) behind; with one buffer behind a period's first step, which its
-                    // products wait with
-                    if (SPLIT && mine >= PERIOD / 2 * (drained + S::DB) + (S::DB == 1)) {
+                    // SPLIT: a period (a step of each set) behind, whose sums the other buffer holds
+                    if (SPLIT && mine >= PERIOD / 2 * (drained + S::DB)) {
                         ok = ok && drain(n_d++, false);
                         ++drained;
                     }

@@ -585,7 +585,7 @@ int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtyp
  *   weight is formed from, |scale| x the largest code + |minimum|, has to be below 255: else the device error word is set
  *   (MMQ_ERR_RANGE) and the outputs of that weight row (backward: all) are unspecified.
  *   Sums of 16-bit rows stay in the tensor cores, which round towards zero: 2^-22 of the sum at most for every 16 values; f32
- *   rows' leave them every 256 values (up to 16 rows: every 32).
+ *   rows' leave them every 128 values (up to 16 rows: every 32).
  * Finite inputs are required: a NaN or an infinity in a row leaves that row's outputs unspecified, and
  * no other's.  The order of summation depends on the sizes alone, so repeated calls give the same bits.
  * Scratch: stream-ordered, as the expanded path's.

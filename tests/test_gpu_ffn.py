@@ -670,6 +670,21 @@ def test_few_columns_of_a_long_reduction(fmt, dtype, N, K):
     gated(fmt, dtype, 2, N // 4, K, seed=N)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K", [512, 8704])
+def test_few_f32_rows_keep_their_precision(fmt, K):
+    """A block's products and its minimum's leave the tensor core after four cuts of 2^-24 of the largest product, which is a few
+    times the block's sum: 16 x 2^-24 of the norm in all, beside the rows' own two terms (2^-23)."""
+    N = 395
+    w = Weights(fmt, 5, N, K)
+    for M in (1, 14):
+        x = rows(6, M, K, "f32")
+        z = x.double() @ w.v.double().T
+        y = mmq.mmq_project(x, w.bytes, fmt, N)
+        clean()
+        assert float((y.double() - z).norm() / z.norm()) <= 2.0 ** -20 + 2.0 ** -23
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 @pytest.mark.parametrize("N", [4090, 4100, 26000])
 def test_wide_gradients(dtype, N):
