@@ -671,6 +671,36 @@ def test_few_columns_of_a_long_reduction(fmt, dtype, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_clusters_in_a_graph_and_on_two_streams(fmt):
+    """Reductions that CTAs share: replayed with other rows, and two calls at once, the bits of single calls; wide gradients too."""
+    N, K, wide = 333, 13824, 5000
+    w, back = Weights(fmt, 3, N, K), Weights(fmt, 4, wide, 256)
+    xs = [rows(i, 3, K, "bf16") for i in range(2)]
+    dys, zs = ([rows(i + k, 30, wide, "bf16") for i in range(2)] for k in (10, 20))
+    run = lambda x, dy, z: (mmq.mmq_project(x, w.bytes, fmt, N), mmq.mmq_project_backward(dy, back.bytes, fmt, 256, act="silu", pre=z))
+    want = [run(*t) for t in zip(xs, dys, zs)]
+    kept = [t[0].clone() for t in (xs, dys, zs)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(*kept)
+    for i in (1, 0):
+        for t, new in zip(kept, (xs[i], dys[i], zs[i])):
+            t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(4):
+        for i, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                outs[i].append(run(xs[i], dys[i], zs[i]))
+    torch.cuda.synchronize()
+    clean()
+    assert all(torch.equal(a, b) for i in range(2) for o in outs[i] for a, b in zip(o, want[i]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("K", [512, 8704])
 def test_few_f32_rows_keep_their_precision(fmt, K):
     """A block's products and its minimum's leave the tensor core after four cuts of 2^-24 of the largest product, which is a few
