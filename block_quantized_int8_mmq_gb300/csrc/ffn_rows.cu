@@ -7,7 +7,9 @@
 // but what lies 2^-38 below it, and written as f16 (bf16 rows exactly, f16 rows as they are but for the
 // scaling; f32 rows in two terms) in the order in which the tensor cores read them: per 64 values and 8 rows 1024
 // bytes, a row 128 of them, its 16-byte pieces exchanged by the row's number (piece c at c ^ row: 128-byte swizzle).  `up` takes
-// the scaling back, and the 2^8 of the weights.  f16 rows are operands as they are: no scaling, so they are cut at will.
+// the scaling back, and the 2^8 of the weights.  f16 rows are operands as they are: no scaling, so they are cut at will; but
+// where blocks' sums are wanted too they are scaled as the others, since the two f16 terms of a sum hold 2^-19 of it only
+// where x is of the size of one (unscaled rows of 1e-4: 4.6e-3 of the outputs' norm).
 #include "ffn_rows.cuh"
 
 namespace mmq {
@@ -32,13 +34,12 @@ __device__ __forceinline__ void clear_counters(const Rows& r) {
         for (int i = threadIdx.x; i < r.n_counters; i += blockDim.x) r.counters[i] = 0u;
 }
 
-// A CTA per row (f16 rows: several), a thread per run of eight values; eight neighbouring threads write a line.
+// A CTA per row (rows that are not scaled: several), a thread per run of eight values; eight neighbouring threads write a line.
 constexpr int GRADIENT_THREADS = 256;
 constexpr int HELD = 5;  // runs a thread keeps between looking for the largest value and writing
 
-template <typename T, int THREADS>
+template <typename T, int THREADS, bool SCALED>
 __global__ void __launch_bounds__(THREADS) k_ffn_rows(const Rows r) {
-    constexpr bool SCALED = !std::is_same<T, __half>::value;
     __shared__ float s_max[THREADS / 32];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch_dependents();
@@ -243,13 +244,13 @@ int gradients(const Rows& r, int smem, bool go, const char* fn, cudaStream_t s) 
     return pdl_status(ffn_cluster_launch(k, r.rows * CTAS, GRADIENT_THREADS, CTAS, smem, s, r), fn);
 }
 
-template <typename T, int THREADS>
+template <typename T, int THREADS, bool SCALED>
 int rows(const Rows& r, const char* fn, cudaStream_t s) {
-    // f16 rows: CTAs enough for every SM's threads, as long as each has what its threads hold
+    // not scaled: CTAs enough for every SM's threads, as long as each has what its threads hold
     const int each = THREADS * HELD, runs = r.width / 8, want = 4 * device_shape().sms / r.rows + 1;
-    const int most = (runs + each - 1) / each, cuts = std::is_same<T, __half>::value ? (want < most ? want : most) : 1;
+    const int most = (runs + each - 1) / each, cuts = SCALED ? 1 : want < most ? want : most;
     ProfScope ps("k_ffn_rows", s);
-    return pdl_status(launch_pdl(&k_ffn_rows<T, THREADS>, dim3((unsigned)r.rows, (unsigned)cuts), dim3(THREADS), 0, s, r), fn);
+    return pdl_status(launch_pdl(&k_ffn_rows<T, THREADS, SCALED>, dim3((unsigned)r.rows, (unsigned)cuts), dim3(THREADS), 0, s, r), fn);
 }
 
 template <typename T>
@@ -262,8 +263,10 @@ int launch(const Rows& r, bool back, bool go, const char* fn, cudaStream_t s) {
         return each <= KEEP_MOST ? gradients<T, true, CTAS>(r, each, go, fn, s) : gradients<T, false, CTAS>(r, 0, go, fn, s);
     }
     if (!go) return MMQ_OK;
+    constexpr bool SCALED = !std::is_same<T, __half>::value;
+    if (!SCALED && r.sums) return rows<T, 512, true>(r, fn, s);
     // a narrow row in small CTAs where there are many; one row's latency in a large one
-    return r.rows >= 2 * device_shape().sms && r.width <= 8 * 128 * HELD ? rows<T, 128>(r, fn, s) : rows<T, 512>(r, fn, s);
+    return r.rows >= 2 * device_shape().sms && r.width <= 8 * 128 * HELD ? rows<T, 128, SCALED>(r, fn, s) : rows<T, 512, SCALED>(r, fn, s);
 }
 
 }  // namespace

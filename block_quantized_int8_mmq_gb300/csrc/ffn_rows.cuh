@@ -58,8 +58,9 @@ __device__ __forceinline__ void put(const Rows& r, int m, int step, int chunk, c
            r.dtype == MMQ_F32, v, down);
 }
 
-// The sum of a block of 32 values, held by four neighbouring threads, in two f16 terms, times 2^-6 so that they fit:
-// in the order in which k_ffn_stream's product takes them, per 256 values and eight rows 256 bytes.
+// The sum of a block of 32 values, held by four neighbouring threads, in two f16 terms, times 2^-6 so that they fit (rows are
+// scaled to [2^13, 2^14) here, so what the terms leave, 2^-19, is 2^-32 of the row's largest value): in the order in which
+// k_ffn_stream's product takes them, per 256 values and eight rows 256 bytes.
 __device__ __forceinline__ void put_sum(uint8_t* sums, int groups, int m, int run, const float (&v)[8], float down) {
     float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     s += __shfl_xor_sync(0xffffffffu, s, 1);

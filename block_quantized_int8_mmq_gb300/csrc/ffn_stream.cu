@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
         const int from = (int)((long long)a.chunks * rank / a.cluster) * 32, to = min(places, (int)((long long)a.chunks * (rank + 1) / a.cluster) * 32);
         auto lay_out = [&](auto type) {
             using T = decltype(type);
-            constexpr bool SCALED = !std::is_same<T, __half>::value;
+            constexpr bool SCALED = !std::is_same<T, __half>::value || MINS;
             const T* x = static_cast<const T*>(a.rows);
             if (SCALED) {
                 for (int m = 0; m < a.M; ++m) {
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
             if (n >= a.N) continue;
             const long long at = (long long)m * a.N + n;
             // (the weights' 2^8, which `up` takes back, these weights have not)
-            const float up = (!HELD ? __ldg(a.up + m) : TERMS == 1 && a.dtype == MMQ_F16 ? 1.f / 256.f : row_scale(__uint_as_float(s_top[m])).up) * 256.f;
+            const float up = (!HELD ? __ldg(a.up + m) : !MINS && std::is_same<T, __half>::value ? 1.f / 256.f : row_scale(__uint_as_float(s_top[m])).up) * 256.f;
             float z[2] = {0.f, 0.f};
             for (int w = 0; w < a.mats; ++w) {
                 z[w] = fmaf(total(w * per + run, m, k), up, a.bias[w] ? __ldg(a.bias[w] + n) : 0.f);

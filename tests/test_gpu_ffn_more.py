@@ -1,0 +1,80 @@
+"""The feed-forward operators where their arithmetic is most at risk: rows of small f16 values, rows of one sign through blocks
+whose minimum cancels their codes, activations far out on the way back, blocks of zeros behind large scales, weights that a
+call shortly before has written.
+
+Outputs are rounded to their type: an error of at most half a step, that of many values spread evenly over a step, whose
+square is a twelfth of a step's on the average (`steps2`; of N values to within 1 / sqrt(N), for which a fifth more is given)."""
+import numpy as np
+import pytest
+import torch
+
+import ffn_ref
+from test_gpu_ffn import Weights, clean, mmq, rows
+
+pytestmark = pytest.mark.gpu
+
+BITS = {"f32": (24, -149), "bf16": (8, -133), "f16": (11, -24)}  # of a value, exponent of the smallest step
+
+
+def steps2(want, dtype):
+    """The square that roundings of `want` to its type add up to."""
+    digits, least = BITS[dtype]
+    e = torch.frexp(want)[1] - digits
+    return float(torch.exp2(2.0 * e.clamp(min=least).double()).sum()) / 12 * 1.2
+
+
+def pack(fmt, d, dmin, sc, mn, q):
+    """Q4_K or Q5_K bytes [N, row bytes] of d, dmin [N, B], sc, mn [N, B, 8] and codes [N, B, 8, 32]."""
+    N, B = d.shape
+    out = np.zeros((N, B, ffn_ref.BYTES[fmt]), np.uint8)
+    out[..., 0:2] = d.astype(np.float16)[..., None].view(np.uint8)
+    out[..., 2:4] = dmin.astype(np.float16)[..., None].view(np.uint8)
+    out[..., 4:8] = sc[..., :4] | sc[..., 4:] >> 4 << 6
+    out[..., 8:12] = mn[..., :4] | mn[..., 4:] >> 4 << 6
+    out[..., 12:16] = (sc[..., 4:] & 15) | (mn[..., 4:] & 15) << 4
+    if fmt == "q5_k":
+        for b in range(8):
+            out[..., 16:48] |= (q[..., b, :] >> 4 & 1) << b
+    low = (q & 15).reshape(N, B, 4, 2, 32)
+    out[..., -128:] = (low[..., 0, :] | low[..., 1, :] << 4).reshape(N, B, 128)
+    return out.reshape(N, -1)
+
+
+class Blocks(Weights):
+    """Normal weights as Q4_K or Q5_K: their minimum is half of the codes' range, as a quantizer leaves it."""
+
+    def __init__(self, fmt, seed, N, K, by=0.02):
+        rng = np.random.default_rng(seed)
+        B, top = K // 256, 15 if fmt == "q4_k" else 31
+        sc = rng.integers(35, 64, (N, B, 8)).astype(np.uint8)
+        d = (rng.uniform(0.7, 1.3, (N, B)) * by * 4.6 / top / 50).astype(np.float16)
+        dmin = (d.astype(np.float64) * (top / 2)).astype(np.float16)
+        q = np.clip(np.rint(rng.standard_normal((N, B, 8, 32)) * (top / 4.6) + top / 2), 0, top).astype(np.uint8)
+        raw = pack(fmt, d, dmin, sc, sc, q)
+        v, size = ffn_ref.values(fmt, raw)
+        self.fmt, self.N, self.K, self.bytes = fmt, N, K, torch.from_numpy(raw).cuda()
+        self.v, self.size = torch.from_numpy(v).cuda(), torch.from_numpy(size).cuda()
+        # of every 32-value block, and of every 256
+        self.scale = torch.from_numpy((d.astype(np.float64)[..., None] * sc).reshape(N, -1)).cuda()
+        self.dmin = torch.from_numpy(dmin.astype(np.float64)).cuda()
+
+
+@pytest.mark.parametrize("fmt", ["q4_k", "q5_k"])
+@pytest.mark.parametrize("M,N,K", [(1, 500, 1024), (16, 333, 512), (7, 200, 18944), (1, 150, 75776)])
+@pytest.mark.parametrize("by", [1e-5, 1e-4, 1e-3, 1.0])
+def test_few_f16_rows_of_any_size(fmt, M, N, K, by):
+    """Up to 16 rows the codes enter exactly and rows to 2^-38 of their largest value.  What is left: a block's two products
+    cut what lies 2^-24 below a product's exponent by its operands' fields, which a code as a subnormal has 2^10 too large: 34 cuts
+    of 2^-14 of the block's largest x, and 17 of its sums in the minimum's product of a chunk."""
+    w = Blocks(fmt, 3, N, K, by=1.0)
+    x = rows(4, M, K, "f16", by)
+    y = mmq.mmq_project(x, w.bytes, fmt, N)
+    clean()
+    xd = x.double()
+    want = xd @ w.v.T
+    top = xd.view(M, -1, 32).abs().amax(-1)
+    sums = xd.view(M, -1, 8, 32).sum(-1).abs().amax(-1)
+    cuts = (34 * 2.0 ** -14) ** 2 * top.square() @ w.scale.square().T + (17 * 2.0 ** -14) ** 2 * sums.square() @ w.dmin.square().T
+    allowed = (float(cuts.sum()) + steps2(want, "f16")) ** 0.5
+    off = float((y.double() - want).norm())
+    assert off <= allowed, f"off by {off / float(want.norm()):.3g} of the norm, {allowed / float(want.norm()):.3g} is allowed"
