@@ -82,7 +82,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     if (tid < STREAM_ROWS) s_top[tid] = 0u;
     ptx::fence_barrier_init();
     __syncthreads();
-    ptx::grid_dep_launch_dependents();
     volatile int* abort = &s_abort;
     unsigned* err = &g_ffn_stream_error;
 
@@ -130,7 +129,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) k_ffn_stream(const __grid_const
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    ptx::grid_dep_wait();  // the rows are laid out
+    ptx::grid_dep_wait();  // the rows are there
+    // (not before: the next call asks for its weights before it waits, and must find those that any kernel but this one wrote)
+    ptx::grid_dep_launch_dependents();
     // HELD: all of x in shared memory, after the rings, laid out here while the first weights are on their way; so there
     // is no other kernel and no memory beside
     const int x_steps = (a.K + STEP - 1) / STEP;

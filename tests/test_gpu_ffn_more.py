@@ -78,3 +78,30 @@ def test_few_f16_rows_of_any_size(fmt, M, N, K, by):
     allowed = (float(cuts.sum()) + steps2(want, "f16")) ** 0.5
     off = float((y.double() - want).norm())
     assert off <= allowed, f"off by {off / float(want.norm()):.3g} of the norm, {allowed / float(want.norm()):.3g} is allowed"
+
+
+def test_weights_that_a_call_before_the_last_has_written():
+    """The outputs of a long call are the weights of a short one, with another call between them: few rows, whose weights are
+    asked for early, but never before the kernels up to the last but one have ended."""
+    N, K = 512, 1 << 19
+    long_w, x = torch.zeros((N, K // 32 * 34), dtype=torch.uint8, device="cuda"), rows(1, 1, K, "bf16")
+    rng = np.random.default_rng(3)
+    blocks = rng.integers(1, 100, (30, 34)).astype(np.uint8)  # (pairs of bytes that are finite bf16 values: a residual passes them on)
+    blocks[:, 0:2] = np.frombuffer(np.float16(2.0 ** -7).tobytes(), np.uint8)
+    wanted = torch.zeros(2 * N, dtype=torch.uint8)
+    wanted[:blocks.size] = torch.from_numpy(blocks.reshape(-1))
+    residual = wanted.view(torch.bfloat16).view(1, N).cuda()
+    between, bx = Weights("q8_0", 2, 40, 64), rows(2, 3, 64, "bf16")
+    cx = rows(3, 2, 32, "bf16")
+    want = mmq.mmq_project(cx, wanted[:blocks.size].cuda(), "q8_0", 30)
+    buf = torch.empty((1, N), dtype=torch.bfloat16, device="cuda")
+    weights = buf.view(torch.uint8).view(-1)[:blocks.size]
+    for _ in range(10):
+        buf.zero_()
+        torch.cuda.synchronize()
+        mmq.mmq_project(x, long_w, "q8_0", N, residual=residual, out=buf)
+        mmq.mmq_project(bx, between.bytes, "q8_0", 40)
+        got = mmq.mmq_project(cx, weights, "q8_0", 30)
+        torch.cuda.synchronize()
+        assert torch.equal(buf, residual) and torch.equal(got, want)
+    clean()
