@@ -4,8 +4,8 @@
 //
 // Weights enter the product times 2^8: f16 is then normal from 2^-22 up, and whatever a weight is formed
 // from, |scale| times the largest code and the minimum, has to stay below 255 (Check).
-// For bf16 rows the scale and the minimum are rounded to f16 first and the weight once more, 2^-11 each: little beside
-// what the rows' own type loses (2^-8), and four instructions for two weights.  For f16 rows only the weight is (Fine).
+// For bf16 rows a block's scale is rounded to f16 first and the weight once more, 2^-11 each: little beside what the rows' own
+// type loses (2^-8), and four instructions for two weights.  For f16 rows only the weight is (Fine).  Minimums: Centred.
 // For f32 rows the weight is formed in f32 and split in two f16 terms (2^-22).
 #pragma once
 
@@ -53,23 +53,40 @@ struct Check {
     __device__ __forceinline__ bool bad() const { return f != 0.f || !__hbeq2(h, __float2half2_rn(0.f)); }
 };
 
-// f16 rows: s q - m with no rounding but the weight's own (2^-11, 2.1e-4 of the weights' norm; scale and minimum rounded
-// too, as bf16 rows have them, come to 6.6e-4, three times what f16 outputs lose).  The minimum is c scales and a
-// remainder of half of one, the codes are centred on c, which their placing takes off anyway, and the scale is two
-// terms: s1 (q - c) + (s2 (q - c) + r).
+// Q4_K, Q5_K, 16-bit rows: s q - m as s (q - c) + r, c a whole number near m / s that the codes' placing takes off with their
+// 1024 and r = c s - m, at most some 0.6 s.  s q and m are each many times what they leave; a rounding of either alone is
+// the same for 32 weights, and rows of one sign add it up (bf16 rows, |normal|: 3.4e-3 of the outputs' norm with s and m rounded
+// by themselves).  Of two blocks, side by side: s = s1 + s2 and m = m1 + m2 exactly (products of 11 and 6 bits, multiples of
+// 2^-16), r from all four.  (m / s beyond 1000: r is most of the weight.)
+struct Centred {
+    __half2 s1, s2, r, bias;
+    __device__ __forceinline__ Centred(uint32_t sc, uint32_t mn, uint32_t dd, float most, Check& check) {
+        const __half2 up2 = __float2half2_rn(W_UP), b = umma::bits_h2(0x64006400u), d2 = umma::bits_h2(dd);
+        const __half2 sq = __hmul2(__hsub2(umma::bits_h2(__byte_perm(sc, 0x64646464u, 0x4140)), b), up2);
+        const __half2 mq = __hmul2(__hsub2(umma::bits_h2(__byte_perm(mn, 0x64646464u, 0x4140)), b), up2);
+        s1 = __hmul2(sq, low2(d2));
+        s2 = __hfma2(sq, low2(d2), __hneg2(s1));
+        const __half2 m1 = __hmul2(mq, high2(d2)), m2 = __hfma2(mq, high2(d2), __hneg2(m1));
+        check.add(s1, m1, most);
+        const float2 s = __half22float2(s1), m = __half22float2(m1);
+        const __half2 t = __floats2half2_rn(__fdividef(m.x, s.x), __fdividef(m.y, s.y));
+        const __half2 c = h2rint(__hmax2(__hmin2(t, __float2half2_rn(1000.f)), __float2half2_rn(-1000.f)));  // (0 / 0: any will do)
+        r = __hadd2(__hfma2(c, s1, __hneg2(m1)), __hfma2(c, s2, __hneg2(m2)));
+        bias = __hadd2(__float2half2_rn(1024.f), c);
+    }
+};
+
+// f16 rows: no rounding but the weight's own (2^-11, 2.1e-4 of the weights' norm; with the scale in one term 2.5e-4), the
+// scale in two terms: s1 (q - c) + (s2 (q - c) + r).
 struct Fine {
     __half2 s1, s2, r;
     uint32_t bias;
-    __device__ __forceinline__ Fine(float s, float m, float centre) {
-        float c = centre, rest = 0.f;
-        if (centre == 0.f) {  // a minimum
-            c = fmaxf(-1000.f, fminf(1000.f, rintf(__fdividef(m, s))));
-            rest = fmaf(c, s, -m);
-        }
+    __device__ __forceinline__ Fine(const Centred& w, int b)
+        : s1(b ? high2(w.s1) : low2(w.s1)), s2(b ? high2(w.s2) : low2(w.s2)), r(b ? high2(w.r) : low2(w.r)),
+          bias(h2(b ? high2(w.bias) : low2(w.bias))) {}
+    __device__ __forceinline__ explicit Fine(float s) : r(__float2half2_rn(0.f)), bias(0x64206420u) {  // Q6_K: no minimum, codes centred on 32
         s1 = __float2half2_rn(s);
         s2 = __float2half2_rn(s - __low2float(s1));
-        r = __float2half2_rn(rest);
-        bias = h2(__float2half2_rn(1024.f + c));
     }
 };
 __device__ __forceinline__ void four(uint32_t codes, const Fine& l, uint32_t* hi) {
@@ -81,7 +98,7 @@ __device__ __forceinline__ void four(uint32_t codes, const Fine& l, uint32_t* hi
     }
 }
 
-// Four codes (one per byte) to two pairs of f16, s q + m: bf16 rows.
+// Four codes (one per byte) to two pairs of f16, s (q - bias) + m: bf16 rows.
 template <bool MIN>
 __device__ __forceinline__ void four(uint32_t codes, uint32_t bias, __half2 s, __half2 m, uint32_t* hi) {
     const __half2 b = umma::bits_h2(bias);
@@ -178,7 +195,7 @@ __device__ __forceinline__ void quarter_q6(const Q6Half& w, int P, Check& check,
             const __half2 s2 = g ? high2(sp[b]) : low2(sp[b]);
             if (SPLIT || FINE) check.add(s, 0.f, 32.f);
             const Scale2 w2(s, 0.f, false);
-            const Fine fine(s, 0.f, 32.f);
+            const Fine fine(s);
 #pragma unroll
             for (int i = 4 * g; i < 4 * g + 4; ++i) {
                 const uint32_t c = ((w.ql[8 * b + i] >> (4 * P)) & 0x0f0f0f0fu) |
@@ -271,21 +288,15 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
         mn >>= 16 * (J & 1);
         constexpr float MOST = FMT == FMT_Q5_K ? 31.f : 15.f;
         const uint32_t dd = valid ? head.x : 0u;
-        __half2 s2{}, m2{};
-        if (!SPLIT && !FINE) {
-            const __half2 d2 = __hmul2(umma::bits_h2(dd), __floats2half2_rn(W_UP, -W_UP)), bias = umma::bits_h2(0x64006400u);
-            s2 = __hmul2(__hsub2(umma::bits_h2(__byte_perm(sc, 0x64646464u, 0x4140)), bias), low2(d2));
-            m2 = __hmul2(__hsub2(umma::bits_h2(__byte_perm(mn, 0x64646464u, 0x4140)), bias), high2(d2));
-            check.add(s2, m2, MOST);
-        }
+        Check none;
+        const Centred two(sc, mn, dd, MOST, SPLIT ? none : check);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const float s = f16_bits_to_f32(dd) * W_UP * (float)((sc >> (8 * b)) & 63);
             const float m = f16_bits_to_f32(dd >> 16) * -W_UP * (float)((mn >> (8 * b)) & 63);
-            if (SPLIT || FINE) check.add(s, m, MOST);
+            if (SPLIT) check.add(s, m, MOST);
             const Scale2 w2(s, m, true);
-            const Fine fine(s, -m, 0.f);
-            const __half2 sb = b ? high2(s2) : low2(s2), mb = b ? high2(m2) : low2(m2);
+            const Fine fine(two, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t c = (b ? q[i] >> 4 : q[i]) & 0x0f0f0f0fu;
@@ -295,7 +306,7 @@ __device__ __forceinline__ void quarter(const uint8_t* slot, int J, int mis, boo
                 else if (FINE)
                     four(c, fine, hi + 2 * i);
                 else
-                    four<true>(c, 0x64006400u, sb, mb, hi + 2 * i);
+                    four<true>(c, fine.bias, fine.s1, fine.r, hi + 2 * i);
             }
             emit(b, hi, lo);
         }

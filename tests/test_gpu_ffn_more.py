@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import ffn_ref
-from test_gpu_ffn import Weights, clean, mmq, rows
+from test_gpu_ffn import DT, Product, Weights, check, clean, mmq, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -59,6 +59,11 @@ class Blocks(Weights):
         self.dmin = torch.from_numpy(dmin.astype(np.float64)).cuda()
 
 
+def block_sums(x, v):
+    """sum over each block of 32 of x v: [M, N, K / 32] of x [M, K], v [N, K]."""
+    return torch.einsum("mbk,nbk->mnb", x.view(x.shape[0], -1, 32), v.view(v.shape[0], -1, 32))
+
+
 @pytest.mark.parametrize("fmt", ["q4_k", "q5_k"])
 @pytest.mark.parametrize("M,N,K", [(1, 500, 1024), (16, 333, 512), (7, 200, 18944), (1, 150, 75776)])
 @pytest.mark.parametrize("by", [1e-5, 1e-4, 1e-3, 1.0])
@@ -78,6 +83,36 @@ def test_few_f16_rows_of_any_size(fmt, M, N, K, by):
     allowed = (float(cuts.sum()) + steps2(want, "f16")) ** 0.5
     off = float((y.double() - want).norm())
     assert off <= allowed, f"off by {off / float(want.norm()):.3g} of the norm, {allowed / float(want.norm()):.3g} is allowed"
+
+
+@pytest.mark.parametrize("fmt", ["q4_k", "q5_k"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sign", ["any", "relu", "abs"])
+@pytest.mark.parametrize("M,N,K", [(40, 300, 3584), (150, 257, 1024)])
+def test_rows_of_one_sign_through_centred_blocks(fmt, dtype, sign, M, N, K):
+    """A block's products with its codes and with its minimum are each many times their difference.  A weight is s (q - c) + r with
+    c within 3/4 of minimum / s, so that nothing is as large as either: s off by 2^-11 (bf16 rows) of what its block
+    comes to, r by 2^-11 of 3/4 s for all 32 alike, each weight by 2^-11 of itself; the tile's sum as everywhere."""
+    w = Blocks(fmt, 5, N, K)
+    x = rows(6, M, K, "f32")
+    x = (x if sign == "any" else x.abs() if sign == "abs" else x.clamp(min=0)).to(DT[dtype])
+    y = mmq.mmq_project(x, w.bytes, fmt, N)
+    clean()
+    xd = x.double()
+    want = xd @ w.v.T
+    most = 0.75 * xd.abs().view(M, -1, 32).sum(-1)[:, None] * w.scale[None]
+    err = most if dtype == "f16" else 2 * most + block_sums(xd, w.v).abs()
+    off2 = float(err.square().sum() + (xd.square() @ w.v.square().T).sum()) * 2.0 ** -22
+    off2 += float(((K / 16 + 2) * 2.0 ** -22 * want).square().sum())
+    allowed = (off2 + steps2(want, dtype)) ** 0.5
+    off = float((y.double() - want).norm())
+    assert off <= allowed, f"off by {off / float(want.norm()):.3g} of the norm, {allowed / float(want.norm()):.3g} is allowed"
+    # and back: a row of gradients of one sign
+    dy = xd[:, :N].to(DT[dtype])
+    dx = mmq.mmq_project_backward(dy, w.bytes, fmt, K)
+    clean()
+    p = Product(dtype, [dy], [w], back=True)
+    check(dx, p.z, p.err, p.walk, dtype, "dx")
 
 
 def test_weights_that_a_call_before_the_last_has_written():
