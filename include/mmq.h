@@ -585,8 +585,9 @@ int mmq_kv_attend(const mmq_kv_cache* cache, const mmq_kv_batch* batch, int dtyp
  *   2^-33).  16-bit rows: each rounded, 2^-11 of it at most.  Q4_K and Q5_K form it as scale (code - c) + r, c whole and
  *   r = c scale - minimum some 0.6 scales at most, which is rounded too: so nothing is lost of a size that codes and minimum
  *   have only before they cancel.  (Minimums beyond 1000 scales: r is most of the weight.)  bf16 rows of Q4_K, Q5_K and Q6_K: the
- *   scale in that product too, 2^-11.  Of the outputs' norm, with normal rows and weights, beside the outputs' own rounding
- *   (f16 2.1e-4, bf16 1.7e-3): a projection 1.8e-4 and 3.0e-4, the gated block 2.9e-4 and 4.3e-4 (two factors).  What a
+ *   scale in that product too, 2^-11.  Of the outputs' norm, with normal weights, beside the outputs' own rounding (f16 2.1e-4,
+ *   bf16 1.7e-3): a projection of f16 rows 2.1e-4 (rows of one sign 3.6e-4), of bf16 rows 3.0e-4 (4.6e-4); the gated block,
+ *   with two such factors, 3.0e-4 and 4.3e-4.  What a
  *   weight is formed from, |scale| x the largest code + |minimum|, has to be below 255: else the device error word is set
  *   (MMQ_ERR_RANGE) and the outputs of that weight row (backward: all) are unspecified.
  *   Sums of 16-bit rows stay in the tensor cores, which round towards zero: 2^-22 of the sum at most for every 16 values; f32

@@ -115,6 +115,25 @@ def test_rows_of_one_sign_through_centred_blocks(fmt, dtype, sign, M, N, K):
     check(dx, p.z, p.err, p.walk, dtype, "dx")
 
 
+@pytest.mark.parametrize("fmt", ["q4_k", "q5_k"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_long_rows_of_one_sign_have_no_drift(fmt, dtype):
+    """What weights are off by has no sign: over N output columns, whose weights are drawn apart, errors average out to their own size
+    over sqrt(N), five of which are allowed (rows share their weights, so that all rows of a column count as one)."""
+    M, N, K = 40, 500, 18944
+    w = Blocks(fmt, 7, N, K)
+    x = rows(8, M, K, "f32").abs().to(DT[dtype])
+    y = mmq.mmq_project(x, w.bytes, fmt, N)
+    clean()
+    want = x.double() @ w.v.T
+    off = (y.double() - want).mean(0)
+    # a value's error: a part in 2^11 of its blocks' sums as above, some 2^-10 of the norm, and the outputs' rounding; f16's sums in the
+    # tensor cores are cut towards zero, 2^-22 of them for every 16 values
+    size = float((want.square().mean() * 2.0 ** -20 + steps2(want, dtype) / want.numel()).sqrt())
+    cut = 2.0 ** -22 * K / 16 * float(want.abs().mean())
+    assert abs(float(off.mean())) <= 5 * size / N ** 0.5 + cut, f"{float(off.mean()) / float(want.abs().mean()):.3g} of the mean size"
+
+
 def test_weights_that_a_call_before_the_last_has_written():
     """The outputs of a long call are the weights of a short one, with another call between them: few rows, whose weights are
     asked for early, but never before the kernels up to the last but one have ended."""
