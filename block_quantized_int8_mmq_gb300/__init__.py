@@ -212,8 +212,9 @@ def mmq_debug_refuse_smem(on: bool) -> bool:
 
 
 def mmq_debug_set_wait_limit(ns: int) -> None:
-    """Test switch: the bound of the expanded-path contraction's waits for its operand copies, in
-    ns (0: give up at the first such wait whose copy has not landed; < 0: the 2 s default)."""
+    """Test switch: the bound of the expanded-path contraction's waits for its operand copies and of the
+    feed-forward tiles' waits for a unit's sums, in ns (0: give up at the first such wait that is not over
+    already; < 0: the 2 s default)."""
     _check("mmq_debug_set_wait_limit", _lib.mmq_debug_set_wait_limit(int(ns)))
 
 

@@ -34,6 +34,8 @@ unsigned kv_tile_take_error();
 unsigned ffn_forward_take_error();
 unsigned ffn_backward_take_error();
 unsigned ffn_stream_take_error();
+int ffn_forward_set_wait_limit(unsigned long long ns);
+int ffn_backward_set_wait_limit(unsigned long long ns);
 
 DeviceShape device_shape() {
     static std::atomic<int> sms[MAX_DEVICES], smem[MAX_DEVICES], l2[MAX_DEVICES];
@@ -484,7 +486,11 @@ int mmq_debug_expand_tiling(int fmt, int64_t M, int64_t N, int64_t K, int32_t* t
 }
 
 int mmq_debug_set_wait_limit(int64_t ns) {
-    return tcx_set_wait_limit(ns >= 0 ? (unsigned long long)ns : 2000000000ull);
+    const unsigned long long limit = ns >= 0 ? (unsigned long long)ns : 2000000000ull;
+    int st = tcx_set_wait_limit(limit);
+    if (st == MMQ_OK) st = ffn_forward_set_wait_limit(limit);
+    if (st == MMQ_OK) st = ffn_backward_set_wait_limit(limit);
+    return st;
 }
 
 int mmq_set_path(int path) {

@@ -22,5 +22,6 @@ int ffn_backward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, bool go
 }
 
 unsigned ffn_backward_take_error() { return ffn::take_tile_error(); }
+int ffn_backward_set_wait_limit(unsigned long long ns) { return ffn::set_tile_wait_limit(ns); }
 
 }  // namespace mmq

@@ -26,5 +26,6 @@ int ffn_forward_launch(int fmt, const ffn::Tile& a, int smem, int ctas, bool go,
 }
 
 unsigned ffn_forward_take_error() { return ffn::take_tile_error(); }
+int ffn_forward_set_wait_limit(unsigned long long ns) { return ffn::set_tile_wait_limit(ns); }
 
 }  // namespace mmq

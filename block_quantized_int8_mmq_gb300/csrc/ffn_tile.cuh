@@ -32,6 +32,8 @@ namespace mmq {
 namespace ffn {
 
 static __device__ unsigned g_ffn_tile_error;  // of each translation unit its own
+// the bound of the weight warps' wait for a unit's sums, in ns (mmq_debug_set_wait_limit)
+static __device__ unsigned long long g_ffn_tile_wait_limit = umma::WAIT_LIMIT_NS;
 
 // SPLIT: steps between two moves of the accumulators.  Measured two against four: 8.4e-7 -> 3.8e-7 of a projection's norm,
 // 66 -> 69 us (517 x 3584 x 3584 of Q5_K).
@@ -67,7 +69,22 @@ __device__ __forceinline__ int run_owner(const Tile& a, long long x) {
     return (int)(((x + 1) * gridDim.x - 1) / ((long long)a.rest * a.chunks));
 }
 
-__device__ __forceinline__ void sync_weight_warps() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// A barrier of the weight warps: whether all of them came with ok.  One whose wait gave up comes too, wherever another
+// may be waiting for it.
+__device__ __forceinline__ bool sync_weight_warps(bool ok) {
+    uint32_t all;
+    __syncwarp();
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, 512, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(all)
+                 : "r"((uint32_t)ok)
+                 : "memory");
+    return all != 0u;
+}
+// A barrier of all warps, each at the end of its role: no wait is left that could give up.
+__device__ __forceinline__ void sync_roles() {
+    __syncwarp();
+    asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory");
+}
 
 template <bool FAST>
 __device__ __forceinline__ void activate8(int act, float (&v)[8]) {
@@ -283,9 +300,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
         int base = 0, before = -1;         // steps of the pieces before, this set's last step
         constexpr int RUN = SPLIT ? S::NT / 2 : 1;
         float run[RUN];                    // SPLIT: sums of this thread's lane of tile g, half of its columns
+        auto wait_sums = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, umma::wait_bar_bounded(bar, parity, abort, err, g_ffn_tile_wait_limit)) != 0;
+        };
         auto drain = [&](uint32_t period, bool last) {
             const uint32_t b = S::DB == 2 ? period & 1 : 0;
-            if (!umma::warp_wait(d_full + 8 * b, (S::DB == 2 ? period >> 1 : period) & 1, abort, err)) return false;
+            const uint32_t parity = (S::DB == 2 ? period >> 1 : period) & 1;
+            if (!(last ? wait_sums(d_full + 8 * b, parity) : umma::warp_wait(d_full + 8 * b, parity, abort, err))) return false;
             ptx::tc_fence_after();
 #pragma unroll
             for (int c = 0; c < RUN / 16; ++c) {
@@ -303,7 +324,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
         };
         Pieces pc(a);
         int unit, c0, c1;
-        while (ok && pc.next(a, unit, c0, c1)) {
+        // A warp whose wait gave up skips the work that is left, but not the barriers: it leaves with the others at the first
+        // one, or at the end.
+        while (pc.next(a, unit, c0, c1)) {
             const int pair = unit / a.mtiles, mt = unit - pair * a.mtiles;
             int s0, s1;
             step_range(c0, c1, s0, s1);
@@ -419,37 +442,37 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
             int any;
             bad |= check.bad() && (BACK || row_at(pair, 0, any) >= 0);  // (lanes past the last row hold anything)
             check = Check();
-            if (!ok) break;
             if (!waited) ptx::grid_dep_wait();  // what follows reads and writes the call's rows
             waited = true;
+            const bool whole = c0 == 0 && c1 == a.chunks;
             uint32_t buf = 0;
             if (SPLIT) {
                 // the periods that are left: the last stays in its buffer's hands
                 for (; ok && drained + 1 < (s1 - s0 + PERIOD - 1) / PERIOD; ++drained) ok = drain(n_d++, false);
-                if (!ok) break;
                 buf = S::DB == 2 ? n_d & 1 : 0;
                 ok = ok && drain(n_d++, true);
-                if (!ok) break;
+                if (ok) {
 #pragma unroll
-                for (int c = 0; c < RUN / 16; ++c) {
-                    if (e * RUN + 16 * c >= a.nt) break;
-                    uint32_t v[16];
+                    for (int c = 0; c < RUN / 16; ++c) {
+                        if (e * RUN + 16 * c >= a.nt) break;
+                        uint32_t v[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(run[SPLIT ? 16 * c + k : 0]);
-                    ptx::tmem_st16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + buf * S::D_COLS + g * S::NT + e * RUN + 16 * c, v);
+                        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(run[SPLIT ? 16 * c + k : 0]);
+                        ptx::tmem_st16(tmem + ((uint32_t)(32 * (wid & 3)) << 16) + buf * S::D_COLS + g * S::NT + e * RUN + 16 * c, v);
+                    }
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
                 }
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                sync_weight_warps();
+                ok = sync_weight_warps(ok);
+                if (!ok) break;
                 ptx::tc_fence_after();
             } else {
-                ok = umma::warp_wait(d_full, n_d & 1, abort, err);
+                ok = ok && wait_sums(d_full, n_d & 1);
                 ++n_d;
-                if (!ok) break;
+                if (!ok && whole) continue;
                 ptx::tc_fence_after();
             }
             // ---- the output, or this CTA's part of it: the lane's row, half of the tile's columns
-            const bool whole = c0 == 0 && c1 == a.chunks;
             const int m0 = mt * a.nt, m1 = min(a.M, m0 + a.nt);
             const uint32_t src = tmem + ((uint32_t)(32 * (wid & 3)) << 16) + buf * S::D_COLS;
             auto part = [&](int cta, int which, int tile) {
@@ -485,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                     output(__nv_bfloat16{});
                 else
                     output(__half{});
-            } else {
+            } else if (ok) {
 #pragma unroll 1
                 for (int b = b0; m0 + b < m1; b += 32) {
                     uint32_t v0[8], v1[8];
@@ -504,13 +527,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(d_empty + 8 * buf);
+            if (ok && lane == 0) ptx::mbar_arrive(d_empty + 8 * buf);
             if (!whole) {
+                ok = sync_weight_warps(ok);  // every warp's part is written; the counter releases and acquires them
+                if (!ok) break;
                 const int u = unit - (a.units - a.rest);
                 const int first = run_owner(a, (long long)u * a.chunks), last = run_owner(a, (long long)(u + 1) * a.chunks - 1);
-                sync_weight_warps();  // every warp's part is written; the counter releases and acquires them
                 if (tid == 0) s_last = ptx::atom_inc_acq_rel(a.counters + u) == (unsigned)(last - first);
-                sync_weight_warps();
+                sync_weight_warps(true);
                 auto join = [&](auto type) {
                     using T = decltype(type);
 #pragma unroll 1
@@ -555,6 +579,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
         }
         if (bad) atomicOr(err, ERR_RANGE);
         if (ROWS) cp_async_wait_all();
+        sync_roles();
     } else if (wid < W_WARPS + C_WARPS) {
         // ------------------------------------------------ weight chunks as boxes of 32 rows
         Pieces pc(a);
@@ -594,7 +619,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 }
             }
         }
-        if (!ok && a.aligned)  // let the boxes in flight land before the shared memory goes
+        sync_roles();
+        if (*abort && a.aligned)  // let the boxes in flight land before the shared memory goes
             for (int r = 0; r < NG; ++r)
                 for (int i = 0; i < a.rs; ++i)
                     if (const int n = (asked[r] - i + a.rs - 1) / a.rs; asked[r] > i)
@@ -630,7 +656,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 if (++st == a.xs) st = 0;
             }
         }
-        if (!ok) {
+        sync_roles();
+        if (*abort) {
             // let the copies in flight land before the shared memory goes (a step's barrier counts the weights too, which may
             // never come: the copies are given the time of a wait)
             const uint64_t t0 = ptx::globaltimer_ns();
@@ -693,7 +720,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_tile(const __grid_constant__
                 if (++xst == a.xs) xst = 0;
             }
         }
-        if (!ok) {  // let the products in flight end
+        sync_roles();
+        if (*abort) {  // let the products in flight end: those whose sums nobody waited for
             if (ptx::elect_one()) ptx::umma_commit(done + 8 * g);
             __syncwarp();
             umma::drain_bar(done + 8 * g, 0, err);
@@ -722,6 +750,9 @@ int launch_tile(const Tile& a, int smem, int ctas, bool go, const char* fn, cuda
     return pdl_status(launch_pdl(k, dim3((unsigned)ctas), dim3(THREADS), smem, s, a), fn);
 }
 
+static int set_tile_wait_limit(unsigned long long ns) {
+    return cudaMemcpyToSymbol(g_ffn_tile_wait_limit, &ns, sizeof(ns)) == cudaSuccess ? MMQ_OK : MMQ_ERR_CUDA;
+}
 static unsigned take_tile_error() {
     unsigned v = 0;
     if (cudaMemcpyFromSymbol(&v, g_ffn_tile_error, sizeof(v)) != cudaSuccess) return 0;

@@ -284,12 +284,13 @@ int mmq_debug_product_dots(int fmt, const void* xq, const void* wq, int64_t M, i
  *    launch nothing (MMQ_PATH_EXPAND and MMQ_PATH_TC always need one).  Returns the
  *    previous setting (0 or 1).  Process-wide.
  *  - mmq_debug_set_wait_limit(ns): the wall-time bound of the expanded-path contraction
- *    kernel's waits for its operand copies (default 2 s, the bound of every other wait;
- *    ns < 0 restores it; 0 gives up at the first such wait whose copy has not already
- *    landed).  A wait that runs out sets the kernel's device error word (read by
+ *    kernel's waits for its operand copies, and of the feed-forward tiles' waits for a unit's
+ *    sums (default 2 s, the bound of every other wait; ns < 0 restores it; 0 gives up at the
+ *    first such wait whose copy or sums are not there already).  A wait that runs out sets the kernel's device error word (read by
  *    mmq_get_device_error as MMQ_ERR_TIMEOUT); the kernel then stops its pipeline, lets
  *    its in-flight copies and MMAs finish (those drains keep the default bound), releases
- *    its tensor memory and exits without storing.  Returns MMQ_OK or MMQ_ERR_CUDA.
+ *    its tensor memory and exits without storing (the feed-forward tiles: without what is left,
+ *    the outputs are unspecified).  Returns MMQ_OK or MMQ_ERR_CUDA.
  *    Applies to the current device.
  */
 int mmq_debug_refuse_smem(int on);

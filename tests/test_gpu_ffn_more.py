@@ -13,6 +13,7 @@ from test_gpu_ffn import DT, Product, Weights, check, clean, mmq, rows
 
 pytestmark = pytest.mark.gpu
 
+MMQ_ERR_TIMEOUT = -7
 BITS = {"f32": (24, -149), "bf16": (8, -133), "f16": (11, -24)}  # of a value, exponent of the smallest step
 
 
@@ -158,4 +159,34 @@ def test_weights_that_a_call_before_the_last_has_written():
         got = mmq.mmq_project(cx, weights, "q8_0", 30)
         torch.cuda.synchronize()
         assert torch.equal(buf, residual) and torch.equal(got, want)
+    clean()
+
+
+@pytest.mark.parametrize("fmt,dtype,call", [
+    ("q4_k", "bf16", ("project", 40, 300, 9216)), ("q6_k", "f16", ("gated", 400, 9000, 256)), ("q5_k", "f32", ("project", 130, 520, 4096)),
+    ("q8_0", "bf16", ("project", 70, 700, 288)), ("q4_k", "f32", ("back", 100, 4200, 512)), ("q6_k", "bf16", ("back", 300, 700, 2048)),
+    ("q8_0", "f32", ("back", 33, 150, 288)), ("q4_k", "f16", ("back", 600, 300, 9216))])
+def test_a_wait_that_gives_up_ends_the_call(fmt, dtype, call):
+    """The wait for a unit's sums runs out, in all of the warps or in some: the call ends with a status, and the next one is right."""
+    op, M, N, K = call
+    w = [Weights(fmt, s, N, K).bytes for s in (1, 2)]
+    x, dy = rows(3, M, K, dtype), rows(4, M, N, dtype)
+
+    def run():
+        if op == "back":
+            return mmq.mmq_project_backward(dy, w[0], fmt, K)
+        return mmq.mmq_gated(x, *w, fmt, N) if op == "gated" else mmq.mmq_project(x, w[0], fmt, N)
+    want = run()
+    clean()
+    try:
+        mmq.mmq_debug_set_wait_limit(0)  # (gives up where the sums are not there already, as some warps may find them)
+        seen = set()
+        for _ in range(40):
+            run()
+            torch.cuda.synchronize()
+            seen.add(mmq.mmq_get_device_error())
+        assert MMQ_ERR_TIMEOUT in seen and seen <= {0, MMQ_ERR_TIMEOUT}
+    finally:
+        mmq.mmq_debug_set_wait_limit(-1)
+    assert torch.equal(run(), want)
     clean()
