@@ -145,7 +145,7 @@ __device__ __forceinline__ void activate(float z, float& a, float& d) {
         a = z * s;
         d = s + z * 0.39894228040143268f * exponential<FAST>(-0.5f * z * z);
     } else {  // gelu, by tanh: (1 + tanh(t)) / 2 = 1 / (1 + exp(-2 t))
-        const float z2 = z * z;
+        const float z2 = fminf(z * z, 1e30f);  // (infinite, it would make NaN of the derivative's s (1 - s), which is 0 there)
         const float s = __fdividef(1.f, 1.f + exponential<FAST>(-1.5957691216057308f * z * (1.f + 0.044715f * z2)));
         a = z * s;
         d = s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z2);

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import ffn_ref
-from test_gpu_ffn import DT, Product, Weights, check, clean, mmq, rows
+from test_gpu_ffn import ACT_ERR, DT, Product, Weights, check, clean, mmq, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -133,6 +133,41 @@ def test_long_rows_of_one_sign_have_no_drift(fmt, dtype):
     size = float((want.square().mean() * 2.0 ** -20 + steps2(want, dtype) / want.numel()).sqrt())
     cut = 2.0 ** -22 * K / 16 * float(want.abs().mean())
     assert abs(float(off.mean())) <= 5 * size / N ** 0.5 + cut, f"{float(off.mean()) / float(want.abs().mean()):.3g} of the mean size"
+
+
+@pytest.mark.parametrize("act", [a for a in ffn_ref.ACTS if a != "none"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_derivatives_far_out(act, dtype):
+    """Pre-activations of 10 to 1e20: the derivative is 0 or 1 to f32, and nothing overflows on the way."""
+    N, K, far = 70, 64, [10.0, 100.0, 1e4] + ([1e10, 1e18, 1e20, 1e30] if dtype != "f16" else [6e4])
+    z = torch.tensor([s * f for f in far for s in (1, -1)], device="cuda")
+    M = z.numel()
+    pre = (z[:, None] * (1 + torch.rand((M, N), device="cuda") / 16)).to(DT[dtype])
+    up, dy = rows(1, M, N, dtype), rows(2, M, N, dtype)
+    w = [Weights("q8_0", s, N, K) for s in (3, 4)]
+    zd = pre.double()
+    a, d = ffn_ref.act(act, zd.clamp(-60, 60))  # (beyond, the activation is z or 0 and its derivative 1 or 0, to e^-60)
+    a, d = (torch.where(zd.abs() > 60, t, u) for t, u in ((zd.clamp(min=0), a), ((zd > 0).double(), d)))
+    dz, dg, du = (torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda") for _ in range(3))
+    dx = mmq.mmq_project_backward(dy, w[0].bytes, "q8_0", K, act=act, pre=pre, dz=dz)
+    want = dy.double() * d
+    err = ACT_ERR * 1.13 * dy.double().abs()
+    check(dz, want, err, err, dtype, "dz")
+    p = Product(dtype, [want], w[:1], back=True, formed=True)
+    extra = err @ w[0].size
+    check(dx, p.z, p.err + extra, p.walk + extra, dtype, "dx")
+    small = up * 2.0 ** -10 if dtype == "f16" else up
+    near = (a.abs() <= 1e4).all(1)  # (larger ones leave the other product's gradients far behind: their rows' own test is above)
+    dx = mmq.mmq_gated_backward(small, pre, up, w[0].bytes, w[1].bytes, "q8_0", K, act=act, dgate=dg, dup=du)
+    clean()
+    sd = small.double()
+    check(dg, sd * up.double() * d, ACT_ERR * 1.13 * (sd * up.double()).abs(), ACT_ERR * 1.13 * (sd * up.double()).abs(), dtype, "dg")
+    check(du, sd * a, ACT_ERR * (sd * zd).abs(), ACT_ERR * (sd * zd).abs(), dtype, "du")
+    assert torch.isfinite(dx).all()
+    want = [sd * up.double() * d, sd * a]
+    p = Product(dtype, [t[near] for t in want], w, back=True, formed=True)
+    extra = ACT_ERR * 1.13 * ((sd * up.double()).abs()[near] @ w[0].size + (sd * zd).abs()[near] @ w[1].size)
+    check(dx[near], p.z, p.err + extra, p.walk + extra, dtype, "dx")
 
 
 def test_weights_that_a_call_before_the_last_has_written():
