@@ -182,10 +182,11 @@ __device__ __forceinline__ void quarter_q6(const Q6Half& w, int P, Check& check,
     const float d = f16_bits_to_f32(w.d) * W_UP;
     __half2 sp[2];
     if (!SPLIT && !FINE) {
-        const __half2 d2 = __hmul2(umma::bits_h2(w.d), __float2half2_rn(W_UP)), bias = umma::bits_h2(0x64806480u);
+        const __half2 d2 = umma::bits_h2(w.d), up2 = __float2half2_rn(W_UP), bias = umma::bits_h2(0x64806480u);
         const uint32_t u = sc ^ 0x80808080u;
-        sp[0] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias), d2);
-        sp[1] = __hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias), d2);
+        // (the sub-scale times 2^8 first, which f16 holds exactly whatever d is)
+        sp[0] = __hmul2(__hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias), up2), d2);
+        sp[1] = __hmul2(__hmul2(__hsub2(umma::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias), up2), d2);
         check.add(sp[0], __float2half2_rn(0.f), 32.f);
         check.add(sp[1], __float2half2_rn(0.f), 32.f);
     }

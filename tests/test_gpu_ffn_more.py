@@ -170,6 +170,27 @@ def test_derivatives_far_out(act, dtype):
     check(dx[near], p.z, p.err + extra, p.walk + extra, dtype, "dx")
 
 
+@pytest.mark.parametrize("fmt", ["q4_k", "q5_k", "q6_k"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_blocks_of_zeros_behind_any_scale(fmt, dtype):
+    """Sub-scales (and minimums) of 0 make zeros, whatever the block's scale: nothing there is out of range."""
+    N, K, M = 130, 768, 40
+    w = Weights(fmt, 3, N, K)
+    raw = w.bytes.view(N, -1, ffn_ref.BYTES[fmt]).clone()
+    at, zero = (208, slice(192, 208)) if fmt == "q6_k" else (0, slice(4, 16))
+    raw[:, 1, zero] = 0
+    out = []
+    x, dy = rows(4, M, K, dtype), rows(5, M, N, dtype)
+    for d in (0.0, 300.0, 65504.0):
+        for i in (at,) if fmt == "q6_k" else (0, 2):
+            raw[:, 1, i:i + 2] = torch.tensor(np.frombuffer(np.float16(d).tobytes(), np.uint8).copy(), device="cuda")
+        b = raw.view(N, -1)
+        out.append([mmq.mmq_project(x, b, fmt, N), mmq.mmq_project(x[:9], b, fmt, N), mmq.mmq_project_backward(dy, b, fmt, K)])
+        clean()
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0], other))
+
+
 def test_weights_that_a_call_before_the_last_has_written():
     """The outputs of a long call are the weights of a short one, with another call between them: few rows, whose weights are
     asked for early, but never before the kernels up to the last but one have ended."""
