@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import ffn_ref
-from test_gpu_ffn import ACT_ERR, DT, Product, Weights, check, clean, mmq, rows
+from test_gpu_ffn import ACT_ERR, DT, UNIT, Product, Weights, backward, check, clean, gated, mmq, project, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -246,3 +246,107 @@ def test_a_wait_that_gives_up_ends_the_call(fmt, dtype, call):
         mmq.mmq_debug_set_wait_limit(-1)
     assert torch.equal(run(), want)
     clean()
+
+
+def weights_off(fmt, w, M):
+    """What tiles make of the weights themselves, forward, less the weights: rows of the identity, M at a time, take them one
+    by one, and a residual leaves of them what outputs in 16 bits would not show."""
+    N, K = w.N, w.K
+    out = {}
+    for dtype in ("f16", "bf16"):
+        near = w.v.T.contiguous().to(DT[dtype])
+        eye = torch.eye(K, device="cuda", dtype=DT[dtype])
+        y = torch.cat([mmq.mmq_project(eye[i:i + M], w.bytes, fmt, N, residual=-near[i:i + M]) for i in range(0, K, M)])
+        clean()
+        out[dtype] = (y.double() - (w.v.T - near.double())).T
+        # (the outputs' rounding of what is left)
+        out[dtype] = (out[dtype].abs() - (UNIT[dtype] * y.double().abs().T + (2.0 ** -25 if dtype == "f16" else 0.0))).clamp(min=0)
+    return out
+
+
+def close(fmt, w, off, scale, least):
+    """Each weight within its bound: rounded once, 2^-11; what the minimum leaves of the nearest number of scales, `rest`, twice and its two
+    parts before, 2^-11 each; for bf16 rows the scale's product with what is left of a code, 2^-11; numbers below f16's normal ones 2^-33."""
+    size, rest, small = w.v.abs(), torch.zeros_like(w.v), 4 * 2.0 ** -33
+    if least is not None:
+        by = least / scale.clamp(min=1e-300)
+        rest = torch.where(by <= 1000, (0.5 + by * 2.0 ** -9) * scale, least + 1000 * scale)
+        rest = rest + 2.0 ** -10 * least
+    for dtype, t in off.items():
+        bound = 2.0 ** -11 * (size + 3 * rest + (size + rest if dtype == "bf16" and fmt != "q8_0" else 0)) * 1.01 + small
+        worst = float((t / bound).max())
+        assert worst <= 1.0, f"{dtype}: a weight is {worst:.3g} of its bound off"
+
+
+@pytest.mark.parametrize("M", [32, 256])
+@pytest.mark.parametrize("fmt", ["q4_k", "q5_k"])
+@pytest.mark.parametrize("kind", ["any", "centred", "far", "sizes"])
+def test_every_weight_with_a_minimum(fmt, kind, M):
+    """Scales and minimums of either sign, of 0, far apart (a minimum of more than a thousand scales), from the smallest up to 250."""
+    N, K = 72, 512
+    rng = np.random.default_rng(4)
+    B = K // 256
+    sc, mn = (rng.integers(0, 64, (N, B, 8)).astype(np.uint8) for _ in range(2))
+    q = rng.integers(0, 16 if fmt == "q4_k" else 32, (N, B, 8, 32)).astype(np.uint8)
+    d, dmin = (rng.uniform(1e-4, 2e-3, (N, B)) * rng.choice([-1, 1], (N, B)) for _ in range(2))
+    if kind == "centred":
+        mn, dmin = sc, d * (7.5 if fmt == "q4_k" else 15.5)
+    elif kind == "far":
+        d = 2.0 ** rng.integers(-24, -8, (N, B)) * rng.choice([-1, 1], (N, B))
+        dmin = np.clip(d * 2.0 ** rng.uniform(-6, 14, (N, B)), -3.9, 3.9)
+    elif kind == "sizes":
+        by = np.logspace(-5, np.log10(250), N)[:, None] / (63 * (32 if fmt == "q5_k" else 16) + 63)
+        d, dmin = (by * rng.choice([-1, 1], (N, B)) for _ in range(2))
+    d, dmin = (t.astype(np.float16) for t in (d, dmin))
+    w = Weights.__new__(Weights)
+    raw = pack(fmt, d, dmin, sc, mn, q)
+    w.v, w.size = (torch.from_numpy(t).cuda() for t in ffn_ref.values(fmt, raw))
+    w.fmt, w.N, w.K, w.bytes = fmt, N, K, torch.from_numpy(raw).cuda()
+    scale, least = (torch.from_numpy(np.abs(t.astype(np.float64)[..., None] * u).reshape(N, -1).repeat(32, 1)).cuda()
+                    for t, u in ((d, sc), (dmin, mn)))
+    close(fmt, w, weights_off(fmt, w, M), scale, least)
+
+
+@pytest.mark.parametrize("M", [32, 256])
+@pytest.mark.parametrize("fmt", ["q6_k", "q8_0"])
+@pytest.mark.parametrize("kind", ["any", "sizes"])
+def test_every_weight_without_a_minimum(fmt, kind, M):
+    N, K = 72, 512
+    w = Weights(fmt, 3, N, K)
+    if kind == "sizes":
+        raw = w.bytes.cpu().numpy().reshape(N, -1, ffn_ref.BYTES[fmt]).copy()
+        by = np.logspace(-5, np.log10(250), N)[:, None] / (128 * 32 if fmt == "q6_k" else 128)
+        at = 208 if fmt == "q6_k" else 0
+        raw[:, :, at:at + 2] = np.broadcast_to(by, raw.shape[:2]).astype(np.float16)[..., None].view(np.uint8)
+        w.bytes = torch.from_numpy(raw.reshape(N, -1)).cuda()
+        w.v = torch.from_numpy(ffn_ref.values(fmt, raw.reshape(N, -1))[0]).cuda()
+    close(fmt, w, weights_off(fmt, w, M), None, None)
+
+
+@pytest.mark.parametrize("fmt", ["q4_k", "q5_k", "q6_k", "q8_0"])
+def test_f16_rows_report_weights_out_of_range(fmt):
+    N, K, at = 150, 512, {"q6_k": 208}.get(fmt, 0)
+    raw = Weights(fmt, 3, N, K).bytes.view(N, -1, ffn_ref.BYTES[fmt]).clone()
+    x, dy, keep = rows(4, 40, K, "f16"), rows(5, 40, N, "f16"), [n for n in range(N) if n != 70]
+    if fmt in ("q4_k", "q5_k"):
+        raw[70, 1, 4:8] |= 16  # (sub-scales that are not all 0)
+    good = mmq.mmq_project(x, raw.view(N, -1), fmt, N)
+    clean()
+    raw[70, 1, at:at + 2] = torch.tensor(np.frombuffer(np.float16(60000.0).tobytes(), np.uint8).copy(), device="cuda")
+    bad = mmq.mmq_project(x, raw.view(N, -1), fmt, N)
+    torch.cuda.synchronize()
+    assert mmq.mmq_get_device_error() == -11
+    assert torch.equal(good[:, keep], bad[:, keep])
+    mmq.mmq_project_backward(dy, raw.view(N, -1), fmt, K)
+    torch.cuda.synchronize()
+    assert mmq.mmq_get_device_error() == -11
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("K", [128, 384, 640, 1152])
+def test_q8_0_of_an_odd_number_of_128_values(dtype, K):
+    """Rows off 16 bytes whose last chunk is a half: steps of 128 values, of which it has one."""
+    for M, N in ((3, 40), (21, 131), (128, 300), (200, 70)):
+        project("q8_0", dtype, M, N, K, seed=K)
+        gated("q8_0", dtype, M, N, K, seed=K)
+        backward("q8_0", dtype, M, N, K, 1, seed=K)
