@@ -21,7 +21,8 @@ struct Deal {
 // where that takes longer (a 64-value step of 256 weight rows: 16-bit rows 0.55, backward 0.4, of Q6_K 0.9, f32 rows
 // 1.1).  A unit's output 1.5 and 0.02 for each row of x.  What cutting costs: a counter's trip, 3, and a part written and
 // `parts` read back by the last to arrive, 0.02 for each row and part (525 x 469 x 9472 in 25 parts a unit: 85 of 106 us).
-// Smaller tiles are more units, which share fewer parts each but turn the same weights to f16 on more SMs.
+// Smaller tiles are more units, which share fewer parts each but turn the same weights to f16 on more SMs.  (Q5_K counts as Q4_K and
+// f16 rows as bf16, a little too cheap.)
 Deal deal(long long M, long long pairs, int chunks, double pieces, int nt_most, int fmt, bool split, bool back, int sms) {
     Deal best;
     const double weights = split ? 1.1 : fmt == FMT_Q6_K ? 0.9 : back ? 0.4 : 0.55;
@@ -176,6 +177,11 @@ int stream(const Call& c, cudaStream_t s) {
 }  // namespace
 
 int ffn_launch(const Call& c, cudaStream_t s) {
+    // Up to 16 rows, forward, as a stream.  Measured at 1 / 8 / 16 rows against these tiles (us): project 3584 x 18944 of Q6_K 22 / 25 /
+    // 29 against 37 / 37 / 38, 512 x 3584 of Q8_0 in f32 4.8 / 6.6 / 7.7 against 19, gated 18944 x 3584 of Q6_K in f16 32 / 36 / 56
+    // against 58, in f32 of Q4_K 26 / 36 / 55 against 57, of Q4_K in bf16 22 / 30 / 45 against 38: there alone the tiles would be
+    // faster from 13 rows on, but round the weights.  17 rows take the tiles' time.  Backward all rows take tiles: the stream's order of
+    // the reduction is along a weight row.
     if (!c.backward && c.M <= STREAM_ROWS) return stream(c, s);
     const bool split = c.dtype == MMQ_F32;
     const int terms = split ? 2 : 1;

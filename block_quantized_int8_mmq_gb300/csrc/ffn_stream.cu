@@ -10,7 +10,7 @@
 // the blocks' sums of x (16 values of the reduction: eight sums in two terms): one product a chunk.
 // The products leave the tensor core every 32 values (16 for Q6_K).
 // Measured, weights not in L2: gated 1 x 18944 x 3584 of Q4_K 22.5 us (3.4 TB/s), 1 x 3584 x 18944 of Q8_0 18.8 (3.8 TB/s), what
-// starts and ends included; 1 x 512 x 3584 4.5.
+// starts and ends included; 1 x 512 x 3584 4.8.
 //
 // A CTA is `groups` runs of 16 weight rows (gate and up of the same columns are two) times `splits` shares of the
 // reduction, added up in shared memory in their order.  Few columns and a long reduction: a cluster of CTAs shares it, and

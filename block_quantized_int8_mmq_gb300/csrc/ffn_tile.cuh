@@ -16,9 +16,10 @@
 // every 128 values of the reduction: the tensor core's additions round towards zero, and over a long sum that
 // would be more than f32 allows.
 //
-// Bound: the tensor cores at 192 rows (a 64-value step 0.50 us of 0.59; gated 2048 x 18944 x 3584 of Q4_K, bf16, 360 us, 1.54
-// PFLOP/s, 0.8 of the library's plain product), the weights' way to f16 at few rows (0.55 us a step, Q6_K 0.9, f32 rows 1.1)
-// and for Q5_K and Q6_K at all; backward 0.65 us a step, both operands read from shared memory (2048 rows 386 us, 1.44 PFLOP/s).
+// Bound: the tensor cores at 192 rows (a 64-value step 0.50 us of 0.59; gated 2048 x 18944 x 3584 of Q4_K, bf16, 371 us in a graph
+// and 400 called back to back, under the power cap: 1.50 and 1.39 PFLOP/s), the weights' way to f16 at few rows (0.55 us a step, f32
+// rows 1.1; Q6_K 0.9: 9.4 instructions a weight, the ALU pipe 0.66 busy) and for Q5_K and Q6_K at all; backward 0.65 us a step,
+// both operands read from shared memory (2048 rows 390 to 400 us, 1.4 PFLOP/s).
 //
 // The work is dealt unit by unit in rounds; where the last round would leave too many SMs idle it and the one before
 // are laid end to end instead and cut into equal runs.  A unit that is cut leaves its parts in scratch memory, and the
@@ -36,7 +37,7 @@ static __device__ unsigned g_ffn_tile_error;  // of each translation unit its ow
 static __device__ unsigned long long g_ffn_tile_wait_limit = umma::WAIT_LIMIT_NS;
 
 // SPLIT: steps between two moves of the accumulators.  Measured two against four: 8.4e-7 -> 3.8e-7 of a projection's norm,
-// 66 -> 69 us (517 x 3584 x 3584 of Q5_K).
+// 66 -> 69 us (517 x 3584 x 3584 of Q5_K; 70 by now).
 constexpr int PERIOD = 2;
 
 // The pieces of work of a CTA: (unit, first chunk, end).

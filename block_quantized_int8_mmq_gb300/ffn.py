@@ -8,7 +8,9 @@ both to their inputs.
     dx = mmq_gated_backward(dh, gate, up, w_gate, w_up, "q4_k", K)  # gate, up: kept by mmq_gated
 
 Rows are float32, bfloat16 or float16 and enter unquantized; weights are uint8 blocks as for mmq_gemm_*.
-The tensors' device has to be the current one.
+The tensors' device has to be the current one.  The calls do not record themselves for autograd: outputs carry no
+graph, whether inputs require gradients or not, and a program that wants one calls the ways back from a
+torch.autograd.Function of its own (examples/feed_forward.py has one).
 """
 from __future__ import annotations
 
